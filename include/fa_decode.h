@@ -255,6 +255,29 @@ int fa_decode_run_head_scales(fa_decode_plan_t plan, const void* q, const void* 
                               const float* v_head_scales, void* o, float* lse,
                               void* cuda_stream);
 
+/* run with one FP8 scale per block of tokens and kv head: like fa_decode_run
+ * for a plan whose kv dtype is E4M3, but the K (V) elements of page p and kv
+ * head h are dequantised with k_block_scales[p * num_kv_heads + h] - the block
+ * is a page's page_size tokens, so scales follow the cache along its length
+ * at 8 bytes per (page, kv head), a sixteenth of fa_decode_run_token_scales'.
+ * fa_append_run_block_scales writes such a cache.
+ *
+ *  k_block_scales, v_block_scales  [num_pages, num_kv_heads] float32, device,
+ *                      4-byte aligned: the element has the value code * scale.
+ *                      A scale is 0 (the block's values are 0) or a positive
+ *                      normal number; powers of two are exact, others round
+ *                      the softmax weights once more.  The scales of one
+ *                      kv head's blocks may differ by up to 2^64.
+ * Other arguments as fa_decode_run (sm_scale <= 0 selects 1/sqrt(head_dim)).
+ * Every plan kind takes it (plain, multi-token, ragged query rows) on the
+ * shapes and dtypes built for it; plans whose kv dtype is not E4M3 return
+ * FA_ERR_UNSUPPORTED, NULL scales and a current device that is not the
+ * plan's FA_ERR_INVALID_ARG. */
+int fa_decode_run_block_scales(fa_decode_plan_t plan, const void* q, const void* paged_kv,
+                               int64_t num_pages, float sm_scale, const float* k_block_scales,
+                               const float* v_block_scales, void* o, float* lse,
+                               void* cuda_stream);
+
 /* run with a unified max (page "FlashDecoding + FlashInfer", section
  * "FlashDecoding++", item 1 "Async-softmax with unified max"): instead of a
  * running maximum per query head, every weight is exp(s - max_bound) for a
@@ -522,6 +545,132 @@ typedef struct {
   int64_t staged_uploads;
 } fa_library_stats;
 int fa_library_get_stats(fa_library_stats* stats);
+
+/* ---- append (writing the paged cache) -----------------------------------
+ *
+ * Writes new tokens' K and V into the pages of the cache that the decode
+ * calls read, rotating K (and, on request, q) at the tokens' positions and
+ * rounding once into the cache's type.  The batch is described as for
+ * fa_decode_plan, after the append: request i's last n_i tokens are the new
+ * ones, so that the same indptr, indices and last_page_len plan the decode
+ * that follows.  (The pages describe the paged cache and its FP8 form - "Paged
+ * attention (vLLM)" in "FlashDecoding + FlashInfer", "Production War Story" in
+ * "FlashInfer vs FlashAttention-3" - but not the step that fills it.)
+ *
+ * Rotation (rotary position embedding): with a_j = position * inv_freq[j],
+ * each pair (x1, x2) of the first rotary_dim dims becomes
+ * (x1 cos a_j - x2 sin a_j, x2 cos a_j + x1 sin a_j); the pairs are dims
+ * (j, j + rotary_dim / 2), or (2j, 2j + 1) when interleaved.  The angles keep
+ * full precision at any position.
+ *
+ * E4M3 caches: an element's code is x / scale rounded to nearest, saturated
+ * at +-448 for finite x; infinities and NaN are stored as NaN and never enter
+ * a scale.
+ *
+ * Not written: slots before a request's first new token (but for codes
+ * re-rounded under a grown block scale), slots after its last, pages without
+ * new tokens, their scales. */
+typedef struct fa_append_plan_s* fa_append_plan_t;
+
+/* [rows, heads, head_dim] of the plan's q dtype: the innermost dim contiguous,
+ * the strides in elements.  data and both strides (in bytes) are multiples of
+ * 16, so a slice of a fused projection's output can be passed as it is. */
+typedef struct {
+  const void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} fa_rows;
+
+/* Upper bound of the workspace fa_append_plan needs for a batch with
+ * num_tokens new tokens; 0 for invalid arguments. */
+size_t fa_append_workspace_size(int batch, int64_t num_tokens);
+
+/* plan: where the new tokens of a batch go.
+ *
+ *  indptr_host, indices_dev, last_page_len_host, batch, num_qo_heads,
+ *  num_kv_heads, head_dim, page_size, q_dtype, kv_dtype, workspace, stream:
+ *                      as fa_decode_plan, the new tokens included in the
+ *                      lengths.  num_qo_heads may be any multiple of
+ *                      num_kv_heads.  indices_dev is kept by pointer and read
+ *                      by every run.  A page that receives tokens belongs to
+ *                      one request alone: where two requests (or two entries
+ *                      of one) append to the same page, the contents of that
+ *                      page's new tokens and its scales are unspecified.
+ *  append_indptr_host  [batch + 1] int32, host: request i's new tokens are
+ *                      rows append_indptr[i] .. append_indptr[i+1] of k, v and
+ *                      q; 0 first, non-decreasing, n_i <= len_i.  n_i = 0
+ *                      leaves the request alone.
+ *  position_offset_host  [batch] int32, host, or NULL: added to a token's
+ *                      index in its request to give its position (e.g. the
+ *                      tokens of a prefix that a cascade plan holds apart);
+ *                      >= 0, offset + len below 2^31.
+ *  inv_freq_host       [rotary_dim / 2] double, host, finite: radians per
+ *                      position of each pair.  Read during the call.
+ *  rotary_dim          dims that rotate, a multiple of 16 up to head_dim
+ *                      (FA_ERR_UNSUPPORTED otherwise); 0: no rotation.
+ * Built for page_size 16, head_dim 64 and 128 and fa_decode_plan's dtype
+ * pairs.  Errors as fa_decode_plan. */
+int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
+                   const int32_t* last_page_len_host, const int32_t* append_indptr_host,
+                   const int32_t* position_offset_host, int batch, int num_qo_heads,
+                   int num_kv_heads, int head_dim, int page_size, fa_dtype q_dtype,
+                   fa_dtype kv_dtype, const double* inv_freq_host, int rotary_dim,
+                   int interleaved, void* workspace_dev, size_t workspace_bytes,
+                   void* cuda_stream, fa_append_plan_t* out_plan);
+
+/* run: append k and v [rows, num_kv_heads, head_dim] to the cache.
+ *
+ *  q, q_out   q [rows, num_qo_heads, head_dim] rotated into the contiguous
+ *             q_out, for the decode that follows; NULL q: K and V only.
+ *             q_out may be q itself (contiguous); it overlaps no input
+ *             otherwise.
+ *  paged_kv   as fa_decode_run, written; num_pages its leading extent.  A page
+ *             id outside [0, num_pages) is skipped (its rows of q_out are
+ *             written) and sets bit 0 of the device-check word
+ *             (fa_append_check).
+ *  k_scale,   per-tensor scales of an E4M3 cache, positive and finite; 1 for
+ *  v_scale    other kv types (FA_ERR_INVALID_ARG otherwise).
+ * One kernel on cuda_stream, no allocation, no synchronisation: it can be
+ * captured into a CUDA graph.  Results are bitwise reproducible.  Running a
+ * plan again writes the same slots again.
+ * Errors: FA_ERR_INVALID_ARG (NULL or misaligned pointers and strides, scales,
+ * a current device that is not the plan's), FA_ERR_CUDA. */
+int fa_append_run(fa_append_plan_t plan, const fa_rows* k, const fa_rows* v, const fa_rows* q,
+                  void* q_out, void* paged_kv, int64_t num_pages, float k_scale, float v_scale,
+                  void* cuda_stream);
+
+/* run into an E4M3 cache with one scale per kv head, given:
+ * k_head_scales, v_head_scales [num_kv_heads] float32, device, positive (as
+ * fa_decode_run_head_scales reads them). */
+int fa_append_run_head_scales(fa_append_plan_t plan, const fa_rows* k, const fa_rows* v,
+                              const fa_rows* q, void* q_out, void* paged_kv, int64_t num_pages,
+                              const float* k_head_scales, const float* v_head_scales,
+                              void* cuda_stream);
+
+/* run into an E4M3 cache with one scale per token and kv head, written here:
+ * k_scales, v_scales [num_pages, num_kv_heads, page_size] float32, device (as
+ * fa_decode_run_token_scales reads them): the largest finite magnitude of the
+ * token's row over 448, at least 2^-126, or 0 for a row of zeros. */
+int fa_append_run_token_scales(fa_append_plan_t plan, const fa_rows* k, const fa_rows* v,
+                               const fa_rows* q, void* q_out, void* paged_kv, int64_t num_pages,
+                               float* k_scales, float* v_scales, void* cuda_stream);
+
+/* run into an E4M3 cache with one scale per page and kv head, read and
+ * written here: k_scales, v_scales [num_pages, num_kv_heads] float32, device
+ * (as fa_decode_run_block_scales reads them).  The scale is the smallest
+ * power of two s >= 2^-126 with every finite magnitude of the page's new
+ * tokens at most 448 s (0 if all are 0).  A page that held tokens of the
+ * request before keeps the larger of its scale and that; where it grows, the
+ * codes it held are re-rounded to the same values under the new scale
+ * (exactly, but for values that become subnormal). */
+int fa_append_run_block_scales(fa_append_plan_t plan, const fa_rows* k, const fa_rows* v,
+                               const fa_rows* q, void* q_out, void* paged_kv, int64_t num_pages,
+                               float* k_scales, float* v_scales, void* cuda_stream);
+
+/* As fa_decode_check, for an append plan (bit 0: a page id out of range). */
+int fa_append_check(fa_append_plan_t plan, void* cuda_stream, int* flags);
+
+int fa_append_plan_destroy(fa_append_plan_t plan);
 
 /* ---- cascade decode (shared prefix) ------------------------------------
  *

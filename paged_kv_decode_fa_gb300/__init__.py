@@ -23,6 +23,7 @@ __all__ = [
     "FA_OK", "FaError", "DecodePlan", "plan", "plan_multi_token", "plan_ragged_q", "run",
     "merge_states",
     "CascadePlan", "cascade_plan",
+    "RotaryTable", "AppendPlan", "plan_append", "append_workspace_size",
     "workspace_size", "plan_work_host", "plan_work_host_buckets",
     "BatchDecodeWithPagedKVCacheWrapper",
     "LIB_PATH", "EXPORTED_SYMBOLS", "library", "library_stats",
@@ -44,6 +45,10 @@ EXPORTED_SYMBOLS = (
     "fa_decode_plan_ragged_q", "fa_decode_workspace_size_ragged_q", "fa_cascade_run_scaled",
     "fa_plan_work_host_buckets",
     "fa_decode_run_head_scales", "fa_plan_work_host_heads",
+    "fa_decode_run_block_scales",
+    "fa_append_workspace_size", "fa_append_plan", "fa_append_run", "fa_append_run_head_scales",
+    "fa_append_run_token_scales", "fa_append_run_block_scales", "fa_append_check",
+    "fa_append_plan_destroy",
 )
 
 FA_OK = 0
@@ -77,6 +82,12 @@ class PlanInfo(ctypes.Structure):
             v = getattr(self, n)
             out[n] = list(v) if isinstance(v, ctypes.Array) else v
         return out
+
+
+class Rows(ctypes.Structure):
+    """fa_rows: [rows, heads, head_dim] with element strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
 
 
 class LibraryStats(ctypes.Structure):
@@ -116,6 +127,25 @@ def _load() -> ctypes.CDLL:
     lib.fa_decode_run_token_scales.restype = i32
     lib.fa_decode_run_head_scales.argtypes = [P, P, P, i64, f32, P, P, P, P, P]
     lib.fa_decode_run_head_scales.restype = i32
+    lib.fa_decode_run_block_scales.argtypes = [P, P, P, i64, f32, P, P, P, P, P]
+    lib.fa_decode_run_block_scales.restype = i32
+    rows = ctypes.POINTER(Rows)
+    lib.fa_append_workspace_size.argtypes = [i32, i64]
+    lib.fa_append_workspace_size.restype = sz
+    lib.fa_append_plan.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, i32, i32,
+                                   P, sz, P, ctypes.POINTER(P)]
+    lib.fa_append_plan.restype = i32
+    lib.fa_append_run.argtypes = [P, rows, rows, rows, P, P, i64, f32, f32, P]
+    lib.fa_append_run.restype = i32
+    for name in ("fa_append_run_head_scales", "fa_append_run_token_scales",
+                 "fa_append_run_block_scales"):
+        f = getattr(lib, name)
+        f.argtypes = [P, rows, rows, rows, P, P, i64, P, P, P]
+        f.restype = i32
+    lib.fa_append_check.argtypes = [P, P, ctypes.POINTER(i32)]
+    lib.fa_append_check.restype = i32
+    lib.fa_append_plan_destroy.argtypes = [P]
+    lib.fa_append_plan_destroy.restype = i32
     lib.fa_decode_run_unified_max.argtypes = [P, P, P, i64, f32, f32, f32, f32, P, P, P]
     lib.fa_decode_run_unified_max.restype = i32
     lib.fa_decode_unified_max_fallbacks.argtypes = [P, P, ctypes.POINTER(i32)]
@@ -346,6 +376,22 @@ class DecodePlan:
             _stream_handle(stream)), "fa_decode_run_head_scales")
         return out, lse
 
+    def run_block_scales(self, q: torch.Tensor, paged_kv: torch.Tensor, k_scales: torch.Tensor,
+                         v_scales: torch.Tensor, *, sm_scale: float | None = None,
+                         out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                         return_lse: bool = True, stream=None):
+        """Decode over an E4M3 cache with one scale per block of tokens (a page)
+        and kv head: k_scales / v_scales [num_pages, num_kv_heads] float32 CUDA
+        tensors, as AppendPlan.run_block_scales writes them; returns (o, lse)."""
+        out, lse = self._outputs(q, paged_kv, out, lse, return_lse)
+        _check_scales((k_scales, v_scales), (paged_kv.shape[0], self.num_kv_heads), paged_kv)
+        _check(_L().fa_decode_run_block_scales(
+            self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
+            0.0 if sm_scale is None else float(sm_scale), k_scales.data_ptr(),
+            v_scales.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+            _stream_handle(stream)), "fa_decode_run_block_scales")
+        return out, lse
+
     def unified_max_fallbacks(self, stream=None) -> int:
         """Synchronise; return and clear the count of unified-max re-centrings."""
         n = ctypes.c_int(0)
@@ -422,6 +468,14 @@ class DecodePlan:
         event once from torch before handing it over."""
         _check(_L().fa_decode_set_timing_events(self._h, *_event_handles(before, after)),
                "fa_decode_set_timing_events")
+
+
+def _check_scales(scales, shape, paged_kv) -> None:
+    for s in scales:
+        if (s.dtype != torch.float32 or tuple(s.shape) != shape or not s.is_contiguous()
+                or s.device != paged_kv.device):
+            raise ValueError(f"scales must be contiguous float32 tensors {list(shape)} on the "
+                             "device of paged_kv")
 
 
 def _event_handles(before, after):
@@ -713,6 +767,200 @@ def cascade_plan(prefix_indices: torch.Tensor, indptr, indices: torch.Tensor, la
         _stream_handle(stream), ctypes.byref(handle)), "fa_cascade_plan")
     return CascadePlan(handle.value, (prefix_indices, indices, workspace), q_data_type,
                        (B, num_qo_heads, num_kv_heads, head_dim), kv_dtype=kv_data_type)
+
+
+class RotaryTable:
+    """The rotation of a model's positions: rotary_dim dims turn, pair j by
+    position * inv_freq[j] radians.  inv_freq defaults to
+    theta ** (-2 j / rotary_dim); pass it (rotary_dim / 2 values, kept in 64
+    bits) for scaled variants.  interleaved: pairs (2j, 2j + 1) instead of
+    (j, j + rotary_dim / 2)."""
+
+    def __init__(self, rotary_dim: int, theta: float = 10000.0, *, inv_freq=None,
+                 interleaved: bool = False):
+        if rotary_dim <= 0 or rotary_dim % 16:
+            raise ValueError("rotary_dim must be a positive multiple of 16")
+        if inv_freq is None:
+            inv_freq = float(theta) ** (-2.0 * np.arange(rotary_dim // 2) / rotary_dim)
+        elif isinstance(inv_freq, torch.Tensor):
+            inv_freq = inv_freq.detach().to("cpu", torch.float64).numpy()
+        self.inv_freq = np.array(inv_freq, dtype=np.float64)
+        if self.inv_freq.shape != (rotary_dim // 2,) or not np.isfinite(self.inv_freq).all():
+            raise ValueError(f"inv_freq must be {rotary_dim // 2} finite values")
+        self.rotary_dim = int(rotary_dim)
+        self.interleaved = bool(interleaved)
+
+
+def append_workspace_size(batch: int, num_tokens: int) -> int:
+    """Bytes of device workspace a plan_append of this batch may need."""
+    n = _L().fa_append_workspace_size(batch, num_tokens)
+    if n == 0:
+        raise ValueError("invalid batch or token count")
+    return int(n)
+
+
+class AppendPlan:
+    """A planned append: where a batch's new tokens go in the paged cache.
+    Keeps the index tensor and the workspace alive."""
+
+    def __init__(self, handle, indices, workspace, q_dtype, kv_dtype, shape, num_tokens):
+        self._h = handle
+        self._indices = indices
+        self._workspace = workspace
+        self.q_dtype = q_dtype
+        self.kv_dtype = kv_dtype
+        self.batch, self.num_qo_heads, self.num_kv_heads, self.head_dim, self.page_size = shape
+        self.num_tokens = num_tokens
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h:
+            _L().fa_append_plan_destroy(h)
+            self._h = None
+
+    def run(self, k: torch.Tensor, v: torch.Tensor, paged_kv: torch.Tensor, *,
+            q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+            k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+        """Append k and v [num_tokens, Hkv, D] (innermost dim contiguous, other
+        strides free) to the cache; with q [num_tokens, Hq, D], also rotate it
+        and return it (in q_out, contiguous; q itself to rotate in place).
+        k_scale / v_scale are an E4M3 cache's per-tensor scales."""
+        rows, q_out = self._rows(k, v, paged_kv, q, q_out)
+        _check(_L().fa_append_run(
+            self._h, *rows, q_out.data_ptr() if q_out is not None else None,
+            paged_kv.data_ptr(), paged_kv.shape[0], float(k_scale), float(v_scale),
+            _stream_handle(stream)), "fa_append_run")
+        return q_out
+
+    def run_head_scales(self, k: torch.Tensor, v: torch.Tensor, paged_kv: torch.Tensor,
+                        k_scales: torch.Tensor, v_scales: torch.Tensor, *,
+                        q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                        stream=None):
+        """As run, into an E4M3 cache with one given scale per kv head:
+        k_scales / v_scales [num_kv_heads] float32."""
+        return self._run_scales("fa_append_run_head_scales", (self.num_kv_heads,), k, v,
+                                paged_kv, k_scales, v_scales, q, q_out, stream)
+
+    def run_token_scales(self, k: torch.Tensor, v: torch.Tensor, paged_kv: torch.Tensor,
+                         k_scales: torch.Tensor, v_scales: torch.Tensor, *,
+                         q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                         stream=None):
+        """As run, into an E4M3 cache with one scale per token and kv head, which
+        it writes to k_scales / v_scales [num_pages, num_kv_heads, page_size]
+        float32."""
+        shape = (paged_kv.shape[0], self.num_kv_heads, self.page_size)
+        return self._run_scales("fa_append_run_token_scales", shape, k, v, paged_kv, k_scales,
+                                v_scales, q, q_out, stream)
+
+    def run_block_scales(self, k: torch.Tensor, v: torch.Tensor, paged_kv: torch.Tensor,
+                         k_scales: torch.Tensor, v_scales: torch.Tensor, *,
+                         q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                         stream=None):
+        """As run, into an E4M3 cache with one power-of-two scale per page and
+        kv head, k_scales / v_scales [num_pages, num_kv_heads] float32, which
+        it writes - and raises, re-rounding the page, where a page goes on."""
+        return self._run_scales("fa_append_run_block_scales",
+                                (paged_kv.shape[0], self.num_kv_heads), k, v, paged_kv, k_scales,
+                                v_scales, q, q_out, stream)
+
+    def check(self, stream=None) -> int:
+        """Synchronise and return the device-check flags (0 = clean)."""
+        flags = ctypes.c_int(0)
+        st = _L().fa_append_check(self._h, _stream_handle(stream), ctypes.byref(flags))
+        if st not in (FA_OK, -5):
+            _check(st, "fa_append_check")
+        return int(flags.value)
+
+    def _run_scales(self, name, shape, k, v, paged_kv, k_scales, v_scales, q, q_out, stream):
+        rows, q_out = self._rows(k, v, paged_kv, q, q_out)
+        _check_scales((k_scales, v_scales), shape, paged_kv)
+        _check(getattr(_L(), name)(
+            self._h, *rows, q_out.data_ptr() if q_out is not None else None,
+            paged_kv.data_ptr(), paged_kv.shape[0], k_scales.data_ptr(), v_scales.data_ptr(),
+            _stream_handle(stream)), name)
+        return q_out
+
+    def _rows(self, k, v, paged_kv, q, q_out):
+        """Check the tensors against the plan; fa_rows of k, v and q, and q_out."""
+        T, Hkv, D = self.num_tokens, self.num_kv_heads, self.head_dim
+        if paged_kv.dtype != self.kv_dtype:
+            raise TypeError("paged_kv dtype differs from the plan")
+        if (paged_kv.dim() != 5 or tuple(paged_kv.shape[1:]) != (2, self.page_size, Hkv, D)
+                or not paged_kv.is_contiguous() or paged_kv.device != self._workspace.device):
+            raise ValueError("paged_kv must be a contiguous CUDA tensor "
+                             "[num_pages, 2, page_size, num_kv_heads, head_dim] on the plan's "
+                             "device")
+        out = [self._row(k, (T, Hkv, D)), self._row(v, (T, Hkv, D)), None]
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out without q")
+            return out, None
+        shape = (T, self.num_qo_heads, D)
+        out[2] = self._row(q, shape)
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        elif (q_out.dtype != q.dtype or tuple(q_out.shape) != shape
+              or not q_out.is_contiguous() or q_out.device != q.device):
+            raise ValueError(f"q_out must be a contiguous tensor {list(shape)} of q's dtype on "
+                             "its device")
+        return out, q_out
+
+    def _row(self, t, shape):
+        if t.dtype != self.q_dtype:
+            raise TypeError("k / v / q dtype differs from the plan")
+        if tuple(t.shape) != shape or t.device != self._workspace.device:
+            raise ValueError(f"k / v / q must be CUDA tensors on the plan's device, here "
+                             f"{list(shape)}")
+        if t.numel() == 0:
+            return Rows(None, 0, 0)
+        # a stride that is never taken may be anything
+        token = t.stride(0) if shape[0] > 1 else 0
+        head = t.stride(1) if shape[1] > 1 else 0
+        es = t.element_size()
+        if t.stride(2) != 1 or token * es % 16 or head * es % 16 or t.data_ptr() % 16:
+            raise ValueError("k / v / q need a contiguous innermost dim, and an address and "
+                             "strides in whole 16 bytes")
+        return Rows(t.data_ptr(), token, head)
+
+
+def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num_qo_heads: int,
+                num_kv_heads: int, head_dim: int, page_size: int, *, q_data_type=torch.bfloat16,
+                kv_data_type=None, rotary: RotaryTable | None = None, position_offset=None,
+                workspace: torch.Tensor | None = None, stream=None) -> AppendPlan:
+    """Plan the append of append_indptr[i+1] - append_indptr[i] new tokens to
+    request i.  indptr / indices / last_page_len describe the batch after the
+    append, as plan takes them for the decode that follows; the new tokens are
+    each request's last.  rotary: the rotation of k and q (None: none), at the
+    token's index in its request plus position_offset[i]."""
+    kv_data_type = q_data_type if kv_data_type is None else kv_data_type
+    indptr_h, indptr_p, n_indptr = _host_i32_ptr(indptr)
+    last_h, last_p, n_last = _host_i32_ptr(last_page_len)
+    app_h, app_p, n_app = _host_i32_ptr(append_indptr)
+    B = n_indptr - 1
+    if n_last < B or n_app != B + 1:
+        raise ValueError("last_page_len shorter than the batch, or append_indptr not batch + 1 "
+                         "long")
+    off_p = None
+    if position_offset is not None:
+        off_h, off_p, n_off = _host_i32_ptr(position_offset)
+        if n_off != B:
+            raise ValueError("position_offset must have one value per request")
+    if indices.dtype != torch.int32 or not _reachable(indices) or not indices.is_contiguous():
+        raise ValueError("indices must be a contiguous int32 CUDA or page-locked tensor")
+    total = int(np.asarray(app_h)[B]) if B >= 0 else 0
+    if workspace is None:
+        workspace = torch.empty(append_workspace_size(max(B, 0), max(total, 0)),
+                                dtype=torch.uint8, device=_cuda_device(indices))
+    handle = ctypes.c_void_p()
+    _check(_L().fa_append_plan(
+        indptr_p, indices.data_ptr() if indices.numel() else None, last_p if B else None, app_p,
+        off_p, B, num_qo_heads, num_kv_heads, head_dim, page_size, _dtype_code(q_data_type),
+        _dtype_code(kv_data_type), rotary.inv_freq.ctypes.data if rotary else None,
+        rotary.rotary_dim if rotary else 0, int(rotary.interleaved) if rotary else 0,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream_handle(stream), ctypes.byref(handle)), "fa_append_plan")
+    return AppendPlan(handle.value, indices, workspace, q_data_type, kv_data_type,
+                      (B, num_qo_heads, num_kv_heads, head_dim, page_size), total)
 
 
 class BatchDecodeWithPagedKVCacheWrapper:

@@ -237,6 +237,28 @@ bool find_token_scale_kernel(fa_dtype q, fa_dtype kv, int D, int G, DecodeKernel
   return false;
 }
 
+// The per-block-scale kernel of a plan of this shape and kind.
+bool find_block_scale_kernel(fa_dtype q, fa_dtype kv, int D, int G, int q_len, bool ragged,
+                             DecodeKernel* k) {
+  if (kv != FA_DTYPE_E4M3) return false;
+  if (q == FA_DTYPE_F16)
+    return !ragged && q_len == 1 && fadecode::find_block_scale_kernel_f16_e4m3(D, G, k);
+  if (q != FA_DTYPE_BF16) return false;
+  if (ragged) return fadecode::find_block_scale_ragged_q_kernel_bf16_e4m3(D, G, q_len, k);
+  if (q_len > 1) return fadecode::find_block_scale_multi_token_kernel_bf16_e4m3(D, G, q_len, k);
+  return fadecode::find_block_scale_kernel_bf16_e4m3(D, G, k);
+}
+
+// The same for the ragged kernel of requests of `tiles` 8-column tiles (see
+// find_ragged_tiles_kernel).
+bool find_block_scale_tiles_kernel(fa_dtype q, fa_dtype kv, int D, int G, int tiles,
+                                   DecodeKernel* k) {
+  if (q != FA_DTYPE_BF16 || kv != FA_DTYPE_E4M3) return false;
+  if (tiles == 1 || tiles == 4)
+    return fadecode::find_block_scale_ragged_q_kernel_bf16_e4m3(D, G, 8 * tiles / G, k);
+  return fadecode::find_block_scale_ragged_q_tiles_kernel_bf16_e4m3(D, G, tiles, k);
+}
+
 // Whether a decode launch of `func` on `st` may be a programmatic dependent
 // of the stream's previous kernel, and record it as the stream's last decode
 // kernel.  The decode kernels let the next launch in at their start
@@ -307,13 +329,15 @@ int kernel_occupancy(const DecodeKernel& k) {
 }  // namespace
 
 // Kernel variants a plan can launch.
-enum Variant { kPlain = 0, kTokenScales = 1, kUnifiedMax = 2, kNumVariants = 3 };
+enum Variant { kPlain = 0, kTokenScales = 1, kUnifiedMax = 2, kBlockScales = 3, kNumVariants = 4 };
 
 namespace {
 
 // The kernels a plan of these dtypes and shape may launch (kPlain always,
 // the others where built) and the persistent grid's CTAs per SM: the
-// smallest occupancy among them, so that every variant fits the grid.
+// smallest occupancy among them, so that every variant fits the grid (the
+// per-block-scale kernel apart: a grid's CTAs do not wait on one another, so
+// it runs on any grid, and the other variants' grid stays theirs).
 int select_kernels(fa_dtype q_dtype, fa_dtype kv_dtype, int head_dim, int G, int q_len,
                    DecodeKernel (&kv)[kNumVariants], bool (&has)[kNumVariants],
                    int* ctas_per_sm, bool ragged = false) {
@@ -336,6 +360,8 @@ int select_kernels(fa_dtype q_dtype, fa_dtype kv_dtype, int head_dim, int G, int
   kv[kPlain] = base;
   has[kPlain] = true;
   has[kTokenScales] = has[kUnifiedMax] = false;
+  has[kBlockScales] =
+      find_block_scale_kernel(q_dtype, kv_dtype, head_dim, G, q_len, ragged, &kv[kBlockScales]);
   if (q_len == 1 && !ragged) {
     has[kTokenScales] = find_token_scale_kernel(q_dtype, kv_dtype, head_dim, G, &kv[kTokenScales]);
     has[kUnifiedMax] = find_unified_max_kernel(q_dtype, kv_dtype, head_dim, G, &kv[kUnifiedMax]);
@@ -344,7 +370,7 @@ int select_kernels(fa_dtype q_dtype, fa_dtype kv_dtype, int head_dim, int G, int
     if (!has[v]) continue;
     const int occ_v = kernel_occupancy(kv[v]);
     if (occ_v == 0) return FA_ERR_CUDA;
-    occ = std::min(occ, occ_v);
+    if (v != kBlockScales) occ = std::min(occ, occ_v);
   }
   *ctas_per_sm = std::max(1, std::min(occ, kMaxCtasPerSmBound));
   return FA_OK;
@@ -388,10 +414,10 @@ struct fa_decode_plan_s {
   int device = 0;
   int batch = 0, hq = 0, hkv = 0, d = 0, page_size = 0, group = 0;
   fa_dtype q_dtype = FA_DTYPE_F32, kv_dtype = FA_DTYPE_F32;
-  // kern[kPlain] always; kern[kTokenScales] / kern[kUnifiedMax] where
-  // has[...] says the plan's dtypes and shape have that variant built
+  // kern[kPlain] always; the other variants where has[...] says the plan's
+  // dtypes and shape have them built
   DecodeKernel kern[kNumVariants];
-  bool has[kNumVariants] = {true, false, false};
+  bool has[kNumVariants] = {true, false, false, false};
   int num_sms = 0, ctas_per_sm = 0;
   WorkList wl;
   std::vector<int32_t> merge_flat;
@@ -411,7 +437,8 @@ struct fa_decode_plan_s {
   // kern[variant] over the whole work list.
   struct Bucket {
     DecodeKernel kern;
-    MapCache map;
+    DecodeKernel block_kern;  // with per-block scales (plans that have kBlockScales)
+    MapCache map;             // the KV cache's view, the same for both kernels
     int tiles = 0, cta_first = 0, num_ctas = 0, merge_first = 0, num_merge = 0;
   };
   int num_buckets = 0;
@@ -640,13 +667,18 @@ bool plan_buckets(fa_decode_plan_s* plan, const int32_t* indptr, const int32_t* 
   fadecode::BucketPolicy pol;
   pol.group = G;
   pol.widest = nc_max / 8;
-  DecodeKernel kern[kMaxBuckets + 1];
+  DecodeKernel kern[kMaxBuckets + 1], block_kern[kMaxBuckets + 1];
   for (int t = 1; t <= pol.widest; ++t) {
     if (!find_ragged_tiles_kernel(plan->q_dtype, plan->kv_dtype, plan->d, G, t, &kern[t]))
       return false;
     const int occ = std::min(kernel_occupancy(kern[t]), 8);
     if (occ <= 0) return false;
     pol.max_ctas[t] = sms * occ;
+    if (plan->has[kBlockScales] &&
+        (!find_block_scale_tiles_kernel(plan->q_dtype, plan->kv_dtype, plan->d, G, t,
+                                        &block_kern[t]) ||
+         kernel_occupancy(block_kern[t]) <= 0))
+      return false;
   }
   pol.one_tile_own = plan->kv_dtype == FA_DTYPE_E4M3;
   pol.min_own_units = (int64_t)kMinBucketUnitsPerSm * sms;
@@ -669,6 +701,7 @@ bool plan_buckets(fa_decode_plan_s* plan, const int32_t* indptr, const int32_t* 
   for (int b = 0; b < bl.num; ++b) {
     fa_decode_plan_s::Bucket& bk = plan->bucket[b];
     bk.kern = kern[bl.tiles[b]];
+    bk.block_kern = block_kern[bl.tiles[b]];
     bk.tiles = bl.tiles[b];
     bk.cta_first = bl.cta_first[b];
     bk.num_ctas = bl.num_ctas[b];
@@ -728,7 +761,7 @@ static int plan_impl(const int32_t* indptr_host, const int32_t* indices_dev,
     return FA_ERR_CUDA;
   // The persistent grid must fit for every variant a run may launch.
   DecodeKernel kv[kNumVariants];
-  bool has[kNumVariants] = {true, false, false};
+  bool has[kNumVariants] = {true, false, false, false};
   const int sel = select_kernels(q_dtype, kv_dtype, head_dim, G, q_len, kv, has, &occ, ragged);
   if (sel != FA_OK) return sel;
   // query tokens a partial state holds columns for: the kernel's bucket
@@ -879,6 +912,21 @@ int fa_decode_run_head_scales(fa_decode_plan_t plan, const void* q, const void* 
     return FA_ERR_INVALID_ARG;
   return run_impl(plan, kPlain, q, paged_kv, num_pages, sm_scale, 1.f, 1.f, nullptr, nullptr,
                   0.f, o, lse, cuda_stream, k_head_scales, v_head_scales);
+}
+
+int fa_decode_run_block_scales(fa_decode_plan_t plan, const void* q, const void* paged_kv,
+                               int64_t num_pages, float sm_scale, const float* k_scales,
+                               const float* v_scales, void* o, float* lse, void* cuda_stream) {
+  if (!plan) return FA_ERR_INVALID_ARG;
+  if (plan->kv_dtype != FA_DTYPE_E4M3 || !plan->has[kBlockScales]) return FA_ERR_UNSUPPORTED;
+  if (plan->batch > 0 && (!k_scales || !v_scales)) return FA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(k_scales) % 4 || reinterpret_cast<uintptr_t>(v_scales) % 4)
+    return FA_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  if (dev != plan->device) return FA_ERR_INVALID_ARG;
+  return run_impl(plan, kBlockScales, q, paged_kv, num_pages, sm_scale, 1.f, 1.f, k_scales,
+                  v_scales, 0.f, o, lse, cuda_stream);
 }
 
 int fa_merge_states(const void* o_a, const float* lse_a, const void* o_b, const float* lse_b,
@@ -1036,7 +1084,7 @@ int static_decode(void* scratch, size_t scratch_bytes, const int32_t* indptr_hos
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FA_ERR_CUDA;
   DecodeKernel kv[kNumVariants];
-  bool has[kNumVariants] = {true, false, false};
+  bool has[kNumVariants] = {true, false, false, false};
   // the same kernels and grid as fa_decode_plan picks, so both paths give
   // bitwise the same result
   const int sel = select_kernels(q_dtype, kv_dtype, head_dim, G, 1, kv, has, &occ);
@@ -1128,14 +1176,14 @@ static int run_impl(fa_decode_plan_s* plan, Variant variant, const void* q,
                          v_scales, max_bound, o, lse, cuda_stream, head_k_scales,
                          head_v_scales);
   // one launch per bucket, in order; the timing events (if set) bracket all
-  if (variant != kPlain) return FA_ERR_UNSUPPORTED;
+  if (variant != kPlain && variant != kBlockScales) return FA_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const bool timed = plan->batch > 0 && plan->ev_before && plan->ev_after;
   if (timed && cudaEventRecord(plan->ev_before, st) != cudaSuccess) return FA_ERR_CUDA;
   lv.ev_before = lv.ev_after = nullptr;
   for (int b = 0; b < plan->num_buckets; ++b) {
     fa_decode_plan_s::Bucket& bk = plan->bucket[b];
-    lv.kern = &bk.kern;
+    lv.kern = variant == kBlockScales ? &bk.block_kern : &bk.kern;
     lv.map = &bk.map;
     lv.q_len = bk.kern.q_len;
     lv.cta_first = bk.cta_first;

@@ -1,0 +1,12 @@
+// Compiled instances of the decode kernel over E4M3 KV with per-block scales
+// and ragged query rows (qo_indptr), q = __nv_bfloat16 (a translation unit of
+// their own so the build runs in parallel).
+#include "decode_mma.cuh"
+
+namespace fadecode {
+bool find_block_scale_ragged_q_kernel_bf16_e4m3(int head_dim, int group, int max_q,
+                                                DecodeKernel* k) {
+  return find_ragged_q_kernel_for<__nv_bfloat16, __nv_fp8_e4m3, kScalePerBlock>(head_dim, group,
+                                                                                max_q, k);
+}
+}  // namespace fadecode

@@ -176,6 +176,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
                : "memory");
 }
 
+// 4 bytes global -> shared (cp.async); both addresses 4-byte aligned.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+
 // One of the mbarrier's expected arrivals, made once this thread's earlier
 // cp.async copies have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -431,14 +438,22 @@ __device__ __forceinline__ void prefetch_first_segment(const DecodeParams& p, in
 // pool segment starts on a stream position that is a multiple of `align`
 // (empty stages fill the gap), so that the consumer warps split its pages the
 // same way whichever CTA claims it.
-// With SCALES, each page also brings the 16 per-token K scales and the 16 V
-// scales of its kv head (64 contiguous bytes each) into scales[stage][0..31]:
-// lanes 0-7 copy 16 bytes each with cp.async (the load path, which keeps
-// these small rows off the copy engine the page itself goes through), and
-// the stage's "full" barrier counts their arrivals as well (kScaleLanes + 1).
-constexpr int kScaleLanes = 8;  // producer lanes that copy a page's scales
+// With per-token scales (SC), each page also brings the 16 per-token K scales
+// and the 16 V scales of its kv head (64 contiguous bytes each) into
+// scales[stage][0..31]: lanes 0-7 copy 16 bytes each with cp.async (the load
+// path, which keeps these small rows off the copy engine the page itself goes
+// through), and the stage's "full" barrier counts their arrivals as well
+// (scale_lanes(SC) + 1).  With per-block scales, the page's one K and one V
+// scale of the kv head go to scales[stage][0..1] the same way, 4 bytes from
+// each of lanes 0 and 1.
+__host__ __device__ constexpr int scale_lanes(int sc) {  // producer lanes that copy scales
+  return sc == kScalePerToken ? 8 : sc == kScalePerBlock ? 2 : 0;
+}
+__host__ __device__ constexpr int scale_floats(int sc) {  // scales held per stage
+  return sc == kScalePerToken ? 2 * kPageSize : sc == kScalePerBlock ? 2 : 0;
+}
 
-template <int S, int STAGE_BYTES, int BOXES, int BOX_X, int BOX_BYTES, bool SCALES = false>
+template <int S, int STAGE_BYTES, int BOXES, int BOX_X, int BOX_BYTES, int SC = kScaleNone>
 __device__ __forceinline__ void produce_pages(const CUtensorMap* map, const DecodeParams& p,
                                               int seg_begin, int seg_end, uint8_t* ring,
                                               uint64_t* full, uint64_t* empty, int lane,
@@ -485,7 +500,7 @@ __device__ __forceinline__ void produce_pages(const CUtensorMap* map, const Deco
           const int kk = k + i;
           dev::mbar_wait(dev::smem_addr(&empty[kk % S]), (uint32_t)(((kk / S) & 1) ^ 1), aborted,
                          p.err);
-          dev::mbar_arrive_n(dev::smem_addr(&full[kk % S]), SCALES ? kScaleLanes + 1 : 1);
+          dev::mbar_arrive_n(dev::smem_addr(&full[kk % S]), scale_lanes(SC) + 1);
         }
       k += pad;
     }
@@ -514,16 +529,23 @@ __device__ __forceinline__ void produce_pages(const CUtensorMap* map, const Deco
             dev::tma_load_4d(dev::smem_addr(ring + stage * STAGE_BYTES + b * BOX_BYTES), map,
                              b * BOX_X, kvh, 0, 2 * page, fb, policy);
         }
-        if constexpr (SCALES) {
+        if constexpr (SC != kScaleNone) {
           // lane 0 found the stage free; the scale rows have no bounds check
           // of their own: a flagged out-of-range page reads page 0's scales
           __syncwarp();
-          if (lane < kScaleLanes) {
+          if (lane < scale_lanes(SC)) {
             const int stage = k % S;
             const int64_t pg = (page < 0 || (int64_t)page >= p.num_pages) ? 0 : page;
-            const size_t row = ((size_t)pg * p.num_kv_heads + kvh) * kPageSize;
-            const float* src = (lane < 4 ? p.k_scales : p.v_scales) + row + 4 * (lane & 3);
-            dev::cp_async16(dev::smem_addr(scales + stage * 2 * kPageSize + 4 * lane), src);
+            const size_t row = (size_t)pg * p.num_kv_heads + kvh;
+            float* dst = scales + stage * scale_floats(SC);
+            if constexpr (SC == kScalePerToken) {
+              const float* src =
+                  (lane < 4 ? p.k_scales : p.v_scales) + row * kPageSize + 4 * (lane & 3);
+              dev::cp_async16(dev::smem_addr(dst + 4 * lane), src);
+            } else {
+              dev::cp_async4(dev::smem_addr(dst + lane),
+                             (lane == 0 ? p.k_scales : p.v_scales) + row);
+            }
             dev::cp_async_arrive(dev::smem_addr(&full[stage]));
           }
         }
@@ -533,7 +555,7 @@ __device__ __forceinline__ void produce_pages(const CUtensorMap* map, const Deco
   }
   // No copy may still be landing in shared memory when the CTA exits (only
   // possible if a consumer gave up waiting).
-  if constexpr (SCALES) dev::cp_async_wait_all();
+  if constexpr (SC != kScaleNone) dev::cp_async_wait_all();
   if (lane == 0) {
     const int first = k > S ? k - S : 0;
     for (int kk = first; kk < k; ++kk)
@@ -858,7 +880,7 @@ __device__ __forceinline__ void fold_pending(const DecodeParams& p, float* mo, F
   }
 }
 
-template <typename QT, typename KVT, int D, int G, int NW>
+template <typename QT, typename KVT, int D, int G, int NW, int SC = kScaleNone>
 struct DecodeCfg {
   static constexpr int P = kPageSize;
   static constexpr int KV_ES = sizeof(KVT);
@@ -883,18 +905,21 @@ struct DecodeCfg {
   static constexpr int OFF_MD = OFF_MM + 4 * NW * G;
   static constexpr int OFF_FOLDS = OFF_MD + 4 * NW * G;
   static constexpr int OFF_QUEUE = OFF_FOLDS + kFoldListBytes;
-  static constexpr int SMEM = OFF_QUEUE + kSegQueueBytes;
+  static constexpr int OFF_SCALES = OFF_QUEUE + kSegQueueBytes;  // [S][2] fp32 per-block scales
+  static constexpr int SMEM = OFF_SCALES + 4 * S * scale_floats(SC);
+  static_assert(SC == kScaleNone || (SC == kScalePerBlock && KV_ES == 1),
+                "per-block scales of E4M3 KV, or none");
   static_assert(LPR <= 32 && 32 % LPR == 0 && P % RPS == 0, "row mapping");
   static_assert(G <= LPR, "group size larger than lanes per row");
   static_assert(STAGE_BYTES % 128 == 0, "stage alignment");
   static_assert(S % NW == 0, "each ring stage must belong to exactly one consumer warp");
 };
 
-template <typename QT, typename KVT, int D, int G, int NW>
-__global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW>::THREADS)
+template <typename QT, typename KVT, int D, int G, int NW, int SC>
+__global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW, SC>::THREADS)
     fa_decode_split_kernel(const __grid_constant__ CUtensorMap kv_map,
                            const DecodeParams p) {
-  using C = DecodeCfg<QT, KVT, D, G, NW>;
+  using C = DecodeCfg<QT, KVT, D, G, NW, SC>;
   constexpr int P = C::P, VEC = C::VEC, LPR = C::LPR, RPS = C::RPS,
                 STEPS = C::STEPS, HPL = C::HPL, S = C::S;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -909,7 +934,7 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW>::THREADS)
   FoldList* folds = reinterpret_cast<FoldList*>(smem + C::OFF_FOLDS);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      dev::mbar_init(dev::smem_addr(&full[s]), 1);
+      dev::mbar_init(dev::smem_addr(&full[s]), scale_lanes(SC) + 1);
       dev::mbar_init(dev::smem_addr(&empty[s]), 1);
     }
     seg_queue_init(queue, NW);
@@ -929,8 +954,9 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW>::THREADS)
   dev::grid_dependency_wait();
 
   if (warp == NW) {
-    produce_pages<S, C::STAGE_BYTES, 1, 0, C::STAGE_BYTES>(&kv_map, p, seg_begin, seg_end, ring,
-                                                          full, empty, lane, nullptr, queue, NW);
+    produce_pages<S, C::STAGE_BYTES, 1, 0, C::STAGE_BYTES, SC>(
+        &kv_map, p, seg_begin, seg_end, ring, full, empty, lane,
+        reinterpret_cast<float*>(smem + C::OFF_SCALES), queue, NW);
     return;
   }
 
@@ -980,6 +1006,11 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW>::THREADS)
       const uint8_t* kt = ring + stage * C::STAGE_BYTES;
       const uint8_t* vt = kt + P * C::ROW_BYTES;
       const int valid = (lp == npg - 1) ? last_valid : P;
+      // the page's scales: on its scores, and on its weights for P.V (fp32
+      // both, so any scale fits)
+      float2 bs = make_float2(1.f, 1.f);
+      if constexpr (SC == kScalePerBlock)
+        bs = *(reinterpret_cast<const float2*>(smem + C::OFF_SCALES) + stage);
 
       float sc[STEPS];
 #pragma unroll
@@ -995,7 +1026,8 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW>::THREADS)
           for (int v = 0; v < VEC; ++v) a = fmaf(qf[h][v], kf[v], a);
           part[h] = a;
         }
-        const float s = dev::reduce_scatter<G, LPR>(part, c);
+        float s = dev::reduce_scatter<G, LPR>(part, c);
+        if constexpr (SC == kScalePerBlock) s *= bs.x;
         sc[st] = j < valid ? s : -INFINITY;
       }
       float mx = sc[0];
@@ -1017,7 +1049,8 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW>::THREADS)
       m_l = m_new;
       if (c % HPL == 0) {
 #pragma unroll
-        for (int st = 0; st < STEPS; ++st) pw[(st * RPS + rs) * G + hl] = sc[st];
+        for (int st = 0; st < STEPS; ++st)
+          pw[(st * RPS + rs) * G + hl] = SC == kScalePerBlock ? sc[st] * bs.y : sc[st];
       }
 #pragma unroll
       for (int h = 0; h < G; ++h) {
@@ -1084,10 +1117,10 @@ __global__ void __launch_bounds__(128) fa_merge_partials_kernel(const MergeParam
                                             threadIdx.x, blockDim.x, 0);
 }
 
-template <typename QT, typename KVT, int D, int G, int NW = 4>
+template <typename QT, typename KVT, int D, int G, int NW = 4, int SC = kScaleNone>
 inline void fill_kernel(DecodeKernel* k) {
-  using C = DecodeCfg<QT, KVT, D, G, NW>;
-  k->func = reinterpret_cast<const void*>(&fa_decode_split_kernel<QT, KVT, D, G, NW>);
+  using C = DecodeCfg<QT, KVT, D, G, NW, SC>;
+  k->func = reinterpret_cast<const void*>(&fa_decode_split_kernel<QT, KVT, D, G, NW, SC>);
   k->merge_func = reinterpret_cast<const void*>(&fa_merge_partials_kernel<QT, D, G>);
   k->threads = C::THREADS;
   k->smem_bytes = C::SMEM;
@@ -1098,6 +1131,7 @@ inline void fill_kernel(DecodeKernel* k) {
   k->box_x = D;
   k->swizzle_128b = false;
   k->tensor_cores = false;
+  k->block_scales = SC == kScalePerBlock;
 }
 
 }  // namespace fadecode

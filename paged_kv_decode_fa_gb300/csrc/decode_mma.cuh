@@ -129,7 +129,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w, bool bf16) {
 
 }  // namespace mma
 
-template <typename QT, typename KVT, int D, int G, int NW, bool TS = false, int QL = 1>
+template <typename QT, typename KVT, int D, int G, int NW, int SC = kScaleNone, int QL = 1>
 struct MmaCfg {
   static constexpr int NC = G * QL;  // MMA columns: heads of the group x query tokens
   // Column split: with more than 8 columns every consumer warp takes every
@@ -182,9 +182,10 @@ struct MmaCfg {
   static constexpr int OFF_MD = OFF_MM + 4 * NS * NC;
   static constexpr int OFF_FOLDS = OFF_MD + 4 * NS * NC;
   static constexpr int OFF_QUEUE = OFF_FOLDS + kFoldListBytes;
-  static constexpr int OFF_SCALES = OFF_QUEUE + kSegQueueBytes;    // [S][32] fp32 if TS
-  static constexpr int SMEM = OFF_SCALES + (TS ? S * 2 * P * 4 : 0);
-  static_assert(!TS || kFp8, "per-token scales are for E4M3 KV");
+  // [S][32] fp32 per-token or [S][2] per-block scales
+  static constexpr int OFF_SCALES = OFF_QUEUE + kSegQueueBytes;
+  static constexpr int SMEM = OFF_SCALES + 4 * S * scale_floats(SC);
+  static_assert(SC == kScaleNone || kFp8, "scales read page by page are for E4M3 KV");
   static_assert(ROW_BYTES % 128 == 0, "rows must be whole 128-byte swizzle rows");
   static_assert(NC >= 1 && (NC <= 8 || NC <= 8 * NW), "8 columns (the MMA N side) per warp");
   static_assert(STAGE_BYTES % 1024 == 0, "swizzled boxes need 1024-byte alignment");
@@ -215,12 +216,13 @@ constexpr float kLazyAbove = 8.f;
 // scores and release the stage then, instead of after P.V.
 constexpr bool kEarlyVRelease = true;
 
-template <typename QT, typename KVT, int D, int G, int NW, bool TS, int QL, bool UM,
+template <typename QT, typename KVT, int D, int G, int NW, int SC, int QL, bool UM,
           bool RQ = false>
-__global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
-                                  MmaCfg<QT, KVT, D, G, NW, TS, QL>::MIN_CTAS)
+__global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
+                                  MmaCfg<QT, KVT, D, G, NW, SC, QL>::MIN_CTAS)
     fa_decode_mma_kernel(const __grid_constant__ CUtensorMap kv_map, const DecodeParams p) {
-  using C = MmaCfg<QT, KVT, D, G, NW, TS, QL>;
+  using C = MmaCfg<QT, KVT, D, G, NW, SC, QL>;
+  constexpr bool TS = SC == kScalePerToken, BS = SC == kScalePerBlock;
   constexpr int NC = C::NC;
   constexpr bool CS = C::CS;
   // causal masking among the query tokens (multi-token and ragged plans)
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
   // per segment to sit well inside the f16 range.
   constexpr bool kConvertQ = kFp8 && std::is_same<QT, __nv_bfloat16>::value;
   // the unified-max window relies on the 8-bit exponent of bf16 weights
-  static_assert(!UM || (!TS && QL == 1 && !RQ), "unified max: plain decode");
+  static_assert(!UM || (SC == kScaleNone && QL == 1 && !RQ), "unified max: plain decode");
   constexpr float kUmAbove = kBf16 ? kUmAboveBf16 : kUmAboveF16;
   constexpr float kUmBelow = kBf16 ? kUmBelowBf16 : kUmBelowF16;
   static_assert(!RQ || !TS, "ragged q: no per-token scales");
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
   FoldList* folds = reinterpret_cast<FoldList*>(smem + C::OFF_FOLDS);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      dev::mbar_init(dev::smem_addr(&full[s]), TS ? kScaleLanes + 1 : 1);
+      dev::mbar_init(dev::smem_addr(&full[s]), scale_lanes(SC) + 1);
       dev::mbar_init(dev::smem_addr(&empty[s]), CS ? NW : 1);  // its consumer warps
     }
     seg_queue_init(queue, NW);
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
   dev::grid_dependency_wait();
 
   if (warp == NW) {
-    produce_pages<S, C::STAGE_BYTES, SEGS, C::BOX_X, C::BOX_BYTES, TS>(
+    produce_pages<S, C::STAGE_BYTES, SEGS, C::BOX_X, C::BOX_BYTES, SC>(
         &kv_map, p, seg_begin, seg_end, ring, full, empty, lane,
         reinterpret_cast<float*>(smem + C::OFF_SCALES), queue, CS ? 1 : NW);
     return;
@@ -408,6 +410,15 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
     // that has seen nothing yet (every token so far masked), whose weights
     // exp2(-inf - 0) = 0 keep its state empty; it changes only on a rescale
     float mref[2] = {0.f, 0.f};
+    // Per-block scales: o is kept in units of a reference V scale (0 before
+    // the first page with a non-zero one), and a page's weights enter P.V
+    // times its scale over the reference.  The reference is a recent page's
+    // scale: it moves when a page's scale leaves [2^-6, 2^6] of it, with an
+    // exact rescale of o where the scales are powers of two, so the f16
+    // weights (at most 2^8 before the factor) stay below 2^14, and a page that
+    // the softmax favours keeps its full precision however small its scale
+    // is next to an earlier page's.
+    float vref = 0.f, vref_inv = 0.f;
 
     // ---- O^T[dim][head] += V^T . P^T for one page (stage address st).
     // Slots past the last valid token may hold anything (NaN included): a
@@ -518,6 +529,9 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
 
       // ---- scores S^T[token][head] = K . q^T (two accumulators a page to halve the chain)
       float s[NPP][4], vs_lo[NPP], vs_hi[NPP];  // vs: per-token V scales of tokens g, g+8
+      // per-block scales: the page's weight factor, and the factor o takes
+      // before the page (1 unless the reference moves)
+      float wf[NPP], of[NPP];
       const int sw = g & 7;  // swizzle of rows g and g+8
 #pragma unroll
       for (int u = 0; u < NPP; ++u) {
@@ -550,8 +564,22 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
             }
           }
         }
+        float page_qscale = qscale;
+        if constexpr (BS) {
+          const float2 bs = *(reinterpret_cast<const float2*>(smem + C::OFF_SCALES) + stage[u]);
+          page_qscale *= bs.x;
+          wf[u] = bs.y * vref_inv;
+          of[u] = 1.f;
+          if (wf[u] > 64.f || (wf[u] < 1.f / 64.f && bs.y > 0.f)) {
+            const float inv = 1.f / bs.y;
+            of[u] = vref * inv;
+            vref = bs.y;
+            vref_inv = inv;
+            wf[u] = 1.f;
+          }
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[u][e] = (sc[0][e] + sc[1][e]) * qscale;
+        for (int e = 0; e < 4; ++e) s[u][e] = (sc[0][e] + sc[1][e]) * page_qscale;
         vs_lo[u] = vs_hi[u] = 1.f;
         if constexpr (TS) {
           const float* scl =
@@ -565,8 +593,15 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
           s[u][3] *= ks_hi;
         }
         if (valid[u] < P) {
-          if (g >= valid[u]) s[u][0] = s[u][1] = -INFINITY;
-          if (g + 8 >= valid[u]) s[u][2] = s[u][3] = -INFINITY;
+          // a slot past the end weighs 0, whatever its per-token scale holds
+          if (g >= valid[u]) {
+            s[u][0] = s[u][1] = -INFINITY;
+            vs_lo[u] = 1.f;
+          }
+          if (g + 8 >= valid[u]) {
+            s[u][2] = s[u][3] = -INFINITY;
+            vs_hi[u] = 1.f;
+          }
         }
         if constexpr (kCausal) {
           const int pos = lp[u] * P + g;  // token position from the segment start
@@ -638,14 +673,25 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
       }
 #pragma unroll
       for (int u = 0; u < NPP; ++u) {
-        const uint32_t p01 = mma::pack2(dev::fast_exp2(s[u][0] - mref[0]),
-                                        dev::fast_exp2(s[u][1] - mref[1]), kBf16);
-        const uint32_t p23 = mma::pack2(dev::fast_exp2(s[u][2] - mref[0]),
-                                        dev::fast_exp2(s[u][3] - mref[1]), kBf16);
-        // sums from the rounded weights, so numerator and denominator agree
-        const float2 a = mma::unpack2(p01, kBf16), b = mma::unpack2(p23, kBf16);
-        uint32_t pv01 = p01, pv23 = p23;  // weights times the per-token V scale
-        if constexpr (TS) {
+        const float e0 = dev::fast_exp2(s[u][0] - mref[0]), e1 = dev::fast_exp2(s[u][1] - mref[1]);
+        const float e2 = dev::fast_exp2(s[u][2] - mref[0]), e3 = dev::fast_exp2(s[u][3] - mref[1]);
+        float2 a, b;              // the weights the denominator sums
+        uint32_t pv01, pv23;      // the weights of P.V
+        if constexpr (BS) {
+          // lse keeps fp32's precision: the sums take the weights unrounded,
+          // and P.V's are rounded once, after the block's factor
+          a = make_float2(e0, e1);
+          b = make_float2(e2, e3);
+          pv01 = mma::pack2(e0 * wf[u], e1 * wf[u], kBf16);
+          pv23 = mma::pack2(e2 * wf[u], e3 * wf[u], kBf16);
+        } else {
+          pv01 = mma::pack2(e0, e1, kBf16);
+          pv23 = mma::pack2(e2, e3, kBf16);
+          // sums from the rounded weights, so numerator and denominator agree
+          a = mma::unpack2(pv01, kBf16);
+          b = mma::unpack2(pv23, kBf16);
+        }
+        if constexpr (TS) {  // weights times the per-token V scale
           pv01 = mma::pack2(a.x * vs_lo[u], a.y * vs_lo[u], kBf16);
           pv23 = mma::pack2(b.x * vs_hi[u], b.y * vs_hi[u], kBf16);
         }
@@ -680,6 +726,14 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
         const uint32_t pb0 = *reinterpret_cast<const uint32_t*>(pu + g * P + 2 * t);
         const uint32_t pb1 = *reinterpret_cast<const uint32_t*>(pu + g * P + 2 * t + 8);
         const uint32_t* vf = kEarlyV ? &vfrag[kEarlyV ? u : 0][0][0] : nullptr;
+        if constexpr (BS) {
+          if (of[u] != 1.f) {
+#pragma unroll
+            for (int mt = 0; mt < MTILES; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[mt][e] *= of[u];
+          }
+        }
         if (valid[u] < P)
           pv_step(std::true_type{}, st[u], pb0, pb1, valid[u], vf);
         else
@@ -724,8 +778,8 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
         for (int mt = 0; mt < MTILES; ++mt) {
           const int dlo = kFp8 ? mt * 16 + 2 * g : mt * 16 + g;
           const int dhi = kFp8 ? mt * 16 + 2 * g + 1 : mt * 16 + g + 8;
-          mo[(srow * NC + h) * D + dlo] = o[mt][e];
-          mo[(srow * NC + h) * D + dhi] = o[mt][2 + e];
+          mo[(srow * NC + h) * D + dlo] = BS ? o[mt][e] * vref : o[mt][e];
+          mo[(srow * NC + h) * D + dhi] = BS ? o[mt][2 + e] * vref : o[mt][2 + e];
         }
         if (g == 0) {
           mm[srow * NC + h] = m_h[e];
@@ -744,11 +798,11 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, TS, QL>::THREADS,
   if (threadIdx.x == 0) pool_finish(p);
 }
 
-template <typename QT, typename KVT, int D, int G, int NW = 4, bool TS = false, int QL = 1,
+template <typename QT, typename KVT, int D, int G, int NW = 4, int SC = kScaleNone, int QL = 1,
           bool UM = false, bool RQ = false>
 inline void fill_mma_kernel(DecodeKernel* k) {
-  using C = MmaCfg<QT, KVT, D, G, NW, TS, QL>;
-  k->func = reinterpret_cast<const void*>(&fa_decode_mma_kernel<QT, KVT, D, G, NW, TS, QL, UM, RQ>);
+  using C = MmaCfg<QT, KVT, D, G, NW, SC, QL>;
+  k->func = reinterpret_cast<const void*>(&fa_decode_mma_kernel<QT, KVT, D, G, NW, SC, QL, UM, RQ>);
   k->merge_func = reinterpret_cast<const void*>(&fa_merge_partials_kernel<QT, D, G, QL, RQ>);
   k->threads = C::THREADS;
   k->smem_bytes = C::SMEM + 1024;  // room to align the ring to 1024 bytes
@@ -759,7 +813,8 @@ inline void fill_mma_kernel(DecodeKernel* k) {
   k->box_x = C::BOX_X;
   k->swizzle_128b = true;
   k->tensor_cores = true;
-  k->token_scales = TS;
+  k->token_scales = SC == kScalePerToken;
+  k->block_scales = SC == kScalePerBlock;
   k->q_len = QL;
   k->unified_max = UM;
   k->ragged_q = RQ;
@@ -793,12 +848,12 @@ inline bool find_kernel_for(int head_dim, int group, bool allow_mma, DecodeKerne
 }
 
 // Multi-token decode: tensor-core consumer, head_dim 128, group * q_len <= 8.
-template <typename QT, typename KVT>
+template <typename QT, typename KVT, int SC = kScaleNone>
 inline bool find_multi_token_kernel_for(int head_dim, int group, int q_len, DecodeKernel* k) {
   if (head_dim != 128) return false;
 #define FA_QL_CASE(GG, QQ)                                 \
   if (group == GG && q_len == QQ) {                        \
-    fill_mma_kernel<QT, KVT, 128, GG, 4, false, QQ>(k);    \
+    fill_mma_kernel<QT, KVT, 128, GG, 4, SC, QQ>(k);       \
     return true;                                           \
   }
   FA_QL_CASE(1, 2) FA_QL_CASE(1, 4) FA_QL_CASE(1, 8)
@@ -811,12 +866,12 @@ inline bool find_multi_token_kernel_for(int head_dim, int group, int q_len, Deco
 // smallest built bucket of query tokens per request that holds max_q: at most
 // 8 columns (group x tokens) with the pages split over the warps, else up to
 // 32 columns split over the warps (8 each).
-template <typename QT, typename KVT>
+template <typename QT, typename KVT, int SC = kScaleNone>
 inline bool find_ragged_q_kernel_for(int head_dim, int group, int max_q, DecodeKernel* k) {
   if (head_dim != 128 || max_q < 1) return false;
 #define FA_RQ_CASE(GG, QQ)                                          \
   if (group == GG && max_q <= QQ) {                                 \
-    fill_mma_kernel<QT, KVT, 128, GG, 4, false, QQ, false, true>(k); \
+    fill_mma_kernel<QT, KVT, 128, GG, 4, SC, QQ, false, true>(k);   \
     return true;                                                    \
   }
   FA_RQ_CASE(1, 8) FA_RQ_CASE(1, 32) FA_RQ_CASE(2, 4) FA_RQ_CASE(2, 16)
@@ -827,12 +882,12 @@ inline bool find_ragged_q_kernel_for(int head_dim, int group, int max_q, DecodeK
 
 // Ragged query rows on the kernel of a request's 8-column tiles: a column
 // split of `tiles` warps (8 x tiles columns: 2 or 3), each warp one tile.
-template <typename QT, typename KVT>
+template <typename QT, typename KVT, int SC = kScaleNone>
 inline bool find_ragged_q_tiles_kernel_for(int head_dim, int group, int tiles, DecodeKernel* k) {
   if (head_dim != 128) return false;
 #define FA_RT_CASE(GG, TT)                                                           \
   if (group == GG && tiles == TT) {                                                  \
-    fill_mma_kernel<QT, KVT, 128, GG, TT, false, 8 * TT / GG, false, true>(k);       \
+    fill_mma_kernel<QT, KVT, 128, GG, TT, SC, 8 * TT / GG, false, true>(k);          \
     return true;                                                                     \
   }
   FA_RT_CASE(1, 2) FA_RT_CASE(1, 3) FA_RT_CASE(2, 2) FA_RT_CASE(2, 3)
@@ -848,7 +903,7 @@ inline bool find_unified_max_kernel_for(int head_dim, int group, DecodeKernel* k
 #define FA_UM_CASE(DD, GG)                                       \
   if (head_dim == DD && group == GG) {                           \
     if constexpr ((DD * sizeof(KVT)) % 128 == 0) {               \
-      fill_mma_kernel<QT, KVT, DD, GG, 4, false, 1, true>(k);    \
+      fill_mma_kernel<QT, KVT, DD, GG, 4, kScaleNone, 1, true>(k); \
       return true;                                               \
     }                                                            \
     return false;                                                \
@@ -863,9 +918,28 @@ inline bool find_unified_max_kernel_for(int head_dim, int group, DecodeKernel* k
 template <typename QT>
 inline bool find_token_scale_kernel_for(int head_dim, int group, DecodeKernel* k) {
   if (head_dim != 128) return false;
-  if (group == 2) { fill_mma_kernel<QT, __nv_fp8_e4m3, 128, 2, 4, true>(k); return true; }
-  if (group == 4) { fill_mma_kernel<QT, __nv_fp8_e4m3, 128, 4, 4, true>(k); return true; }
-  if (group == 8) { fill_mma_kernel<QT, __nv_fp8_e4m3, 128, 8, 4, true>(k); return true; }
+  if (group == 2) { fill_mma_kernel<QT, __nv_fp8_e4m3, 128, 2, 4, kScalePerToken>(k); return true; }
+  if (group == 4) { fill_mma_kernel<QT, __nv_fp8_e4m3, 128, 4, 4, kScalePerToken>(k); return true; }
+  if (group == 8) { fill_mma_kernel<QT, __nv_fp8_e4m3, 128, 8, 4, kScalePerToken>(k); return true; }
+  return false;
+}
+
+// E4M3 KV with per-block scales, one query token: the consumer that a plain
+// plan of this shape takes by default.
+template <typename QT>
+inline bool find_block_scale_kernel_for(int head_dim, int group, DecodeKernel* k) {
+  using KVT = __nv_fp8_e4m3;
+#define FA_BS_CASE(DD, GG)                                             \
+  if (head_dim == DD && group == GG) {                                 \
+    if constexpr (GG >= 2 && DD % 128 == 0)                            \
+      fill_mma_kernel<QT, KVT, DD, GG, 4, kScalePerBlock>(k);          \
+    else                                                               \
+      fill_kernel<QT, KVT, DD, GG, 4, kScalePerBlock>(k);              \
+    return true;                                                       \
+  }
+  FA_BS_CASE(64, 1) FA_BS_CASE(64, 2) FA_BS_CASE(64, 4) FA_BS_CASE(64, 8)
+  FA_BS_CASE(128, 1) FA_BS_CASE(128, 2) FA_BS_CASE(128, 4) FA_BS_CASE(128, 8)
+#undef FA_BS_CASE
   return false;
 }
 

@@ -10,6 +10,11 @@ namespace fadecode {
 
 constexpr int kPageSize = 16;
 
+// Scales of an E4M3 cache that a kernel reads page by page: none (one per
+// tensor or kv head, folded into the segment), one per token and kv head, or
+// one per block (page and kv head), for K and V each.
+constexpr int kScaleNone = 0, kScalePerToken = 1, kScalePerBlock = 2;
+
 // Kernel parameters of the split-KV decode kernel (the TMA descriptor of the
 // KV cache travels beside it as a __grid_constant__ argument).
 struct DecodeParams {
@@ -25,7 +30,8 @@ struct DecodeParams {
   const int32_t* merge;        // [n_merge * 4] {request, kv_head, first_slot, num_slots}
   int* merge_count;            // [n_merge] arrivals per split unit, zero between runs
   int fused_merge;             // 1: the last CTA of a split unit merges it
-  const float* k_scales;       // [num_pages, Hkv, page_size] per-token scales, or nullptr
+  const float* k_scales;       // [num_pages, Hkv, page_size] per-token or [num_pages, Hkv]
+                               // per-block scales, or nullptr
   const float* v_scales;       // same for V
   const float* head_k_scales;  // [Hkv] one K scale per kv head (times q_scale), or nullptr
   const float* head_v_scales;  // [Hkv] one V scale per kv head (times v_scale), or nullptr
@@ -75,6 +81,7 @@ struct DecodeKernel {
   bool swizzle_128b = false;  // stage rows in TMA 128-byte swizzle order
   bool tensor_cores = false;  // per-page products on mma.sync
   bool token_scales = false;  // reads per-token K/V scales (E4M3 only)
+  bool block_scales = false;  // reads per-block K/V scales (E4M3 only)
   int q_len = 1;              // query tokens per request the kernel was built for (ragged:
                               // the most a request may have)
   bool unified_max = false;   // softmax against a static bound (no running max)
@@ -110,6 +117,16 @@ bool find_unified_max_kernel_f16_e4m3(int head_dim, int group, DecodeKernel* k);
 // E4M3 KV with per-token, per-kv-head scales (tensor-core consumer only).
 bool find_token_scale_kernel_bf16_e4m3(int head_dim, int group, DecodeKernel* k);
 bool find_token_scale_kernel_f16_e4m3(int head_dim, int group, DecodeKernel* k);
+// E4M3 KV with per-block (page, kv head) scales: the kernels of every E4M3
+// plan kind, with the same grid and partial-state layout.
+bool find_block_scale_kernel_bf16_e4m3(int head_dim, int group, DecodeKernel* k);
+bool find_block_scale_kernel_f16_e4m3(int head_dim, int group, DecodeKernel* k);
+bool find_block_scale_multi_token_kernel_bf16_e4m3(int head_dim, int group, int q_len,
+                                                   DecodeKernel* k);
+bool find_block_scale_ragged_q_kernel_bf16_e4m3(int head_dim, int group, int max_q,
+                                                DecodeKernel* k);
+bool find_block_scale_ragged_q_tiles_kernel_bf16_e4m3(int head_dim, int group, int tiles,
+                                                      DecodeKernel* k);
 
 // Plan + run of one batch with the workspace replaced by `scratch` (the
 // library's own device array) and no allocation of any kind: the path

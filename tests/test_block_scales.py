@@ -1,0 +1,305 @@
+"""Decode over an E4M3 cache with one scale per block (page, kv head) against
+the float64 oracle on the dequantised cache, on every plan kind.
+
+Tolerance of an output element, for weights w over tokens with values v:
+half a step of the output's type (bf16 2^-8, f16 2^-11) of itself; 3 * 2^-11 of
+sum w |v| for the f16 rounding of a weight, of a weight times its block's
+scale, and of the weights' sum; twice the logit error, 2e-4, of sum w |v|; and
+2^-25 of the largest |v| for each token whose weight is below f16's normal range
+(half its smallest step), of at most as many as the request has.  lse: the
+weights' rounding 2^-11, the logit error 1e-4, fp32's rounding of the value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from paged_kv_decode_fa_gb300 import workloads as W
+from tests.helpers import as_bits
+
+E4M3 = torch.float8_e4m3fn
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+def make(lengths, counts, hq, hkv, d, q_dtype, seed, device, spread=2.0, pow2=True, zero=0.05):
+    """A batch whose blocks' scales are spread over 2^+-spread, some of V's
+    and (rarely) K's 0; NaN codes in every slot past a request's end."""
+    if counts is None:
+        b = W.make_batch(batch_lengths=lengths, num_qo_heads=hq, num_kv_heads=hkv, head_dim=d,
+                         q_dtype=q_dtype, kv_dtype=E4M3, seed=seed, device=device)
+    else:
+        b = W.make_ragged_q_batch(batch_lengths=lengths, q_counts=counts, num_qo_heads=hq,
+                                  num_kv_heads=hkv, head_dim=d, q_dtype=q_dtype, kv_dtype=E4M3,
+                                  seed=seed, device=device)
+    rng = np.random.default_rng(seed)
+    shape = (b.num_pages, hkv)
+    u = rng.uniform(-1, 1, (2,) + shape) * np.array([min(spread, 1.5), spread])[:, None, None]
+    s = 2.0 ** (-6.5 + (np.rint(u) if pow2 else u))
+    if pow2:
+        s *= 2.0 ** 0.5
+    s[1][rng.random(shape) < zero] = 0
+    s[0][rng.random(shape) < zero / 5] = 0
+    b.extra["ks"], b.extra["vs"] = (torch.from_numpy(x.astype(np.float32)).to(device) for x in s)
+    raw = b.paged_kv.view(torch.uint8)
+    ids = b.indices.cpu().numpy()
+    for i, n in enumerate(b.lengths):
+        if n % 16:
+            raw[int(ids[b.indptr[i + 1] - 1]), :, int(n % 16):] = 0x7f
+    return b
+
+
+def plan(lib, b):
+    args = (b.num_qo_heads, b.num_kv_heads, b.head_dim, 16)
+    kw = dict(q_data_type=b.q.dtype, kv_data_type=E4M3)
+    if "qo_indptr" in b.extra:
+        return lib.plan_ragged_q(b.indptr, b.indices, b.last_page_len, b.extra["qo_indptr"], *args,
+                                 **kw)
+    return lib.plan(b.indptr, b.indices, b.last_page_len, *args, **kw)
+
+
+def reference(b):
+    """(o, lse, sum w |v|, per-row largest |v| times 2^-25 tokens)."""
+    kv = b.paged_kv.float()
+    kv *= torch.stack([b.extra["ks"], b.extra["vs"]], 1)[:, :, None, :, None]
+    qb, qc = as_bits(b.q)
+    ids, indptr = b.indices.cpu().numpy(), b.indptr.numpy()
+    qo = b.extra.get("qo_indptr", np.arange(b.batch + 1))
+
+    def run(x):
+        return oracle.batch_decode_ragged_q(qb, qc, x.cpu().numpy(), oracle.F32, indptr, ids,
+                                            b.last_page_len.numpy(), qo, b.num_qo_heads,
+                                            b.num_kv_heads, b.head_dim, 16)
+
+    # the plain oracle for a request without a context, which has a row
+    def plain(x):
+        return oracle.batch_decode(qb, qc, x.cpu().numpy(), oracle.F32, indptr, ids,
+                                   b.last_page_len.numpy(), b.num_qo_heads, b.num_kv_heads,
+                                   b.head_dim, 16)
+
+    fn = run if "qo_indptr" in b.extra else plain
+    o, lse = fn(kv)
+    mag = kv.clone()
+    mag[:, 1].abs_()
+    a, _ = fn(mag)
+    big = kv[:, 1].nan_to_num().abs().amax((1, 3)).double().cpu().numpy()  # [pages, hkv]
+    tail = np.zeros(lse.shape)
+    g = b.num_qo_heads // b.num_kv_heads
+    for i in range(b.batch):
+        pages = ids[indptr[i]:indptr[i + 1]]
+        if len(pages):
+            tail[qo[i]:qo[i + 1]] = np.repeat(big[pages].max(0), g) * int(b.lengths[i]) * 2.0 ** -25
+    return o, lse, a, tail
+
+
+def check(b, o, lse, ref):
+    ro, rl, a, tail = ref
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    o, lse = o.reshape(ro.shape), lse.reshape(rl.shape)
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(lse), empty)
+    tol = HALF[b.q.dtype] * np.abs(ro) + (3 * 2.0 ** -11 + 2e-4) * a * 1.01 + tail[..., None]
+    if b.q.dtype == torch.float16:
+        tol = tol + 2.0 ** -25  # f16's subnormal outputs
+    bad = ~(np.abs(o - ro) <= tol + 1e-30)
+    assert not bad.any(), (np.argwhere(bad)[:4], o[bad][:4], ro[bad][:4], tol[bad][:4])
+    tol = 2.0 ** -11 + 1e-4 + 2.0 ** -23 * np.abs(rl[~empty])
+    assert (np.abs(lse[~empty] - rl[~empty]) <= tol).all(), np.abs(lse[~empty] - rl[~empty]).max()
+
+
+def run(p, b, **kw):
+    o, lse = p.run_block_scales(b.q, b.paged_kv, b.extra["ks"], b.extra["vs"], **kw)
+    torch.cuda.synchronize()
+    return o, lse
+
+
+LENGTHS = [1, 0, 16, 17, 250, 1000, 33, 611, 3000]
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("spread,pow2", [(0.0, True), (3.0, True), (14.0, True), (3.0, False)])
+@pytest.mark.parametrize("q_dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("group", [1, 2, 4, 8])
+def test_against_oracle(lib, cuda, group, head_dim, q_dtype, spread, pow2):
+    if q_dtype == torch.float16 and spread > 8:
+        spread = 8.0  # f16 outputs end at 65504
+    b = make(LENGTHS, None, 3 * group, 3, head_dim, q_dtype, 11 * group + head_dim, cuda, spread,
+             pow2)
+    p = plan(lib, b)
+    o, lse = run(p, b)
+    assert p.check() == 0 and p.info["num_merge_units"] > 0
+    check(b, o, lse, reference(b))
+    o2, lse2 = run(p, b)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("merge", ["fused", "kernel"])
+@pytest.mark.parametrize("buckets", ["default", "all"])
+@pytest.mark.parametrize("group,counts", [(8, [1, 4, 2, 0, 3, 4, 1, 1, 2]),
+                                          (4, [2, 8, 1, 0, 3, 6, 2, 1, 5]),
+                                          (2, [4, 12, 2, 0, 5, 16, 4, 1, 9]),
+                                          (1, [8, 20, 4, 0, 9, 32, 8, 1, 17]),
+                                          (1, [8, 1, 0, 3, 8, 5, 2, 7, 4]),
+                                          (2, [4, 1, 0, 3, 2, 4, 2, 1, 4]),
+                                          (4, [2, 1, 0, 1, 2, 2, 2, 1, 2]),
+                                          (8, [1, 1, 0, 1, 1, 1, 1, 0, 1])])
+def test_ragged_q(lib, cuda, monkeypatch, group, counts, buckets, merge):
+    """Every ragged kernel: one tile, the column splits of two, three and four
+    warps, in one launch or a bucket each."""
+    if buckets == "all":
+        monkeypatch.setenv("FADECODE_BUCKETS", "all")
+    else:
+        monkeypatch.delenv("FADECODE_BUCKETS", raising=False)
+    if merge == "kernel":
+        monkeypatch.setenv("FADECODE_MERGE", "kernel")
+    else:
+        monkeypatch.delenv("FADECODE_MERGE", raising=False)
+    lengths = [3000, 40, 2500, 17, 1000, 611, 5000, 9, 250]
+    b = make(lengths, counts, 2 * group, 2, 128, torch.bfloat16, 7 + group, cuda, spread=5.0)
+    p = plan(lib, b)
+    o, lse = run(p, b)
+    assert p.check() == 0
+    check(b, o, lse, reference(b))
+
+
+@pytest.mark.parametrize("group,q_len", [(1, 2), (1, 4), (1, 8), (2, 2), (2, 4), (4, 2), (8, 3)])
+def test_multi_token(lib, cuda, group, q_len):
+    lengths = [8, 16, 17, 250, 1000, 33, 2000]
+    b = make(lengths, [q_len] * len(lengths), 2 * group, 2, 128, torch.bfloat16, 31 + group, cuda)
+    p = lib.plan_multi_token(b.indptr, b.indices, b.last_page_len, q_len, 2 * group, 2, 128, 16,
+                             q_data_type=torch.bfloat16, kv_data_type=E4M3)
+    q = b.q.view(len(lengths), q_len, 2 * group, 128)
+    o, lse = p.run_block_scales(q, b.paged_kv, b.extra["ks"], b.extra["vs"])
+    torch.cuda.synchronize()
+    assert o.shape == q.shape and lse.shape == q.shape[:-1] and p.check() == 0
+    check(b, o, lse, reference(b))
+
+
+@pytest.mark.parametrize("group,head_dim", [(1, 64), (4, 64), (1, 128), (2, 128), (8, 128)])
+def test_equal_scales_are_a_per_tensor_scale(lib, cuda, group, head_dim):
+    """One power of two for every block: the per-tensor result bit for bit on
+    the CUDA cores.  The tensor-core kernel sums its weights before they are
+    rounded to f16, the per-tensor one after: 2^-11 of the sum at most, in lse
+    and in o, and the two outputs' own rounding."""
+    b = make(LENGTHS, None, 2 * group, 2, head_dim, torch.bfloat16, 3, cuda)
+    b.extra["ks"].fill_(2.0 ** -5)
+    b.extra["vs"].fill_(2.0 ** -3)
+    p = plan(lib, b)
+    o, lse = run(p, b)
+    ref_o, ref_lse = p.run(b.q, b.paged_kv, k_scale=2.0 ** -5, v_scale=2.0 ** -3)
+    torch.cuda.synchronize()
+    if not p.info["tensor_cores"]:
+        assert torch.equal(o, ref_o) and torch.equal(lse, ref_lse)
+        return
+    empty = torch.isneginf(ref_lse)
+    assert torch.equal(torch.isneginf(lse), empty)
+    assert ((lse - ref_lse)[~empty].abs() <= 2.0 ** -11 + 2.0 ** -22 * ref_lse[~empty].abs()).all()
+    o, ref_o = o.float(), ref_o.float()
+    assert ((o - ref_o).abs() <= (2 * 2.0 ** -8 + 2.0 ** -10) * ref_o.abs() + 1e-30).all()
+
+
+@pytest.mark.parametrize("tiny,first", [(30, True), (30, False), (60, True), (60, False)])
+@pytest.mark.parametrize("group,head_dim,counts", [(2, 128, None), (8, 128, None), (1, 128, None),
+                                                   (4, 64, None), (8, 128, [4, 3])])
+def test_attended_blocks_of_small_scale(lib, cuda, group, head_dim, counts, tiny, first):
+    """Blocks the softmax ignores (a logit lower by 300: weight 0) have V
+    scales 2^tiny above those it attends to, before or after them: the
+    attended values keep their precision all the same."""
+    lengths = [300, 700]
+    b = make(lengths, counts, 2 * group, 2, head_dim, torch.bfloat16, 5, cuda, zero=0.0)
+    b.q.abs_().clamp_(0.5, 2.0)
+    raw = b.paged_kv.view(torch.uint8)
+    raw[:, 0] &= 0x7f
+    raw[:, 0] = torch.where(raw[:, 0] > 0x40, 0x40, raw[:, 0])  # K codes 0 .. 2
+    b.extra["ks"].fill_(2.0 ** -6)
+    ids = b.indices.cpu().numpy()
+    for i in range(2):
+        pages = ids[b.indptr[i]:b.indptr[i + 1]]
+        half = len(pages) // 2 if counts is None else len(pages) - 2
+        off = pages[:half] if (first or counts is not None) else pages[half:]
+        if not first and counts is not None:
+            off = pages[1:half]
+        off = torch.from_numpy(off.astype(np.int64)).to(cuda)
+        kc = raw[off, 0] & 0
+        raw[off, 0] = kc + (0x7e | 0x80)         # K code -448
+        b.extra["ks"][off] = 4.0
+        b.extra["vs"][off] = b.extra["vs"][off] * 2.0 ** tiny
+    p = plan(lib, b)
+    o, lse = run(p, b)
+    ref = reference(b)
+    # no token has a weight between 0 and f16's normal range
+    check(b, o, lse, (ref[0], ref[1], ref[2], ref[3] * 0))
+
+
+def test_bad_page_ids_and_empty(lib, cuda):
+    b = make([40, 0, 70], None, 8, 2, 128, torch.bfloat16, 24, cuda)
+    good = b.indices.clone()
+    b.indices[1] = b.num_pages + 5
+    b.indices[4] = -7
+    p = plan(lib, b)
+    run(p, b)
+    assert p.check() == 1
+    b.indices.copy_(good)
+    o, lse = run(p, b)
+    assert p.check() == 0
+    check(b, o, lse, reference(b))
+    e = lib.plan(np.zeros(3, np.int32), b.indices[:0], np.ones(2, np.int32), 8, 2, 128, 16,
+                 q_data_type=torch.bfloat16, kv_data_type=E4M3)
+    o, lse = e.run_block_scales(b.q[:2], b.paged_kv, b.extra["ks"], b.extra["vs"])
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+def test_graph_capture_and_other_stream(lib, cuda):
+    b = make([3000, 17, 0, 900], None, 16, 4, 128, torch.bfloat16, 131, cuda)
+    p = plan(lib, b)
+    o, lse = torch.empty_like(b.q), torch.empty(b.q.shape[:2], device=cuda)
+    run(p, b, out=o, lse=lse)
+    ref = o.clone(), lse.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.run_block_scales(b.q, b.paged_kv, b.extra["ks"], b.extra["vs"], out=o, lse=lse)
+    for _ in range(3):
+        o.zero_()
+        lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o.zero_()
+    p.run_block_scales(b.q, b.paged_kv, b.extra["ks"], b.extra["vs"], out=o, return_lse=False,
+                       stream=side)
+    side.synchronize()
+    assert torch.equal(o, ref[0])
+
+
+def test_many_short_requests(lib, cuda):
+    """Thousands of segments of 0 to 3 pages, fresh plans, on the first launch
+    right after another kernel's."""
+    for seed in range(6):
+        rng = np.random.default_rng(seed)
+        lengths = rng.integers(0, 48, 2500)
+        b = make(list(lengths), None, 64, 8, 128, torch.bfloat16, seed, cuda, spread=3.0)
+        p = plan(lib, b)
+        p.run(b.q, b.paged_kv)
+        o, lse = run(p, b)
+        assert p.check() == 0
+        check(b, o, lse, reference(b))
+
+
+def test_refusals(lib, cuda):
+    b = make([40], None, 8, 2, 128, torch.bfloat16, 1, cuda)
+    p = plan(lib, b)
+    ks = b.extra["ks"]
+    for bad in (ks[:-1], ks.double(), ks.cpu(), torch.ones((b.num_pages, 2, 16), device=cuda),
+                torch.ones((2, b.num_pages), device=cuda).T):
+        with pytest.raises(ValueError):
+            p.run_block_scales(b.q, b.paged_kv, bad, ks)
+        with pytest.raises(ValueError):
+            p.run_block_scales(b.q, b.paged_kv, ks, bad)
+    n = W.make_batch(batch_lengths=[40], num_qo_heads=8, num_kv_heads=2, head_dim=128,
+                     q_dtype=torch.bfloat16, kv_dtype=torch.bfloat16, seed=1, device=cuda)
+    pn = lib.plan(n.indptr, n.indices, n.last_page_len, 8, 2, 128, 16)
+    with pytest.raises(lib.FaError):
+        pn.run_block_scales(n.q, n.paged_kv, *(torch.ones((n.num_pages, 2), device=cuda),) * 2)
