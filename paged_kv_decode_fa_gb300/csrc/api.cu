@@ -188,7 +188,9 @@ int kv_tensor_map(MapCache* c, const DecodeKernel& k, fa_dtype kv_dtype, const v
                                                           : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   CUresult r = encode(&c->tmap, dt, 4, const_cast<void*>(paged_kv), dims, strides, box, estr,
                       CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      k.swizzle_128b ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                      k.swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                      : k.swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                              : CU_TENSOR_MAP_SWIZZLE_NONE,
                       promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     c->base = nullptr;

@@ -176,13 +176,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
                : "memory");
 }
 
-// 4 bytes global -> shared (cp.async); both addresses 4-byte aligned.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src))
-               : "memory");
-}
-
 // One of the mbarrier's expected arrivals, made once this thread's earlier
 // cp.async copies have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -443,22 +436,62 @@ __device__ __forceinline__ void prefetch_first_segment(const DecodeParams& p, in
 // scales[stage][0..31]: lanes 0-7 copy 16 bytes each with cp.async (the load
 // path, which keeps these small rows off the copy engine the page itself goes
 // through), and the stage's "full" barrier counts their arrivals as well
-// (scale_lanes(SC) + 1).  With per-block scales, the page's one K and one V
-// scale of the kv head go to scales[stage][0..1] the same way, 4 bytes from
-// each of lanes 0 and 1.
+// (scale_lanes(SC) + 1).  With per-block scales, a lane loads the K and V scale
+// of the page whose id it holds, for 32 pages at once and one batch of 32 (or
+// the next segment's first) ahead of the pages being issued, and puts them
+// into a ring of their own, scales[k % 64][0..1] for page k of the stream:
+// before a batch's first page k0 is issued, page k0 - 1 - S has been released,
+// so with S <= 32 the batch's slots (pages k0 - 64 .. k0 - 33 held them) are free,
+// and lane 0's arrivals on "full" publish them.  (Copies of 4 bytes a page
+// with cp.async, and a second arrival, took 11 us of the 195 of fp8_kv's
+// shape; a store a page by lane 0, between a stage's release and its refill, 5.)
 __host__ __device__ constexpr int scale_lanes(int sc) {  // producer lanes that copy scales
-  return sc == kScalePerToken ? 8 : sc == kScalePerBlock ? 2 : 0;
+  return sc == kScalePerToken ? 8 : 0;
 }
 __host__ __device__ constexpr int scale_floats(int sc) {  // scales held per stage
-  return sc == kScalePerToken ? 2 * kPageSize : sc == kScalePerBlock ? 2 : 0;
+  return sc == kScalePerToken ? 2 * kPageSize : 0;
+}
+// With PL > 1, that many lanes issue a page each at a time, in step (a stage
+// they refill was filled by an earlier step, so none waits on another): one
+// lane's wait, arrival and copy take about 200 ns a page, which holds up a CTA
+// of many consumer warps (16: 176 to 79 us with eight lanes, see
+// block_scale_warps) and slows the others a little (four lanes: fp8_kv's
+// shape 193.7 to 191.1 us, a 65536-token sequence of 32 heads 96.0 to 92.3).
+constexpr int kBlockScaleRing = 64;  // pages whose per-block scales are held
+__host__ __device__ constexpr int scale_bytes(int sc, int stages) {
+  return sc == kScalePerBlock ? 8 * kBlockScaleRing : 4 * stages * scale_floats(sc);
 }
 
-template <int S, int STAGE_BYTES, int BOXES, int BOX_X, int BOX_BYTES, int SC = kScaleNone>
+// Page ids and per-block scales of up to 32 pages of a segment, one per lane.
+struct BlockScaleBatch {
+  int at = -1;  // first page position, -1: none
+  int id;
+  float2 scales;
+};
+
+// Fetch the batch of `cnt` pages from position `at`.  The scales have no
+// bounds check of their own: an out-of-range page (flagged when it is issued)
+// reads page 0's.  They are read past L1 (32 sectors of 32 rows; keeping
+// them out of it took fp8_kv's shape from 196.7 to 193.7 us).
+__device__ __forceinline__ void fetch_block_scales(const DecodeParams& p, int kvh, int at, int cnt,
+                                                   int lane, BlockScaleBatch* b) {
+  b->at = at;
+  b->id = lane < cnt ? __ldg(p.indices + at + lane) : 0;
+  const int64_t pg = (b->id < 0 || (int64_t)b->id >= p.num_pages) ? 0 : b->id;
+  const size_t row = (size_t)pg * p.num_kv_heads + kvh;
+  if (lane < cnt) b->scales = make_float2(__ldcg(p.k_scales + row), __ldcg(p.v_scales + row));
+}
+
+template <int S, int STAGE_BYTES, int BOXES, int BOX_X, int BOX_BYTES, int SC = kScaleNone,
+          int PL = 1>
 __device__ __forceinline__ void produce_pages(const CUtensorMap* map, const DecodeParams& p,
                                               int seg_begin, int seg_end, uint8_t* ring,
                                               uint64_t* full, uint64_t* empty, int lane,
                                               float* scales = nullptr, SegQueue* queue = nullptr,
                                               int align = 1) {
+  static_assert(SC != kScalePerBlock || S <= 32, "a batch's scale slots must be free");
+  static_assert(PL == 1 || (PL <= S && 32 % PL == 0 && SC != kScalePerToken),
+                "the lanes' stages are distinct; per-token scales go with one lane");
   bool aborted = false;
   // the descriptor loads while the first segment and its page ids are read
   if (lane == 0) dev::prefetch_tensormap(map);
@@ -468,6 +501,7 @@ __device__ __forceinline__ void produce_pages(const CUtensorMap* map, const Deco
   // copies of its last static segment - so that a claim's round trip
   // overlaps the copies of the segment before it
   const bool pooled = queue && p.pool_count > 0;
+  BlockScaleBatch next;
   int ahead = -1;
   bool claiming = false;
   for (int si = seg_begin;; ++si) {
@@ -511,14 +545,35 @@ __device__ __forceinline__ void produce_pages(const CUtensorMap* map, const Deco
     if (p.q_row_bytes > 0) prefetch_q_rows(p, sa.x, kvh, lane);
     for (int p0 = pb; p0 < pe; p0 += 32) {
       const int cnt = min(32, pe - p0);
-      int id = lane < cnt ? __ldg(p.indices + p0 + lane) : 0;
+      int id;
+      if constexpr (SC == kScalePerBlock) {
+        if (next.at != p0) fetch_block_scales(p, kvh, p0, cnt, lane, &next);
+        id = next.id;
+        if (lane < cnt)
+          *(reinterpret_cast<float2*>(scales) + (k + lane) % kBlockScaleRing) = next.scales;
+        __syncwarp();
+        // the batch after this one: of this segment, or of the CTA's next
+        // static one (pool segments are fetched once they are claimed)
+        int nk = kvh, na = p0 + 32, ne = pe;
+        if (na >= pe && si + 1 < seg_end) {
+          const int4 sn = *reinterpret_cast<const int4*>(p.segments + 8 * (si + 1));
+          nk = sn.y;
+          na = sn.z;
+          ne = sn.w;
+        }
+        next.at = -1;
+        if (na < ne) fetch_block_scales(p, nk, na, min(32, ne - na), lane, &next);
+      } else {
+        id = lane < cnt ? __ldg(p.indices + p0 + lane) : 0;
+      }
       const bool bad = lane < cnt && (id < 0 || (int64_t)id >= p.num_pages);
       if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, 1);
-      for (int i = 0; i < cnt; ++i, ++k) {
-        const int page = __shfl_sync(0xffffffffu, id, i);
-        if (lane == 0) {
-          const int stage = k % S;
-          const uint32_t round = (uint32_t)(k / S);
+      for (int i = 0; i < cnt; i += PL, k += PL) {
+        const int page = __shfl_sync(0xffffffffu, id, i + (PL > 1 ? lane % PL : 0));
+        if (PL > 1 ? lane < min(PL, cnt - i) : lane == 0) {
+          const int kl = PL > 1 ? k + lane : k;
+          const int stage = kl % S;
+          const uint32_t round = (uint32_t)(kl / S);
           dev::mbar_wait(dev::smem_addr(&empty[stage]), (round & 1u) ^ 1u, aborted, p.err);
           const uint32_t fb = dev::smem_addr(&full[stage]);
           dev::mbar_arrive_expect_tx(fb, STAGE_BYTES);
@@ -529,7 +584,7 @@ __device__ __forceinline__ void produce_pages(const CUtensorMap* map, const Deco
             dev::tma_load_4d(dev::smem_addr(ring + stage * STAGE_BYTES + b * BOX_BYTES), map,
                              b * BOX_X, kvh, 0, 2 * page, fb, policy);
         }
-        if constexpr (SC != kScaleNone) {
+        if constexpr (SC == kScalePerToken) {
           // lane 0 found the stage free; the scale rows have no bounds check
           // of their own: a flagged out-of-range page reads page 0's scales
           __syncwarp();
@@ -537,25 +592,21 @@ __device__ __forceinline__ void produce_pages(const CUtensorMap* map, const Deco
             const int stage = k % S;
             const int64_t pg = (page < 0 || (int64_t)page >= p.num_pages) ? 0 : page;
             const size_t row = (size_t)pg * p.num_kv_heads + kvh;
-            float* dst = scales + stage * scale_floats(SC);
-            if constexpr (SC == kScalePerToken) {
-              const float* src =
-                  (lane < 4 ? p.k_scales : p.v_scales) + row * kPageSize + 4 * (lane & 3);
-              dev::cp_async16(dev::smem_addr(dst + 4 * lane), src);
-            } else {
-              dev::cp_async4(dev::smem_addr(dst + lane),
-                             (lane == 0 ? p.k_scales : p.v_scales) + row);
-            }
+            const float* src =
+                (lane < 4 ? p.k_scales : p.v_scales) + row * kPageSize + 4 * (lane & 3);
+            dev::cp_async16(dev::smem_addr(scales + stage * scale_floats(SC) + 4 * lane), src);
             dev::cp_async_arrive(dev::smem_addr(&full[stage]));
           }
         }
+        if constexpr (PL > 1) __syncwarp();
       }
+      if constexpr (PL > 1) k -= (PL - cnt % PL) % PL;  // the pages of this batch, exactly
     }
     if (si >= seg_end) si = seg_end;  // a pool segment: the next one is claimed again
   }
   // No copy may still be landing in shared memory when the CTA exits (only
   // possible if a consumer gave up waiting).
-  if constexpr (SC != kScaleNone) dev::cp_async_wait_all();
+  if constexpr (SC == kScalePerToken) dev::cp_async_wait_all();
   if (lane == 0) {
     const int first = k > S ? k - S : 0;
     for (int kk = first; kk < k; ++kk)
@@ -880,7 +931,7 @@ __device__ __forceinline__ void fold_pending(const DecodeParams& p, float* mo, F
   }
 }
 
-template <typename QT, typename KVT, int D, int G, int NW, int SC = kScaleNone>
+template <typename QT, typename KVT, int D, int G, int NW>
 struct DecodeCfg {
   static constexpr int P = kPageSize;
   static constexpr int KV_ES = sizeof(KVT);
@@ -905,21 +956,18 @@ struct DecodeCfg {
   static constexpr int OFF_MD = OFF_MM + 4 * NW * G;
   static constexpr int OFF_FOLDS = OFF_MD + 4 * NW * G;
   static constexpr int OFF_QUEUE = OFF_FOLDS + kFoldListBytes;
-  static constexpr int OFF_SCALES = OFF_QUEUE + kSegQueueBytes;  // [S][2] fp32 per-block scales
-  static constexpr int SMEM = OFF_SCALES + 4 * S * scale_floats(SC);
-  static_assert(SC == kScaleNone || (SC == kScalePerBlock && KV_ES == 1),
-                "per-block scales of E4M3 KV, or none");
+  static constexpr int SMEM = OFF_QUEUE + kSegQueueBytes;
   static_assert(LPR <= 32 && 32 % LPR == 0 && P % RPS == 0, "row mapping");
   static_assert(G <= LPR, "group size larger than lanes per row");
   static_assert(STAGE_BYTES % 128 == 0, "stage alignment");
   static_assert(S % NW == 0, "each ring stage must belong to exactly one consumer warp");
 };
 
-template <typename QT, typename KVT, int D, int G, int NW, int SC>
-__global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW, SC>::THREADS)
+template <typename QT, typename KVT, int D, int G, int NW>
+__global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW>::THREADS)
     fa_decode_split_kernel(const __grid_constant__ CUtensorMap kv_map,
                            const DecodeParams p) {
-  using C = DecodeCfg<QT, KVT, D, G, NW, SC>;
+  using C = DecodeCfg<QT, KVT, D, G, NW>;
   constexpr int P = C::P, VEC = C::VEC, LPR = C::LPR, RPS = C::RPS,
                 STEPS = C::STEPS, HPL = C::HPL, S = C::S;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -934,7 +982,7 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW, SC>::THREADS)
   FoldList* folds = reinterpret_cast<FoldList*>(smem + C::OFF_FOLDS);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      dev::mbar_init(dev::smem_addr(&full[s]), scale_lanes(SC) + 1);
+      dev::mbar_init(dev::smem_addr(&full[s]), 1);
       dev::mbar_init(dev::smem_addr(&empty[s]), 1);
     }
     seg_queue_init(queue, NW);
@@ -954,9 +1002,8 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW, SC>::THREADS)
   dev::grid_dependency_wait();
 
   if (warp == NW) {
-    produce_pages<S, C::STAGE_BYTES, 1, 0, C::STAGE_BYTES, SC>(
-        &kv_map, p, seg_begin, seg_end, ring, full, empty, lane,
-        reinterpret_cast<float*>(smem + C::OFF_SCALES), queue, NW);
+    produce_pages<S, C::STAGE_BYTES, 1, 0, C::STAGE_BYTES>(&kv_map, p, seg_begin, seg_end, ring,
+                                                          full, empty, lane, nullptr, queue, NW);
     return;
   }
 
@@ -1006,11 +1053,6 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW, SC>::THREADS)
       const uint8_t* kt = ring + stage * C::STAGE_BYTES;
       const uint8_t* vt = kt + P * C::ROW_BYTES;
       const int valid = (lp == npg - 1) ? last_valid : P;
-      // the page's scales: on its scores, and on its weights for P.V (fp32
-      // both, so any scale fits)
-      float2 bs = make_float2(1.f, 1.f);
-      if constexpr (SC == kScalePerBlock)
-        bs = *(reinterpret_cast<const float2*>(smem + C::OFF_SCALES) + stage);
 
       float sc[STEPS];
 #pragma unroll
@@ -1026,8 +1068,7 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW, SC>::THREADS)
           for (int v = 0; v < VEC; ++v) a = fmaf(qf[h][v], kf[v], a);
           part[h] = a;
         }
-        float s = dev::reduce_scatter<G, LPR>(part, c);
-        if constexpr (SC == kScalePerBlock) s *= bs.x;
+        const float s = dev::reduce_scatter<G, LPR>(part, c);
         sc[st] = j < valid ? s : -INFINITY;
       }
       float mx = sc[0];
@@ -1049,8 +1090,7 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW, SC>::THREADS)
       m_l = m_new;
       if (c % HPL == 0) {
 #pragma unroll
-        for (int st = 0; st < STEPS; ++st)
-          pw[(st * RPS + rs) * G + hl] = SC == kScalePerBlock ? sc[st] * bs.y : sc[st];
+        for (int st = 0; st < STEPS; ++st) pw[(st * RPS + rs) * G + hl] = sc[st];
       }
 #pragma unroll
       for (int h = 0; h < G; ++h) {
@@ -1117,10 +1157,10 @@ __global__ void __launch_bounds__(128) fa_merge_partials_kernel(const MergeParam
                                             threadIdx.x, blockDim.x, 0);
 }
 
-template <typename QT, typename KVT, int D, int G, int NW = 4, int SC = kScaleNone>
+template <typename QT, typename KVT, int D, int G, int NW = 4>
 inline void fill_kernel(DecodeKernel* k) {
-  using C = DecodeCfg<QT, KVT, D, G, NW, SC>;
-  k->func = reinterpret_cast<const void*>(&fa_decode_split_kernel<QT, KVT, D, G, NW, SC>);
+  using C = DecodeCfg<QT, KVT, D, G, NW>;
+  k->func = reinterpret_cast<const void*>(&fa_decode_split_kernel<QT, KVT, D, G, NW>);
   k->merge_func = reinterpret_cast<const void*>(&fa_merge_partials_kernel<QT, D, G>);
   k->threads = C::THREADS;
   k->smem_bytes = C::SMEM;
@@ -1129,9 +1169,8 @@ inline void fill_kernel(DecodeKernel* k) {
   k->group = G;
   k->head_dim = D;
   k->box_x = D;
-  k->swizzle_128b = false;
+  k->swizzle_bytes = 0;
   k->tensor_cores = false;
-  k->block_scales = SC == kScalePerBlock;
 }
 
 }  // namespace fadecode

@@ -1,6 +1,6 @@
 // Split-KV paged decode with the per-page products on the tensor cores
 // (mma.sync m16n8k16, fp32 accumulate), for groups of 2..8 query heads per
-// kv head over 16-bit or E4M3 KV.
+// kv head over 16-bit or E4M3 KV (1..8 with per-block scales).
 //
 // Same pipeline, planner contract and epilogue as fa_decode_split_kernel
 // (decode_kernel.cuh); only the consumer arithmetic differs.  With a group
@@ -19,7 +19,9 @@
 //    row segment, with 128-bit loads; the reduction index of the MMA is
 //    permuted so that these are exactly the lane's A-fragment elements, and
 //    q's B fragment (held in registers for the whole segment) uses the same
-//    permutation; E4M3 K is widened to f16 in registers;
+//    permutation; E4M3 K is widened to f16 in registers.  Rows of 64 bytes
+//    (E4M3 at head_dim 64, the per-block-scale kernels) lie in "64B swizzle"
+//    order (granule c of row r at c ^ (r >> 1 & 3)) and a lane takes granule t;
 //  - softmax on the C fragment (tokens g, g+8 x heads 2t, 2t+1): weights
 //    against a per-column reference that moves only when a page's maximum
 //    passes it by more than 2^8 (or against a caller's static bound, the
@@ -148,9 +150,11 @@ struct MmaCfg {
   // MMA operand type: bf16 for bf16 KV, f16 for f16 and E4M3 KV.
   static constexpr bool kBf16 = std::is_same<KVT, __nv_bfloat16>::value;
   static constexpr int ROW_BYTES = D * KV_ES;
-  static constexpr int SEGS = ROW_BYTES / 128;    // 128-byte row segments = TMA boxes
-  static constexpr int BOX_X = 128 / KV_ES;       // elements per box row
-  static constexpr int BOX_BYTES = 2 * P * 128;   // K and V rows of one segment
+  static constexpr int SWZ = ROW_BYTES < 128 ? ROW_BYTES : 128;  // TMA swizzle span
+  static constexpr int SEGS = ROW_BYTES / SWZ;    // row segments of a span = TMA boxes
+  static constexpr int BOX_X = SWZ / KV_ES;       // elements per box row
+  static constexpr int BOX_BYTES = 2 * P * SWZ;   // K and V rows of one segment
+  static constexpr int GPL = SWZ / 64;            // 16-byte granules of a segment's row per lane
   static constexpr int STAGE_BYTES = SEGS * BOX_BYTES;
   static constexpr int E = 16 / KV_ES;            // elements per 16-byte granule
   static constexpr int KSTEPS = D / 16;
@@ -163,8 +167,10 @@ struct MmaCfg {
   // split (three pages a warp step) 48 KB at three CTAs per SM.  A column
   // split of two or three warps (16 or 24 columns) takes 32 KB, so that five
   // or four CTAs fit per SM.
+  // More than four warps are for a grid of fewer CTAs per SM: two stages a warp.
   static constexpr int RING_BYTES =
       CS && NW < 4 ? 32768
+      : NW > 4     ? 2 * NW * STAGE_BYTES
                    : (KV_ES == 1 ? (CS ? 49152 : 32768) : (NC >= 8 ? 49152 : 65536));
   static constexpr int SPW0 = RING_BYTES / STAGE_BYTES / NW;
   static constexpr int SPW = SPW0 < 1 ? 1 : (SPW0 > 4 ? 4 : SPW0);
@@ -173,7 +179,10 @@ struct MmaCfg {
   static constexpr int THREADS = (NW + 1) * 32;
   // CTAs per SM the ring size is chosen for; the register budget must allow
   // it (column split: 480 or 512 threads per SM at two or three warps)
-  static constexpr int MIN_CTAS = CS ? (NW <= 2 ? 5 : NW == 3 ? 4 : 3) : (KV_ES == 1 ? 4 : 3);
+  static constexpr int MIN_CTAS = NW > 8   ? 1
+                                  : NW > 4 ? 3
+                                  : CS     ? (NW <= 2 ? 5 : NW == 3 ? 4 : 3)
+                                           : (KV_ES == 1 ? 4 : 3);
   static constexpr int OFF_FULL = S * STAGE_BYTES;
   static constexpr int OFF_EMPTY = OFF_FULL + 8 * S;
   static constexpr int OFF_PT = OFF_EMPTY + 8 * S;  // [NW][NPP][8 heads][16 tokens] 16-bit
@@ -182,11 +191,12 @@ struct MmaCfg {
   static constexpr int OFF_MD = OFF_MM + 4 * NS * NC;
   static constexpr int OFF_FOLDS = OFF_MD + 4 * NS * NC;
   static constexpr int OFF_QUEUE = OFF_FOLDS + kFoldListBytes;
-  // [S][32] fp32 per-token or [S][2] per-block scales
+  // [S][32] fp32 per-token scales, or the ring of per-block ones
   static constexpr int OFF_SCALES = OFF_QUEUE + kSegQueueBytes;
-  static constexpr int SMEM = OFF_SCALES + 4 * S * scale_floats(SC);
+  static constexpr int SMEM = OFF_SCALES + scale_bytes(SC, S);
   static_assert(SC == kScaleNone || kFp8, "scales read page by page are for E4M3 KV");
-  static_assert(ROW_BYTES % 128 == 0, "rows must be whole 128-byte swizzle rows");
+  static_assert(ROW_BYTES % 128 == 0 || (kFp8 && ROW_BYTES == 64),
+                "rows must be whole 128-byte swizzle rows, or E4M3 ones of 64 bytes");
   static_assert(NC >= 1 && (NC <= 8 || NC <= 8 * NW), "8 columns (the MMA N side) per warp");
   static_assert(STAGE_BYTES % 1024 == 0, "swizzled boxes need 1024-byte alignment");
   static_assert(CS || S % NW == 0, "each ring stage must belong to exactly one consumer warp");
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
   dev::grid_dependency_wait();
 
   if (warp == NW) {
-    produce_pages<S, C::STAGE_BYTES, SEGS, C::BOX_X, C::BOX_BYTES, SC>(
+    produce_pages<S, C::STAGE_BYTES, SEGS, C::BOX_X, C::BOX_BYTES, SC, BS ? (NW > 8 ? 8 : 4) : 1>(
         &kv_map, p, seg_begin, seg_end, ring, full, empty, lane,
         reinterpret_cast<float*>(smem + C::OFF_SCALES), queue, CS ? 1 : NW);
     return;
@@ -345,12 +355,13 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
         // Load L (16 bytes, 8 consecutive elements) feeds reduction steps 2L
         // and 2L+1.  16-bit KV: step j = 4*seg + 2*half + u covers dims
         // seg*BOX_X + (2t + half)*8 + 4u .. +3.  E4M3 KV: step j = 4*half + w
-        // covers dims (2t + half)*16 + 4w .. +3.
+        // covers dims (2t + half)*16 + 4w .. +3 (rows of 64 bytes: step w dims
+        // 16t + 4w .. +3).
 #pragma unroll
         for (int L = 0; L < KSTEPS / 2; ++L) {
           int d0;
           if constexpr (kFp8)
-            d0 = (2 * t + (L >> 1)) * 16 + (L & 1) * 8;
+            d0 = (C::GPL * t + (L >> 1)) * 16 + (L & 1) * 8;
           else
             d0 = (L >> 1) * C::BOX_X + (2 * t + (L & 1)) * 8;
           const uint4 v = __ldg(reinterpret_cast<const uint4*>(qrow + d0));
@@ -417,7 +428,9 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
     // exact rescale of o where the scales are powers of two, so the f16
     // weights (at most 2^8 before the factor) stay below 2^14, and a page that
     // the softmax favours keeps its full precision however small its scale
-    // is next to an earlier page's.
+    // is next to an earlier page's.  A step of several pages leaves it alone,
+    // so that they share one test and no branch lies between their MMAs: where
+    // a scale is outside, they are taken one at a time.
     float vref = 0.f, vref_inv = 0.f;
 
     // ---- O^T[dim][head] += V^T . P^T for one page (stage address st).
@@ -436,8 +449,9 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
       for (int c2 = 0; c2 < MTILES / 2; ++c2) {
         const int mi = lane >> 3, r = lane & 7;
         const int gran = 2 * c2 + (mi >> 1), tok = (mi & 1) * 8 + r;
-        mma::ldsm_x4_trans(st + (P + tok) * 128 + ((gran ^ (tok & 7)) * 16), vf[c2][0],
-                           vf[c2][1], vf[c2][2], vf[c2][3]);
+        const int sw = C::SWZ == 128 ? (tok & 7) : ((tok >> 1) & 3);
+        mma::ldsm_x4_trans(st + (P + tok) * C::SWZ + ((gran ^ sw) * 16), vf[c2][0], vf[c2][1],
+                           vf[c2][2], vf[c2][3]);
       }
     };
     auto pv_step = [&](auto masked, uint32_t st, uint32_t pb0, uint32_t pb1, int valid,
@@ -485,7 +499,7 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
           const int tok = (mi >> 1) * 8 + r;
           uint32_t a0, a1, a2, a3;
           mma::ldsm_x4_trans(
-              st + sgi * C::BOX_BYTES + (P + tok) * 128 + ((gran ^ (tok & 7)) * 16), a0, a1,
+              st + sgi * C::BOX_BYTES + (P + tok) * C::SWZ + ((gran ^ (tok & 7)) * 16), a0, a1,
               a2, a3);
           // matrices 0 and 1 hold tokens 2t, 2t+1; 2 and 3 tokens 2t+8, 2t+9
           if constexpr (kMask) {
@@ -503,7 +517,8 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
     // (PS: the distance between the warp's pages, 1 for the column split,
     // NW for the page split): scores, one softmax update over all of them,
     // P.V.  Several pages a step keep their independent loads and MMA chains
-    // in flight in the warp at once.
+    // in flight in the warp at once.  Returns false, with nothing done, where
+    // the pages must be taken one at a time (per-block scales).
     constexpr int PS = CS ? 1 : NW;
     auto step = [&](auto npp_tag, int k) {
       constexpr int NPP = decltype(npp_tag)::value;
@@ -524,25 +539,47 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
 #pragma unroll
           for (int u = 0; u < NPP; ++u) dev::mbar_arrive(dev::smem_addr(&empty[stage[u]]));
         }
-        return;
+        return true;
       }
 
       // ---- scores S^T[token][head] = K . q^T (two accumulators a page to halve the chain)
       float s[NPP][4], vs_lo[NPP], vs_hi[NPP];  // vs: per-token V scales of tokens g, g+8
-      // per-block scales: the page's weight factor, and the factor o takes
-      // before the page (1 unless the reference moves)
-      float wf[NPP], of[NPP];
-      const int sw = g & 7;  // swizzle of rows g and g+8
+      float wf[NPP], ks[NPP];  // per-block scales: the page's weight factor, its K scale
+      if constexpr (BS) {
+        bool inside = true;
+        float v_scale = 0.f;
+#pragma unroll
+        for (int u = 0; u < NPP; ++u) {
+          const float2 bs = *(reinterpret_cast<const float2*>(smem + C::OFF_SCALES) +
+                              (k + u * PS) % kBlockScaleRing);
+          ks[u] = bs.x;
+          v_scale = bs.y;
+          wf[u] = bs.y * vref_inv;
+          inside = inside && wf[u] <= 64.f && (wf[u] >= 1.f / 64.f || bs.y == 0.f);
+        }
+        if (!inside) {
+          if (NPP > 1) return false;
+          const float inv = 1.f / v_scale, f = vref * inv;
+#pragma unroll
+          for (int mt = 0; mt < MTILES; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][e] *= f;
+          vref = v_scale;
+          vref_inv = inv;
+          wf[0] = 1.f;
+        }
+      }
+      const int sw = C::SWZ == 128 ? (g & 7) : ((g >> 1) & 3);  // swizzle of rows g and g+8
 #pragma unroll
       for (int u = 0; u < NPP; ++u) {
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int sgi = 0; sgi < SEGS; ++sgi) {
 #pragma unroll
-          for (int qq = 0; qq < 2; ++qq) {
-            const uint32_t gran = (uint32_t)(((2 * t + qq) ^ sw) * 16);
-            const uint4 ka = mma::lds128(st[u] + sgi * C::BOX_BYTES + g * 128 + gran);
-            const uint4 kb = mma::lds128(st[u] + sgi * C::BOX_BYTES + (g + 8) * 128 + gran);
+          for (int qq = 0; qq < C::GPL; ++qq) {
+            const uint32_t gran = (uint32_t)(((C::GPL * t + qq) ^ sw) * 16);
+            const uint4 ka = mma::lds128(st[u] + sgi * C::BOX_BYTES + g * C::SWZ + gran);
+            const uint4 kb = mma::lds128(st[u] + sgi * C::BOX_BYTES + (g + 8) * C::SWZ + gran);
             const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w};
             const uint32_t wb[4] = {kb.x, kb.y, kb.z, kb.w};
             if constexpr (kFp8) {
@@ -564,20 +601,7 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
             }
           }
         }
-        float page_qscale = qscale;
-        if constexpr (BS) {
-          const float2 bs = *(reinterpret_cast<const float2*>(smem + C::OFF_SCALES) + stage[u]);
-          page_qscale *= bs.x;
-          wf[u] = bs.y * vref_inv;
-          of[u] = 1.f;
-          if (wf[u] > 64.f || (wf[u] < 1.f / 64.f && bs.y > 0.f)) {
-            const float inv = 1.f / bs.y;
-            of[u] = vref * inv;
-            vref = bs.y;
-            vref_inv = inv;
-            wf[u] = 1.f;
-          }
-        }
+        const float page_qscale = BS ? qscale * ks[u] : qscale;
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[u][e] = (sc[0][e] + sc[1][e]) * page_qscale;
         vs_lo[u] = vs_hi[u] = 1.f;
@@ -726,20 +750,13 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
         const uint32_t pb0 = *reinterpret_cast<const uint32_t*>(pu + g * P + 2 * t);
         const uint32_t pb1 = *reinterpret_cast<const uint32_t*>(pu + g * P + 2 * t + 8);
         const uint32_t* vf = kEarlyV ? &vfrag[kEarlyV ? u : 0][0][0] : nullptr;
-        if constexpr (BS) {
-          if (of[u] != 1.f) {
-#pragma unroll
-            for (int mt = 0; mt < MTILES; ++mt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[mt][e] *= of[u];
-          }
-        }
         if (valid[u] < P)
           pv_step(std::true_type{}, st[u], pb0, pb1, valid[u], vf);
         else
           pv_step(std::false_type{}, st[u], pb0, pb1, valid[u], vf);
         if constexpr (!kEarlyV) dev::release_stage(dev::smem_addr(&empty[stage[u]]), lane);
       }
+      return true;
     };
 
     // page split: page k to warp k % NW, one page a step; column split:
@@ -748,7 +765,8 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
       int k = CS ? kbase : kbase + (warp - kbase % NW + NW) % NW;
       if constexpr (C::NPP > 1) {
         for (; k + (C::NPP - 1) * PS < kbase + npg; k += C::NPP * PS)
-          step(std::integral_constant<int, C::NPP>{}, k);
+          if (!step(std::integral_constant<int, C::NPP>{}, k))
+            for (int u = 0; u < C::NPP; ++u) step(std::integral_constant<int, 1>{}, k + u * PS);
       }
       for (; k < kbase + npg; k += PS) step(std::integral_constant<int, 1>{}, k);
     }
@@ -811,7 +829,7 @@ inline void fill_mma_kernel(DecodeKernel* k) {
   k->group = G;
   k->head_dim = D;
   k->box_x = C::BOX_X;
-  k->swizzle_128b = true;
+  k->swizzle_bytes = C::SWZ;
   k->tensor_cores = true;
   k->token_scales = SC == kScalePerToken;
   k->block_scales = SC == kScalePerBlock;
@@ -924,18 +942,25 @@ inline bool find_token_scale_kernel_for(int head_dim, int group, DecodeKernel* k
   return false;
 }
 
-// E4M3 KV with per-block scales, one query token: the consumer that a plain
-// plan of this shape takes by default.
+// E4M3 KV with per-block scales, one query token: the tensor-core consumer at
+// every group and both head dims (group 1 leaves seven of an MMA's eight
+// columns empty and still beat the CUDA cores: 96.0 to 103.8 us for one
+// 65536-token sequence of 32 heads at head_dim 128, 56.4 to 83.3 us for 64
+// requests of 2000-6000 tokens, 8 heads, at head_dim 64).  The grid is the
+// plan's, made for the plain kernel of the shape, and at head_dim 64 that is the
+// CUDA-core one, whose registers leave one CTA per SM at group 8 and three at
+// group 4 (four elsewhere): there each CTA gets 16 or 6 consumer warps in place
+// of 4 (64 requests as above: 176 to 79 us at group 8, 77 to 56 us at group 4).
+constexpr int block_scale_warps(int head_dim, int group) {
+  return head_dim != 64 ? 4 : group == 8 ? 16 : group == 4 ? 6 : 4;
+}
 template <typename QT>
 inline bool find_block_scale_kernel_for(int head_dim, int group, DecodeKernel* k) {
   using KVT = __nv_fp8_e4m3;
-#define FA_BS_CASE(DD, GG)                                             \
-  if (head_dim == DD && group == GG) {                                 \
-    if constexpr (GG >= 2 && DD % 128 == 0)                            \
-      fill_mma_kernel<QT, KVT, DD, GG, 4, kScalePerBlock>(k);          \
-    else                                                               \
-      fill_kernel<QT, KVT, DD, GG, 4, kScalePerBlock>(k);              \
-    return true;                                                       \
+#define FA_BS_CASE(DD, GG)                                                               \
+  if (head_dim == DD && group == GG) {                                                   \
+    fill_mma_kernel<QT, KVT, DD, GG, block_scale_warps(DD, GG), kScalePerBlock>(k);      \
+    return true;                                                                         \
   }
   FA_BS_CASE(64, 1) FA_BS_CASE(64, 2) FA_BS_CASE(64, 4) FA_BS_CASE(64, 8)
   FA_BS_CASE(128, 1) FA_BS_CASE(128, 2) FA_BS_CASE(128, 4) FA_BS_CASE(128, 8)

@@ -78,7 +78,7 @@ struct DecodeKernel {
   int group = 0;
   int head_dim = 0;
   int box_x = 0;              // elements per TMA box row (D, or 128 bytes' worth)
-  bool swizzle_128b = false;  // stage rows in TMA 128-byte swizzle order
+  int swizzle_bytes = 0;      // stage rows in TMA 64- or 128-byte swizzle order (0: none)
   bool tensor_cores = false;  // per-page products on mma.sync
   bool token_scales = false;  // reads per-token K/V scales (E4M3 only)
   bool block_scales = false;  // reads per-block K/V scales (E4M3 only)
