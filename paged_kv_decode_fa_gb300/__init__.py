@@ -84,10 +84,9 @@ class PlanInfo(ctypes.Structure):
         return out
 
 
-class Rows(ctypes.Structure):
-    """fa_rows: [rows, heads, head_dim] with element strides."""
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64)]
+# fa_rows of k, v and q in a row: {address, token stride, head stride} each
+_Rows3 = ctypes.c_int64 * 9
+_ROWS_BYTES = 24
 
 
 class LibraryStats(ctypes.Structure):
@@ -129,18 +128,17 @@ def _load() -> ctypes.CDLL:
     lib.fa_decode_run_head_scales.restype = i32
     lib.fa_decode_run_block_scales.argtypes = [P, P, P, i64, f32, P, P, P, P, P]
     lib.fa_decode_run_block_scales.restype = i32
-    rows = ctypes.POINTER(Rows)
     lib.fa_append_workspace_size.argtypes = [i32, i64]
     lib.fa_append_workspace_size.restype = sz
     lib.fa_append_plan.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, i32, i32,
                                    P, sz, P, ctypes.POINTER(P)]
     lib.fa_append_plan.restype = i32
-    lib.fa_append_run.argtypes = [P, rows, rows, rows, P, P, i64, f32, f32, P]
+    lib.fa_append_run.argtypes = [P, P, P, P, P, P, i64, f32, f32, P]
     lib.fa_append_run.restype = i32
     for name in ("fa_append_run_head_scales", "fa_append_run_token_scales",
                  "fa_append_run_block_scales"):
         f = getattr(lib, name)
-        f.argtypes = [P, rows, rows, rows, P, P, i64, P, P, P]
+        f.argtypes = [P, P, P, P, P, P, i64, P, P, P]
         f.restype = i32
     lib.fa_append_check.argtypes = [P, P, ctypes.POINTER(i32)]
     lib.fa_append_check.restype = i32
@@ -413,13 +411,11 @@ class DecodePlan:
                 or not paged_kv.is_contiguous() or not paged_kv.is_cuda):
             raise ValueError("paged_kv must be a contiguous CUDA tensor "
                              "[num_pages, 2, page_size, num_kv_heads, head_dim]")
-        pinned = not q.is_cuda  # outputs follow q: device, or page-locked host memory
-        if out is None:
-            out = torch.empty(self._q_shape(), dtype=q.dtype, device=q.device,
-                              pin_memory=pinned)
+        pinned = {} if q.is_cuda else {"pin_memory": True}  # outputs follow q: device, or
+        if out is None:                                     # page-locked host memory
+            out = torch.empty_like(q, **pinned)
         if return_lse and lse is None:
-            lse = torch.empty(self._q_shape()[:-1], dtype=torch.float32, device=q.device,
-                              pin_memory=pinned)
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device, **pinned)
         for t in (out, lse):
             if t is not None and (not _reachable(t) or not t.is_contiguous()):
                 raise ValueError("out / lse must be contiguous CUDA or page-locked tensors")
@@ -471,9 +467,10 @@ class DecodePlan:
 
 
 def _check_scales(scales, shape, paged_kv) -> None:
+    device = paged_kv.get_device()
     for s in scales:
-        if (s.dtype != torch.float32 or tuple(s.shape) != shape or not s.is_contiguous()
-                or s.device != paged_kv.device):
+        if (s.dtype is not torch.float32 or s.shape != shape or not s.is_contiguous()
+                or s.get_device() != device):
             raise ValueError(f"scales must be contiguous float32 tensors {list(shape)} on the "
                              "device of paged_kv")
 
@@ -811,6 +808,10 @@ class AppendPlan:
         self.kv_dtype = kv_dtype
         self.batch, self.num_qo_heads, self.num_kv_heads, self.head_dim, self.page_size = shape
         self.num_tokens = num_tokens
+        self._device = workspace.get_device()
+        self._page_shape = (2, self.page_size, self.num_kv_heads, self.head_dim)
+        self._kv_shape = (num_tokens, self.num_kv_heads, self.head_dim)
+        self._q_shape = (num_tokens, self.num_qo_heads, self.head_dim)
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -825,9 +826,10 @@ class AppendPlan:
         strides free) to the cache; with q [num_tokens, Hq, D], also rotate it
         and return it (in q_out, contiguous; q itself to rotate in place).
         k_scale / v_scale are an E4M3 cache's per-tensor scales."""
-        rows, q_out = self._rows(k, v, paged_kv, q, q_out)
+        rows, q_out, out = self._rows(k, v, paged_kv, q, q_out)
+        at = ctypes.addressof(rows)
         _check(_L().fa_append_run(
-            self._h, *rows, q_out.data_ptr() if q_out is not None else None,
+            self._h, at, at + _ROWS_BYTES, at + 2 * _ROWS_BYTES if q is not None else None, out,
             paged_kv.data_ptr(), paged_kv.shape[0], float(k_scale), float(v_scale),
             _stream_handle(stream)), "fa_append_run")
         return q_out
@@ -872,55 +874,58 @@ class AppendPlan:
         return int(flags.value)
 
     def _run_scales(self, name, shape, k, v, paged_kv, k_scales, v_scales, q, q_out, stream):
-        rows, q_out = self._rows(k, v, paged_kv, q, q_out)
+        rows, q_out, out = self._rows(k, v, paged_kv, q, q_out)
         _check_scales((k_scales, v_scales), shape, paged_kv)
+        at = ctypes.addressof(rows)
         _check(getattr(_L(), name)(
-            self._h, *rows, q_out.data_ptr() if q_out is not None else None,
+            self._h, at, at + _ROWS_BYTES, at + 2 * _ROWS_BYTES if q is not None else None, out,
             paged_kv.data_ptr(), paged_kv.shape[0], k_scales.data_ptr(), v_scales.data_ptr(),
             _stream_handle(stream)), name)
         return q_out
 
     def _rows(self, k, v, paged_kv, q, q_out):
-        """Check the tensors against the plan; fa_rows of k, v and q, and q_out."""
-        T, Hkv, D = self.num_tokens, self.num_kv_heads, self.head_dim
-        if paged_kv.dtype != self.kv_dtype:
+        """Check the tensors against the plan; fa_rows of k, v and q, q_out, its
+        address (None without q)."""
+        if paged_kv.dtype is not self.kv_dtype:
             raise TypeError("paged_kv dtype differs from the plan")
-        if (paged_kv.dim() != 5 or tuple(paged_kv.shape[1:]) != (2, self.page_size, Hkv, D)
-                or not paged_kv.is_contiguous() or paged_kv.device != self._workspace.device):
+        if (paged_kv.shape[1:] != self._page_shape or not paged_kv.is_contiguous()
+                or paged_kv.get_device() != self._device):
             raise ValueError("paged_kv must be a contiguous CUDA tensor "
                              "[num_pages, 2, page_size, num_kv_heads, head_dim] on the plan's "
                              "device")
-        out = [self._row(k, (T, Hkv, D)), self._row(v, (T, Hkv, D)), None]
+        kv = self._row(k, self._kv_shape) + self._row(v, self._kv_shape)
         if q is None:
             if q_out is not None:
                 raise ValueError("q_out without q")
-            return out, None
-        shape = (T, self.num_qo_heads, D)
-        out[2] = self._row(q, shape)
+            return _Rows3(*kv), None, None
+        rows = _Rows3(*kv, *self._row(q, self._q_shape))
         if q_out is None:
-            q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
-        elif (q_out.dtype != q.dtype or tuple(q_out.shape) != shape
-              or not q_out.is_contiguous() or q_out.device != q.device):
-            raise ValueError(f"q_out must be a contiguous tensor {list(shape)} of q's dtype on "
-                             "its device")
-        return out, q_out
+            q_out = torch.empty(self._q_shape, dtype=q.dtype, device=q.device)
+        elif (q_out.dtype is not q.dtype or q_out.shape != self._q_shape
+              or not q_out.is_contiguous() or q_out.get_device() != self._device):
+            raise ValueError(f"q_out must be a contiguous tensor {list(self._q_shape)} of q's "
+                             "dtype on its device")
+        return rows, q_out, q_out.data_ptr()
 
     def _row(self, t, shape):
-        if t.dtype != self.q_dtype:
+        """(address, token stride, head stride) of a k, v or q."""
+        if t.dtype is not self.q_dtype:
             raise TypeError("k / v / q dtype differs from the plan")
-        if tuple(t.shape) != shape or t.device != self._workspace.device:
+        if t.shape != shape or t.get_device() != self._device:
             raise ValueError(f"k / v / q must be CUDA tensors on the plan's device, here "
                              f"{list(shape)}")
-        if t.numel() == 0:
-            return Rows(None, 0, 0)
+        if not shape[0]:
+            return 0, 0, 0
+        address, (token, head, inner) = t.data_ptr(), t.stride()
         # a stride that is never taken may be anything
-        token = t.stride(0) if shape[0] > 1 else 0
-        head = t.stride(1) if shape[1] > 1 else 0
-        es = t.element_size()
-        if t.stride(2) != 1 or token * es % 16 or head * es % 16 or t.data_ptr() % 16:
+        if shape[0] == 1:
+            token = 0
+        if shape[1] == 1:
+            head = 0
+        if inner != 1 or (address | token * t.itemsize | head * t.itemsize) & 15:
             raise ValueError("k / v / q need a contiguous innermost dim, and an address and "
                              "strides in whole 16 bytes")
-        return Rows(t.data_ptr(), token, head)
+        return address, token, head
 
 
 def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num_qo_heads: int,

@@ -20,13 +20,14 @@
 // codes it holds are divided by a power of two, exactly but for subnormals,
 // so a page filled a token at a time reads as one filled at once.
 //
-// Work: one CTA per (page run, up to 4 kv heads); a run is the new tokens of
-// one request in one page, at most 16.  The angles of a run are computed once
-// into shared memory (they depend on the token and the pair only) and kept in
-// registers by a thread, which serves one token and 16 bytes of a row and
-// goes over its heads.  All K and V loads of a thread are issued before the
-// angles are computed.  A block's amax needs all its tokens, which the CTA
-// holds: one reduction in shared memory, no second pass over the inputs.
+// Work: one CTA per (page run, a few kv heads: heads_of_cta); a run is the new
+// tokens of one request in one page, at most 16.  A thread serves one token and
+// both halves of eight of its pairs (or 16 dims in a row), so that a pair never
+// leaves its registers, and goes over its heads with the same eight angles.  The
+// angles of a run are computed once, into shared memory.  All K and V loads of
+// a thread are issued before that.  A block's amax needs all its tokens, which
+// the CTA holds: one reduction in shared memory, no second pass over the
+// inputs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -48,8 +49,10 @@
 namespace fadecode {
 namespace {
 
-constexpr int kHeads = 4;        // kv heads of one CTA
-constexpr int kItems = 2 * kHeads;  // K rows, then V rows, of a token in one CTA
+constexpr int kHeads = 2;      // kv heads a thread holds K and V of
+constexpr int kMaxHeads = 16;  // kv heads of one CTA at most
+constexpr int kQRows = 4;      // q rows a thread loads at a time
+constexpr int kCtasPerSm = 6;  // CTAs per SM the registers are held to (80 each)
 constexpr int kMaxPairs = 64;    // rotary_dim / 2 at most
 
 // How an E4M3 cache is scaled (kNative: q's type, no scale).
@@ -84,6 +87,7 @@ struct AppendParams {
   int* err;
   int64_t num_pages;
   int hq, hkv;
+  int heads;  // kv heads of one CTA, kHeads per thread at most
   int pairs;  // rotary_dim / 2
   int interleaved;
 };
@@ -109,14 +113,23 @@ __device__ __forceinline__ uint32_t pack(float a, float b, __half) {
   return w;
 }
 
-template <typename T, int E>
-__device__ __forceinline__ void widen(const uint4& r, float (&x)[E]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight consecutive elements: as stored, and widened.
+template <typename T>
+struct Group {
+  uint4 w[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ void widen(const Group<T>& g, float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t w[8] = {g.w[0].x, g.w[0].y, g.w[0].z, g.w[0].w,
+                           g.w[1].x, g.w[1].y, g.w[1].z, g.w[1].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (E == 4) {
-      x[i] = __uint_as_float(w[i]);
-    } else {
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+  } else {
+    const uint32_t w[4] = {g.w[0].x, g.w[0].y, g.w[0].z, g.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       const float2 f = unpack(w[i], T{});
       x[2 * i] = f.x;
       x[2 * i + 1] = f.y;
@@ -124,24 +137,100 @@ __device__ __forceinline__ void widen(const uint4& r, float (&x)[E]) {
   }
 }
 
-template <typename T, int E>
-__device__ __forceinline__ uint4 narrow(const float (&x)[E]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (E == 4)
-      w[i] = __float_as_uint(x[i]);
-    else
-      w[i] = pack(x[2 * i], x[2 * i + 1], T{});
+template <typename T>
+__device__ __forceinline__ Group<T> narrow(const float (&x)[8]) {
+  Group<T> g;
+  if constexpr (sizeof(T) == 4) {
+    g.w[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                        __float_as_uint(x[3]));
+    g.w[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]),
+                        __float_as_uint(x[7]));
+  } else {
+    g.w[0] = make_uint4(pack(x[0], x[1], T{}), pack(x[2], x[3], T{}), pack(x[4], x[5], T{}),
+                        pack(x[6], x[7], T{}));
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return g;
 }
 
-// x * inv as an E4M3 code: finite values saturate at 448; a non-finite x,
-// which E4M3 cannot tell from a large one, becomes NaN (x - x is 0 or NaN).
+// Plain loads, not through the read-only path: q_out may be q itself.
+template <typename T>
+__device__ __forceinline__ Group<T> load_group(const T* p, bool ok) {
+  Group<T> g;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    g.w[i] = ok ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0u, 0u, 0u, 0u);
+  return g;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_group(T* p, const Group<T>& g) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = g.w[i];
+}
+
+// A thread's 16 elements of a row: dims da .. da+7 and db .. db+7.
+struct Piece {
+  float a[8], b[8];
+};
+
+// Its rotation: eight pairs, (a[j], b[j]), or interleaved within a and b.
+struct Turn {
+  float c[8], s[8];
+  bool on, interleaved;
+};
+
+__device__ __forceinline__ void rotate(const Turn& r, Piece* x) {
+  if (!r.on) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (r.interleaved) {
+      float* y = j < 4 ? x->a : x->b;
+      const int e = 2 * (j % 4);
+      const float u = y[e], v = y[e + 1];
+      y[e] = u * r.c[j] - v * r.s[j];
+      y[e + 1] = v * r.c[j] + u * r.s[j];
+    } else {
+      const float u = x->a[j], v = x->b[j];
+      x->a[j] = u * r.c[j] - v * r.s[j];
+      x->b[j] = v * r.c[j] + u * r.s[j];
+    }
+  }
+}
+
+// The largest magnitude of the piece's finite elements.  E4M3 cannot tell an
+// infinity from a large value: infinities become NaN here, which fmaxf passes
+// over and the conversion keeps.
+__device__ __forceinline__ float finite_amax(Piece* x) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(x->a[j]), fabsf(x->b[j])));
+  if (m == INFINITY) {
+    m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (fabsf(x->a[j]) == INFINITY) x->a[j] = NAN;
+      if (fabsf(x->b[j]) == INFINITY) x->b[j] = NAN;
+      m = fmaxf(m, fmaxf(fabsf(x->a[j]), fabsf(x->b[j])));
+    }
+  }
+  return m;
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_max(float m) {
+#pragma unroll
+  for (int off = LPR / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  return m;
+}
+
+// Codes of x * inv, saturated at 448.
 __device__ __forceinline__ uint32_t code2(float a, float b, float inv) {
-  const float2 y = make_float2(fmaf(a, inv, a - a), fmaf(b, inv, b - b));
-  return __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+  return __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[8], float inv) {
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(code2(x[0], x[1], inv) | (code2(x[2], x[3], inv) << 16),
+                 code2(x[4], x[5], inv) | (code2(x[6], x[7], inv) << 16));
 }
 
 // The smallest power of two s >= 2^-126 with amax <= 448 s (448 = 1.75 * 2^8: the
@@ -154,94 +243,49 @@ __device__ __forceinline__ float block_scale(float amax) {
 
 __device__ __forceinline__ float inverse(float scale) { return scale > 0.f ? 1.f / scale : 0.f; }
 
-template <typename T, int D>
+template <int D>
 struct Cfg {
-  static constexpr int E = 16 / (int)sizeof(T);  // elements of a thread's 16 bytes
-  static constexpr int LPR = D / E;              // threads of a row
-  static constexpr int THREADS = LPR * 16 < 256 ? 256 : LPR * 16;
-  static constexpr int ROWS = THREADS / LPR;  // rows in step, at least a page's tokens
+  static constexpr int THREADS = 128;
+  static constexpr int LPR = D / 16;          // threads of a row
+  static constexpr int ROWS = THREADS / LPR;  // rows in step
+  static_assert(ROWS >= kPageSize && 2 * kMaxHeads <= THREADS, "a run's tokens; a thread a scale");
 };
-
-// A thread's rotation: cos and sin of its E elements (interleaved: E / 2
-// pairs), and the lane that holds the other halves of its pairs.
-template <int E>
-struct Turn {
-  float c[E], s[E];
-  int partner;
-  bool on, first, interleaved;
-};
-
-template <typename T, int E>
-__device__ __forceinline__ void rotate(const uint4& raw, const Turn<E>& r, float (&x)[E]) {
-  widen<T, E>(raw, x);
-  if (r.interleaved) {
-    if (!r.on) return;
-#pragma unroll
-    for (int j = 0; j < E; j += 2) {
-      const float a = x[j], b = x[j + 1];
-      x[j] = a * r.c[j / 2] - b * r.s[j / 2];
-      x[j + 1] = b * r.c[j / 2] + a * r.s[j / 2];
-    }
-    return;
-  }
-  uint4 other;
-  other.x = __shfl_sync(0xffffffffu, raw.x, r.partner);
-  other.y = __shfl_sync(0xffffffffu, raw.y, r.partner);
-  other.z = __shfl_sync(0xffffffffu, raw.z, r.partner);
-  other.w = __shfl_sync(0xffffffffu, raw.w, r.partner);
-  if (!r.on) return;
-  float y[E];
-  widen<T, E>(other, y);
-#pragma unroll
-  for (int j = 0; j < E; ++j)
-    x[j] = r.first ? x[j] * r.c[j] - y[j] * r.s[j] : x[j] * r.c[j] + y[j] * r.s[j];
-}
-
-template <int E, int LPR>
-__device__ __forceinline__ float row_amax(const float (&x)[E]) {
-  float m = 0.f;
-#pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const float a = fabsf(x[j]);
-    m = fmaxf(m, a < INFINITY ? a : 0.f);
-  }
-#pragma unroll
-  for (int off = LPR / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  return m;
-}
 
 template <typename T, int D, int MODE>
-__global__ void __launch_bounds__(Cfg<T, D>::THREADS)
-    fa_append_kernel(const AppendParams p) {
-  using C = Cfg<T, D>;
-  constexpr int E = C::E, LPR = C::LPR;
+__global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
+    fa_append_kernel(const __grid_constant__ AppendParams p) {
+  using C = Cfg<D>;
+  constexpr int LPR = C::LPR;
   __shared__ float2 angle[kPageSize * kMaxPairs];
-  __shared__ int amax_bits[kItems];
-  __shared__ float item_scale[kItems], item_ratio[kItems];
+  __shared__ int amax_bits[2 * kMaxHeads];                 // K heads, then V heads
+  __shared__ float item_scale[2 * kMaxHeads], item_ratio[2 * kMaxHeads];
 
   const AppendUnit u = p.units[blockIdx.x];
   const int slot0 = u.slots & 0xff, n = u.slots >> 8;
-  const int h0 = blockIdx.y * kHeads, heads = min(kHeads, p.hkv - h0), items = 2 * heads;
-  const int tid = threadIdx.x, lane = tid & 31;
-  // this thread: 16 bytes of a row from dim d0, of token `tok`, and of rows
-  // hg, hg + HG, ... of the CTA's K and V rows, and then of its q rows
-  const int c = tid % LPR, r = tid / LPR, d0 = c * E;
+  const int h0 = blockIdx.y * p.heads, heads = min(p.heads, p.hkv - h0);
+  const int tid = threadIdx.x;
+  // this thread: 16 elements of rows of token `tok`, of heads hg, hg + HG, ...
+  const int c = tid % LPR, r = tid / LPR;
   const int lg = n > 8 ? 4 : n > 4 ? 3 : n > 2 ? 2 : n > 1 ? 1 : 0;
   const int tok = r & ((1 << lg) - 1), hg = r >> lg, HG = C::ROWS >> lg;
   const bool live = tok < n;
   const int64_t row = u.row + tok;
+  // its dims: the two halves of eight pairs, or 16 in a row
+  const bool split = !p.interleaved && 8 * c < p.pairs;
+  const int da = split ? 8 * c : 16 * c, db = split ? p.pairs + 8 * c : 16 * c + 8;
 
-  uint4 raw[kItems];
+  Group<T> kr[kHeads][2], vr[kHeads][2];
+  {
+    const T* k = static_cast<const T*>(p.k.p) + row * p.k.token + h0 * p.k.head;
+    const T* v = static_cast<const T*>(p.v.p) + row * p.v.token + h0 * p.v.head;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    if (i * HG >= items) break;
-    const int it = i * HG + hg;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (live && it < items) {
-      const Rows& in = it < heads ? p.k : p.v;
-      const int h = h0 + (it < heads ? it : it - heads);
-      raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(in.p) +
-                                                    row * in.token + h * in.head + d0));
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = i * HG + hg;
+      const bool ok = live && h < heads;
+      kr[i][0] = load_group(k + h * p.k.head + da, ok);
+      kr[i][1] = load_group(k + h * p.k.head + db, ok);
+      vr[i][0] = load_group(v + h * p.v.head + da, ok);
+      vr[i][1] = load_group(v + h * p.v.head + db, ok);
     }
   }
   const int page = __ldg(p.indices + u.entry);
@@ -257,45 +301,39 @@ __global__ void __launch_bounds__(Cfg<T, D>::THREADS)
     sincospif((float)half_turns * 4.656612873077393e-10f, &cs.y, &cs.x);
     angle[t * kMaxPairs + (i - t * p.pairs)] = cs;
   }
-  if (MODE == kBlock && tid < kItems) amax_bits[tid] = 0;
+  if (MODE == kBlock && tid < 2 * heads) amax_bits[tid] = 0;
   __syncthreads();
 
-  Turn<E> turn;
+  Turn turn;
   turn.interleaved = p.interleaved != 0;
-  turn.on = live && d0 < 2 * p.pairs;
-  turn.first = d0 < p.pairs;
-  turn.partner = lane;
-  if (!turn.interleaved && d0 < 2 * p.pairs)
-    turn.partner = turn.first ? lane + p.pairs / E : lane - p.pairs / E;
+  turn.on = live && 8 * c < p.pairs;
 #pragma unroll
-  for (int j = 0; j < E; ++j) turn.c[j] = turn.s[j] = 0.f;
-  if (turn.on) {
-    const int at = tok * kMaxPairs + (turn.interleaved ? d0 / 2 : turn.first ? d0 : d0 - p.pairs);
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      if (j < E / 2 || !turn.interleaved) {
-        const float2 cs = angle[at + j];
-        turn.c[j] = cs.x;
-        turn.s[j] = cs.y;
-      }
-    }
+  for (int j = 0; j < 8; ++j) {
+    const float2 cs = turn.on ? angle[tok * kMaxPairs + 8 * c + j] : make_float2(1.f, 0.f);
+    turn.c[j] = cs.x;
+    turn.s[j] = cs.y;
   }
+  auto piece = [&](const Group<T>(&g)[2]) {
+    Piece x;
+    widen<T>(g[0], x.a);
+    widen<T>(g[1], x.b);
+    return x;
+  };
 
   if constexpr (MODE == kBlock) {
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      if (i * HG >= items) break;
-      const int it = i * HG + hg;
-      Turn<E> t = turn;
-      // K and V rows may share a warp: V rows take part in the exchange only
-      t.on = turn.on && it < heads;
-      float x[E];
-      rotate<T, E>(raw[i], t, x);
-      const float m = row_amax<E, LPR>(x);
-      if (c == 0 && live && it < items) atomicMax(&amax_bits[it], __float_as_int(m));
+    for (int i = 0; i < kHeads; ++i) {
+      if (i * HG >= heads) break;
+      Piece k = piece(kr[i]), v = piece(vr[i]);
+      rotate(turn, &k);
+      const float km = row_max<LPR>(finite_amax(&k)), vm = row_max<LPR>(finite_amax(&v));
+      if (c == 0 && live && i * HG + hg < heads) {
+        atomicMax(&amax_bits[i * HG + hg], __float_as_int(km));
+        atomicMax(&amax_bits[heads + i * HG + hg], __float_as_int(vm));
+      }
     }
     __syncthreads();
-    if (tid < items) {
+    if (tid < 2 * heads) {
       const bool is_k = tid < heads;
       float* scales = is_k ? p.k_scales : p.v_scales;
       const float need = block_scale(__int_as_float(amax_bits[tid]));
@@ -312,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<T, D>::THREADS)
     __syncthreads();
     if (slot0 > 0 && page_ok) {
       // codes the page already holds, under the scales that grew
-      for (int it = 0; it < items; ++it) {
+      for (int it = 0; it < 2 * heads; ++it) {
         const float ratio = item_ratio[it];
         if (ratio == 1.f) continue;
         const bool is_k = it < heads;
@@ -333,74 +371,87 @@ __global__ void __launch_bounds__(Cfg<T, D>::THREADS)
     }
   }
 
-#pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    if (i * HG >= items) break;
-    const int it = i * HG + hg;
-    const bool is_k = it < heads;
-    const int h = h0 + (is_k ? it : it - heads);
-    Turn<E> t = turn;
-    t.on = turn.on && is_k;
-    float x[E];
-    rotate<T, E>(raw[i], t, x);
+  // K rows, then V rows
+  auto write = [&](Piece x, bool is_k, const Group<T>(&raw)[2], int h, bool ok) {
     float inv = 1.f, scale = 1.f;
-    if constexpr (MODE == kStatic) {
-      const float* hs = is_k ? p.head_k_scales : p.head_v_scales;
-      inv = inverse(!hs ? (is_k ? p.k_scale : p.v_scale) : it < items ? __ldg(hs + h) : 1.f);
-    } else if constexpr (MODE == kToken) {
-      const float m = row_amax<E, LPR>(x);
-      scale = m > 0.f ? fmaxf(m / 448.f, 1.17549435e-38f) : 0.f;
-      inv = inverse(scale);
-    } else if constexpr (MODE == kBlock) {
-      inv = it < items ? inverse(item_scale[it]) : 0.f;
-    }
-    if (!live || it >= items || !page_ok) continue;
-    const int64_t at =
-        ((((int64_t)page * 2 + (is_k ? 0 : 1)) * kPageSize + slot0 + tok) * p.hkv + h) * D + d0;
-    if constexpr (MODE == kNative) {
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.kv) + at) = narrow<T, E>(x);
-    } else {
-      if constexpr (MODE == kToken) {
-        if (c == 0)
-          (is_k ? p.k_scales : p.v_scales)[((int64_t)page * p.hkv + h) * kPageSize + slot0 + tok] =
-              scale;
+    if constexpr (MODE != kNative) {
+      const float m = finite_amax(&x);
+      if constexpr (MODE == kStatic) {
+        const float* hs = is_k ? p.head_k_scales : p.head_v_scales;
+        inv = inverse(!hs ? (is_k ? p.k_scale : p.v_scale) : ok ? __ldg(hs + h0 + h) : 1.f);
+      } else if constexpr (MODE == kToken) {
+        const float rm = row_max<LPR>(m);
+        scale = rm > 0.f ? fmaxf(rm / 448.f, 1.17549435e-38f) : 0.f;
+        inv = inverse(scale);
+      } else {
+        inv = ok ? inverse(item_scale[is_k ? h : heads + h]) : 0.f;
       }
-      static_assert(MODE == kNative || E == 8, "E4M3 caches take 16-bit inputs");
-      uint2 w;
-      w.x = code2(x[0], x[1], inv) | (code2(x[2], x[3], inv) << 16);
-      w.y = code2(x[E - 4], x[E - 3], inv) | (code2(x[E - 2], x[E - 1], inv) << 16);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kv) + at) = w;
     }
+    if (!ok || !page_ok) return;
+    const int64_t at =
+        ((((int64_t)page * 2 + (is_k ? 0 : 1)) * kPageSize + slot0 + tok) * p.hkv + h0 + h) * D;
+    if constexpr (MODE == kNative) {
+      T* out = static_cast<T*>(p.kv) + at;
+      store_group(out + da, is_k ? narrow<T>(x.a) : raw[0]);
+      store_group(out + db, is_k ? narrow<T>(x.b) : raw[1]);
+    } else {
+      if (MODE == kToken && c == 0)
+        (is_k ? p.k_scales : p.v_scales)[((int64_t)page * p.hkv + h0 + h) * kPageSize + slot0 +
+                                         tok] = scale;
+      uint8_t* out = static_cast<uint8_t*>(p.kv) + at;
+      store_codes(out + da, x.a, inv);
+      store_codes(out + db, x.b, inv);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (i * HG >= heads) break;
+    const int h = i * HG + hg;
+    const bool ok = live && h < heads;
+    Piece k = piece(kr[i]);
+    rotate(turn, &k);
+    write(k, true, kr[i], h, ok);
+    write(piece(vr[i]), false, vr[i], h, ok);
   }
 
   if (p.q.p == nullptr) return;
+  // q rows, kQRows at a time so that as many loads are in flight; q_out may be
+  // q itself: a row's elements are read and written by one thread
   const int group = p.hq / p.hkv, rows_q = heads * group;
-  for (int i0 = 0; i0 < rows_q; i0 += HG) {
-    const int h = h0 * group + i0 + hg;
-    const bool ok = live && i0 + hg < rows_q;
-    uint4 in = make_uint4(0u, 0u, 0u, 0u);
-    // not through the read-only path: q_out may be q itself
-    if (ok)
-      in = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q.p) + row * p.q.token +
-                                           h * p.q.head + d0);
-    float x[E];
-    rotate<T, E>(in, turn, x);
-    if (ok)
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + (row * p.hq + h) * D + d0) =
-          narrow<T, E>(x);
+  const T* q = static_cast<const T*>(p.q.p) + row * p.q.token + (int64_t)h0 * group * p.q.head;
+  T* out = static_cast<T*>(p.q_out) + (row * p.hq + h0 * group) * D;
+  for (int i0 = hg; i0 - hg < rows_q; i0 += kQRows * HG) {
+    Group<T> in[kQRows][2];
+#pragma unroll
+    for (int i = 0; i < kQRows; ++i) {
+      const int h = i0 + i * HG;
+      in[i][0] = load_group(q + h * p.q.head + da, live && h < rows_q);
+      in[i][1] = load_group(q + h * p.q.head + db, live && h < rows_q);
+    }
+#pragma unroll
+    for (int i = 0; i < kQRows; ++i) {
+      const int h = i0 + i * HG;
+      if (!live || h >= rows_q) break;
+      Piece x = piece(in[i]);
+      rotate(turn, &x);
+      store_group(out + h * D + da, narrow<T>(x.a));
+      store_group(out + h * D + db, narrow<T>(x.b));
+    }
   }
 }
 
 struct AppendKernel {
   const void* func = nullptr;
-  int threads = 0;
+  int threads = 0, rows = 0;
 };
 
 template <typename T, int MODE>
 AppendKernel kernel_of(int head_dim) {
   if (head_dim == 64)
-    return {reinterpret_cast<const void*>(&fa_append_kernel<T, 64, MODE>), Cfg<T, 64>::THREADS};
-  return {reinterpret_cast<const void*>(&fa_append_kernel<T, 128, MODE>), Cfg<T, 128>::THREADS};
+    return {reinterpret_cast<const void*>(&fa_append_kernel<T, 64, MODE>), Cfg<64>::THREADS,
+            Cfg<64>::ROWS};
+  return {reinterpret_cast<const void*>(&fa_append_kernel<T, 128, MODE>), Cfg<128>::THREADS,
+          Cfg<128>::ROWS};
 }
 
 // A kernel for q's type, the cache being E4M3 unless mode is kNative.
@@ -416,6 +467,25 @@ AppendKernel find_append_kernel(fa_dtype q, int head_dim, Mode mode) {
   if (mode == kToken) return kernel_of<__half, kToken>(head_dim);
   if (mode == kBlock) return kernel_of<__half, kBlock>(head_dim);
   return kernel_of<__half, kNative>(head_dim);
+}
+
+// kv heads of one CTA, for runs of `longest` tokens at most, `tokens` in all:
+// as many (a power of two) as keep a thread's rows of K, V and q to kMaxRows,
+// and its kv heads to kHeads.
+constexpr int kMaxRows = 24;
+int heads_of_cta(const AppendKernel& k, int64_t tokens, int64_t units, int longest, int hkv,
+                 int group) {
+  auto step = [&](int64_t n) {  // rows of one token in step, for runs of n
+    int t = 1;
+    while (t < n) t *= 2;
+    return k.rows / t;
+  };
+  const int64_t mean = (tokens + units - 1) / units;
+  int heads = 1;
+  while (2 * heads <= kMaxHeads && heads < hkv && 2 * heads <= kHeads * step(longest) &&
+         2 * heads * (2 + group) <= kMaxRows * step(mean))
+    heads *= 2;
+  return heads;
 }
 
 constexpr size_t kAlign = 256;
@@ -461,6 +531,7 @@ struct fa_append_plan_s {
   uint8_t* ws = nullptr;
   AppendLayout layout{};
   int64_t num_units = 0, num_rows = 0;
+  int longest = 0;  // tokens of the longest run
   int pairs = 0, interleaved = 0;
 };
 
@@ -515,7 +586,9 @@ int append_run(fa_append_plan_s* plan, Mode mode, const fa_rows* k, const fa_row
   p.interleaved = plan->interleaved;
   const AppendKernel kern = find_append_kernel(plan->q_dtype, plan->d, mode);
   void* args[1] = {&p};
-  const dim3 grid((unsigned)plan->num_units, (unsigned)((plan->hkv + kHeads - 1) / kHeads));
+  p.heads = heads_of_cta(kern, plan->num_rows, plan->num_units, plan->longest, plan->hkv,
+                         plan->hq / plan->hkv);
+  const dim3 grid((unsigned)plan->num_units, (unsigned)((plan->hkv + p.heads - 1) / p.heads));
   return cudaLaunchKernel(kern.func, grid, dim3(kern.threads), args, 0,
                           static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? FA_OK
@@ -553,13 +626,14 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
     if (!std::isfinite(inv_freq_host[i])) return FA_ERR_INVALID_ARG;
   if (page_size != kPageSize || (head_dim != 64 && head_dim != 128) ||
       !append_pair_built(q_dtype, kv_dtype) || rotary_dim % 16 ||
-      num_kv_heads > 65535 * kHeads)
+      num_kv_heads > 65535)
     return FA_ERR_UNSUPPORTED;
   if (indptr_host[0] != 0 || append_indptr_host[0] != 0) return FA_ERR_INVALID_ARG;
 
   std::vector<uint8_t> meta;
   fa_append_plan_s* plan = nullptr;
   int64_t units = 0;
+  int longest = 0;
   AppendLayout L{};
   for (int pass = 0; pass < 2; ++pass) {  // count the units, then write them
     AppendUnit* out =
@@ -582,6 +656,7 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
                                   (int32_t)(indptr_host[i] + page),
                                   (int32_t)(t - page * page_size) | (int32_t)((end - t) << 8),
                                   (int32_t)(off + t)};
+        longest = std::max(longest, (int)(end - t));
         ++units;
         t = end;
       }
@@ -612,6 +687,7 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
   plan->layout = L;
   plan->num_units = units;
   plan->num_rows = append_indptr_host[batch];
+  plan->longest = longest;
   plan->pairs = rotary_dim / 2;
   plan->interleaved = interleaved ? 1 : 0;
   if (cudaGetDevice(&plan->device) != cudaSuccess ||
