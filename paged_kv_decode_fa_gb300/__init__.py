@@ -293,12 +293,12 @@ class DecodePlan:
         self.q_len = q_len
         self.total_q_rows = total_q_rows  # ragged plans: rows of q / o
         self.batch, self.num_qo_heads, self.num_kv_heads, self.head_dim, self.page_size = shape
-
-    def _q_shape(self):
         B, Hq, D = self.batch, self.num_qo_heads, self.head_dim
-        if self.total_q_rows is not None:
-            return (self.total_q_rows, Hq, D)
-        return (B, Hq, D) if self.q_len == 1 else (B, self.q_len, Hq, D)
+        if total_q_rows is not None:
+            self._q_shape = (total_q_rows, Hq, D)
+        else:
+            self._q_shape = (B, Hq, D) if q_len == 1 else (B, q_len, Hq, D)
+        self._page_shape = (2, self.page_size, self.num_kv_heads, D)
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -400,14 +400,12 @@ class DecodePlan:
 
     def _outputs(self, q, paged_kv, out, lse, return_lse):
         """Check q / paged_kv against the plan; allocate missing outputs."""
-        D = self.head_dim
-        if q.dtype != self.q_dtype or paged_kv.dtype != self.kv_dtype:
+        if q.dtype is not self.q_dtype or paged_kv.dtype is not self.kv_dtype:
             raise TypeError("q / paged_kv dtype differs from the plan")
-        if tuple(q.shape) != self._q_shape() or not q.is_contiguous() or not _reachable(q):
+        if q.shape != self._q_shape or not q.is_contiguous() or not _reachable(q):
             raise ValueError(f"q must be a contiguous CUDA or page-locked tensor "
-                             f"{list(self._q_shape())}")
-        if (paged_kv.dim() != 5 or paged_kv.shape[1] != 2 or paged_kv.shape[2] != self.page_size
-                or paged_kv.shape[3] != self.num_kv_heads or paged_kv.shape[4] != D
+                             f"{list(self._q_shape)}")
+        if (paged_kv.dim() != 5 or paged_kv.shape[1:] != self._page_shape
                 or not paged_kv.is_contiguous() or not paged_kv.is_cuda):
             raise ValueError("paged_kv must be a contiguous CUDA tensor "
                              "[num_pages, 2, page_size, num_kv_heads, head_dim]")

@@ -10,7 +10,7 @@
 // it at far positions (t = 10^6 at inv_freq 1: 0.06 radians).  So the plan
 // stores inv_freq[i] / 2 pi modulo 1 as a 64-bit fraction f_i; t * f_i modulo
 // 2^64 is then the exact fraction of a turn, whatever t, in integer
-// multiplies, and its top 32 bits go to sincospi as half-turns in [-1, 1).
+// multiplies; its top 32 bits, less the nearest quarter turn, go to sincospi.
 //
 // E4M3 caches: code = rn(x / s) saturated at 448, with s per tensor, per kv
 // head, per token (amax over the row / 448, written here) or per block, a
@@ -216,6 +216,22 @@ __device__ __forceinline__ float finite_amax(Piece* x) {
   return m;
 }
 
+// (cos, sin) of a fraction of a turn, in 2^-32 turns: the nearest quarter turn
+// is taken off in integers, so that the rest, at most an eighth, goes to fp32
+// with an error of 2^-29 turns.
+__device__ __forceinline__ float2 cos_sin(unsigned turn) {
+  const unsigned quarter = (turn + (1u << 29)) >> 30;
+  const int rest = (int)(turn - (quarter << 30));
+  float s, c;
+  sincospif((float)rest * 4.656612873077393e-10f, &s, &c);  // 2^-31: in half-turns
+  if (quarter & 1) {
+    const float x = c;
+    c = -s;
+    s = x;
+  }
+  return (quarter & 2) ? make_float2(-c, -s) : make_float2(c, s);
+}
+
 template <int LPR>
 __device__ __forceinline__ float row_max(float m) {
 #pragma unroll
@@ -296,10 +312,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
     const int t = i / p.pairs;
     const unsigned long long turn =
         (unsigned long long)(unsigned)(u.position + t) * p.turns[i - t * p.pairs];
-    const int half_turns = (int)(turn >> 32);  // 2^-31 half-turns
-    float2 cs;
-    sincospif((float)half_turns * 4.656612873077393e-10f, &cs.y, &cs.x);
-    angle[t * kMaxPairs + (i - t * p.pairs)] = cs;
+    angle[t * kMaxPairs + (i - t * p.pairs)] = cos_sin((unsigned)(turn >> 32));
   }
   if (MODE == kBlock && tid < 2 * heads) amax_bits[tid] = 0;
   __syncthreads();
