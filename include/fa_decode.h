@@ -604,8 +604,9 @@ size_t fa_append_workspace_size(int batch, int64_t num_tokens);
  *                      index in its request to give its position (e.g. the
  *                      tokens of a prefix that a cascade plan holds apart);
  *                      >= 0, offset + len below 2^31.
- *  inv_freq_host       [rotary_dim / 2] double, host, finite: radians per
- *                      position of each pair.  Read during the call.
+ *  inv_freq_host       [rotary_dim / 2] double, host: radians per position of
+ *                      each pair, at most 2^32 in magnitude.  Read during the
+ *                      call.
  *  rotary_dim          dims that rotate, a multiple of 16 up to head_dim
  *                      (FA_ERR_UNSUPPORTED otherwise); 0: no rotation.
  * Built for page_size 16, head_dim 64 and 128 and fa_decode_plan's dtype
@@ -662,7 +663,8 @@ int fa_append_run_token_scales(fa_append_plan_t plan, const fa_rows* k, const fa
  * tokens at most 448 s (0 if all are 0).  A page that held tokens of the
  * request before keeps the larger of its scale and that; where it grows, the
  * codes it held are re-rounded to the same values under the new scale
- * (exactly, but for values that become subnormal). */
+ * (exactly, but for values that become subnormal).  Tokens taken back (rejected
+ * drafts) and appended over leave a page's scale as large as they made it. */
 int fa_append_run_block_scales(fa_append_plan_t plan, const fa_rows* k, const fa_rows* v,
                                const fa_rows* q, void* q_out, void* paged_kv, int64_t num_pages,
                                float* k_scales, float* v_scales, void* cuda_stream);

@@ -382,6 +382,8 @@ class DecodePlan:
         and kv head: k_scales / v_scales [num_pages, num_kv_heads] float32 CUDA
         tensors, as AppendPlan.run_block_scales writes them; returns (o, lse)."""
         out, lse = self._outputs(q, paged_kv, out, lse, return_lse)
+        if paged_kv.get_device() != self._workspace.get_device():
+            raise ValueError("paged_kv must be on the plan's device")
         _check_scales((k_scales, v_scales), (paged_kv.shape[0], self.num_kv_heads), paged_kv)
         _check(_L().fa_decode_run_block_scales(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
@@ -780,8 +782,9 @@ class RotaryTable:
         elif isinstance(inv_freq, torch.Tensor):
             inv_freq = inv_freq.detach().to("cpu", torch.float64).numpy()
         self.inv_freq = np.array(inv_freq, dtype=np.float64)
-        if self.inv_freq.shape != (rotary_dim // 2,) or not np.isfinite(self.inv_freq).all():
-            raise ValueError(f"inv_freq must be {rotary_dim // 2} finite values")
+        if (self.inv_freq.shape != (rotary_dim // 2,)
+                or not (np.abs(self.inv_freq) <= 2.0 ** 32).all()):
+            raise ValueError(f"inv_freq must be {rotary_dim // 2} values of at most 2^32")
         self.rotary_dim = int(rotary_dim)
         self.interleaved = bool(interleaved)
 
@@ -951,6 +954,12 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
     if indices.dtype != torch.int32 or not _reachable(indices) or not indices.is_contiguous():
         raise ValueError("indices must be a contiguous int32 CUDA or page-locked tensor")
     total = int(np.asarray(app_h)[B]) if B >= 0 else 0
+    device = torch.cuda.current_device()
+    if indices.is_cuda and indices.get_device() != device:
+        raise ValueError("indices must be on the current device")
+    if workspace is not None and (workspace.get_device() != device
+                                  or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the current device")
     if workspace is None:
         workspace = torch.empty(append_workspace_size(max(B, 0), max(total, 0)),
                                 dtype=torch.uint8, device=_cuda_device(indices))

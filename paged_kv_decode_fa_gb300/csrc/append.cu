@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
         const int64_t at = (int64_t)page * p.hkv + h0 + (is_k ? tid : tid - heads);
         if (slot0 > 0) old = scales[at];
         now = fmaxf(old, need);
-        if (slot0 == 0 || now > old) scales[at] = now;
+        if (slot0 == 0 || !(now == old)) scales[at] = now;
       }
       item_scale[tid] = now;
       item_ratio[tid] = now > old ? old * inverse(now) : 1.f;
@@ -516,6 +516,10 @@ AppendLayout append_layout(int64_t n_units, int pairs) {
   return L;
 }
 
+// Radians a position at most (models use at most 1): the turns below then keep
+// 64 bits of their fraction, the rounding of freq / 2 pi included.
+constexpr double kMaxFrequency = 4294967296.0;
+
 // freq / 2 pi modulo 1 in units of 2^-64, rounded down in magnitude: the
 // product with 1 / 2 pi in two doubles (its rounding error recovered by fma),
 // so that the 64 bits carry the double's own precision.
@@ -635,8 +639,8 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
   if (batch > 0 && !last_page_len_host) return FA_ERR_INVALID_ARG;
   if (rotary_dim < 0 || rotary_dim > head_dim || (rotary_dim > 0 && !inv_freq_host))
     return FA_ERR_INVALID_ARG;
-  for (int i = 0; i < rotary_dim / 2; ++i)
-    if (!std::isfinite(inv_freq_host[i])) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < rotary_dim / 2; ++i)  // NaN fails the comparison
+    if (!(std::fabs(inv_freq_host[i]) <= kMaxFrequency)) return FA_ERR_INVALID_ARG;
   if (page_size != kPageSize || (head_dim != 64 && head_dim != 128) ||
       !append_pair_built(q_dtype, kv_dtype) || rotary_dim % 16 ||
       num_kv_heads > 65535)

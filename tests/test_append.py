@@ -574,6 +574,7 @@ def test_plan_refusals(lib):
             (dict(rotary=144, freq=[1.0] * 72), invalid), (dict(rotary=16), invalid),
             (dict(rotary=16, freq=[float("nan")] * 8), invalid),
             (dict(rotary=16, freq=[float("inf")] * 8), invalid),
+            (dict(rotary=16, freq=[-1e10] * 8), invalid),
             (dict(rotary=8, freq=[1.0] * 4), unsupported), (dict(d=96), unsupported),
             (dict(page=32, last=(32,)), unsupported), (dict(q=0, kv=1), unsupported),
             (dict(q=0, kv=3), unsupported), (dict(q=1, kv=2), unsupported),
@@ -640,6 +641,10 @@ def test_run_refusals(lib, cuda):
             bad()
     torch.cuda.synchronize()
     assert torch.equal(b.kv.view(torch.uint8), before)
+    with pytest.raises(ValueError):
+        b.plan(lib, workspace=torch.empty(1 << 16, dtype=torch.uint8))
+    with pytest.raises(lib.FaError):
+        b.plan(lib, workspace=torch.empty(16, dtype=torch.uint8, device=cuda))
     n = Batch([0], [4], 8, 2, 128, BF16, BF16)
     pn = n.plan(lib)
     s = torch.ones((n.num_pages, 2), device=cuda)
@@ -647,3 +652,28 @@ def test_run_refusals(lib, cuda):
                 lambda: pn.run_block_scales(n.k, n.v, n.kv, s, s)):
         with pytest.raises(lib.FaError):
             bad()
+
+
+@pytest.mark.gpu
+def test_another_current_device_is_refused(lib, cuda, monkeypatch):
+    """Index tensors and workspaces of a device that is not the current one."""
+    b = Batch([0], [4], 8, 2, 128, BF16, BF16)
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device=cuda)
+    other = torch.cuda.current_device() + 1
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: other)
+    for kw in ({}, {"workspace": ws}):
+        with pytest.raises(ValueError):
+            b.plan(lib, **kw)
+
+
+@pytest.mark.gpu
+def test_continued_page_without_a_scale(lib, cuda):
+    """A page that is continued although nothing wrote its scale (NaN) takes the
+    scale its new tokens need."""
+    b = Batch([5], [3], 2, 2, 64, BF16, E4M3, seed=4)
+    ks, vs = (torch.full((b.num_pages, 2), float("nan"), device=cuda) for _ in range(2))
+    b.plan(lib).run_block_scales(b.k, b.v, b.kv, ks, vs)
+    page = int(b.ids[0])
+    want = block_scale(np.abs(f64(b.k)).max((0, 2)))
+    assert np.array_equal(f64(ks[page]), want)
+    assert torch.isnan(ks[[i for i in range(b.num_pages) if i != page]]).all()

@@ -272,6 +272,26 @@ def test_graph_capture_and_other_stream(lib, cuda):
     assert torch.equal(o, ref[0])
 
 
+@pytest.mark.parametrize("env", [("FADECODE_POOL", "0.25"), ("FADECODE_PLAN", "stream"),
+                                 ("FADECODE_KERNEL", "simt")], ids=lambda e: e[0])
+@pytest.mark.parametrize("group,head_dim", [(1, 128), (8, 128), (2, 64), (4, 64), (8, 64)])
+def test_other_plans(lib, cuda, monkeypatch, group, head_dim, env):
+    """Segments claimed at run time, the stream plan, and a plan whose plain
+    kernel is the CUDA-core one."""
+    monkeypatch.setenv(*env)
+    lengths = [60000, 3, 0, 16, 17, 30000] + list(range(0, 400, 7))
+    b = make(lengths, None, 3 * group, 3, head_dim, torch.bfloat16, 17, cuda, spread=4.0)
+    p = plan(lib, b)
+    if env[0] == "FADECODE_POOL":
+        assert p.info["num_pool_segments"] > 0
+    o, lse = run(p, b)
+    assert p.check() == 0
+    check(b, o, lse, reference(b))
+    for _ in range(3):
+        o2, lse2 = run(p, b)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_many_short_requests(lib, cuda):
     """Thousands of segments of 0 to 3 pages, fresh plans, on the first launch
     right after another kernel's."""
