@@ -269,8 +269,8 @@ int fa_decode_run_head_scales(fa_decode_plan_t plan, const void* q, const void* 
  *                      the softmax weights once more.  The scales of one
  *                      kv head's blocks may differ by up to 2^64.
  * Other arguments as fa_decode_run (sm_scale <= 0 selects 1/sqrt(head_dim)).
- * Every plan kind takes it (plain, multi-token, ragged query rows) on the
- * shapes and dtypes built for it; plans whose kv dtype is not E4M3 return
+ * Every plan kind takes it (plain, multi-token, ragged query rows; for a
+ * cascade, fa_cascade_run_block_scales) on the shapes and dtypes built for it; plans whose kv dtype is not E4M3 return
  * FA_ERR_UNSUPPORTED, NULL scales and a current device that is not the
  * plan's FA_ERR_INVALID_ARG. */
 int fa_decode_run_block_scales(fa_decode_plan_t plan, const void* q, const void* paged_kv,
@@ -732,6 +732,16 @@ int fa_cascade_run(fa_cascade_plan_t plan, const void* q, const void* paged_kv,
 int fa_cascade_run_scaled(fa_cascade_plan_t plan, const void* q, const void* paged_kv,
                           int64_t num_pages, float sm_scale, float k_scale,
                           float v_scale, void* o, float* lse, void* cuda_stream);
+
+/* fa_cascade_run over an E4M3 cache with one scale per page and kv head
+ * (k_block_scales, v_block_scales [num_pages, num_kv_heads] float32, device, as
+ * fa_decode_run_block_scales): the shared pages' scales in the prefix pass,
+ * each request's own pages' in the other.  FA_ERR_UNSUPPORTED for other
+ * caches; FA_ERR_INVALID_ARG as there. */
+int fa_cascade_run_block_scales(fa_cascade_plan_t plan, const void* q, const void* paged_kv,
+                                int64_t num_pages, float sm_scale, const float* k_block_scales,
+                                const float* v_block_scales, void* o, float* lse,
+                                void* cuda_stream);
 
 int fa_cascade_plan_destroy(fa_cascade_plan_t plan);
 

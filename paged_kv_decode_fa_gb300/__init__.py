@@ -48,7 +48,7 @@ EXPORTED_SYMBOLS = (
     "fa_decode_run_block_scales",
     "fa_append_workspace_size", "fa_append_plan", "fa_append_run", "fa_append_run_head_scales",
     "fa_append_run_token_scales", "fa_append_run_block_scales", "fa_append_check",
-    "fa_append_plan_destroy",
+    "fa_append_plan_destroy", "fa_cascade_run_block_scales",
 )
 
 FA_OK = 0
@@ -128,6 +128,8 @@ def _load() -> ctypes.CDLL:
     lib.fa_decode_run_head_scales.restype = i32
     lib.fa_decode_run_block_scales.argtypes = [P, P, P, i64, f32, P, P, P, P, P]
     lib.fa_decode_run_block_scales.restype = i32
+    lib.fa_cascade_run_block_scales.argtypes = [P, P, P, i64, f32, P, P, P, P, P]
+    lib.fa_cascade_run_block_scales.restype = i32
     lib.fa_append_workspace_size.argtypes = [i32, i64]
     lib.fa_append_workspace_size.restype = sz
     lib.fa_append_plan.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, i32, i32,
@@ -705,6 +707,38 @@ class CascadePlan:
             lse: torch.Tensor | None = None, return_lse: bool = True, stream=None):
         """Cascade decode; k_scale / v_scale are an E4M3 cache's per-tensor
         scales (1 for a 16-bit cache)."""
+        out, lse = self._outputs(q, paged_kv, out, lse, return_lse)
+        _check(_L().fa_cascade_run_scaled(
+            self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
+            0.0 if sm_scale is None else float(sm_scale), float(k_scale), float(v_scale),
+            out.data_ptr(), lse.data_ptr() if lse is not None else None,
+            _stream_handle(stream)), "fa_cascade_run_scaled")
+        return out, lse
+
+    def run_block_scales(self, q: torch.Tensor, paged_kv: torch.Tensor, k_scales: torch.Tensor,
+                         v_scales: torch.Tensor, *, sm_scale: float | None = None,
+                         out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                         return_lse: bool = True, stream=None):
+        """Cascade decode over an E4M3 cache with one scale per page and kv head:
+        k_scales / v_scales [num_pages, num_kv_heads] float32."""
+        for t in (q, out, lse):
+            if t is not None and (t.device != paged_kv.device or not t.is_contiguous()):
+                raise ValueError("q / out / lse must be contiguous, on the device of paged_kv")
+        want = (2, 16, self.num_kv_heads, self.head_dim)
+        if paged_kv.shape[1:] != want or paged_kv.get_device() != self._keep[-1].get_device():
+            raise ValueError(f"paged_kv must be [num_pages, {', '.join(map(str, want))}] on the "
+                             "plan's device")
+        out, lse = self._outputs(q, paged_kv, out, lse, return_lse)
+        _check_scales((k_scales, v_scales), (paged_kv.shape[0], self.num_kv_heads), paged_kv)
+        _check(_L().fa_cascade_run_block_scales(
+            self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
+            0.0 if sm_scale is None else float(sm_scale), k_scales.data_ptr(),
+            v_scales.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+            _stream_handle(stream)), "fa_cascade_run_block_scales")
+        return out, lse
+
+    def _outputs(self, q, paged_kv, out, lse, return_lse):
+        """Check q / paged_kv against the plan; allocate missing outputs."""
         B, Hq, D = self.batch, self.num_qo_heads, self.head_dim
         if q.dtype != self.q_dtype or paged_kv.dtype != self.kv_dtype:
             raise TypeError("q / paged_kv dtype differs from the plan")
@@ -714,11 +748,6 @@ class CascadePlan:
             out = torch.empty_like(q)
         if return_lse and lse is None:
             lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-        _check(_L().fa_cascade_run_scaled(
-            self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
-            0.0 if sm_scale is None else float(sm_scale), float(k_scale), float(v_scale),
-            out.data_ptr(), lse.data_ptr() if lse is not None else None,
-            _stream_handle(stream)), "fa_cascade_run_scaled")
         return out, lse
 
     def set_timing_events(self, before, after) -> None:

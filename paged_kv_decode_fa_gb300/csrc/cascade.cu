@@ -66,7 +66,7 @@ struct CombineParams {
 
 constexpr int kPrefixRows = 128;  // rows per CTA: 8 consumer warps x 16
 
-template <typename KVT, int D, int NW>
+template <typename KVT, int D, int NW, int SC = kScaleNone>
 struct PrefixCfg {
   static constexpr int P = kPageSize;
   static constexpr int KV_ES = sizeof(KVT);
@@ -81,7 +81,9 @@ struct PrefixCfg {
   static constexpr int THREADS = (NW + 1) * 32;
   static constexpr int OFF_FULL = S * STAGE_BYTES;
   static constexpr int OFF_EMPTY = OFF_FULL + 8 * S;
-  static constexpr int SMEM = OFF_EMPTY + 8 * S;
+  static constexpr int OFF_SCALES = OFF_EMPTY + 8 * S;  // ring of per-block scales
+  static constexpr int SMEM = OFF_SCALES + scale_bytes(SC, S);
+  static_assert(SC == kScaleNone || (SC == kScalePerBlock && kFp8), "block scales: E4M3 KV");
   static_assert(NW * 16 == kPrefixRows, "16 rows per consumer warp");
   static_assert((D * KV_ES) % 128 == 0, "rows must be whole 128-byte swizzle rows");
   static_assert(!kFp8 || D == 128, "E4M3 prefix rows are laid out for head_dim 128");
@@ -91,12 +93,15 @@ struct PrefixCfg {
 // type and q is its A fragment as stored.  E4M3 KV: the MMAs run in f16 -
 // K and V are widened in registers (exact), q is scaled by a power of two
 // per warp into f16 range (the scores are scaled back), k_scale is folded
-// into q_scale and v_scale into the partial outputs.
-template <typename QT, typename KVT, int D, int NW>
-__global__ void __launch_bounds__(PrefixCfg<KVT, D, NW>::THREADS)
+// into q_scale and v_scale into the partial outputs.  With per-block scales (SC)
+// a page's K scale joins its scores' and its V scale its weights, relative to
+// a reference that o is kept in units of, as in the decode kernel.
+template <typename QT, typename KVT, int D, int NW, int SC>
+__global__ void __launch_bounds__(PrefixCfg<KVT, D, NW, SC>::THREADS)
     fa_prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const DecodeParams p,
                      const PrefixParams pp) {
-  using C = PrefixCfg<KVT, D, NW>;
+  using C = PrefixCfg<KVT, D, NW, SC>;
+  constexpr bool BS = SC == kScalePerBlock;
   constexpr int P = C::P, S = C::S, SEGS = C::SEGS, KSTEPS = C::KSTEPS, NT = C::NT;
   constexpr bool kFp8 = C::kFp8;
   constexpr bool kQBf16 = std::is_same<QT, __nv_bfloat16>::value;
@@ -120,8 +125,9 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW>::THREADS)
   }
   __syncthreads();
   if (warp == NW) {
-    produce_pages<S, C::STAGE_BYTES, SEGS, C::BOX_X, C::BOX_BYTES>(&kv_map, p, item, item + 1,
-                                                                   ring, full, empty, lane);
+    produce_pages<S, C::STAGE_BYTES, SEGS, C::BOX_X, C::BOX_BYTES, SC>(
+        &kv_map, p, item, item + 1, ring, full, empty, lane,
+        reinterpret_cast<float*>(smem + C::OFF_SCALES));
     return;
   }
 
@@ -205,6 +211,7 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW>::THREADS)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
   float m_r[2] = {-INFINITY, -INFINITY}, d_r[2] = {0.f, 0.f};  // rows g, g+8
+  float vref = 0.f, vref_inv = 0.f;  // per-block scales: the V scale o is in units of
   bool aborted = false;
   const uint32_t ring_addr = dev::smem_addr(ring);
 
@@ -212,6 +219,24 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW>::THREADS)
     const int stage = k % S;
     dev::mbar_wait(dev::smem_addr(&full[stage]), (uint32_t)((k / S) & 1), aborted, p.err);
     const uint32_t st = ring_addr + stage * C::STAGE_BYTES;
+
+    float page_qscale = qscale, wf = 1.f;
+    if constexpr (BS) {
+      const float2 bs =
+          *(reinterpret_cast<const float2*>(smem + C::OFF_SCALES) + k % kBlockScaleRing);
+      page_qscale *= bs.x;
+      wf = bs.y * vref_inv;
+      if (!(wf <= 64.f && (wf >= 1.f / 64.f || bs.y == 0.f))) {
+        const float inv = 1.f / bs.y, f = vref * inv;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][e] *= f;
+        vref = bs.y;
+        vref_inv = inv;
+        wf = 1.f;
+      }
+    }
 
     // ---- S[rows][tokens]: n-tile 0 = tokens 0..7 (K row g), 1 = tokens 8..15;
     // two accumulators per n-tile (even / odd reduction steps) halve the
@@ -260,7 +285,7 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW>::THREADS)
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[n][e] *= qscale;
+      for (int e = 0; e < 4; ++e) sc[n][e] *= page_qscale;
     float mx[2] = {fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])),
                    fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]))};
 #pragma unroll
@@ -281,13 +306,14 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW>::THREADS)
     float ps[2] = {0.f, 0.f};
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const uint32_t lo = mma::pack2(dev::fast_exp2(sc[n][0] - m_r[0]),
-                                     dev::fast_exp2(sc[n][1] - m_r[0]), kBf16);
-      const uint32_t hi = mma::pack2(dev::fast_exp2(sc[n][2] - m_r[1]),
-                                     dev::fast_exp2(sc[n][3] - m_r[1]), kBf16);
-      pa[2 * n] = lo;
-      pa[2 * n + 1] = hi;
-      const float2 a = mma::unpack2(lo, kBf16), b = mma::unpack2(hi, kBf16);
+      float2 a = make_float2(dev::fast_exp2(sc[n][0] - m_r[0]), dev::fast_exp2(sc[n][1] - m_r[0]));
+      float2 b = make_float2(dev::fast_exp2(sc[n][2] - m_r[1]), dev::fast_exp2(sc[n][3] - m_r[1]));
+      pa[2 * n] = mma::pack2(a.x * wf, a.y * wf, kBf16);
+      pa[2 * n + 1] = mma::pack2(b.x * wf, b.y * wf, kBf16);
+      if constexpr (!BS) {  // sums of the rounded weights, as P.V takes them
+        a = mma::unpack2(pa[2 * n], kBf16);
+        b = mma::unpack2(pa[2 * n + 1], kBf16);
+      }
       ps[0] += a.x + a.y;
       ps[1] += b.x + b.y;
     }
@@ -356,7 +382,7 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW>::THREADS)
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {
     if (rows[rr] >= row_count) continue;
-    const float inv = d_r[rr] > 0.f ? pp.v_scale / d_r[rr] : 0.f;
+    const float inv = d_r[rr] > 0.f ? (BS ? vref : pp.v_scale) / d_r[rr] : 0.f;
     float* dst = pp.part_o + ((size_t)out_item * kPrefixRows + rows[rr]) * D;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -467,8 +493,9 @@ size_t calign(size_t x) { return (x + kCAlign - 1) / kCAlign * kCAlign; }
 
 struct CascadeKernels {
   const void* prefix = nullptr;
+  const void* prefix_block = nullptr;  // with per-block scales (E4M3 KV), else null
   const void* combine = nullptr;
-  int threads = 0, smem = 0;
+  int threads = 0, smem = 0, smem_block = 0;
   bool tcgen05 = false;  // prefix on the tcgen05 tensor cores (K and V boxes apart)
 };
 
@@ -496,7 +523,13 @@ CascadeKernels cascade_kernels() {
     }
   }
   using C = fadecode::PrefixCfg<KVT, D, 8>;
-  k.prefix = reinterpret_cast<const void*>(&fadecode::fa_prefix_kernel<QT, KVT, D, 8>);
+  k.prefix = reinterpret_cast<const void*>(
+      &fadecode::fa_prefix_kernel<QT, KVT, D, 8, fadecode::kScaleNone>);
+  if constexpr (C::kFp8) {
+    k.prefix_block = reinterpret_cast<const void*>(
+        &fadecode::fa_prefix_kernel<QT, KVT, D, 8, fadecode::kScalePerBlock>);
+    k.smem_block = fadecode::PrefixCfg<KVT, D, 8, fadecode::kScalePerBlock>::SMEM + 1024;
+  }
   k.threads = C::THREADS;
   k.smem = C::SMEM + 1024;
   return k;
@@ -615,7 +648,7 @@ bool cascade_overlap() {
 
 // Shared-memory attribute and occupancy of a prefix kernel, set and queried
 // once per kernel and device.
-int prefix_occupancy(const CascadeKernels& k, int dev) {
+int prefix_occupancy(const void* func, int threads, int smem, int dev) {
   struct Entry {
     const void* func;
     int device, occ;
@@ -624,14 +657,13 @@ int prefix_occupancy(const CascadeKernels& k, int dev) {
   static std::vector<Entry> cache;
   std::lock_guard<std::mutex> lock(mu);
   for (const Entry& e : cache)
-    if (e.func == k.prefix && e.device == dev) return e.occ;
+    if (e.func == func && e.device == dev) return e.occ;
   int occ = 0;
-  if (cudaFuncSetAttribute(k.prefix, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) !=
+  if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
           cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k.prefix, k.threads, k.smem) !=
-          cudaSuccess)
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, func, threads, smem) != cudaSuccess)
     return 0;
-  cache.push_back(Entry{k.prefix, dev, occ});
+  cache.push_back(Entry{func, dev, occ});
   return occ;
 }
 
@@ -717,8 +749,10 @@ int fa_cascade_plan(const int32_t* prefix_indices_dev, int num_prefix_pages,
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FA_ERR_CUDA;
-  const int occ = prefix_occupancy(k, dev);
-  if (occ < 1) return FA_ERR_CUDA;
+  const int occ = prefix_occupancy(k.prefix, k.threads, k.smem, dev);
+  if (occ < 1 ||
+      (k.prefix_block && prefix_occupancy(k.prefix_block, k.threads, k.smem_block, dev) < 1))
+    return FA_ERR_CUDA;
 
   fa_cascade_plan_s* plan = new (std::nothrow) fa_cascade_plan_s();
   if (!plan) return FA_ERR_INVALID_ARG;
@@ -824,14 +858,45 @@ int fa_cascade_run(fa_cascade_plan_t plan, const void* q, const void* paged_kv,
                                cuda_stream);
 }
 
+static int cascade_run(fa_cascade_plan_t plan, const void* q, const void* paged_kv,
+                       int64_t num_pages, float sm_scale, float k_scale, float v_scale,
+                       const float* k_block_scales, const float* v_block_scales, void* o,
+                       float* lse, void* cuda_stream);
+
 int fa_cascade_run_scaled(fa_cascade_plan_t plan, const void* q, const void* paged_kv,
                           int64_t num_pages, float sm_scale, float k_scale, float v_scale,
                           void* o, float* lse, void* cuda_stream) {
-  if (!plan || !q || !paged_kv || !o || num_pages <= 0) return FA_ERR_INVALID_ARG;
+  if (!plan) return FA_ERR_INVALID_ARG;
   // per-tensor scales belong to an E4M3 cache; a 16-bit one is used as stored
   if (plan->kv_dtype != FA_DTYPE_E4M3 && (k_scale != 1.f || v_scale != 1.f))
     return FA_ERR_INVALID_ARG;
   if (!(k_scale > 0.f) || !(v_scale > 0.f)) return FA_ERR_INVALID_ARG;
+  return cascade_run(plan, q, paged_kv, num_pages, sm_scale, k_scale, v_scale, nullptr, nullptr,
+                     o, lse, cuda_stream);
+}
+
+int fa_cascade_run_block_scales(fa_cascade_plan_t plan, const void* q, const void* paged_kv,
+                                int64_t num_pages, float sm_scale, const float* k_block_scales,
+                                const float* v_block_scales, void* o, float* lse,
+                                void* cuda_stream) {
+  if (!plan) return FA_ERR_INVALID_ARG;
+  if (!plan->k.prefix_block) return FA_ERR_UNSUPPORTED;
+  if (!k_block_scales || !v_block_scales || reinterpret_cast<uintptr_t>(k_block_scales) % 4 ||
+      reinterpret_cast<uintptr_t>(v_block_scales) % 4)
+    return FA_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  if (dev != plan->device) return FA_ERR_INVALID_ARG;
+  return cascade_run(plan, q, paged_kv, num_pages, sm_scale, 1.f, 1.f, k_block_scales,
+                     v_block_scales, o, lse, cuda_stream);
+}
+
+// The three launches of a run; block scales, or null for the per-tensor ones.
+static int cascade_run(fa_cascade_plan_t plan, const void* q, const void* paged_kv,
+                       int64_t num_pages, float sm_scale, float k_scale, float v_scale,
+                       const float* k_block_scales, const float* v_block_scales, void* o,
+                       float* lse, void* cuda_stream) {
+  if (!q || !paged_kv || !o || num_pages <= 0) return FA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(paged_kv) % 16 || reinterpret_cast<uintptr_t>(q) % 16)
     return FA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
@@ -848,8 +913,11 @@ int fa_cascade_run_scaled(fa_cascade_plan_t plan, const void* q, const void* pag
                cudaStreamWaitEvent(plan->side, plan->ev_fork, 0) != cudaSuccess))
     return FA_ERR_CUDA;
   // 1. each request's own pages
-  int rc = fa_decode_run(plan->suffix, q, paged_kv, num_pages, sm_scale, k_scale, v_scale, so,
-                         slse, cuda_stream);
+  int rc = k_block_scales
+               ? fa_decode_run_block_scales(plan->suffix, q, paged_kv, num_pages, sm_scale,
+                                            k_block_scales, v_block_scales, so, slse, cuda_stream)
+               : fa_decode_run(plan->suffix, q, paged_kv, num_pages, sm_scale, k_scale, v_scale,
+                               so, slse, cuda_stream);
   if (rc != FA_OK) return rc;
   // 2. the shared prefix, once per kv head and row block
   if (paged_kv != plan->map_base || num_pages != plan->map_pages) {
@@ -866,6 +934,8 @@ int fa_cascade_run_scaled(fa_cascade_plan_t plan, const void* q, const void* pag
   prm.cta_offsets = reinterpret_cast<const int32_t*>(ws + plan->L.off_cta);
   prm.segments = reinterpret_cast<const int32_t*>(ws + plan->L.off_items);
   prm.err = reinterpret_cast<int*>(ws + plan->L.off_err);
+  prm.k_scales = k_block_scales;
+  prm.v_scales = v_block_scales;
   prm.num_pages = num_pages;
   prm.num_qo_heads = plan->hq;
   prm.num_kv_heads = plan->hkv;
@@ -884,8 +954,10 @@ int fa_cascade_run_scaled(fa_cascade_plan_t plan, const void* q, const void* pag
   pp.prefix_pages = plan->prefix_pages;
   void* args[3] = {&plan->map, &prm, &pp};
   if (timed && cudaEventRecord(plan->ev_before, st) != cudaSuccess) return FA_ERR_CUDA;
-  if (cudaLaunchKernel(plan->k.prefix, dim3(plan->grid), dim3(plan->k.threads), args,
-                       (size_t)plan->k.smem, pst) != cudaSuccess)
+  if (cudaLaunchKernel(k_block_scales ? plan->k.prefix_block : plan->k.prefix, dim3(plan->grid),
+                       dim3(plan->k.threads), args,
+                       (size_t)(k_block_scales ? plan->k.smem_block : plan->k.smem), pst) !=
+      cudaSuccess)
     return FA_ERR_CUDA;
   if (timed && cudaEventRecord(plan->ev_after, st) != cudaSuccess) return FA_ERR_CUDA;
   if (fork && (cudaEventRecord(plan->ev_join, plan->side) != cudaSuccess ||

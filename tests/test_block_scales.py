@@ -292,6 +292,38 @@ def test_other_plans(lib, cuda, monkeypatch, group, head_dim, env):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("q_dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("batch,group,prefix_pages,spread", [(3, 4, 40, 3.0), (40, 8, 33, 0.0),
+                                                             (5, 1, 1, 3.0), (70, 2, 300, 8.0)])
+def test_cascade(lib, cuda, batch, group, prefix_pages, spread, q_dtype):
+    """A shared prefix and own pages of every length in one block-scaled cache,
+    against the oracle over the full page lists."""
+    b = W.make_cascade_batch(prefix_pages=prefix_pages,
+                             suffix_lengths=[(7 * i) % 61 for i in range(batch)],
+                             num_qo_heads=3 * group, num_kv_heads=3, head_dim=128, dtype=q_dtype,
+                             kv_dtype=E4M3, seed=batch, device=cuda)
+    rng = np.random.default_rng(batch)
+    s = 2.0 ** (-6 + np.rint(rng.uniform(-1, 1, (2, b.num_pages, 3))
+                             * np.array([min(spread, 1.5), spread])[:, None, None]))
+    s[1][rng.random(s[1].shape) < 0.05] = 0
+    b.extra["ks"], b.extra["vs"] = (torch.from_numpy(x.astype(np.float32)).to(cuda) for x in s)
+    p = lib.cascade_plan(*W.cascade_parts(b), 3 * group, 3, 128, 16, q_data_type=q_dtype,
+                         kv_data_type=E4M3)
+    ref = reference(b)
+    for _ in range(2):
+        o, lse = run(p, b)
+        assert p.check() == 0
+        # the suffix' own output passes through q's type once more
+        ro, rl, a, tail = ref
+        check(b, o, lse, (ro, rl, a + HALF[q_dtype] / (3 * 2.0 ** -11) * a, tail))
+    plain, _ = p.run(b.q, b.paged_kv, k_scale=0.02, v_scale=0.02)   # the other pass still runs
+    assert torch.isfinite(plain).all()
+    with pytest.raises(ValueError):
+        p.run_block_scales(b.q, b.paged_kv, b.extra["ks"][:-1], b.extra["vs"])
+    with pytest.raises(ValueError):
+        p.run_block_scales(b.q, b.paged_kv[:, :, :8].contiguous(), b.extra["ks"], b.extra["vs"])
+
+
 def test_many_short_requests(lib, cuda):
     """Thousands of segments of 0 to 3 pages, fresh plans, on the first launch
     right after another kernel's."""
@@ -319,5 +351,8 @@ def test_refusals(lib, cuda):
     n = W.make_batch(batch_lengths=[40], num_qo_heads=8, num_kv_heads=2, head_dim=128,
                      q_dtype=torch.bfloat16, kv_dtype=torch.bfloat16, seed=1, device=cuda)
     pn = lib.plan(n.indptr, n.indices, n.last_page_len, 8, 2, 128, 16)
+    pc = lib.cascade_plan(n.indices[:1], [0, 1], n.indices[1:2], [16], 8, 2, 128, 16)
+    with pytest.raises(lib.FaError):
+        pc.run_block_scales(n.q, n.paged_kv, *(torch.ones((n.num_pages, 2), device=cuda),) * 2)
     with pytest.raises(lib.FaError):
         pn.run_block_scales(n.q, n.paged_kv, *(torch.ones((n.num_pages, 2), device=cuda),) * 2)
