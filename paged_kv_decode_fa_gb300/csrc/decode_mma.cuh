@@ -82,6 +82,14 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t& r0, uint3
                : "r"(addr));
 }
 
+// Transpose an 8x8 matrix of 16-bit elements across the warp: lane 4i + j
+// holds elements 2j, 2j+1 of row i, before and after.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -659,6 +667,7 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
       // inside).  Otherwise it starts empty and takes the column's first
       // observed maximum.  A column leaving its window is re-centred on its
       // true maximum (an exact rescale of its state).
+      uint32_t pb[NPP][2];
       float alpha[2] = {1.f, 1.f};
       bool rescale;
       {
@@ -726,12 +735,18 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
           d_h[0] += a.x + b.x;
           d_h[1] += a.y + b.y;
         }
-        // P^T B fragments: transpose [token][head] -> [head][token] through smem
-        uint16_t* pu = pT + u * 8 * P;
-        pu[(2 * t) * P + g] = (uint16_t)(pv01 & 0xffffu);
-        pu[(2 * t + 1) * P + g] = (uint16_t)(pv01 >> 16);
-        pu[(2 * t) * P + g + 8] = (uint16_t)(pv23 & 0xffffu);
-        pu[(2 * t + 1) * P + g + 8] = (uint16_t)(pv23 >> 16);
+        // P^T B fragments: transpose [token][head] -> [head][token], through
+        // smem, or in registers (per-block scales)
+        if constexpr (BS) {
+          pb[u][0] = mma::transpose8x8(pv01);
+          pb[u][1] = mma::transpose8x8(pv23);
+        } else {
+          uint16_t* pu = pT + u * 8 * P;
+          pu[(2 * t) * P + g] = (uint16_t)(pv01 & 0xffffu);
+          pu[(2 * t + 1) * P + g] = (uint16_t)(pv01 >> 16);
+          pu[(2 * t) * P + g + 8] = (uint16_t)(pv23 & 0xffffu);
+          pu[(2 * t + 1) * P + g + 8] = (uint16_t)(pv23 >> 16);
+        }
       }
       // once the running maxima settle, most steps leave them unchanged
       if (rescale && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
@@ -743,18 +758,31 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
           o[mt][3] *= alpha[1];
         }
       }
-      __syncwarp();
+      if constexpr (!BS) {
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < NPP; ++u) {
+          const uint16_t* pu = pT + u * 8 * P;
+          pb[u][0] = *reinterpret_cast<const uint32_t*>(pu + g * P + 2 * t);
+          pb[u][1] = *reinterpret_cast<const uint32_t*>(pu + g * P + 2 * t + 8);
+        }
+      }
 #pragma unroll
       for (int u = 0; u < NPP; ++u) {
-        const uint16_t* pu = pT + u * 8 * P;
-        const uint32_t pb0 = *reinterpret_cast<const uint32_t*>(pu + g * P + 2 * t);
-        const uint32_t pb1 = *reinterpret_cast<const uint32_t*>(pu + g * P + 2 * t + 8);
         const uint32_t* vf = kEarlyV ? &vfrag[kEarlyV ? u : 0][0][0] : nullptr;
         if (valid[u] < P)
-          pv_step(std::true_type{}, st[u], pb0, pb1, valid[u], vf);
+          pv_step(std::true_type{}, st[u], pb[u][0], pb[u][1], valid[u], vf);
         else
-          pv_step(std::false_type{}, st[u], pb0, pb1, valid[u], vf);
-        if constexpr (!kEarlyV) dev::release_stage(dev::smem_addr(&empty[stage[u]]), lane);
+          pv_step(std::false_type{}, st[u], pb[u][0], pb[u][1], valid[u], vf);
+        if constexpr (!kEarlyV && !BS) dev::release_stage(dev::smem_addr(&empty[stage[u]]), lane);
+      }
+      if constexpr (!kEarlyV && BS) {  // the step's stages behind one fence
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int u = 0; u < NPP; ++u) dev::mbar_arrive(dev::smem_addr(&empty[stage[u]]));
+        }
       }
       return true;
     };
