@@ -92,8 +92,10 @@ def read_bf16_peak():
 
 
 # Sources that are not part of the decode kernels or their launch: the
-# cascade's own kernels, the no-allocation entry point, fa_merge_states.
-NOT_DECODE_SOURCES = ("cascade.cu", "cascade_tc.cuh", "static_scratch.cu", "merge.cu")
+# cascade's own kernels, the no-allocation entry point, fa_merge_states, the
+# append.
+NOT_DECODE_SOURCES = ("cascade.cu", "cascade_tc.cuh", "static_scratch.cu", "merge.cu",
+                      "append.cu")
 
 
 def kernel_source_hash(workload: str = "gqa_uniform") -> str:

@@ -629,8 +629,8 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
  *             id outside [0, num_pages) is skipped (its rows of q_out are
  *             written) and sets bit 0 of the device-check word
  *             (fa_append_check).
- *  k_scale,   per-tensor scales of an E4M3 cache, positive and finite; 1 for
- *  v_scale    other kv types (FA_ERR_INVALID_ARG otherwise).
+ *  k_scale,   per-tensor scales of an E4M3 cache, positive normal numbers; 1
+ *  v_scale    for other kv types (FA_ERR_INVALID_ARG otherwise).
  * One kernel on cuda_stream, no allocation, no synchronisation: it can be
  * captured into a CUDA graph.  Results are bitwise reproducible.  Running a
  * plan again writes the same slots again.
@@ -641,8 +641,9 @@ int fa_append_run(fa_append_plan_t plan, const fa_rows* k, const fa_rows* v, con
                   void* cuda_stream);
 
 /* run into an E4M3 cache with one scale per kv head, given:
- * k_head_scales, v_head_scales [num_kv_heads] float32, device, positive (as
- * fa_decode_run_head_scales reads them). */
+ * k_head_scales, v_head_scales [num_kv_heads] float32, device, positive normal
+ * numbers (as fa_decode_run_head_scales reads them; codes under another scale
+ * are 0). */
 int fa_append_run_head_scales(fa_append_plan_t plan, const fa_rows* k, const fa_rows* v,
                               const fa_rows* q, void* q_out, void* paged_kv, int64_t num_pages,
                               const float* k_head_scales, const float* v_head_scales,

@@ -257,7 +257,12 @@ __device__ __forceinline__ float block_scale(float amax) {
   return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
-__device__ __forceinline__ float inverse(float scale) { return scale > 0.f ? 1.f / scale : 0.f; }
+// 1 / scale, 0 for a scale of 0 (or below the normal numbers, whose inverse
+// may overflow).
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
+__device__ __forceinline__ float inverse(float scale) {
+  return scale >= kMinScale ? 1.f / scale : 0.f;
+}
 
 template <int D>
 struct Cfg {
@@ -392,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
         inv = inverse(!hs ? (is_k ? p.k_scale : p.v_scale) : ok ? __ldg(hs + h0 + h) : 1.f);
       } else if constexpr (MODE == kToken) {
         const float rm = row_max<LPR>(m);
-        scale = rm > 0.f ? fmaxf(rm / 448.f, 1.17549435e-38f) : 0.f;
+        scale = rm > 0.f ? fmaxf(rm / 448.f, kMinScale) : 0.f;
         inv = inverse(scale);
       } else {
         inv = ok ? inverse(item_scale[is_k ? h : heads + h]) : 0.f;
@@ -726,7 +731,7 @@ int fa_append_run(fa_append_plan_t plan, const fa_rows* k, const fa_rows* v, con
   const bool e4m3 = plan->kv_dtype == FA_DTYPE_E4M3;
   // per-tensor scales belong to an E4M3 cache; another one is written as it is
   if (!e4m3 && (k_scale != 1.f || v_scale != 1.f)) return FA_ERR_INVALID_ARG;
-  if (!(k_scale > 0.f && k_scale < INFINITY && v_scale > 0.f && v_scale < INFINITY))
+  if (!(k_scale >= kMinScale && k_scale < INFINITY && v_scale >= kMinScale && v_scale < INFINITY))
     return FA_ERR_INVALID_ARG;
   return append_run(plan, e4m3 ? kStatic : kNative, k, v, q, q_out, paged_kv, num_pages, k_scale,
                     v_scale, nullptr, nullptr, nullptr, nullptr, cuda_stream);

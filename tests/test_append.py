@@ -628,6 +628,7 @@ def test_run_refusals(lib, cuda):
                 lambda: p.run(b.k.transpose(1, 2).contiguous().transpose(1, 2), b.v, b.kv),
                 lambda: p.run(b.k, b.v, b.kv, k_scale=0.0),
                 lambda: p.run(b.k, b.v, b.kv, v_scale=-1.0),
+                lambda: p.run(b.k, b.v, b.kv, k_scale=1e-40),
                 lambda: p.run(b.k, b.v, b.kv, v_scale=float("inf")),
                 lambda: p.run(b.k, b.v, b.kv, k_scale=float("nan")),
                 lambda: p.run(b.k, b.v, b.kv, q=b.q, q_out=b.q),
@@ -677,3 +678,44 @@ def test_continued_page_without_a_scale(lib, cuda):
     want = block_scale(np.abs(f64(b.k)).max((0, 2)))
     assert np.array_equal(f64(ks[page]), want)
     assert torch.isnan(ks[[i for i in range(b.num_pages) if i != page]]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ["native", "block"])
+def test_large_cache(lib, cuda, mode):
+    """Pages whose elements lie beyond 2^31 from the cache's start, and beyond
+    2^32 bytes."""
+    hkv, d = 8, 128
+    pages = (1 << 31) // (2 * 16 * hkv * d) + 70000   # 4.5 GB of E4M3, 9 GB of bf16
+    kvt = BF16 if mode == "native" else E4M3
+    es = 2 if mode == "native" else 1
+    raw = torch.zeros(pages * 2 * 16 * hkv * d * es, dtype=torch.uint8, device=cuda)
+    kv = raw.view(kvt).view(pages, 2, 16, hkv, d)
+    ids = torch.tensor([pages - 1, 3, pages - 65000], dtype=torch.int32, device=cuda)
+    k = torch.randn((40, hkv, d), device=cuda).to(BF16)
+    v = torch.randn((40, hkv, d), device=cuda).to(BF16)
+    p = lib.plan_append([0, 3], ids, [8], [0, 40], 8, hkv, d, 16, q_data_type=BF16,
+                        kv_data_type=kvt)
+    if mode == "native":
+        p.run(k, v, kv)
+        got = kv[ids.long()].transpose(1, 2).reshape(48, 2, hkv, d)[:40]
+        assert torch.equal(got[:, 0], k) and torch.equal(got[:, 1], v)
+    else:
+        ks, vs = (torch.zeros((pages, hkv), device=cuda) for _ in range(2))
+        p.run_block_scales(k, v, kv, ks, vs)
+        s = torch.stack([ks, vs], 1)[ids.long()][:, :, None, :, None]
+        got = (kv[ids.long()].float() * s).transpose(1, 2).reshape(48, 2, hkv, d)[:40]
+        step = s.amax((0, 1, 2)) * 2.0 ** -10
+        for x, y in ((got[:, 0], k.float()), (got[:, 1], v.float())):
+            assert ((x - y).abs() <= torch.maximum(2.0 ** -4 * y.abs(), step)).all()
+        dp = lib.plan([0, 3], ids, [8], 8, hkv, d, 16, q_data_type=BF16, kv_data_type=kvt)
+        q = torch.randn((1, 8, d), device=cuda).to(BF16)
+        o, _ = dp.run_block_scales(q, kv, ks, vs)
+        w = torch.softmax(torch.einsum("hd,thd->ht", q[0].double(), got[:, 0].double()) / d ** 0.5, -1)
+        ref = torch.einsum("ht,thd->hd", w, got[:, 1].double())
+        # bf16's half step, and 3 * 2^-11 + 2e-4 of the weights' values (see the
+        # block-scale tests)
+        mag = torch.einsum("ht,thd->hd", w, got[:, 1].double().abs())
+        assert ((o[0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2e-3 * mag).all()
+    assert p.check() == 0
+    assert not raw[: 3 * 2 * 16 * hkv * d * es].any()
