@@ -80,12 +80,23 @@ int dtype_size(fa_dtype t) {
   return 0;
 }
 
-// FADECODE_MERGE=kernel folds split requests in a separate merge kernel
-// after the decode kernel (for comparisons); by default the last CTA to
-// finish a piece of a split request folds it inside the decode kernel.
-bool fused_merge_enabled() {
+// Pieces x columns of a plan's heaviest split unit from which a merge kernel
+// after the decode kernel folds the plan's units, all at once; below, the
+// last CTA to finish a piece of a unit folds it inside the decode kernel.
+// The results are bitwise the same (but for a unit whose weights the fused
+// fold has no room for, more than 4096 of them at head_dim 128: an ulp).
+// Measured, fused / kernel, us a run: 4800 pieces x columns (two requests of 8K
+// and 46K tokens, 24 columns) 508 / 37, 3648 (65536 tokens, 8 columns, one kv
+// head) 55.8 / 25.3, 1824 90.4 / 67.2, 512 25.1 / 17.5, 416 130 / 127, 252 13.9 / 12.5;
+// below 320 the two are within 3 us and a plan keeps its one launch.
+// FADECODE_MERGE=kernel or =fused selects one of the two (for comparisons).
+constexpr int64_t kMaxFusedColumns = 320;
+bool fused_merge_enabled(int64_t widest_pieces, int64_t heaviest_columns) {
+  if (widest_pieces > fadecode::kMergePieces) return true;
   const char* v = std::getenv("FADECODE_MERGE");
-  return !(v && std::strcmp(v, "kernel") == 0);
+  if (v && std::strcmp(v, "kernel") == 0) return false;
+  if (v && std::strcmp(v, "fused") == 0) return true;
+  return heaviest_columns <= kMaxFusedColumns;
 }
 
 // FADECODE_POOL=<fraction> sets the share of the page stream left to the
@@ -789,7 +800,6 @@ static int plan_impl(const int32_t* indptr_host, const int32_t* indices_dev,
   plan->indices = indices_dev;
   plan->ws = static_cast<uint8_t*>(workspace_dev);
   plan->ws_bytes = workspace_bytes;
-  plan->fused_merge = fused_merge_enabled();
   plan->q_len = ragged ? ql_kernel : q_len;
   plan->ragged_q = ragged;
   plan->total_q = total_q;
@@ -831,6 +841,15 @@ static int plan_impl(const int32_t* indptr_host, const int32_t* indices_dev,
     return rc;
   }
   const WorkList& wl = plan->wl;
+  int64_t heaviest = 0, widest = 0;
+  for (size_t i = 0; i < wl.merge.size(); ++i) {
+    int columns = G * plan->q_len;  // of a partial state: its bucket's kernel's
+    for (int b = 0; b < plan->num_buckets; ++b)
+      if ((int)i >= plan->bucket[b].merge_first) columns = 8 * plan->bucket[b].tiles;
+    widest = std::max(widest, (int64_t)wl.merge[i].num_slots);
+    heaviest = std::max(heaviest, (int64_t)wl.merge[i].num_slots * columns);
+  }
+  plan->fused_merge = fused_merge_enabled(widest, heaviest);
   plan->merge_flat.resize(wl.merge.size() * FA_MERGE_INTS);
   if (!wl.merge.empty())
     std::memcpy(plan->merge_flat.data(), wl.merge.data(), wl.merge.size() * sizeof(wl.merge[0]));
@@ -1139,7 +1158,10 @@ int static_decode(void* scratch, size_t scratch_bytes, const int32_t* indptr_hos
   lv.layout = L;
   lv.num_ctas = fw.num_ctas;
   lv.num_merge = fw.num_merge;
-  lv.fused_merge = fused_merge_enabled();
+  int64_t widest = 0;
+  for (int i = 0; i < fw.num_merge; ++i)
+    widest = std::max(widest, (int64_t)g_static_merge[i].num_slots);
+  lv.fused_merge = fused_merge_enabled(widest, widest * G);
   return launch_decode(lv, q, paged_kv, num_pages, sm_scale, k_scale, v_scale, nullptr,
                        nullptr, 0.f, o, lse, cuda_stream);
 }
@@ -1289,8 +1311,9 @@ int launch_decode(const LaunchView& lv, const void* q, const void* paged_kv, int
     mp.lse = lse;
     mp.num_qo_heads = lv.hq;
     void* margs[1] = {&mp};
-    if (cudaLaunchKernel(kern.merge_func, dim3((unsigned)lv.num_merge), dim3(128), margs, 0,
-                         st) != cudaSuccess)
+    if (cudaLaunchKernel(kern.merge_func,
+                         dim3((unsigned)lv.num_merge, (unsigned)(kern.group * kern.q_len)),
+                         dim3((unsigned)D), margs, 0, st) != cudaSuccess)
       return FA_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;

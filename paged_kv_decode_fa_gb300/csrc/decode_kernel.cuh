@@ -1146,15 +1146,59 @@ __global__ void __launch_bounds__(DecodeCfg<QT, KVT, D, G, NW>::THREADS)
   if (threadIdx.x == 0) pool_finish(p);
 }
 
-// Split-level merge as a separate kernel: one CTA per (request, kv head)
-// that the planner split folds its partial states with the merge rule.
+// Split-level merge as a separate kernel: CTA (u, h) folds column h of the
+// u-th (request, kv head) the planner split, a thread per dim, with the merge
+// rule: the same sums in the same order as fold_split_unit's with its weights
+// in scratch, so that which of the two a plan uses shows in its time alone.
+// A unit of many pieces and columns is bound by the latency of its loads and
+// of its weights' sums when one CTA folds it (two requests of 8K and 46K
+// tokens, 32 columns, two kv heads: 508 us a run); here all columns go at
+// once, thirty-two pieces in flight per thread.
 template <typename QT, int D, int G, int QL = 1, bool RQ = false>
-__global__ void __launch_bounds__(128) fa_merge_partials_kernel(const MergeParams p) {
-  __shared__ float weights[2048];
+__global__ void __launch_bounds__(D) fa_merge_partials_kernel(const MergeParams p) {
+  constexpr int NC = G * QL, WARPS = D / 32;
+  __shared__ float weights[kMergePieces];
+  __shared__ float warp_max[WARPS];
   const int4 u = reinterpret_cast<const int4*>(p.merge)[blockIdx.x];
-  fold_split_unit<QT, D, G * QL, G, QL, RQ>(p.part_o, p.part_lse, u, static_cast<QT*>(p.o),
-                                            p.lse, p.num_qo_heads, p.qo_indptr, weights, 2048,
-                                            threadIdx.x, blockDim.x, 0);
+  const int s0 = u.z, ns = u.w, h = blockIdx.y, tid = threadIdx.x;
+  const QRows qr = query_rows<G, QL, RQ>(p.qo_indptr, u.x);
+  if (h >= qr.ncols) return;
+  float M = -INFINITY;
+  for (int k = tid; k < ns; k += D) {
+    weights[k] = __ldcg(p.part_lse + (size_t)(s0 + k) * NC + h);
+    M = fmaxf(M, weights[k]);
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (tid % 32 == 0) warp_max[tid / 32] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, warp_max[w]);
+  for (int k = tid; k < ns; k += D)
+    weights[k] = M != -INFINITY ? dev::fast_exp2(weights[k] - M) : 0.f;
+  __syncthreads();
+  float den = 0.f;  // every thread its own, in the pieces' order
+#pragma unroll 16
+  for (int k = 0; k < ns; ++k) den += weights[k];
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const size_t row = out_row<G>(qr.q0, u.y, h, p.num_qo_heads);
+  if (p.lse && tid == 0)
+    p.lse[row] = M != -INFINITY ? (M + dev::fast_log2(den)) * dev::kLn2 : -INFINITY;
+  const float* po = p.part_o + ((size_t)s0 * NC + h) * D + tid;
+  float num = 0.f;
+  constexpr int kAhead = 32;
+  for (int k0 = 0; k0 < ns; k0 += kAhead) {
+    float v[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      v[j] = k0 + j < ns ? __ldcg(po + (size_t)(k0 + j) * NC * D) : 0.f;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (k0 + j >= ns) break;
+      num = fmaf(v[j], weights[k0 + j] * inv, num);
+    }
+  }
+  static_cast<QT*>(p.o)[row * D + tid] = dev::from_float<QT>(num);
 }
 
 template <typename QT, typename KVT, int D, int G, int NW = 4>

@@ -57,6 +57,7 @@ struct DecodeParams {
   int* pool_done;
 };
 
+constexpr int kMergePieces = 8192;  // pieces of a unit the merge kernel holds weights for
 struct MergeParams {
   const int32_t* merge;  // [n_merge * 4]
   const int32_t* qo_indptr;  // [B + 1] for ragged q, else nullptr

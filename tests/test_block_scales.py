@@ -324,6 +324,44 @@ def test_cascade(lib, cuda, batch, group, prefix_pages, spread, q_dtype):
         p.run_block_scales(b.q, b.paged_kv[:, :, :8].contiguous(), b.extra["ks"], b.extra["vs"])
 
 
+@pytest.mark.parametrize("lengths,counts,hq,hkv,d", [
+    ([9000, 47000], [5, 6], 8, 2, 128), ([40000], None, 8, 1, 128), ([40000, 5], None, 16, 2, 64),
+    ([30000, 17, 2000, 0], [4, 4, 1, 0], 64, 8, 128), ([60000], None, 4, 4, 128)])
+def test_heavy_merges(lib, cuda, monkeypatch, lengths, counts, hq, hkv, d):
+    """Few requests of long contexts: units of many pieces and columns, folded
+    by the merge kernel by default, give the rows that the fold inside the
+    decode kernel gives - bit for bit where its weights fit its scratch (4096
+    at head_dim 128) - and the oracle's."""
+    b = make(lengths, counts, hq, hkv, d, torch.bfloat16, 9, cuda)
+    kv = b.paged_kv, b.extra["ks"], b.extra["vs"]
+    out = {}
+    for merge in ("fused", "kernel", None):
+        if merge:
+            monkeypatch.setenv("FADECODE_MERGE", merge)
+        else:
+            monkeypatch.delenv("FADECODE_MERGE")
+        p = plan(lib, b)
+        if merge:
+            assert p.info["fused_merge"] == int(merge == "fused")
+        pieces = int(p.work()[2][:, 3].max())
+        columns = hq // hkv * p.info["q_len"]
+        if merge is None:
+            assert p.info["fused_merge"] == int(pieces * columns <= 320)
+        o, lse = p.run_block_scales(b.q, *kv)
+        po, plse = p.run(b.q, b.paged_kv, k_scale=0.01, v_scale=0.01)
+        torch.cuda.synchronize()
+        assert p.check() == 0
+        out[merge] = o, lse, po, plse
+        if merge != "fused" or pieces * columns <= 2048:
+            again = p.run_block_scales(b.q, *kv)
+            assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    check(b, out[None][0], out[None][1], reference(b))
+    for x, y, z in zip(out["fused"], out["kernel"], out[None]):
+        assert torch.equal(y, z) or torch.equal(x, z)
+        if pieces * columns <= 2048:
+            assert torch.equal(x, y)
+
+
 def test_many_short_requests(lib, cuda):
     """Thousands of segments of 0 to 3 pages, fresh plans, on the first launch
     right after another kernel's."""
