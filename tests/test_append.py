@@ -131,7 +131,8 @@ LENGTHS = [([0, 5, 15, 16, 31, 0, 40, 7, 0, 100], [1, 0, 1, 1, 2, 0, 37, 9, 16, 
 @pytest.mark.parametrize("rotary_dim,interleaved", [(0, False), (None, False), (None, True),
                                                     (16, False), (48, True), (32, False)])
 @pytest.mark.parametrize("dtype,d,hq,hkv", [(F32, 64, 8, 8), (F32, 128, 3, 3), (BF16, 128, 32, 8),
-                                            (BF16, 64, 10, 5), (F16, 128, 7, 1), (F16, 64, 16, 2)])
+                                            (BF16, 64, 10, 5), (F16, 128, 7, 1), (F16, 64, 16, 2),
+                                            (BF16, 128, 34, 17)])
 def test_native(lib, cuda, dtype, d, hq, hkv, rotary_dim, interleaved, lengths):
     b = Batch(*LENGTHS[lengths], hq, hkv, d, dtype, dtype, seed=d + hq + lengths)
     rd = d if rotary_dim is None else rotary_dim
@@ -341,7 +342,7 @@ def test_e4m3_given_and_token_scales(lib, cuda, mode, dtype, d, hq, hkv, lengths
 @pytest.mark.gpu
 @pytest.mark.parametrize("lengths", range(len(LENGTHS)))
 @pytest.mark.parametrize("dtype,d,hq,hkv", [(BF16, 128, 64, 8), (F16, 128, 5, 5), (BF16, 64, 6, 3),
-                                            (F16, 64, 8, 1)])
+                                            (F16, 64, 8, 1), (BF16, 64, 33, 33)])
 @pytest.mark.parametrize("spread", [0, 6, 30])
 def test_block_scales(lib, cuda, spread, dtype, d, hq, hkv, lengths):
     """Scales and codes of continued and of new pages; spread: how far (log2)

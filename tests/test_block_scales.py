@@ -356,6 +356,13 @@ def test_heavy_merges(lib, cuda, monkeypatch, lengths, counts, hq, hkv, d):
             again = p.run_block_scales(b.q, *kv)
             assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
     check(b, out[None][0], out[None][1], reference(b))
+    o, lse = torch.zeros_like(out[None][0]), torch.zeros_like(out[None][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.run_block_scales(b.q, *kv, out=o, lse=lse)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, out[None][0]) and torch.equal(lse, out[None][1])
     for x, y, z in zip(out["fused"], out["kernel"], out[None]):
         assert torch.equal(y, z) or torch.equal(x, z)
         if pieces * columns <= 2048:
