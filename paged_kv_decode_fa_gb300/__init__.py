@@ -839,6 +839,7 @@ class AppendPlan:
         self.batch, self.num_qo_heads, self.num_kv_heads, self.head_dim, self.page_size = shape
         self.num_tokens = num_tokens
         self._device = workspace.get_device()
+        self._itemsize = q_dtype.itemsize
         self._page_shape = (2, self.page_size, self.num_kv_heads, self.head_dim)
         self._kv_shape = (num_tokens, self.num_kv_heads, self.head_dim)
         self._q_shape = (num_tokens, self.num_qo_heads, self.head_dim)
@@ -923,12 +924,14 @@ class AppendPlan:
             raise ValueError("paged_kv must be a contiguous CUDA tensor "
                              "[num_pages, 2, page_size, num_kv_heads, head_dim] on the plan's "
                              "device")
-        kv = self._row(k, self._kv_shape) + self._row(v, self._kv_shape)
         if q is None:
             if q_out is not None:
                 raise ValueError("q_out without q")
-            return _Rows3(*kv), None, None
-        rows = _Rows3(*kv, *self._row(q, self._q_shape))
+            return _Rows3(*self._row(k, self._kv_shape), *self._row(v, self._kv_shape)), None, None
+        rows = self._plain_rows(k, v, q)
+        if rows is None:  # refused there, or with strides that are never taken
+            rows = _Rows3(*self._row(k, self._kv_shape), *self._row(v, self._kv_shape),
+                          *self._row(q, self._q_shape))
         if q_out is None:
             q_out = torch.empty(self._q_shape, dtype=q.dtype, device=q.device)
         elif (q_out.dtype is not q.dtype or q_out.shape != self._q_shape
@@ -936,6 +939,22 @@ class AppendPlan:
             raise ValueError(f"q_out must be a contiguous tensor {list(self._q_shape)} of q's "
                              "dtype on its device")
         return rows, q_out, q_out.data_ptr()
+
+    def _plain_rows(self, k, v, q):
+        """fa_rows of k, v and q where each passes the checks of _row at once (a
+        small append is bound by the time of this call), else None."""
+        dtype, device, kv_shape = self.q_dtype, self._device, self._kv_shape
+        if (k.dtype is not dtype or v.dtype is not dtype or q.dtype is not dtype
+                or k.shape != kv_shape or v.shape != kv_shape or q.shape != self._q_shape
+                or k.get_device() != device or v.get_device() != device
+                or q.get_device() != device or not self.num_tokens):
+            return None
+        (kt, kh, ki), (vt, vh, vi), (qt, qh, qi) = k.stride(), v.stride(), q.stride()
+        kp, vp, qp = k.data_ptr(), v.data_ptr(), q.data_ptr()
+        if (ki != 1 or vi != 1 or qi != 1
+                or (kp | vp | qp | (kt | kh | vt | vh | qt | qh) * self._itemsize) & 15):
+            return None
+        return _Rows3(kp, kt, kh, vp, vt, vh, qp, qt, qh)
 
     def _row(self, t, shape):
         """(address, token stride, head stride) of a k, v or q."""
