@@ -185,6 +185,8 @@ struct MmaCfg {
   // column split: every warp reads every stage, any number of stages works
   static constexpr int S = CS ? RING_BYTES / STAGE_BYTES : SPW * NW;
   static constexpr int THREADS = (NW + 1) * 32;
+  // producer lanes that issue a page each at a time (produce_pages)
+  static constexpr int PL = SC == kScalePerBlock ? (NW > 8 ? 8 : 4) : 1;
   // CTAs per SM the ring size is chosen for; the register budget must allow
   // it (column split: 480 or 512 threads per SM at two or three warps)
   static constexpr int MIN_CTAS = NW > 8   ? 1
@@ -207,6 +209,9 @@ struct MmaCfg {
                 "rows must be whole 128-byte swizzle rows, or E4M3 ones of 64 bytes");
   static_assert(NC >= 1 && (NC <= 8 || NC <= 8 * NW), "8 columns (the MMA N side) per warp");
   static_assert(STAGE_BYTES % 1024 == 0, "swizzled boxes need 1024-byte alignment");
+  // the PL stages a producer step waits for are released by warp steps of up
+  // to NPP pages, none of them among the step's own
+  static_assert(S >= PL + NPP - 1, "producer and consumer steps must not wait for one another");
   static_assert(CS || S % NW == 0, "each ring stage must belong to exactly one consumer warp");
   static_assert(!kFp8 || D % 32 == 0, "E4M3 V is transposed two granules at a time");
 };
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
   dev::grid_dependency_wait();
 
   if (warp == NW) {
-    produce_pages<S, C::STAGE_BYTES, SEGS, C::BOX_X, C::BOX_BYTES, SC, BS ? (NW > 8 ? 8 : 4) : 1>(
+    produce_pages<S, C::STAGE_BYTES, SEGS, C::BOX_X, C::BOX_BYTES, SC, C::PL>(
         &kv_map, p, seg_begin, seg_end, ring, full, empty, lane,
         reinterpret_cast<float*>(smem + C::OFF_SCALES), queue, CS ? 1 : NW);
     return;
