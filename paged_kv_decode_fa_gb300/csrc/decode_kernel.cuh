@@ -441,8 +441,9 @@ __device__ __forceinline__ void prefetch_first_segment(const DecodeParams& p, in
 // the next segment's first) ahead of the pages being issued, and puts them
 // into a ring of their own, scales[k % 64][0..1] for page k of the stream:
 // before a batch's first page k0 is issued, page k0 - 1 - S has been released,
-// so with S <= 32 the batch's slots (pages k0 - 64 .. k0 - 33 held them) are free,
-// and lane 0's arrivals on "full" publish them.  (Copies of 4 bytes a page
+// so with S <= 32 the batch's slots (pages k0 - 64 .. k0 - 33 held them) are free -
+// for all lanes once the warp has converged behind the lanes that waited - and
+// the issuing lanes' arrivals on "full" publish them.  (Copies of 4 bytes a page
 // with cp.async, and a second arrival, took 11 us of the 195 of fp8_kv's
 // shape; a store a page by lane 0, between a stage's release and its refill, 5.)
 __host__ __device__ constexpr int scale_lanes(int sc) {  // producer lanes that copy scales
@@ -549,6 +550,9 @@ __device__ __forceinline__ void produce_pages(const CUtensorMap* map, const Deco
       if constexpr (SC == kScalePerBlock) {
         if (next.at != p0) fetch_block_scales(p, kvh, p0, cnt, lane, &next);
         id = next.id;
+        // lane 0's waits (the empty stages of a pool segment, the page before)
+        // come before every lane's store
+        __syncwarp();
         if (lane < cnt)
           *(reinterpret_cast<float2*>(scales) + (k + lane) % kBlockScaleRing) = next.scales;
         __syncwarp();
