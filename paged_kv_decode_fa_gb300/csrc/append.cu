@@ -10,7 +10,8 @@
 // it at far positions (t = 10^6 at inv_freq 1: 0.06 radians).  So the plan
 // stores inv_freq[i] / 2 pi modulo 1 as a 64-bit fraction f_i; t * f_i modulo
 // 2^64 is then the exact fraction of a turn, whatever t, in integer
-// multiplies; its top 32 bits, less the nearest quarter turn, go to sincospi.
+// multiplies.  Its cosine and sine are rounded once, and so is each product and
+// sum of the rotation: the values that elementary operations give.
 //
 // E4M3 caches: code = rn(x / s) saturated at 448, with s per tensor, per kv
 // head, per token (amax over the row / 448, written here) or per block, a
@@ -29,13 +30,13 @@
 // the CTA holds: one reduction in shared memory, no second pass over the
 // inputs.
 //
-// What bounds it.  Long appends are bound by HBM: 779 MB of prompts (32 / 8 heads,
-// head_dim 128, bf16, q included) in 123.9 us = 6.3 TB/s, 0.94 of the copy rate;
-// 910 MB into a block-scaled cache (64 / 8 heads) in 150.5 us = 6.0 TB/s, 0.91, where
-// the conversions keep 58 % of the issue slots busy and a run passes two more
-// barriers.  Single tokens are bound by the launch and one chain of loads (unit,
-// rows and page id, the page's scale): 4 tokens 2.7 us, 450 tokens 3.6 us, 128 tokens
-// into a block-scaled cache 5.1 us.
+// What bounds it (us per launch in a CUDA graph).  Long appends are bound by HBM:
+// 779 MB of prompts (32 / 8 heads, head_dim 128, bf16, q included) in 119.9 us =
+// 6.5 TB/s, 0.97 of the copy rate; 910 MB into a block-scaled cache (64 / 8 heads) in
+// 153.6 us = 5.9 TB/s, 0.89, where a run passes two more barriers around the
+// conversions.  Single tokens are bound by the launch and one chain of loads
+// (unit, rows and page id, the page's scale): 4 tokens 2.6 us, 450 tokens 3.3 us,
+// 128 tokens into a block-scaled cache 4.7 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -101,7 +102,6 @@ struct AppendParams {
   int hq, hkv;
   int heads;  // kv heads of one CTA, kHeads per thread at most
   int pairs;  // rotary_dim / 2
-  int interleaved;
 };
 
 __device__ __forceinline__ float2 unpack(uint32_t w, __nv_bfloat16) {
@@ -180,6 +180,31 @@ __device__ __forceinline__ void store_group(T* p, const Group<T>& g) {
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = g.w[i];
 }
 
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+      "  mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 w, x, y, z; mov.b64 w, {%2, %3}; mov.b64 x, {%4, %5}; mov.b64 y, {%6, %7};\n"
+      "  fma.rn.f32x2 z, w, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float c) {
+  return fma2(a, b, make_float2(c, c));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) {
+  return fma2(a, make_float2(b, b), c);
+}
+__device__ __forceinline__ float2 minus(float2 a) { return make_float2(-a.x, -a.y); }
+
 // A thread's 16 elements of a row: dims da .. da+7 and db .. db+7.
 struct Piece {
   float a[8], b[8];
@@ -188,36 +213,42 @@ struct Piece {
 // Its rotation: eight pairs, (a[j], b[j]), or interleaved within a and b.
 struct Turn {
   float c[8], s[8];
-  bool on, interleaved;
+  bool on;
 };
 
+// Products and sums are rounded one by one, as elementary operations round
+// them: an element fused into one rounding would differ from theirs in fp32's last
+// bit, and now and then in the type it is stored in.  (Scalar, since the assembler
+// fuses add.rn.f32x2 with a product of mul.rn.f32x2.)
+template <bool INTERLEAVED>
 __device__ __forceinline__ void rotate(const Turn& r, Piece* x) {
   if (!r.on) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (r.interleaved) {
+    if constexpr (INTERLEAVED) {
       float* y = j < 4 ? x->a : x->b;
       const int e = 2 * (j % 4);
       const float u = y[e], v = y[e + 1];
-      y[e] = u * r.c[j] - v * r.s[j];
-      y[e + 1] = v * r.c[j] + u * r.s[j];
+      y[e] = __fsub_rn(__fmul_rn(u, r.c[j]), __fmul_rn(v, r.s[j]));
+      y[e + 1] = __fadd_rn(__fmul_rn(v, r.c[j]), __fmul_rn(u, r.s[j]));
     } else {
       const float u = x->a[j], v = x->b[j];
-      x->a[j] = u * r.c[j] - v * r.s[j];
-      x->b[j] = v * r.c[j] + u * r.s[j];
+      x->a[j] = __fsub_rn(__fmul_rn(u, r.c[j]), __fmul_rn(v, r.s[j]));
+      x->b[j] = __fadd_rn(__fmul_rn(v, r.c[j]), __fmul_rn(u, r.s[j]));
     }
   }
 }
 
 // The largest magnitude of the piece's finite elements.  E4M3 cannot tell an
 // infinity from a large value: infinities become NaN here, which fmaxf passes
-// over and the conversion keeps.
-__device__ __forceinline__ float finite_amax(Piece* x) {
+// over and the conversion keeps, and *infinite is set.
+__device__ __forceinline__ float finite_amax(Piece* x, bool* infinite) {
   float m = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(x->a[j]), fabsf(x->b[j])));
   if (m == INFINITY) {
     m = 0.f;
+    *infinite = true;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (fabsf(x->a[j]) == INFINITY) x->a[j] = NAN;
@@ -228,20 +259,88 @@ __device__ __forceinline__ float finite_amax(Piece* x) {
   return m;
 }
 
-// (cos, sin) of a fraction of a turn, in 2^-32 turns: the nearest quarter turn
-// is taken off in integers, so that the rest, at most an eighth, goes to fp32
-// with an error of 2^-29 turns.
-__device__ __forceinline__ float2 cos_sin(unsigned turn) {
-  const unsigned quarter = (turn + (1u << 29)) >> 30;
-  const int rest = (int)(turn - (quarter << 30));
-  float s, c;
-  sincospif((float)rest * 4.656612873077393e-10f, &s, &c);  // 2^-31: in half-turns
-  if (quarter & 1) {
-    const float x = c;
-    c = -s;
-    s = x;
+// Two numbers, each a sum of two floats.
+struct Sum2 {
+  float2 hi, lo;
+};
+
+// c + z * p, |c| above |z p|: the product's and the sum's rounding errors are
+// kept (fma), to about 2^-47 of c.
+__device__ __forceinline__ Sum2 horner(const Sum2& z, float2 p, float c, float2 low) {
+  Sum2 r;
+  r.hi = fma2(z.hi, p, c);
+  const float2 err = fma2(z.hi, p, make_float2(c - r.hi.x, c - r.hi.y));
+  low = fma2(z.lo, p, low);
+  r.lo = make_float2(err.x + low.x, err.y + low.y);
+  return r;
+}
+
+// A whole number below 2^23, exactly (its bits under 2^23's).
+__device__ __forceinline__ float small_float(unsigned n) {
+  return __uint_as_float(0x4b000000u | n) - 8388608.f;
+}
+
+// (cos, sin) of two fractions of a turn, in 2^-64 turns, rounded to nearest but for
+// one angle in 10^5 (2^-37 of a cosine and 2^-40 of a sine before the last
+// rounding; the elementary operations on a float64 angle give the same).
+// The nearest quarter turn is taken off in integers.  The rest, at most an eighth
+// of a turn, becomes radians in a sum of two floats, and the series of sine and
+// cosine keep two floats in the terms that need them.  (sincospif, an ulp off
+// in one angle in six, put elements of q and codes of K on the other side of
+// a rounding border.)
+__device__ __forceinline__ float4 cos_sin(unsigned long long turn0, unsigned long long turn1) {
+  const unsigned long long turn[2] = {turn0, turn1};
+  unsigned quarter[2];
+  float ra[2], rb[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    quarter[i] = (unsigned)((turn[i] + (1ull << 61)) >> 62);
+    const long long rest = (long long)(turn[i] - ((unsigned long long)quarter[i] << 62));
+    // its bits from 39 (signed: under 1.5 * 2^23), 16 and 0
+    const float top = __uint_as_float(0x4b400000u + (unsigned)(int)(rest >> 39)) - 12582912.f;
+    const float mid = small_float((unsigned)(rest >> 16) & 0x7fffffu);
+    ra[i] = fmaf(top, 8388608.f, mid);
+    rb[i] = fmaf(fmaf(top, 8388608.f, -ra[i]) + mid, 65536.f, small_float((unsigned)rest & 0xffffu));
   }
-  return (quarter & 2) ? make_float2(-c, -s) : make_float2(c, s);
+  const float2 a = make_float2(ra[0], ra[1]), b = make_float2(rb[0], rb[1]);
+  // (a * 2^16 + b) * 2 pi / 2^64, 2 pi in two floats
+  constexpr float two_pi = 6.2831855f, two_pi_low = -1.7484555e-7f;
+  constexpr float k16 = 3.5527137e-15f, k0 = 5.4210109e-20f;  // 2^-48, 2^-64
+  const float2 h = mul2(a, make_float2(two_pi * k16, two_pi * k16));
+  const float2 e = fma2(b, two_pi * k0, fma2(a, two_pi_low * k16, fma2(a, two_pi * k16, minus(h))));
+  Sum2 z;  // the angle's square
+  z.hi = mul2(h, h);
+  z.lo = fma2(mul2(h, make_float2(2.f, 2.f)), e, fma2(h, h, minus(z.hi)));
+  auto next = [&](const Sum2& p, float c) {
+    return horner(z, p.hi, c, mul2(z.hi, p.lo));
+  };
+  // sin: coefficients 1 / n!, in two floats from 1 / 5!
+  float2 p = fma2(z.hi, 1.6059044e-10f, make_float2(-2.5052108e-8f, -2.5052108e-8f));
+  p = fma2(z.hi, fma2(z.hi, p, 2.7557319e-6f), -1.9841270e-4f);
+  Sum2 r = horner(z, p, 8.3333337e-3f, make_float2(-4.3461720e-10f, -4.3461720e-10f));
+  r = horner(z, r.hi, -1.6666667e-1f, fma2(z.hi, r.lo, 4.9670534e-9f));
+  r = next(r, 1.f);
+  const float2 v = mul2(h, r.hi);
+  const float2 vl = fma2(e, r.hi, fma2(h, r.lo, fma2(h, r.hi, minus(v))));
+  const float s[2] = {__fadd_rn(v.x, vl.x), __fadd_rn(v.y, vl.y)};
+  // cos, in two floats from 1 / 4!
+  p = fma2(z.hi, -1.1470746e-11f, make_float2(2.0876757e-9f, 2.0876757e-9f));
+  p = fma2(z.hi, fma2(z.hi, p, -2.7557319e-7f), 2.4801587e-5f);
+  p = fma2(z.hi, p, -1.3888889e-3f);
+  r = horner(z, p, 4.1666668e-2f, make_float2(-1.2417634e-9f, -1.2417634e-9f));
+  r = next(next(r, -0.5f), 1.f);
+  const float c[2] = {__fadd_rn(r.hi.x, r.lo.x), __fadd_rn(r.hi.y, r.lo.y)};
+  float x[2], y[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool odd = quarter[i] & 1;
+    x[i] = odd ? s[i] : c[i];
+    y[i] = odd ? c[i] : s[i];
+    // the signs: cos is negative in quarters 1 and 2, sin in 2 and 3
+    x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((quarter[i] ^ (quarter[i] << 1)) & 2) << 30);
+    y[i] = __uint_as_float(__float_as_uint(y[i]) ^ (quarter[i] & 2) << 30);
+  }
+  return make_float4(x[0], y[0], x[1], y[1]);
 }
 
 template <int LPR>
@@ -284,12 +383,14 @@ struct Cfg {
   static_assert(ROWS >= kPageSize && 2 * kMaxHeads <= THREADS, "a run's tokens; a thread a scale");
 };
 
-template <typename T, int D, int MODE>
+// INTERLEAVED as a constant: with both orders in one kernel, its code outgrew the
+// instruction cache (block-scaled prompts 155.9 us for 160.5, others 121.4 for 123.2).
+template <typename T, int D, int MODE, bool INTERLEAVED>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
     fa_append_kernel(const __grid_constant__ AppendParams p) {
   using C = Cfg<D>;
   constexpr int LPR = C::LPR;
-  __shared__ float2 angle[kPageSize * kMaxPairs];
+  __shared__ __align__(16) float2 angle[kPageSize * kMaxPairs];
   __shared__ int amax_bits[2 * kMaxHeads];                 // K heads, then V heads
   __shared__ float item_scale[2 * kMaxHeads], item_ratio[2 * kMaxHeads];
 
@@ -304,7 +405,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
   const bool live = tok < n;
   const int64_t row = u.row + tok;
   // its dims: the two halves of eight pairs, or 16 in a row
-  const bool split = !p.interleaved && 8 * c < p.pairs;
+  const bool split = !INTERLEAVED && 8 * c < p.pairs;
   const int da = split ? 8 * c : 16 * c, db = split ? p.pairs + 8 * c : 16 * c + 8;
   // the page id first: a block's scale hangs on it
   const int page = __ldg(p.indices + u.entry);
@@ -325,11 +426,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
   const bool page_ok = page >= 0 && (int64_t)page < p.num_pages;
   if (!page_ok && tid == 0) atomicOr(p.err, 1);
 
-  for (int i = tid; i < n * p.pairs; i += C::THREADS) {
-    const int t = i / p.pairs;
-    const unsigned long long turn =
-        (unsigned long long)(unsigned)(u.position + t) * p.turns[i - t * p.pairs];
-    angle[t * kMaxPairs + (i - t * p.pairs)] = cos_sin((unsigned)(turn >> 32));
+  // two pairs of a token at a time (their number is a multiple of eight)
+  for (int i = 2 * tid; i < n * p.pairs; i += 2 * C::THREADS) {
+    const int t = i / p.pairs, j = i - t * p.pairs;
+    const ulonglong2 turns = *reinterpret_cast<const ulonglong2*>(p.turns + j);
+    const unsigned long long at = (unsigned)(u.position + t);
+    *reinterpret_cast<float4*>(angle + t * kMaxPairs + j) = cos_sin(at * turns.x, at * turns.y);
   }
   const int64_t scale_at = (int64_t)page * p.hkv + h0 + (tid < heads ? tid : tid - heads);
   float old_scale = 0.f;
@@ -340,7 +442,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
   __syncthreads();
 
   Turn turn;
-  turn.interleaved = p.interleaved != 0;
   turn.on = live && 8 * c < p.pairs;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -355,13 +456,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
     return x;
   };
 
+  bool infinite = false;  // among this thread's K and V
   if constexpr (MODE == kBlock) {
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
       if (i * HG >= heads) break;
       Piece k = piece(kr[i]), v = piece(vr[i]);
-      rotate(turn, &k);
-      const float km = row_max<LPR>(finite_amax(&k)), vm = row_max<LPR>(finite_amax(&v));
+      rotate<INTERLEAVED>(turn, &k);
+      const float km = row_max<LPR>(finite_amax(&k, &infinite));
+      const float vm = row_max<LPR>(finite_amax(&v, &infinite));
       if (c == 0 && live && i * HG + hg < heads) {
         atomicMax(&amax_bits[i * HG + hg], __float_as_int(km));
         atomicMax(&amax_bits[heads + i * HG + hg], __float_as_int(vm));
@@ -403,7 +506,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
   auto write = [&](Piece x, bool is_k, const Group<T>(&raw)[2], int h, bool ok) {
     float inv = 1.f, scale = 1.f;
     if constexpr (MODE != kNative) {
-      const float m = finite_amax(&x);
+      // the block form has its amax already: 154.5 us for 155.9 without the second look
+      const float m = MODE != kBlock || infinite ? finite_amax(&x, &infinite) : 0.f;
       if constexpr (MODE == kStatic) {
         const float* hs = is_k ? p.head_k_scales : p.head_v_scales;
         inv = inverse(!hs ? (is_k ? p.k_scale : p.v_scale) : ok ? __ldg(hs + h0 + h) : 1.f);
@@ -437,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
     const int h = i * HG + hg;
     const bool ok = live && h < heads;
     Piece k = piece(kr[i]);
-    rotate(turn, &k);
+    rotate<INTERLEAVED>(turn, &k);
     write(k, true, kr[i], h, ok);
     write(piece(vr[i]), false, vr[i], h, ok);
   }
@@ -461,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
       const int h = i0 + i * HG;
       if (!live || h >= rows_q) break;
       Piece x = piece(in[i]);
-      rotate(turn, &x);
+      rotate<INTERLEAVED>(turn, &x);
       store_group(out + h * D + da, narrow<T>(x.a));
       store_group(out + h * D + db, narrow<T>(x.b));
     }
@@ -474,27 +578,30 @@ struct AppendKernel {
 };
 
 template <typename T, int MODE>
-AppendKernel kernel_of(int head_dim) {
-  if (head_dim == 64)
-    return {reinterpret_cast<const void*>(&fa_append_kernel<T, 64, MODE>), Cfg<64>::THREADS,
-            Cfg<64>::ROWS};
-  return {reinterpret_cast<const void*>(&fa_append_kernel<T, 128, MODE>), Cfg<128>::THREADS,
-          Cfg<128>::ROWS};
+AppendKernel kernel_of(int head_dim, bool interleaved) {
+  auto of = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    const void* f = interleaved ? reinterpret_cast<const void*>(&fa_append_kernel<T, D, MODE, true>)
+                                : reinterpret_cast<const void*>(&fa_append_kernel<T, D, MODE, false>);
+    return AppendKernel{f, Cfg<D>::THREADS, Cfg<D>::ROWS};
+  };
+  return head_dim == 64 ? of(std::integral_constant<int, 64>{})
+                        : of(std::integral_constant<int, 128>{});
 }
 
 // A kernel for q's type, the cache being E4M3 unless mode is kNative.
-AppendKernel find_append_kernel(fa_dtype q, int head_dim, Mode mode) {
-  if (q == FA_DTYPE_F32) return kernel_of<float, kNative>(head_dim);
+AppendKernel find_append_kernel(fa_dtype q, int head_dim, Mode mode, bool interleaved) {
+  if (q == FA_DTYPE_F32) return kernel_of<float, kNative>(head_dim, interleaved);
   if (q == FA_DTYPE_BF16) {
-    if (mode == kStatic) return kernel_of<__nv_bfloat16, kStatic>(head_dim);
-    if (mode == kToken) return kernel_of<__nv_bfloat16, kToken>(head_dim);
-    if (mode == kBlock) return kernel_of<__nv_bfloat16, kBlock>(head_dim);
-    return kernel_of<__nv_bfloat16, kNative>(head_dim);
+    if (mode == kStatic) return kernel_of<__nv_bfloat16, kStatic>(head_dim, interleaved);
+    if (mode == kToken) return kernel_of<__nv_bfloat16, kToken>(head_dim, interleaved);
+    if (mode == kBlock) return kernel_of<__nv_bfloat16, kBlock>(head_dim, interleaved);
+    return kernel_of<__nv_bfloat16, kNative>(head_dim, interleaved);
   }
-  if (mode == kStatic) return kernel_of<__half, kStatic>(head_dim);
-  if (mode == kToken) return kernel_of<__half, kToken>(head_dim);
-  if (mode == kBlock) return kernel_of<__half, kBlock>(head_dim);
-  return kernel_of<__half, kNative>(head_dim);
+  if (mode == kStatic) return kernel_of<__half, kStatic>(head_dim, interleaved);
+  if (mode == kToken) return kernel_of<__half, kToken>(head_dim, interleaved);
+  if (mode == kBlock) return kernel_of<__half, kBlock>(head_dim, interleaved);
+  return kernel_of<__half, kNative>(head_dim, interleaved);
 }
 
 // kv heads of one CTA, for runs of `longest` tokens at most, `tokens` in all:
@@ -568,7 +675,8 @@ struct fa_append_plan_s {
   AppendLayout layout{};
   int64_t num_units = 0, num_rows = 0;
   int longest = 0;  // tokens of the longest run
-  int pairs = 0, interleaved = 0;
+  int pairs = 0;
+  bool interleaved = false;
 };
 
 namespace {
@@ -619,8 +727,7 @@ int append_run(fa_append_plan_s* plan, Mode mode, const fa_rows* k, const fa_row
   p.hq = plan->hq;
   p.hkv = plan->hkv;
   p.pairs = plan->pairs;
-  p.interleaved = plan->interleaved;
-  const AppendKernel kern = find_append_kernel(plan->q_dtype, plan->d, mode);
+  const AppendKernel kern = find_append_kernel(plan->q_dtype, plan->d, mode, plan->interleaved);
   void* args[1] = {&p};
   p.heads = heads_of_cta(kern, plan->num_rows, plan->num_units, plan->longest, plan->hkv,
                          plan->hq / plan->hkv);
@@ -729,7 +836,7 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
   plan->num_rows = append_indptr_host[batch];
   plan->longest = longest;
   plan->pairs = rotary_dim / 2;
-  plan->interleaved = interleaved ? 1 : 0;
+  plan->interleaved = interleaved != 0;
   if (cudaGetDevice(&plan->device) != cudaSuccess ||
       upload_async(plan->ws, meta.data(), meta.size(), static_cast<cudaStream_t>(cuda_stream)) !=
           cudaSuccess) {
