@@ -226,16 +226,8 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW, SC>::THREADS)
           *(reinterpret_cast<const float2*>(smem + C::OFF_SCALES) + k % kBlockScaleRing);
       page_qscale *= bs.x;
       wf = bs.y * vref_inv;
-      if (!(wf <= 64.f && (wf >= 1.f / 64.f || bs.y == 0.f))) {
-        const float inv = 1.f / bs.y, f = vref * inv;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] *= f;
-        vref = bs.y;
-        vref_inv = inv;
-        wf = 1.f;
-      }
+      if (!block_weight_inside(wf, bs.y))
+        wf = move_block_reference(bs.y, wf, o, &vref, &vref_inv);
     }
 
     // ---- S[rows][tokens]: n-tile 0 = tokens 0..7 (K row g), 1 = tokens 8..15;

@@ -239,6 +239,34 @@ constexpr float kLazyAbove = 8.f;
 // scores and release the stage then, instead of after P.V.
 constexpr bool kEarlyVRelease = true;
 
+// Per-block V scales.  o is kept in units of a reference, and a page's weights
+// enter P.V times wf, its scale over the reference.  The weights are f16 and at
+// most 2^8 before that factor: with wf in [1, 2^7] they stay below 2^15, and low
+// ones (2^-25 is lost, 2^-14 the last of full precision) are kept as far down as a
+// per-tensor scale keeps them, whatever scales ignored pages have.  The reference
+// moves when a page leaves that window, by little more than it has to, so
+// that scales within 2^7 of one another soon lie inside it for good.
+__device__ __forceinline__ bool block_weight_inside(float wf, float v_scale) {
+  return wf <= 128.f && (wf >= 1.f || v_scale == 0.f);
+}
+
+// Move the reference for a page outside the window and rescale o (exactly where
+// the scales are powers of two); returns the page's factor.
+template <int N>
+__device__ __forceinline__ float move_block_reference(float v_scale, float wf, float (&o)[N][4],
+                                                      float* vref, float* vref_inv) {
+  const float below = *vref == 0.f ? 1.f / 16 : wf > 128.f ? 1.f / 64 : 1.f / 2;
+  const float to = fmaxf(v_scale * below, 1.17549435e-38f);  // a normal number: so is its inverse
+  const float inv = 1.f / to, f = *vref * inv;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[n][e] *= f;
+  *vref = to;
+  *vref_inv = inv;
+  return v_scale * inv;
+}
+
 template <typename QT, typename KVT, int D, int G, int NW, int SC, int QL, bool UM,
           bool RQ = false>
 __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
@@ -434,16 +462,11 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
     // that has seen nothing yet (every token so far masked), whose weights
     // exp2(-inf - 0) = 0 keep its state empty; it changes only on a rescale
     float mref[2] = {0.f, 0.f};
-    // Per-block scales: o is kept in units of a reference V scale (0 before
-    // the first page with a non-zero one), and a page's weights enter P.V
-    // times its scale over the reference.  The reference is a recent page's
-    // scale: it moves when a page's scale leaves [2^-6, 2^6] of it, with an
-    // exact rescale of o where the scales are powers of two, so the f16
-    // weights (at most 2^8 before the factor) stay below 2^14, and a page that
-    // the softmax favours keeps its full precision however small its scale
-    // is next to an earlier page's.  A step of several pages leaves it alone,
-    // so that they share one test and no branch lies between their MMAs: where
-    // a scale is outside, they are taken one at a time.
+    // Per-block scales: o is kept in units of a reference (0 before the first
+    // page with a non-zero V scale), see block_weight_inside.  A step of
+    // several pages leaves it alone, so that they share one test and no branch
+    // lies between their MMAs: where a scale is outside, they are taken one at
+    // a time.
     float vref = 0.f, vref_inv = 0.f;
 
     // ---- O^T[dim][head] += V^T . P^T for one page (stage address st).
@@ -568,18 +591,11 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
           ks[u] = bs.x;
           v_scale = bs.y;
           wf[u] = bs.y * vref_inv;
-          inside = inside && wf[u] <= 64.f && (wf[u] >= 1.f / 64.f || bs.y == 0.f);
+          inside = inside && block_weight_inside(wf[u], bs.y);
         }
         if (!inside) {
           if (NPP > 1) return false;
-          const float inv = 1.f / v_scale, f = vref * inv;
-#pragma unroll
-          for (int mt = 0; mt < MTILES; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[mt][e] *= f;
-          vref = v_scale;
-          vref_inv = inv;
-          wf[0] = 1.f;
+          wf[0] = move_block_reference(v_scale, wf[0], o, &vref, &vref_inv);
         }
       }
       const int sw = C::SWZ == 128 ? (g & 7) : ((g >> 1) & 3);  // swizzle of rows g and g+8
