@@ -266,8 +266,10 @@ int fa_decode_run_head_scales(fa_decode_plan_t plan, const void* q, const void* 
  *                      4-byte aligned: the element has the value code * scale.
  *                      A scale is 0 (the block's values are 0) or a positive
  *                      normal number; powers of two are exact, others round
- *                      the softmax weights once more.  The scales of one
- *                      kv head's blocks may differ by up to 2^64.
+ *                      the softmax weights once more.  They may be as
+ *                      far apart as they like: next to a V scale 2^64 times its
+ *                      own and more, a block's values may lose low bits, at most
+ *                      2^-64 of the larger ones.
  * Other arguments as fa_decode_run (sm_scale <= 0 selects 1/sqrt(head_dim)).
  * Every plan kind takes it (plain, multi-token, ragged query rows; for a
  * cascade, fa_cascade_run_block_scales) on the shapes and dtypes built for it; plans whose kv dtype is not E4M3 return

@@ -251,13 +251,32 @@ __device__ __forceinline__ bool block_weight_inside(float wf, float v_scale) {
 }
 
 // Move the reference for a page outside the window and rescale o (exactly where
-// the scales are powers of two); returns the page's factor.
+// the scales are powers of two); returns the page's factor.  The reference falls
+// no further than leaves o below 2^120: where the sums so far are of values 2^64
+// times this page's and more, its weights lose low bits instead, an
+// absolute error below 2^-64 of those values.
 template <int N>
 __device__ __forceinline__ float move_block_reference(float v_scale, float wf, float (&o)[N][4],
                                                       float* vref, float* vref_inv) {
   const float below = *vref == 0.f ? 1.f / 16 : wf > 128.f ? 1.f / 64 : 1.f / 2;
-  const float to = fmaxf(v_scale * below, 1.17549435e-38f);  // a normal number: so is its inverse
-  const float inv = 1.f / to, f = *vref * inv;
+  float to = fmaxf(v_scale * below, 1.17549435e-38f);  // a normal number: so is its inverse
+  float inv = 1.f / to, f = *vref * inv;
+  if (f > 1.f) {
+    float top = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(o[n][e]));
+    const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    const int room = min(119 - ((int)(bits >> 23) - 127), 126);  // top * 2^room < 2^120
+    if (bits == 0u) {
+      f = 0.f;  // nothing to rescale (f itself may be infinite)
+    } else if (f > ldexpf(1.f, room)) {
+      f = ldexpf(1.f, max(room, 0));
+      to = *vref / f;
+      inv = *vref_inv * f;
+    }
+  }
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll

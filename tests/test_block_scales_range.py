@@ -125,3 +125,149 @@ def test_low_weights_cascade(lib, cuda, dtype, ratio, e):
     o, lse = p.run_block_scales(q, s.kv, s.ks, s.vs, sm_scale=s.sm_scale)
     s.check(o, lse, dtype, repeats=repeats)
     assert p.check() == 0
+
+
+# ---------------------------------------------------------------- V scales far apart
+
+def tiny_and_ordinary(order, n, tiny=2.0 ** -120):
+    """Per page, the factor of V's values: 1, or `tiny` (2^-120: values near 1e-36,
+    whose block scale is 2^-126)."""
+    f = np.ones(n)
+    third = n // 3
+    if order == "before":
+        f[:third] = tiny
+    elif order == "between":
+        f[third:2 * third] = tiny
+    elif order == "after":
+        f[2 * third:] = tiny
+    elif order == "one":
+        f[n // 2] = tiny
+    else:                                     # each smaller than the one before
+        f = 2.0 ** (-np.linspace(0, 120, n))
+    return f
+
+
+def appended(lib, lengths, order, hq, hkv, d, device, seed, tiny=2.0 ** -120):
+    """A cache written by run_block_scales, V's pages of such values."""
+    from tests.test_append import Batch
+    b = Batch([0] * len(lengths), lengths, hq, hkv, d, BF16, E4M3, seed=seed, device=device)
+    v = torch.cat([torch.randn((n, hkv, d), device=device)
+                   * torch.from_numpy(np.repeat(tiny_and_ordinary(order, (n + 15) // 16, tiny), 16)[:n])
+                   .float().to(device)[:, None, None] for n in lengths]).to(BF16)
+    k = torch.randn((b.T, hkv, d), device=device).to(BF16)
+    ks, vs = (torch.full((b.num_pages, hkv), float("nan"), device=device) for _ in range(2))
+    b.plan(lib).run_block_scales(k, v, b.kv, ks, vs)
+    assert float(vs.nan_to_num(1.0).min()) <= tiny * 2.0 ** -5
+    return b, ks, vs
+
+
+def reference(b, ks, vs, q, rows, prefix=0, repeats=1):
+    """(o, lse, sum w |v|) in 64 bits over the dequantised cache, its first `prefix`
+    tokens taken `repeats` times."""
+    o, lse, mag = [], [], []
+    at = 0
+    for i, r in enumerate(rows):
+        n = int(b.new[i])
+        ids = torch.from_numpy(b.ids[b.indptr[i]:b.indptr[i + 1]].astype(np.int64)).to(q.device)
+        kv = b.kv[ids].double()
+        k = (kv[:, 0] * ks[ids].double()[:, None, :, None]).flatten(0, 1)[:n]
+        v = (kv[:, 1] * vs[ids].double()[:, None, :, None]).flatten(0, 1)[:n]
+        x = q[at:at + r].double().unflatten(1, (b.hkv, -1))          # [r, hkv, g, d]
+        w = torch.einsum("rhgd,nhd->rhgn", x, k) * b.d ** -0.5
+        w[..., :prefix] += math.log(repeats)
+        seen = torch.arange(n, device=q.device) <= n - r + torch.arange(r, device=q.device)[:, None]
+        w = w.masked_fill(~seen[:, None, None], -math.inf)
+        lse.append(torch.logsumexp(w, -1).flatten(1))
+        w = torch.softmax(w, -1)
+        o.append(torch.einsum("rhgn,nhd->rhgd", w, v).flatten(1, 2))
+        mag.append(torch.einsum("rhgn,nhd->rhgd", w, v.abs()).flatten(1, 2))
+        at += r
+    return torch.cat(o), torch.cat(lse), torch.cat(mag)
+
+
+def close(o, lse, ref, extra=0.0):
+    """As the block-scale tests: half a step of the output, 3 * 2^-11 for the f16
+    weights and 2e-4 for the logits, of sum w |v|."""
+    ro, rl, mag = ref
+    assert torch.isfinite(o).all()
+    err = (o.double().reshape(ro.shape) - ro).abs()
+    tol = HALF[o.dtype] * ro.abs() + (3 * 2.0 ** -11 + 2e-4 + extra) * mag
+    assert (err <= tol * 1.01 + 1e-38).all(), float((err / tol).max())
+    assert float((lse.double().reshape(rl.shape) - rl).abs().max()) <= 1e-4
+
+
+ORDERS = ["before", "between", "after", "one", "falling"]
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("d,group", [(128, 1), (128, 8), (64, 4), (64, 8)])
+def test_appended_tiny_values_page_split(lib, cuda, d, group, order):
+    lengths = [700, 3000, 16, 1500]
+    b, ks, vs = appended(lib, lengths, order, 2 * group, 2, d, cuda, 1)
+    p = lib.plan(b.indptr, b.indices, b.last, 2 * group, 2, d, 16, q_data_type=BF16,
+                 kv_data_type=E4M3)
+    q = torch.randn((4, 2 * group, d), device=cuda).to(BF16)
+    o, lse = p.run_block_scales(q, b.kv, ks, vs)
+    close(o, lse, reference(b, ks, vs, q, [1] * 4))
+    assert p.check() == 0
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("counts", [[4, 4, 4, 4], [2, 1, 2, 1], [3, 1, 0, 2]])
+def test_appended_tiny_values_column_split(lib, cuda, counts, order):
+    lengths = [700, 3000, 16, 1500]
+    b, ks, vs = appended(lib, lengths, order, 16, 2, 128, cuda, 2)
+    p = lib.plan_ragged_q(b.indptr, b.indices, b.last, np.concatenate([[0], np.cumsum(counts)]),
+                          16, 2, 128, 16, q_data_type=BF16, kv_data_type=E4M3)
+    q = torch.randn((sum(counts), 16, 128), device=cuda).to(BF16)
+    o, lse = p.run_block_scales(q, b.kv, ks, vs)
+    close(o, lse, reference(b, ks, vs, q, counts))
+    assert p.check() == 0
+
+
+@pytest.mark.parametrize("order", ORDERS)
+def test_appended_tiny_values_cascade(lib, cuda, order):
+    """The prefix is one request of the append, its pages many times over (a CTA
+    then holds several changes of scale); the cascade's requests have it, and
+    one page more, the last of another."""
+    b, ks, vs = appended(lib, [2400, 16], order, 16, 2, 128, cuda, 3)
+    batch, repeats = 20, 64
+    own = b.indices[150:151].repeat(batch)
+    p = lib.cascade_plan(b.indices[:150].repeat(repeats), np.arange(batch + 1), own, [16] * batch,
+                         16, 2, 128, 16, q_data_type=BF16, kv_data_type=E4M3)
+    q = torch.randn((batch, 16, 128), device=cuda).to(BF16)
+    o, lse = p.run_block_scales(q, b.kv, ks, vs)
+    b.indptr, b.new = np.array([0, 151]), np.array([2416])  # all 151 pages as one request
+    refs = [reference(b, ks, vs, q[i:i + 1], [1], 2400, repeats) for i in range(batch)]
+    close(o, lse, [torch.cat(x) for x in zip(*refs)], extra=HALF[BF16])
+    assert p.check() == 0
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("counts", [None, [4, 3]])
+def test_attended_tiny_values_beside_ignored_ordinary_ones(lib, cuda, counts, first):
+    """The other way round: the softmax ignores the ordinary pages (weight 0), and
+    what is left are values 2^64 below theirs, in full precision."""
+    lengths, hq, hkv, d = [640, 1600], 16, 2, 128
+    b, ks, vs = appended(lib, lengths, "after" if first else "before", hq, hkv, d, cuda, 4,
+                         tiny=2.0 ** -64)
+    q = torch.rand((sum(counts) if counts else 2, hq, d), device=cuda).add_(0.5).to(BF16)
+    ids = torch.from_numpy(b.ids[:b.indptr[2]].astype(np.int64)).to(cuda)
+    raw = b.kv.view(torch.uint8)
+    raw[ids, 0] = raw[ids, 0] & 0x3f                # K codes 0 .. 1.9
+    ks[ids] = 2.0 ** -6
+    ordinary = ids[(vs[ids] > 2.0 ** -40).all(-1)]
+    raw[ordinary, 0] = 0xfe                         # and -448
+    ks[ordinary] = 4.0
+    args = (hq, hkv, d, 16)
+    if counts:
+        p = lib.plan_ragged_q(b.indptr, b.indices, b.last, [0, 4, 7], *args, q_data_type=BF16,
+                              kv_data_type=E4M3)
+    else:
+        p = lib.plan(b.indptr, b.indices, b.last, *args, q_data_type=BF16, kv_data_type=E4M3)
+    o, lse = p.run_block_scales(q, b.kv, ks, vs)
+    ref = reference(b, ks, vs, q, counts or [1, 1])
+    assert 0 < float(ref[0].abs().max()) < 1e-16
+    err = (o.double().reshape(ref[0].shape) - ref[0]).abs()
+    tol = HALF[BF16] * ref[0].abs() + (3 * 2.0 ** -11 + 2e-4) * ref[2]
+    assert (err <= tol * 1.01).all(), float((err / tol).max())
