@@ -270,6 +270,8 @@ int fa_decode_run_head_scales(fa_decode_plan_t plan, const void* q, const void* 
  *                      far apart as they like: next to a V scale 2^64 times its
  *                      own and more, a block's values may lose low bits, at most
  *                      2^-64 of the larger ones.
+ *                      (Values of 2^100 and more may pass fp32's range
+ *                      in the sums, as in any cache.)
  * Other arguments as fa_decode_run (sm_scale <= 0 selects 1/sqrt(head_dim)).
  * Every plan kind takes it (plain, multi-token, ragged query rows; for a
  * cascade, fa_cascade_run_block_scales) on the shapes and dtypes built for it; plans whose kv dtype is not E4M3 return

@@ -262,6 +262,15 @@ def _reachable(t: torch.Tensor) -> bool:
     return t.is_cuda or t.is_pinned()
 
 
+def _check_indices(indices: torch.Tensor, indptr, batch: int) -> None:
+    """The page table of a batch: the kernels read indptr[batch] entries of it."""
+    if indices.dtype != torch.int32 or not _reachable(indices) or not indices.is_contiguous():
+        raise ValueError("indices must be a contiguous int32 CUDA or page-locked tensor")
+    if batch > 0 and indices.numel() < int(indptr[batch]):
+        raise ValueError(f"indices holds {indices.numel()} pages, indptr asks for "
+                         f"{int(indptr[batch])}")
+
+
 def _cuda_device(t: torch.Tensor) -> torch.device:
     """The device a tensor lives on, or the current CUDA device for host memory."""
     return t.device if t.is_cuda else torch.device("cuda", torch.cuda.current_device())
@@ -499,8 +508,7 @@ def plan(indptr, indices: torch.Tensor, last_page_len, num_qo_heads: int, num_kv
     B = n_indptr - 1
     if n_last < B:
         raise ValueError("last_page_len shorter than the batch")
-    if indices.dtype != torch.int32 or not _reachable(indices) or not indices.is_contiguous():
-        raise ValueError("indices must be a contiguous int32 CUDA or page-locked tensor")
+    _check_indices(indices, indptr_h, B)
     if workspace is None:
         workspace = torch.empty(workspace_size(B, num_qo_heads, num_kv_heads, head_dim),
                                 dtype=torch.uint8, device=_cuda_device(indices))
@@ -529,8 +537,7 @@ def plan_multi_token(indptr, indices: torch.Tensor, last_page_len, q_len: int, n
     B = n_indptr - 1
     if n_last < B:
         raise ValueError("last_page_len shorter than the batch")
-    if indices.dtype != torch.int32 or not _reachable(indices) or not indices.is_contiguous():
-        raise ValueError("indices must be a contiguous int32 CUDA or page-locked tensor")
+    _check_indices(indices, indptr_h, B)
     if workspace is None:
         if (num_qo_heads // max(1, num_kv_heads)) * q_len > 8:   # the ragged-q kernels
             n = _L().fa_decode_workspace_size_ragged_q(B, num_qo_heads, num_kv_heads, head_dim)
@@ -565,8 +572,7 @@ def plan_ragged_q(indptr, indices: torch.Tensor, last_page_len, qo_indptr, num_q
     B = n_indptr - 1
     if n_last < B or n_qo != B + 1:
         raise ValueError("last_page_len shorter than the batch, or qo_indptr not batch + 1 long")
-    if indices.dtype != torch.int32 or not _reachable(indices) or not indices.is_contiguous():
-        raise ValueError("indices must be a contiguous int32 CUDA or page-locked tensor")
+    _check_indices(indices, indptr_h, B)
     if workspace is None:
         n = _L().fa_decode_workspace_size_ragged_q(B, num_qo_heads, num_kv_heads, head_dim)
         if n == 0:
@@ -778,6 +784,7 @@ def cascade_plan(prefix_indices: torch.Tensor, indptr, indices: torch.Tensor, la
     for t in (prefix_indices, indices):
         if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
             raise ValueError("index arrays must be contiguous int32 CUDA tensors")
+    _check_indices(indices, indptr_h, B)
     if workspace is None:
         n = _L().fa_cascade_workspace_size(B, num_qo_heads, num_kv_heads, head_dim)
         if n == 0:
@@ -999,8 +1006,7 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
         off_h, off_p, n_off = _host_i32_ptr(position_offset)
         if n_off != B:
             raise ValueError("position_offset must have one value per request")
-    if indices.dtype != torch.int32 or not _reachable(indices) or not indices.is_contiguous():
-        raise ValueError("indices must be a contiguous int32 CUDA or page-locked tensor")
+    _check_indices(indices, indptr_h, B)
     total = int(np.asarray(app_h)[B]) if B >= 0 else 0
     device = torch.cuda.current_device()
     if indices.is_cuda and indices.get_device() != device:
