@@ -901,9 +901,7 @@ int fa_decode_unified_max_fallbacks(fa_decode_plan_t plan, void* cuda_stream, in
   if (!plan || !count) return FA_ERR_INVALID_ARG;
   int word = 0;
   int* dword = reinterpret_cast<int*>(plan->ws + plan->layout.off_umc);
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess ||
-      cudaMemcpy(&word, dword, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(dword, 0, sizeof word) != cudaSuccess)
+  if (fadecode::take_word(dword, &word, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess)
     return FA_ERR_CUDA;
   *count = word;
   return FA_OK;
@@ -1021,16 +1019,14 @@ int fa_decode_check(fa_decode_plan_t plan, void* cuda_stream, int* flags) {
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   int word = 0;
   int* dword = reinterpret_cast<int*>(plan->ws + plan->layout.off_err);
-  if (cudaStreamSynchronize(st) != cudaSuccess ||
-      cudaMemcpy(&word, dword, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(dword, 0, sizeof word) != cudaSuccess)
-    return FA_ERR_CUDA;
+  if (fadecode::take_word(dword, &word, st) != cudaSuccess) return FA_ERR_CUDA;
   // A run that gave up waiting may leave the pool and merge counters short
   // of their re-armed zeros: clear them for the next run.
   if (word &&
-      (cudaMemset(plan->ws + plan->layout.off_pool, 0, 2 * sizeof(int)) != cudaSuccess ||
-       cudaMemset(plan->ws + plan->layout.off_count, 0,
-                  sizeof(int32_t) * plan->wl.merge.size()) != cudaSuccess))
+      (cudaMemsetAsync(plan->ws + plan->layout.off_pool, 0, 2 * sizeof(int), st) != cudaSuccess ||
+       cudaMemsetAsync(plan->ws + plan->layout.off_count, 0,
+                       sizeof(int32_t) * plan->wl.merge.size(), st) != cudaSuccess ||
+       cudaStreamSynchronize(st) != cudaSuccess))
     return FA_ERR_CUDA;
   *flags = word;
   return word ? FA_ERR_DEVICE_CHECK : FA_OK;

@@ -903,9 +903,8 @@ int fa_append_run_block_scales(fa_append_plan_t plan, const fa_rows* k, const fa
 int fa_append_check(fa_append_plan_t plan, void* cuda_stream, int* flags) {
   if (!plan || !flags) return FA_ERR_INVALID_ARG;
   int word = 0;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess ||
-      cudaMemcpy(&word, plan->ws, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(plan->ws, 0, sizeof word) != cudaSuccess)
+  if (take_word(reinterpret_cast<int*>(plan->ws), &word,
+                static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess)
     return FA_ERR_CUDA;
   *flags = word;
   return word ? FA_ERR_DEVICE_CHECK : FA_OK;

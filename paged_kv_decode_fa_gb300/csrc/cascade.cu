@@ -1007,8 +1007,7 @@ int fa_cascade_check(fa_cascade_plan_t plan, void* cuda_stream, int* flags) {
   if (rc != FA_OK && rc != FA_ERR_DEVICE_CHECK) return rc;
   int word = 0;
   int* dword = reinterpret_cast<int*>(plan->ws + plan->L.off_err);
-  if (cudaMemcpy(&word, dword, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(dword, 0, sizeof word) != cudaSuccess)
+  if (fadecode::take_word(dword, &word, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess)
     return FA_ERR_CUDA;
   *flags = f1 | word;
   return *flags ? FA_ERR_DEVICE_CHECK : FA_OK;

@@ -73,4 +73,10 @@ void staging_stats(int64_t* allocations, int64_t* bytes, int64_t* uploads) {
   *uploads = g_uploads.load();
 }
 
+cudaError_t take_word(int* word, int* out, cudaStream_t stream) {
+  cudaError_t e = cudaMemcpyAsync(out, word, sizeof *out, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof *word, stream);
+  return e == cudaSuccess ? cudaStreamSynchronize(stream) : e;
+}
+
 }  // namespace fadecode

@@ -16,6 +16,13 @@ namespace fadecode {
 // Returns cudaSuccess or the failing call's error.
 cudaError_t upload_async(void* dst, const void* src, size_t bytes, cudaStream_t stream);
 
+// Read a device word and clear it, on `stream`: the work queued there before is
+// done and the word is clear when the call returns, so that a kernel launched
+// afterwards on any stream finds it so.  (A clear on the default stream is not
+// ordered with streams that do not wait for that one, and may come after
+// what such a kernel set.)
+cudaError_t take_word(int* word, int* out, cudaStream_t stream);
+
 // Page-locked staging buffers allocated so far (count and bytes) and
 // uploads made through the ring, since the library was loaded.
 void staging_stats(int64_t* allocations, int64_t* bytes, int64_t* uploads);
