@@ -728,7 +728,7 @@ def bench_ours(args, world, rank, local):
     elapsed_s = start.elapsed_time(end) / 1e3
     elapsed_s = max_over_ranks(elapsed_s, world, dev)
     # The decode kernel alone: a second loop of the same length with the
-    # library recording events around the kernel of every step (torch
+    # library recording events around the launches of every step (torch
     # creates an event at its first record, so each is recorded once first).
     evs = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
            for _ in range(args.steps)]
@@ -746,11 +746,11 @@ def bench_ours(args, world, rank, local):
     kern_med_s = statistics.median(kern_ms) / 1e3
     # the dominant kernel's average duration inside the timed region: the
     # region's events over its launches when a step is that one launch, else
-    # the per-launch events of the second loop
+    # the per-step events of the second loop
     if launches_per_step == 1:
         kern_region_s, duration_from = elapsed_s / args.steps, "timed-region events / launches"
     else:
-        kern_region_s, duration_from = kern_avg_s, "events around each decode launch"
+        kern_region_s, duration_from = kern_avg_s, "events around each step's launches"
 
     # End to end through the public API with host buffers.  Every step plans
     # the batch and decodes it with q, the page ids, o and lse in page-locked

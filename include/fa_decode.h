@@ -105,6 +105,10 @@ size_t fa_decode_workspace_size(int batch, int num_qo_heads, int num_kv_heads,
  * stream, one kv head each (fa_plan_work_host_heads shows the same plan on
  * the host); FADECODE_PLAN=stream in the environment selects the plan of
  * fa_plan_work_host instead.
+ * A request that the plan cuts into pieces is folded by the decode kernel
+ * itself, or, where a unit's pieces times its columns (query heads of a kv head x
+ * query tokens) pass 320, all such units by a second launch, a merge kernel
+ * (fa_plan_info: fused_merge 0): the same sums, faster for few long requests.
  * Errors: FA_ERR_INVALID_ARG for a malformed indptr or last_page_len, NULL
  * pointers or non-positive sizes; FA_ERR_UNSUPPORTED for shapes or types that
  * are not built; FA_ERR_WORKSPACE_TOO_SMALL; FA_ERR_CUDA. */
@@ -351,7 +355,8 @@ typedef struct {
   size_t workspace_bytes_used;
   size_t plan_upload_bytes;   /* bytes fa_decode_plan copies host -> device */
   int tensor_cores;           /* 1: per-page products on mma.sync, 0: CUDA cores */
-  int fused_merge;            /* 1: split requests merged inside the decode kernel */
+  int fused_merge;            /* 1: split requests merged inside the decode kernel, 0: by a
+                                 merge kernel after it */
   int q_len;                  /* query tokens per request (ragged plans: the most the
                                  kernel chosen holds) */
   int unified_max;            /* 1: fa_decode_run_unified_max is built for this plan */
@@ -470,9 +475,10 @@ int fa_decode_check(fa_decode_plan_t plan, void* cuda_stream, int* flags);
 
 /* Optional timing hook: when both events are non-NULL, later fa_decode_run
  * calls record ev_before on the stream just before the split-KV decode kernel
- * and ev_after just after it (both launches of a ragged plan in two buckets
- * lie between them; events are cudaEvent_t passed as void*, created by the
- * caller).  Pass NULLs to turn the hook off. */
+ * and ev_after once o and lse are complete: after that kernel, after the
+ * merge kernel where the plan has one (fa_decode_plan), after the last launch
+ * of a ragged plan in buckets (events are cudaEvent_t passed as void*, created
+ * by the caller).  Pass NULLs to turn the hook off. */
 int fa_decode_set_timing_events(fa_decode_plan_t plan, void* ev_before,
                                 void* ev_after);
 

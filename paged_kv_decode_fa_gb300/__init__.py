@@ -468,8 +468,9 @@ class DecodePlan:
         return int(flags.value)
 
     def set_timing_events(self, before, after) -> None:
-        """Record torch.cuda.Events around the decode kernel of later runs (both
-        launches of a ragged plan in two buckets; None = off).
+        """Record torch.cuda.Events around the launches of later runs: the decode
+        kernel, and the merge kernel or a ragged plan's other buckets where the
+        plan has them (None = off).
 
         torch creates an event lazily at its first record, so record each
         event once from torch before handing it over."""

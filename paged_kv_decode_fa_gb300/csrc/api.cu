@@ -1295,7 +1295,6 @@ int launch_decode(const LaunchView& lv, const void* q, const void* paged_kv, int
   cfg.attrs = attr;
   cfg.numAttrs = dependent_launch_ok(st, kern.func) ? 1 : 0;
   if (cudaLaunchKernelExC(&cfg, kern.func, args) != cudaSuccess) return FA_ERR_CUDA;
-  if (timed && cudaEventRecord(lv.ev_after, st) != cudaSuccess) return FA_ERR_CUDA;
   if (!lv.fused_merge && lv.num_merge > 0) {
     MergeParams mp;
     mp.merge = reinterpret_cast<const int32_t*>(ws + L.off_merge) +
@@ -1312,6 +1311,8 @@ int launch_decode(const LaunchView& lv, const void* q, const void* paged_kv, int
                          dim3((unsigned)D), margs, 0, st) != cudaSuccess)
       return FA_ERR_CUDA;
   }
+  // the fold belongs to the decode, whichever kernel does it
+  if (timed && cudaEventRecord(lv.ev_after, st) != cudaSuccess) return FA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
