@@ -235,6 +235,23 @@ def _stream_handle(stream) -> int | None:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _empty(shape, dtype, device, stream, **kw) -> torch.Tensor:
+    """A tensor that a call running on `stream` (None: the current one) writes.
+    It comes from that stream's memory: what the current stream has freed may
+    still be in use there.  And it is given back once the current stream, whose
+    caller gets it, is done with it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device, **kw)
+    if t.is_cuda:
+        t.record_stream(current)
+    return t
+
+
 def _host_i32(t) -> np.ndarray:
     if isinstance(t, torch.Tensor):
         if t.device.type == "cpu" and t.dtype == torch.int32 and t.is_contiguous():
@@ -343,7 +360,7 @@ class DecodePlan:
             k_scale: float = 1.0, v_scale: float = 1.0, out: torch.Tensor | None = None,
             lse: torch.Tensor | None = None, return_lse: bool = True, stream=None):
         """Decode attention; returns (o, lse) (lse None if return_lse is False)."""
-        out, lse = self._outputs(q, paged_kv, out, lse, return_lse)
+        out, lse = self._outputs(q, paged_kv, out, lse, return_lse, stream)
         _check(_L().fa_decode_run(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
             0.0 if sm_scale is None else float(sm_scale), float(k_scale), float(v_scale),
@@ -358,7 +375,7 @@ class DecodePlan:
         """Decode attention with the softmax referenced to a static bound
         `max_bound` on the logits sm_scale * k_scale * (q . k) instead of a
         running maximum (bf16 plans, groups 2/4/8); returns (o, lse)."""
-        out, lse = self._outputs(q, paged_kv, out, lse, return_lse)
+        out, lse = self._outputs(q, paged_kv, out, lse, return_lse, stream)
         _check(_L().fa_decode_run_unified_max(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
             0.0 if sm_scale is None else float(sm_scale), float(k_scale), float(v_scale),
@@ -377,7 +394,7 @@ class DecodePlan:
                     or not s.is_contiguous() or not s.is_cuda):
                 raise ValueError(f"scales must be contiguous float32 CUDA tensors "
                                  f"[{self.num_kv_heads}]")
-        out, lse = self._outputs(q, paged_kv, out, lse, return_lse)
+        out, lse = self._outputs(q, paged_kv, out, lse, return_lse, stream)
         _check(_L().fa_decode_run_head_scales(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
             0.0 if sm_scale is None else float(sm_scale), k_scales.data_ptr(),
@@ -392,7 +409,7 @@ class DecodePlan:
         """Decode over an E4M3 cache with one scale per block of tokens (a page)
         and kv head: k_scales / v_scales [num_pages, num_kv_heads] float32 CUDA
         tensors, as AppendPlan.run_block_scales writes them; returns (o, lse)."""
-        out, lse = self._outputs(q, paged_kv, out, lse, return_lse)
+        out, lse = self._outputs(q, paged_kv, out, lse, return_lse, stream)
         if paged_kv.get_device() != self._workspace.get_device():
             raise ValueError("paged_kv must be on the plan's device")
         _check_scales((k_scales, v_scales), (paged_kv.shape[0], self.num_kv_heads), paged_kv)
@@ -411,7 +428,7 @@ class DecodePlan:
                "fa_decode_unified_max_fallbacks")
         return int(n.value)
 
-    def _outputs(self, q, paged_kv, out, lse, return_lse):
+    def _outputs(self, q, paged_kv, out, lse, return_lse, stream):
         """Check q / paged_kv against the plan; allocate missing outputs."""
         if q.dtype is not self.q_dtype or paged_kv.dtype is not self.kv_dtype:
             raise TypeError("q / paged_kv dtype differs from the plan")
@@ -424,9 +441,9 @@ class DecodePlan:
                              "[num_pages, 2, page_size, num_kv_heads, head_dim]")
         pinned = {} if q.is_cuda else {"pin_memory": True}  # outputs follow q: device, or
         if out is None:                                     # page-locked host memory
-            out = torch.empty_like(q, **pinned)
+            out = _empty(self._q_shape, q.dtype, q.device, stream, **pinned)
         if return_lse and lse is None:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device, **pinned)
+            lse = _empty(self._q_shape[:-1], torch.float32, q.device, stream, **pinned)
         for t in (out, lse):
             if t is not None and (not _reachable(t) or not t.is_contiguous()):
                 raise ValueError("out / lse must be contiguous CUDA or page-locked tensors")
@@ -449,9 +466,9 @@ class DecodePlan:
         if tuple(q.shape) != (B, Hq, D) or not q.is_contiguous():
             raise ValueError(f"q must be a contiguous CUDA tensor [{B}, {Hq}, {D}]")
         if out is None:
-            out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+            out = _empty((B, Hq, D), q.dtype, q.device, stream)
         if return_lse and lse is None:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+            lse = _empty((B, Hq), torch.float32, q.device, stream)
         _check(_L().fa_decode_run_token_scales(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
             0.0 if sm_scale is None else float(sm_scale), k_scales.data_ptr(),
@@ -511,8 +528,8 @@ def plan(indptr, indices: torch.Tensor, last_page_len, num_qo_heads: int, num_kv
         raise ValueError("last_page_len shorter than the batch")
     _check_indices(indices, indptr_h, B)
     if workspace is None:
-        workspace = torch.empty(workspace_size(B, num_qo_heads, num_kv_heads, head_dim),
-                                dtype=torch.uint8, device=_cuda_device(indices))
+        workspace = _empty(workspace_size(B, num_qo_heads, num_kv_heads, head_dim), torch.uint8,
+                           _cuda_device(indices), stream)
     handle = ctypes.c_void_p()
     _check(_L().fa_decode_plan(
         indptr_p, indices.data_ptr() if indices.numel() else None,
@@ -546,7 +563,7 @@ def plan_multi_token(indptr, indices: torch.Tensor, last_page_len, q_len: int, n
             n = workspace_size(B, num_qo_heads * q_len, num_kv_heads, head_dim)
         if n == 0:
             raise ValueError("invalid shape or no CUDA device")
-        workspace = torch.empty(int(n), dtype=torch.uint8, device=_cuda_device(indices))
+        workspace = _empty(int(n), torch.uint8, _cuda_device(indices), stream)
     handle = ctypes.c_void_p()
     _check(_L().fa_decode_plan_multi_token(
         indptr_p, indices.data_ptr() if indices.numel() else None,
@@ -578,7 +595,7 @@ def plan_ragged_q(indptr, indices: torch.Tensor, last_page_len, qo_indptr, num_q
         n = _L().fa_decode_workspace_size_ragged_q(B, num_qo_heads, num_kv_heads, head_dim)
         if n == 0:
             raise ValueError("invalid shape or no CUDA device")
-        workspace = torch.empty(int(n), dtype=torch.uint8, device=_cuda_device(indices))
+        workspace = _empty(int(n), torch.uint8, _cuda_device(indices), stream)
     handle = ctypes.c_void_p()
     _check(_L().fa_decode_plan_ragged_q(
         indptr_p, indices.data_ptr() if indices.numel() else None,
@@ -610,8 +627,9 @@ def merge_states(o_a: torch.Tensor, lse_a: torch.Tensor, o_b: torch.Tensor, lse_
     if lse_a.dtype != torch.float32 or lse_b.dtype != torch.float32:
         raise TypeError("lse must be float32")
     n, H, D = o_a.shape
-    out = torch.empty_like(o_a) if out is None else out
-    lse_out = torch.empty_like(lse_a) if lse_out is None else lse_out
+    out = _empty(o_a.shape, o_a.dtype, o_a.device, stream) if out is None else out
+    if lse_out is None:
+        lse_out = _empty(lse_a.shape, lse_a.dtype, lse_a.device, stream)
     _check(_L().fa_merge_states(o_a.data_ptr(), lse_a.data_ptr(), o_b.data_ptr(),
                                 lse_b.data_ptr(), out.data_ptr(), lse_out.data_ptr(), n, H, D,
                                 _dtype_code(o_a.dtype), _stream_handle(stream)),
@@ -714,7 +732,7 @@ class CascadePlan:
             lse: torch.Tensor | None = None, return_lse: bool = True, stream=None):
         """Cascade decode; k_scale / v_scale are an E4M3 cache's per-tensor
         scales (1 for a 16-bit cache)."""
-        out, lse = self._outputs(q, paged_kv, out, lse, return_lse)
+        out, lse = self._outputs(q, paged_kv, out, lse, return_lse, stream)
         _check(_L().fa_cascade_run_scaled(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
             0.0 if sm_scale is None else float(sm_scale), float(k_scale), float(v_scale),
@@ -735,7 +753,7 @@ class CascadePlan:
         if paged_kv.shape[1:] != want or paged_kv.get_device() != self._keep[-1].get_device():
             raise ValueError(f"paged_kv must be [num_pages, {', '.join(map(str, want))}] on the "
                              "plan's device")
-        out, lse = self._outputs(q, paged_kv, out, lse, return_lse)
+        out, lse = self._outputs(q, paged_kv, out, lse, return_lse, stream)
         _check_scales((k_scales, v_scales), (paged_kv.shape[0], self.num_kv_heads), paged_kv)
         _check(_L().fa_cascade_run_block_scales(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
@@ -744,7 +762,7 @@ class CascadePlan:
             _stream_handle(stream)), "fa_cascade_run_block_scales")
         return out, lse
 
-    def _outputs(self, q, paged_kv, out, lse, return_lse):
+    def _outputs(self, q, paged_kv, out, lse, return_lse, stream):
         """Check q / paged_kv against the plan; allocate missing outputs."""
         B, Hq, D = self.batch, self.num_qo_heads, self.head_dim
         if q.dtype != self.q_dtype or paged_kv.dtype != self.kv_dtype:
@@ -752,9 +770,9 @@ class CascadePlan:
         if tuple(q.shape) != (B, Hq, D) or not q.is_contiguous() or not paged_kv.is_contiguous():
             raise ValueError(f"q must be a contiguous CUDA tensor [{B}, {Hq}, {D}]")
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty((B, Hq, D), q.dtype, q.device, stream)
         if return_lse and lse is None:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+            lse = _empty((B, Hq), torch.float32, q.device, stream)
         return out, lse
 
     def set_timing_events(self, before, after) -> None:
@@ -790,7 +808,7 @@ def cascade_plan(prefix_indices: torch.Tensor, indptr, indices: torch.Tensor, la
         n = _L().fa_cascade_workspace_size(B, num_qo_heads, num_kv_heads, head_dim)
         if n == 0:
             raise ValueError("invalid shape or no CUDA device")
-        workspace = torch.empty(int(n), dtype=torch.uint8, device=prefix_indices.device)
+        workspace = _empty(int(n), torch.uint8, prefix_indices.device, stream)
     handle = ctypes.c_void_p()
     kv_data_type = q_data_type if kv_data_type is None else kv_data_type
     _check(_L().fa_cascade_plan(
@@ -865,7 +883,7 @@ class AppendPlan:
         strides free) to the cache; with q [num_tokens, Hq, D], also rotate it
         and return it (in q_out, contiguous; q itself to rotate in place).
         k_scale / v_scale are an E4M3 cache's per-tensor scales."""
-        rows, q_out, out = self._rows(k, v, paged_kv, q, q_out)
+        rows, q_out, out = self._rows(k, v, paged_kv, q, q_out, stream)
         at = ctypes.addressof(rows)
         _check(_L().fa_append_run(
             self._h, at, at + _ROWS_BYTES, at + 2 * _ROWS_BYTES if q is not None else None, out,
@@ -913,7 +931,7 @@ class AppendPlan:
         return int(flags.value)
 
     def _run_scales(self, name, shape, k, v, paged_kv, k_scales, v_scales, q, q_out, stream):
-        rows, q_out, out = self._rows(k, v, paged_kv, q, q_out)
+        rows, q_out, out = self._rows(k, v, paged_kv, q, q_out, stream)
         _check_scales((k_scales, v_scales), shape, paged_kv)
         at = ctypes.addressof(rows)
         _check(getattr(_L(), name)(
@@ -922,7 +940,7 @@ class AppendPlan:
             _stream_handle(stream)), name)
         return q_out
 
-    def _rows(self, k, v, paged_kv, q, q_out):
+    def _rows(self, k, v, paged_kv, q, q_out, stream):
         """Check the tensors against the plan; fa_rows of k, v and q, q_out, its
         address (None without q)."""
         if paged_kv.dtype is not self.kv_dtype:
@@ -941,7 +959,7 @@ class AppendPlan:
             rows = _Rows3(*self._row(k, self._kv_shape), *self._row(v, self._kv_shape),
                           *self._row(q, self._q_shape))
         if q_out is None:
-            q_out = torch.empty(self._q_shape, dtype=q.dtype, device=q.device)
+            q_out = _empty(self._q_shape, q.dtype, q.device, stream)
         elif (q_out.dtype is not q.dtype or q_out.shape != self._q_shape
               or not q_out.is_contiguous() or q_out.get_device() != self._device):
             raise ValueError(f"q_out must be a contiguous tensor {list(self._q_shape)} of q's "
@@ -1016,8 +1034,8 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
                                   or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the current device")
     if workspace is None:
-        workspace = torch.empty(append_workspace_size(max(B, 0), max(total, 0)),
-                                dtype=torch.uint8, device=_cuda_device(indices))
+        workspace = _empty(append_workspace_size(max(B, 0), max(total, 0)), torch.uint8,
+                           _cuda_device(indices), stream)
     handle = ctypes.c_void_p()
     _check(_L().fa_append_plan(
         indptr_p, indices.data_ptr() if indices.numel() else None, last_p if B else None, app_p,
