@@ -410,8 +410,12 @@ class DecodePlan:
         and kv head: k_scales / v_scales [num_pages, num_kv_heads] float32 CUDA
         tensors, as AppendPlan.run_block_scales writes them; returns (o, lse)."""
         out, lse = self._outputs(q, paged_kv, out, lse, return_lse, stream)
-        if paged_kv.get_device() != self._workspace.get_device():
+        device = self._workspace.get_device()
+        if paged_kv.get_device() != device:
             raise ValueError("paged_kv must be on the plan's device")
+        for t in (q, out, lse):
+            if t is not None and t.is_cuda and t.get_device() != device:
+                raise ValueError("q / out / lse must be on the plan's device, or page-locked")
         _check_scales((k_scales, v_scales), (paged_kv.shape[0], self.num_kv_heads), paged_kv)
         _check(_L().fa_decode_run_block_scales(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
@@ -447,6 +451,7 @@ class DecodePlan:
         for t in (out, lse):
             if t is not None and (not _reachable(t) or not t.is_contiguous()):
                 raise ValueError("out / lse must be contiguous CUDA or page-locked tensors")
+        _check_room(q, self.head_dim, out, lse)
         return out, lse
 
     def run_token_scales(self, q: torch.Tensor, paged_kv: torch.Tensor, k_scales: torch.Tensor,
@@ -469,6 +474,7 @@ class DecodePlan:
             out = _empty((B, Hq, D), q.dtype, q.device, stream)
         if return_lse and lse is None:
             lse = _empty((B, Hq), torch.float32, q.device, stream)
+        _check_room(q, D, out, lse)
         _check(_L().fa_decode_run_token_scales(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
             0.0 if sm_scale is None else float(sm_scale), k_scales.data_ptr(),
@@ -493,6 +499,13 @@ class DecodePlan:
         event once from torch before handing it over."""
         _check(_L().fa_decode_set_timing_events(self._h, *_event_handles(before, after)),
                "fa_decode_set_timing_events")
+
+
+def _check_room(q, head_dim, out, lse) -> None:
+    """out takes q's bytes, lse a float per row of q."""
+    if out.nbytes < q.nbytes or (lse is not None and lse.nbytes < q.numel() // head_dim * 4):
+        raise ValueError(f"out must hold {q.numel()} elements of q's dtype, lse "
+                         f"{q.numel() // head_dim} float32")
 
 
 def _check_scales(scales, shape, paged_kv) -> None:
@@ -773,6 +786,7 @@ class CascadePlan:
             out = _empty((B, Hq, D), q.dtype, q.device, stream)
         if return_lse and lse is None:
             lse = _empty((B, Hq), torch.float32, q.device, stream)
+        _check_room(q, D, out, lse)
         return out, lse
 
     def set_timing_events(self, before, after) -> None:
