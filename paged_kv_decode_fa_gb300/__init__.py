@@ -1040,6 +1040,12 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
         if n_off != B:
             raise ValueError("position_offset must have one value per request")
     _check_indices(indices, indptr_h, B)
+    freq = None
+    if rotary is not None:
+        # the call reads rotary_dim / 2 doubles of it
+        freq = np.ascontiguousarray(rotary.inv_freq, dtype=np.float64)
+        if freq.shape != (rotary.rotary_dim // 2,):
+            raise ValueError("rotary.inv_freq must have rotary_dim / 2 values")
     total = int(np.asarray(app_h)[B]) if B >= 0 else 0
     device = torch.cuda.current_device()
     if indices.is_cuda and indices.get_device() != device:
@@ -1054,7 +1060,7 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
     _check(_L().fa_append_plan(
         indptr_p, indices.data_ptr() if indices.numel() else None, last_p if B else None, app_p,
         off_p, B, num_qo_heads, num_kv_heads, head_dim, page_size, _dtype_code(q_data_type),
-        _dtype_code(kv_data_type), rotary.inv_freq.ctypes.data if rotary else None,
+        _dtype_code(kv_data_type), freq.ctypes.data if rotary else None,
         rotary.rotary_dim if rotary else 0, int(rotary.interleaved) if rotary else 0,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _stream_handle(stream), ctypes.byref(handle)), "fa_append_plan")

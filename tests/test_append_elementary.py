@@ -124,3 +124,17 @@ def test_a_step_gives_the_attention_the_same_inputs(lib, cuda):
         page, slot = where(b, cuda)
         assert differing(q, rotated(b.q, pos, rot).to(BF16)) <= 1
         assert differing(b.kv[page, 0, slot], rotated(b.k, pos, rot).to(BF16)) <= 1
+
+
+def test_a_table_changed_after_its_making(lib, cuda):
+    """A RotaryTable whose frequencies were put in another type is read as doubles
+    all the same, and one of another length is refused."""
+    b = Batch([3, 0], [5, 20], 8, 2, 128, F32, F32, seed=6)
+    rot = lib.RotaryTable(128)
+    rot.inv_freq = rot.inv_freq.astype(np.float32)
+    q = b.plan(lib, rot).run(b.k, b.v, b.kv, q=b.q)
+    same = lib.RotaryTable(128, inv_freq=rot.inv_freq.astype(np.float64))
+    assert torch.equal(q, b.plan(lib, same).run(b.k, b.v, b.kv, q=b.q))
+    rot.inv_freq = rot.inv_freq[:32]
+    with pytest.raises(ValueError):
+        b.plan(lib, rot)
