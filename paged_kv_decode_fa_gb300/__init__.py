@@ -279,13 +279,18 @@ def _reachable(t: torch.Tensor) -> bool:
     return t.is_cuda or t.is_pinned()
 
 
-def _check_indices(indices: torch.Tensor, indptr, batch: int) -> None:
+def _i32_at(address: int, i: int) -> int:
+    """Element i of a host int32 array (indexing a tensor takes 3 us of a plan)."""
+    return ctypes.c_int32.from_address(address + 4 * i).value
+
+
+def _check_indices(indices: torch.Tensor, indptr: int, batch: int) -> None:
     """The page table of a batch: the kernels read indptr[batch] entries of it."""
     if indices.dtype != torch.int32 or not _reachable(indices) or not indices.is_contiguous():
         raise ValueError("indices must be a contiguous int32 CUDA or page-locked tensor")
-    if batch > 0 and indices.numel() < int(indptr[batch]):
+    if batch > 0 and indices.numel() < _i32_at(indptr, batch):
         raise ValueError(f"indices holds {indices.numel()} pages, indptr asks for "
-                         f"{int(indptr[batch])}")
+                         f"{_i32_at(indptr, batch)}")
 
 
 def _cuda_device(t: torch.Tensor) -> torch.device:
@@ -413,9 +418,9 @@ class DecodePlan:
         device = self._workspace.get_device()
         if paged_kv.get_device() != device:
             raise ValueError("paged_kv must be on the plan's device")
-        for t in (q, out, lse):
-            if t is not None and t.is_cuda and t.get_device() != device:
-                raise ValueError("q / out / lse must be on the plan's device, or page-locked")
+        if ((q.get_device() != device and q.is_cuda) or (out.get_device() != device and out.is_cuda)
+                or (lse is not None and lse.get_device() != device and lse.is_cuda)):
+            raise ValueError("q / out / lse must be on the plan's device, or page-locked")
         _check_scales((k_scales, v_scales), (paged_kv.shape[0], self.num_kv_heads), paged_kv)
         _check(_L().fa_decode_run_block_scales(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
@@ -444,14 +449,19 @@ class DecodePlan:
             raise ValueError("paged_kv must be a contiguous CUDA tensor "
                              "[num_pages, 2, page_size, num_kv_heads, head_dim]")
         pinned = {} if q.is_cuda else {"pin_memory": True}  # outputs follow q: device, or
-        if out is None:                                     # page-locked host memory
-            out = _empty(self._q_shape, q.dtype, q.device, stream, **pinned)
-        if return_lse and lse is None:
-            lse = _empty(self._q_shape[:-1], torch.float32, q.device, stream, **pinned)
+        if out is not None:                                 # page-locked host memory
+            _room(out, q.nbytes)
+        elif stream is None:
+            out = torch.empty_like(q, **pinned)
+        else:
+            out = _empty(q.shape, q.dtype, q.device, stream, **pinned)
+        if lse is not None:
+            _room(lse, q.numel() // self.head_dim * 4)
+        elif return_lse:
+            lse = _empty(q.shape[:-1], torch.float32, q.device, stream, **pinned)
         for t in (out, lse):
             if t is not None and (not _reachable(t) or not t.is_contiguous()):
                 raise ValueError("out / lse must be contiguous CUDA or page-locked tensors")
-        _check_room(q, self.head_dim, out, lse)
         return out, lse
 
     def run_token_scales(self, q: torch.Tensor, paged_kv: torch.Tensor, k_scales: torch.Tensor,
@@ -474,7 +484,9 @@ class DecodePlan:
             out = _empty((B, Hq, D), q.dtype, q.device, stream)
         if return_lse and lse is None:
             lse = _empty((B, Hq), torch.float32, q.device, stream)
-        _check_room(q, D, out, lse)
+        _room(out, q.nbytes)
+        if lse is not None:
+            _room(lse, B * Hq * 4)
         _check(_L().fa_decode_run_token_scales(
             self._h, q.data_ptr(), paged_kv.data_ptr(), paged_kv.shape[0],
             0.0 if sm_scale is None else float(sm_scale), k_scales.data_ptr(),
@@ -501,11 +513,11 @@ class DecodePlan:
                "fa_decode_set_timing_events")
 
 
-def _check_room(q, head_dim, out, lse) -> None:
-    """out takes q's bytes, lse a float per row of q."""
-    if out.nbytes < q.nbytes or (lse is not None and lse.nbytes < q.numel() // head_dim * 4):
-        raise ValueError(f"out must hold {q.numel()} elements of q's dtype, lse "
-                         f"{q.numel() // head_dim} float32")
+def _room(t, nbytes) -> torch.Tensor:
+    """An output of the caller's, if it holds what a run writes."""
+    if t.nbytes < nbytes:
+        raise ValueError(f"out / lse too small: {t.nbytes} bytes, a run writes {nbytes}")
+    return t
 
 
 def _check_scales(scales, shape, paged_kv) -> None:
@@ -539,7 +551,7 @@ def plan(indptr, indices: torch.Tensor, last_page_len, num_qo_heads: int, num_kv
     B = n_indptr - 1
     if n_last < B:
         raise ValueError("last_page_len shorter than the batch")
-    _check_indices(indices, indptr_h, B)
+    _check_indices(indices, indptr_p, B)
     if workspace is None:
         workspace = _empty(workspace_size(B, num_qo_heads, num_kv_heads, head_dim), torch.uint8,
                            _cuda_device(indices), stream)
@@ -568,7 +580,7 @@ def plan_multi_token(indptr, indices: torch.Tensor, last_page_len, q_len: int, n
     B = n_indptr - 1
     if n_last < B:
         raise ValueError("last_page_len shorter than the batch")
-    _check_indices(indices, indptr_h, B)
+    _check_indices(indices, indptr_p, B)
     if workspace is None:
         if (num_qo_heads // max(1, num_kv_heads)) * q_len > 8:   # the ragged-q kernels
             n = _L().fa_decode_workspace_size_ragged_q(B, num_qo_heads, num_kv_heads, head_dim)
@@ -603,7 +615,7 @@ def plan_ragged_q(indptr, indices: torch.Tensor, last_page_len, qo_indptr, num_q
     B = n_indptr - 1
     if n_last < B or n_qo != B + 1:
         raise ValueError("last_page_len shorter than the batch, or qo_indptr not batch + 1 long")
-    _check_indices(indices, indptr_h, B)
+    _check_indices(indices, indptr_p, B)
     if workspace is None:
         n = _L().fa_decode_workspace_size_ragged_q(B, num_qo_heads, num_kv_heads, head_dim)
         if n == 0:
@@ -786,7 +798,9 @@ class CascadePlan:
             out = _empty((B, Hq, D), q.dtype, q.device, stream)
         if return_lse and lse is None:
             lse = _empty((B, Hq), torch.float32, q.device, stream)
-        _check_room(q, D, out, lse)
+        _room(out, q.nbytes)
+        if lse is not None:
+            _room(lse, B * Hq * 4)
         return out, lse
 
     def set_timing_events(self, before, after) -> None:
@@ -817,7 +831,7 @@ def cascade_plan(prefix_indices: torch.Tensor, indptr, indices: torch.Tensor, la
     for t in (prefix_indices, indices):
         if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
             raise ValueError("index arrays must be contiguous int32 CUDA tensors")
-    _check_indices(indices, indptr_h, B)
+    _check_indices(indices, indptr_p, B)
     if workspace is None:
         n = _L().fa_cascade_workspace_size(B, num_qo_heads, num_kv_heads, head_dim)
         if n == 0:
@@ -1039,14 +1053,14 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
         off_h, off_p, n_off = _host_i32_ptr(position_offset)
         if n_off != B:
             raise ValueError("position_offset must have one value per request")
-    _check_indices(indices, indptr_h, B)
+    _check_indices(indices, indptr_p, B)
     freq = None
     if rotary is not None:
         # the call reads rotary_dim / 2 doubles of it
         freq = np.ascontiguousarray(rotary.inv_freq, dtype=np.float64)
         if freq.shape != (rotary.rotary_dim // 2,):
             raise ValueError("rotary.inv_freq must have rotary_dim / 2 values")
-    total = int(np.asarray(app_h)[B]) if B >= 0 else 0
+    total = _i32_at(app_p, B) if B >= 0 else 0
     device = torch.cuda.current_device()
     if indices.is_cuda and indices.get_device() != device:
         raise ValueError("indices must be on the current device")
