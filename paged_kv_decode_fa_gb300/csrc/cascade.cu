@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW, SC>::THREADS)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
   float m_r[2] = {-INFINITY, -INFINITY}, d_r[2] = {0.f, 0.f};  // rows g, g+8
-  float vref = 0.f, vref_inv = 0.f;  // per-block scales: the V scale o is in units of
+  BlockReference ref;  // per-block scales: what o is in units of
   bool aborted = false;
   const uint32_t ring_addr = dev::smem_addr(ring);
 
@@ -225,9 +225,9 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW, SC>::THREADS)
       const float2 bs =
           *(reinterpret_cast<const float2*>(smem + C::OFF_SCALES) + k % kBlockScaleRing);
       page_qscale *= bs.x;
-      wf = bs.y * vref_inv;
+      wf = bs.y * ref.inverse;
       if (!block_weight_inside(wf, bs.y))
-        wf = move_block_reference(bs.y, wf, o, &vref, &vref_inv);
+        wf = move_block_reference(bs.y, wf, o, &ref);
     }
 
     // ---- S[rows][tokens]: n-tile 0 = tokens 0..7 (K row g), 1 = tokens 8..15;
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW, SC>::THREADS)
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {
     if (rows[rr] >= row_count) continue;
-    const float inv = d_r[rr] > 0.f ? (BS ? vref : pp.v_scale) / d_r[rr] : 0.f;
+    const float inv = d_r[rr] > 0.f ? (BS ? ref.at : pp.v_scale) / d_r[rr] : 0.f;
     float* dst = pp.part_o + ((size_t)out_item * kPrefixRows + rows[rr]) * D;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {

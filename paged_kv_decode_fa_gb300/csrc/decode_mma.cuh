@@ -250,39 +250,32 @@ __device__ __forceinline__ bool block_weight_inside(float wf, float v_scale) {
   return wf <= 128.f && (wf >= 1.f || v_scale == 0.f);
 }
 
+struct BlockReference {
+  float at = 0.f, inverse = 0.f;  // 0 before the first page with a scale
+  float top = 0.f;                // the largest so far
+};
+
 // Move the reference for a page outside the window and rescale o (exactly where
-// the scales are powers of two); returns the page's factor.  The reference falls
-// no further than leaves o below 2^120: where the sums so far are of values 2^64
-// times this page's and more, its weights lose low bits instead, an
-// absolute error below 2^-64 of those values.
+// the scales are powers of two); returns the page's factor.  The reference stays
+// above 2^-70 of the largest so far: a token adds less than 2^24 to o in units of
+// the reference of its time, so that o stays finite, and a page further down
+// loses low bits of its weights instead, an absolute error below 2^-64 of the
+// larger values.  (A bound from o itself, by a reduction over it, took the
+// prefix kernel of 2048 shared pages from 1452 to 1590 us.)
 template <int N>
 __device__ __forceinline__ float move_block_reference(float v_scale, float wf, float (&o)[N][4],
-                                                      float* vref, float* vref_inv) {
-  const float below = *vref == 0.f ? 1.f / 16 : wf > 128.f ? 1.f / 64 : 1.f / 2;
-  float to = fmaxf(v_scale * below, 1.17549435e-38f);  // a normal number: so is its inverse
-  float inv = 1.f / to, f = *vref * inv;
-  if (f > 1.f) {
-    float top = 0.f;
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(o[n][e]));
-    const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-    const int room = min(119 - ((int)(bits >> 23) - 127), 126);  // top * 2^room < 2^120
-    if (bits == 0u) {
-      f = 0.f;  // nothing to rescale (f itself may be infinite)
-    } else if (f > ldexpf(1.f, room)) {
-      f = ldexpf(1.f, max(room, 0));
-      to = *vref / f;
-      inv = *vref_inv * f;
-    }
-  }
+                                                      BlockReference* ref) {
+  const float below = ref->at == 0.f ? 1.f / 16 : wf > 128.f ? 1.f / 64 : 1.f / 2;
+  const float to = fmaxf(fmaxf(v_scale * below, ref->top * 8.470329e-22f),  // 2^-70
+                         1.17549435e-38f);  // a normal number: so is its inverse
+  const float inv = 1.f / to, f = ref->at * inv;
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[n][e] *= f;
-  *vref = to;
-  *vref_inv = inv;
+  ref->at = to;
+  ref->inverse = inv;
+  ref->top = fmaxf(ref->top, to);
   return v_scale * inv;
 }
 
@@ -486,7 +479,7 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
     // several pages leaves it alone, so that they share one test and no branch
     // lies between their MMAs: where a scale is outside, they are taken one at
     // a time.
-    float vref = 0.f, vref_inv = 0.f;
+    BlockReference ref;
 
     // ---- O^T[dim][head] += V^T . P^T for one page (stage address st).
     // Slots past the last valid token may hold anything (NaN included): a
@@ -609,12 +602,12 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
                               (k + u * PS) % kBlockScaleRing);
           ks[u] = bs.x;
           v_scale = bs.y;
-          wf[u] = bs.y * vref_inv;
+          wf[u] = bs.y * ref.inverse;
           inside = inside && block_weight_inside(wf[u], bs.y);
         }
         if (!inside) {
           if (NPP > 1) return false;
-          wf[0] = move_block_reference(v_scale, wf[0], o, &vref, &vref_inv);
+          wf[0] = move_block_reference(v_scale, wf[0], o, &ref);
         }
       }
       const int sw = C::SWZ == 128 ? (g & 7) : ((g >> 1) & 3);  // swizzle of rows g and g+8
@@ -864,8 +857,8 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
         for (int mt = 0; mt < MTILES; ++mt) {
           const int dlo = kFp8 ? mt * 16 + 2 * g : mt * 16 + g;
           const int dhi = kFp8 ? mt * 16 + 2 * g + 1 : mt * 16 + g + 8;
-          mo[(srow * NC + h) * D + dlo] = BS ? o[mt][e] * vref : o[mt][e];
-          mo[(srow * NC + h) * D + dhi] = BS ? o[mt][2 + e] * vref : o[mt][2 + e];
+          mo[(srow * NC + h) * D + dlo] = BS ? o[mt][e] * ref.at : o[mt][e];
+          mo[(srow * NC + h) * D + dhi] = BS ? o[mt][2 + e] * ref.at : o[mt][2 + e];
         }
         if (g == 0) {
           mm[srow * NC + h] = m_h[e];
