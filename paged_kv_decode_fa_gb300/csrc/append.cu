@@ -31,12 +31,12 @@
 // inputs.
 //
 // What bounds it (us per launch in a CUDA graph).  Long appends are bound by HBM:
-// 779 MB of prompts (32 / 8 heads, head_dim 128, bf16, q included) in 119.9 us =
+// 779 MB of prompts (32 / 8 heads, head_dim 128, bf16, q included) in 120.0 us =
 // 6.5 TB/s, 0.97 of the copy rate; 910 MB into a block-scaled cache (64 / 8 heads) in
-// 153.6 us = 5.9 TB/s, 0.89, where a run passes two more barriers around the
+// 152.3 us = 6.0 TB/s, 0.90, where a run passes two more barriers around the
 // conversions.  Single tokens are bound by the launch and one chain of loads
 // (unit, rows and page id, the page's scale): 4 tokens 2.6 us, 450 tokens 3.3 us,
-// 128 tokens into a block-scaled cache 4.7 us.
+// 128 tokens into a block-scaled cache 4.6 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -219,7 +219,9 @@ struct Turn {
 // Products and sums are rounded one by one, as elementary operations round
 // them: an element fused into one rounding would differ from theirs in fp32's last
 // bit, and now and then in the type it is stored in.  (Scalar, since the assembler
-// fuses add.rn.f32x2 with a product of mul.rn.f32x2.)
+// fuses add.rn.f32x2 with a product of mul.rn.f32x2.  The products' order was
+// timed: block-scaled prompts of 27476 tokens 177.7 us for 179.6, interleaved
+// ones 172.6 for 180.6, the others the same or 2 us less.)
 template <bool INTERLEAVED>
 __device__ __forceinline__ void rotate(const Turn& r, Piece* x) {
   if (!r.on) return;
@@ -229,12 +231,15 @@ __device__ __forceinline__ void rotate(const Turn& r, Piece* x) {
       float* y = j < 4 ? x->a : x->b;
       const int e = 2 * (j % 4);
       const float u = y[e], v = y[e + 1];
+      const float us = __fmul_rn(u, r.s[j]);
       y[e] = __fsub_rn(__fmul_rn(u, r.c[j]), __fmul_rn(v, r.s[j]));
-      y[e + 1] = __fadd_rn(__fmul_rn(v, r.c[j]), __fmul_rn(u, r.s[j]));
+      y[e + 1] = __fadd_rn(__fmul_rn(v, r.c[j]), us);
     } else {
       const float u = x->a[j], v = x->b[j];
-      x->a[j] = __fsub_rn(__fmul_rn(u, r.c[j]), __fmul_rn(v, r.s[j]));
-      x->b[j] = __fadd_rn(__fmul_rn(v, r.c[j]), __fmul_rn(u, r.s[j]));
+      const float vs = __fmul_rn(v, r.s[j]), us = __fmul_rn(u, r.s[j]);
+      const float uc = __fmul_rn(u, r.c[j]), vc = __fmul_rn(v, r.c[j]);
+      x->a[j] = __fsub_rn(uc, vs);
+      x->b[j] = __fadd_rn(vc, us);
     }
   }
 }
@@ -506,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
   auto write = [&](Piece x, bool is_k, const Group<T>(&raw)[2], int h, bool ok) {
     float inv = 1.f, scale = 1.f;
     if constexpr (MODE != kNative) {
-      // the block form has its amax already: 154.5 us for 155.9 without the second look
+      // the block form has its amax already: 155.3 us for 155.9 without the second look
       const float m = MODE != kBlock || infinite ? finite_amax(&x, &infinite) : 0.f;
       if constexpr (MODE == kStatic) {
         const float* hs = is_k ? p.head_k_scales : p.head_v_scales;
