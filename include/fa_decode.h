@@ -108,7 +108,7 @@ size_t fa_decode_workspace_size(int batch, int num_qo_heads, int num_kv_heads,
  * A request that the plan cuts into pieces is folded by the decode kernel
  * itself, or, where a unit's pieces times its columns (query heads of a kv head x
  * query tokens) pass 320, all such units by a second launch, a merge kernel
- * (fa_plan_info: fused_merge 0): the same sums, faster for few long requests.
+ * (fused_merge 0 in fa_decode_plan_info): the same sums, faster for few long requests.
  * Errors: FA_ERR_INVALID_ARG for a malformed indptr or last_page_len, NULL
  * pointers or non-positive sizes; FA_ERR_UNSUPPORTED for shapes or types that
  * are not built; FA_ERR_WORKSPACE_TOO_SMALL; FA_ERR_CUDA. */
