@@ -243,7 +243,9 @@ def _empty(shape, dtype, device, stream, **kw) -> torch.Tensor:
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device, **kw)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        # (an ExternalStream of the null handle would be a new stream)
+        stream = (torch.cuda.ExternalStream(int(stream)) if int(stream)
+                  else torch.cuda.default_stream())
     current = torch.cuda.current_stream()
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device, **kw)

@@ -87,3 +87,23 @@ def test_output_is_not_reused_while_the_current_stream_reads_it(lib, cuda):
     assert again.data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(kept, want)
+
+
+def test_the_null_handle_is_the_default_stream(lib, cuda):
+    """stream=0 from within another stream: the default stream's memory (a block it
+    freed is the first one to be taken again), not some new stream's."""
+    call = calls(lib, cuda)["decode block"]
+    want = call(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(40):                       # more than torch has streams to hand out
+        x = torch.empty(want.shape, dtype=want.dtype, device=cuda)
+        at = x.data_ptr()
+        del x
+        with torch.cuda.stream(side):
+            got = call(0)
+        assert got.data_ptr() == at
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del got
+        torch.cuda.synchronize()
