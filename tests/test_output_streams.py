@@ -107,3 +107,26 @@ def test_the_null_handle_is_the_default_stream(lib, cuda):
         assert torch.equal(got, want)
         del got
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("forked", [False, True])
+@pytest.mark.parametrize("name", ["append block", "decode block", "cascade block", "merge"])
+def test_outputs_made_in_a_captured_call(lib, cuda, name, forked):
+    """stream= the capturing stream, or one forked from it, without outputs."""
+    call = calls(lib, cuda)[name]
+    want = call(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        if forked:
+            side.wait_stream(here)
+        got = call(side if forked else here)
+        if forked:
+            here.wait_stream(side)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        got.zero_()
