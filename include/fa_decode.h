@@ -231,6 +231,10 @@ int fa_decode_run(fa_decode_plan_t plan, const void* q, const void* paged_kv,
  *  k_scales, v_scales  [num_pages, num_kv_heads, page_size] float32, device,
  *                      16-byte aligned: the K (V) element at page p, slot t,
  *                      kv head h has the value code * scales[(p*Hkv + h)*P + t].
+ *                      A scale is 0 or a positive normal number, of any size; a
+ *                      token whose V scale is 2^12 and more below that of
+ *                      another in its page loses low bits of its values, at most
+ *                      2^-23 of the larger ones (2^-64 of those of other pages).
  * Other arguments as fa_decode_run (sm_scale <= 0 selects 1/sqrt(head_dim)).
  * Built for head_dim 128 and groups 2, 4, 8 (the tensor-core consumer); other
  * plans return FA_ERR_UNSUPPORTED, as do plans whose kv dtype is not E4M3. */

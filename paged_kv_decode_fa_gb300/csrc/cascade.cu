@@ -225,9 +225,11 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW, SC>::THREADS)
       const float2 bs =
           *(reinterpret_cast<const float2*>(smem + C::OFF_SCALES) + k % kBlockScaleRing);
       page_qscale *= bs.x;
-      wf = bs.y * ref.inverse;
-      if (!block_weight_inside(wf, bs.y))
-        wf = move_block_reference(bs.y, wf, o, &ref);
+      wf = bs.y * ref.inverse();
+      if (!block_weight_inside(wf, bs.y)) {
+        move_block_reference(bs.y, block_reference_below(wf), o, &ref);
+        wf = bs.y * ref.inverse();
+      }
     }
 
     // ---- S[rows][tokens]: n-tile 0 = tokens 0..7 (K row g), 1 = tokens 8..15;
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(PrefixCfg<KVT, D, NW, SC>::THREADS)
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {
     if (rows[rr] >= row_count) continue;
-    const float inv = d_r[rr] > 0.f ? (BS ? ref.at : pp.v_scale) / d_r[rr] : 0.f;
+    const float inv = d_r[rr] > 0.f ? (BS ? ref.at() : pp.v_scale) / d_r[rr] : 0.f;
     float* dst = pp.part_o + ((size_t)out_item * kPrefixRows + rows[rr]) * D;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {

@@ -239,44 +239,56 @@ constexpr float kLazyAbove = 8.f;
 // scores and release the stage then, instead of after P.V.
 constexpr bool kEarlyVRelease = true;
 
-// Per-block V scales.  o is kept in units of a reference, and a page's weights
-// enter P.V times wf, its scale over the reference.  The weights are f16 and at
-// most 2^8 before that factor: with wf in [1, 2^7] they stay below 2^15, and low
-// ones (2^-25 is lost, 2^-14 the last of full precision) are kept as far down as a
-// per-tensor scale keeps them, whatever scales ignored pages have.  The reference
+// Per-block V scales (and per-token ones, a page's largest standing for it).  o is
+// kept in units of a reference, and a page's weights enter P.V times wf, its
+// scale over the reference.  The weights are f16 and at most 2^8 before that
+// factor: with wf in [1, 2^7] they stay below 2^15, and low ones (2^-25 is lost,
+// 2^-14 the last of full precision) are kept as far down as a per-tensor scale
+// keeps them, whatever scales ignored pages have.  The reference
 // moves when a page leaves that window, by little more than it has to, so
 // that scales within 2^7 of one another soon lie inside it for good.
 __device__ __forceinline__ bool block_weight_inside(float wf, float v_scale) {
   return wf <= 128.f && (wf >= 1.f || v_scale == 0.f);
 }
 
+// A reference and the largest so far, both powers of two, in one register: the
+// float and the other's exponent under it.  (The kernels are held to 96 registers:
+// with three for this, and more of theirs spilled, attend over 128 requests
+// of 1024-8192 tokens took 191 us for 186.)  It starts at the smallest normal number,
+// with o still 0.
 struct BlockReference {
-  float at = 0.f, inverse = 0.f;  // 0 before the first page with a scale
-  float top = 0.f;                // the largest so far
+  uint32_t bits = 0x00800001u;
+  __device__ __forceinline__ float at() const { return __uint_as_float(bits & 0x7f800000u); }
+  __device__ __forceinline__ float inverse() const {
+    return __uint_as_float(0x7f000000u - (bits & 0x7f800000u));
+  }
+  __device__ __forceinline__ float top() const { return __uint_as_float(bits << 23); }
 };
 
-// Move the reference for a page outside the window and rescale o (exactly where
-// the scales are powers of two); returns the page's factor.  The reference stays
-// above 2^-70 of the largest so far: a token adds less than 2^24 to o in units of
-// the reference of its time, so that o stays finite, and a page further down
+// Where the reference goes, as a fraction of the scale of a page with factor wf.
+__device__ __forceinline__ float block_reference_below(float wf) {
+  return wf > 128.f ? 1.f / 32 : 1.f / 2;
+}
+
+// Move the reference for a page outside the window and rescale o, exactly.
+// It stays above 2^-70 of the largest so far: a token adds less than 2^24 to o in units
+// of the reference of its time, so that o stays finite, and a page further down
 // loses low bits of its weights instead, an absolute error below 2^-64 of the
 // larger values.  (A bound from o itself, by a reduction over it, took the
 // prefix kernel of 2048 shared pages from 1452 to 1590 us.)
 template <int N>
-__device__ __forceinline__ float move_block_reference(float v_scale, float wf, float (&o)[N][4],
-                                                      BlockReference* ref) {
-  const float below = ref->at == 0.f ? 1.f / 16 : wf > 128.f ? 1.f / 64 : 1.f / 2;
-  const float to = fmaxf(fmaxf(v_scale * below, ref->top * 8.470329e-22f),  // 2^-70
+__device__ __forceinline__ void move_block_reference(float v_scale, float below, float (&o)[N][4],
+                                                     BlockReference* ref) {
+  const float power = __uint_as_float(__float_as_uint(v_scale) & 0x7f800000u);
+  const float to = fmaxf(fmaxf(power * below, ref->top() * 0x1p-70f),
                          1.17549435e-38f);  // a normal number: so is its inverse
-  const float inv = 1.f / to, f = ref->at * inv;
+  const float top = fmaxf(ref->top(), to), from = ref->at();
+  ref->bits = __float_as_uint(to) | __float_as_uint(top) >> 23;
+  const float f = from * ref->inverse();
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[n][e] *= f;
-  ref->at = to;
-  ref->inverse = inv;
-  ref->top = fmaxf(ref->top, to);
-  return v_scale * inv;
 }
 
 template <typename QT, typename KVT, int D, int G, int NW, int SC, int QL, bool UM,
@@ -474,8 +486,8 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
     // that has seen nothing yet (every token so far masked), whose weights
     // exp2(-inf - 0) = 0 keep its state empty; it changes only on a rescale
     float mref[2] = {0.f, 0.f};
-    // Per-block scales: o is kept in units of a reference (0 before the first
-    // page with a non-zero V scale), see block_weight_inside.  A step of
+    // Per-block and per-token scales: o is kept in units of a reference, see
+    // block_weight_inside.  A step of
     // several pages leaves it alone, so that they share one test and no branch
     // lies between their MMAs: where a scale is outside, they are taken one at
     // a time.
@@ -591,7 +603,8 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
       }
 
       // ---- scores S^T[token][head] = K . q^T (two accumulators a page to halve the chain)
-      float s[NPP][4], vs_lo[NPP], vs_hi[NPP];  // vs: per-token V scales of tokens g, g+8
+      float s[NPP][4];
+      float vs_lo[NPP], vs_hi[NPP];  // per-token V scales of tokens g, g+8
       float wf[NPP], ks[NPP];  // per-block scales: the page's weight factor, its K scale
       if constexpr (BS) {
         bool inside = true;
@@ -602,12 +615,13 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
                               (k + u * PS) % kBlockScaleRing);
           ks[u] = bs.x;
           v_scale = bs.y;
-          wf[u] = bs.y * ref.inverse;
+          wf[u] = bs.y * ref.inverse();
           inside = inside && block_weight_inside(wf[u], bs.y);
         }
         if (!inside) {
           if (NPP > 1) return false;
-          wf[0] = move_block_reference(v_scale, wf[0], o, &ref);
+          move_block_reference(v_scale, block_reference_below(wf[0]), o, &ref);
+          wf[0] = v_scale * ref.inverse();
         }
       }
       const int sw = C::SWZ == 128 ? (g & 7) : ((g >> 1) & 3);  // swizzle of rows g and g+8
@@ -645,7 +659,6 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
         const float page_qscale = BS ? qscale * ks[u] : qscale;
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[u][e] = (sc[0][e] + sc[1][e]) * page_qscale;
-        vs_lo[u] = vs_hi[u] = 1.f;
         if constexpr (TS) {
           const float* scl =
               reinterpret_cast<const float*>(smem + C::OFF_SCALES) + stage[u] * 2 * P;
@@ -661,11 +674,11 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
           // a slot past the end weighs 0, whatever its per-token scale holds
           if (g >= valid[u]) {
             s[u][0] = s[u][1] = -INFINITY;
-            vs_lo[u] = 1.f;
+            vs_lo[u] = 0.f;
           }
           if (g + 8 >= valid[u]) {
             s[u][2] = s[u][3] = -INFINITY;
-            vs_hi[u] = 1.f;
+            vs_hi[u] = 0.f;
           }
         }
         if constexpr (kCausal) {
@@ -712,9 +725,29 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
         }
         const bool first = um_first;
         um_first = false;
-        rescale = first ||
-                  __any_sync(0xffffffffu, tmx[0] > m_h[0] + kAbove || tmx[1] > m_h[1] + kAbove);
+        if constexpr (TS) {
+          static_assert(NPP == 1, "a page a step");
+          // and this lane's larger scale within [2^-2, 2^7] of the reference: one
+          // comparison of their bits (two of floats, and a vote for any lane
+          // outside: 217.4 us; this: 214.2, without the test 213.4)
+          const uint32_t top = __float_as_uint(fmaxf(vs_lo[0], vs_hi[0]));
+          const bool inside = top - ref.bits + (2u << 23) <= 9u << 23;
+          rescale = first || !__all_sync(0xffffffffu, inside && tmx[0] <= m_h[0] + kAbove &&
+                                                          tmx[1] <= m_h[1] + kAbove);
+        } else {
+          rescale = first ||
+                    __any_sync(0xffffffffu, tmx[0] > m_h[0] + kAbove || tmx[1] > m_h[1] + kAbove);
+        }
         if (rescale) {
+          if constexpr (TS) {
+            float top = fmaxf(vs_lo[0], vs_hi[0]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float wf = top * ref.inverse();
+            if (!block_weight_inside(wf, top))
+              move_block_reference(top, wf > 128.f ? 1.f / 64 : 1.f / 8, o, &ref);
+          }
           float mx[2] = {tmx[0], tmx[1]};
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
@@ -737,6 +770,10 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
           }
         }
       }
+      if constexpr (TS) {
+        vs_lo[0] *= ref.inverse();
+        vs_hi[0] *= ref.inverse();
+      }
 #pragma unroll
       for (int u = 0; u < NPP; ++u) {
         const float e0 = dev::fast_exp2(s[u][0] - mref[0]), e1 = dev::fast_exp2(s[u][1] - mref[1]);
@@ -757,7 +794,7 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
           a = mma::unpack2(pv01, kBf16);
           b = mma::unpack2(pv23, kBf16);
         }
-        if constexpr (TS) {  // weights times the per-token V scale
+        if constexpr (TS) {  // weights times the per-token V scale, over the reference
           pv01 = mma::pack2(a.x * vs_lo[u], a.y * vs_lo[u], kBf16);
           pv23 = mma::pack2(b.x * vs_hi[u], b.y * vs_hi[u], kBf16);
         }
@@ -857,8 +894,8 @@ __global__ void __launch_bounds__(MmaCfg<QT, KVT, D, G, NW, SC, QL>::THREADS,
         for (int mt = 0; mt < MTILES; ++mt) {
           const int dlo = kFp8 ? mt * 16 + 2 * g : mt * 16 + g;
           const int dhi = kFp8 ? mt * 16 + 2 * g + 1 : mt * 16 + g + 8;
-          mo[(srow * NC + h) * D + dlo] = BS ? o[mt][e] * ref.at : o[mt][e];
-          mo[(srow * NC + h) * D + dhi] = BS ? o[mt][2 + e] * ref.at : o[mt][2 + e];
+          mo[(srow * NC + h) * D + dlo] = BS || TS ? o[mt][e] * ref.at() : o[mt][e];
+          mo[(srow * NC + h) * D + dhi] = BS || TS ? o[mt][2 + e] * ref.at() : o[mt][2 + e];
         }
         if (g == 0) {
           mm[srow * NC + h] = m_h[e];
