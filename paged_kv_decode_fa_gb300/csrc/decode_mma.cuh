@@ -274,8 +274,8 @@ __device__ __forceinline__ float block_reference_below(float wf) {
 // It stays above 2^-70 of the largest so far: a token adds less than 2^24 to o in units
 // of the reference of its time, so that o stays finite, and a page further down
 // loses low bits of its weights instead, an absolute error below 2^-64 of the
-// larger values.  (A bound from o itself, by a reduction over it, took the
-// prefix kernel of 2048 shared pages from 1452 to 1590 us.)
+// larger values.  (A bound from o itself, by a reduction over it: the prefix
+// kernel of 2048 shared pages took 1590 us, so 1484.)
 template <int N>
 __device__ __forceinline__ void move_block_reference(float v_scale, float below, float (&o)[N][4],
                                                      BlockReference* ref) {
