@@ -633,6 +633,26 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
                    int interleaved, void* workspace_dev, size_t workspace_bytes,
                    void* cuda_stream, fa_append_plan_t* out_plan);
 
+/* plan with positions of several axes (time, height and width of image and
+ * video tokens): pair j of a new token turns by its position on axis
+ * pair_axis[j] times inv_freq[j].
+ *
+ *  positions_dev   [num_axes, append_indptr[batch]] int32, device (or
+ *                  page-locked host memory): a position of each new token on
+ *                  each axis, any int32.  Kept by pointer and read by every run
+ *                  of this plan, so that they may change between runs.
+ *  pair_axis_host  [rotary_dim / 2] int32, host: 0 to num_axes - 1 each.  Read
+ *                  during the call; rotary_dim is 16 at least.
+ * Arguments, runs and errors otherwise as fa_append_plan. */
+int fa_append_plan_axes(const int32_t* indptr_host, const int32_t* indices_dev,
+                        const int32_t* last_page_len_host, const int32_t* append_indptr_host,
+                        const int32_t* positions_dev, int num_axes, const int32_t* pair_axis_host,
+                        int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                        int page_size, fa_dtype q_dtype, fa_dtype kv_dtype,
+                        const double* inv_freq_host, int rotary_dim, int interleaved,
+                        void* workspace_dev, size_t workspace_bytes, void* cuda_stream,
+                        fa_append_plan_t* out_plan);
+
 /* run: append k and v [rows, num_kv_heads, head_dim] to the cache.
  *
  *  q, q_out   q [rows, num_qo_heads, head_dim] rotated into the contiguous

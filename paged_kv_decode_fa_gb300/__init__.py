@@ -48,7 +48,7 @@ EXPORTED_SYMBOLS = (
     "fa_decode_run_block_scales",
     "fa_append_workspace_size", "fa_append_plan", "fa_append_run", "fa_append_run_head_scales",
     "fa_append_run_token_scales", "fa_append_run_block_scales", "fa_append_check",
-    "fa_append_plan_destroy", "fa_cascade_run_block_scales",
+    "fa_append_plan_destroy", "fa_cascade_run_block_scales", "fa_append_plan_axes",
 )
 
 FA_OK = 0
@@ -135,6 +135,9 @@ def _load() -> ctypes.CDLL:
     lib.fa_append_plan.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, i32, i32,
                                    P, sz, P, ctypes.POINTER(P)]
     lib.fa_append_plan.restype = i32
+    lib.fa_append_plan_axes.argtypes = [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, i32,
+                                        P, i32, i32, P, sz, P, ctypes.POINTER(P)]
+    lib.fa_append_plan_axes.restype = i32
     lib.fa_append_run.argtypes = [P, P, P, P, P, P, i64, f32, f32, P]
     lib.fa_append_run.restype = i32
     for name in ("fa_append_run_head_scales", "fa_append_run_token_scales",
@@ -856,10 +859,12 @@ class RotaryTable:
     position * inv_freq[j] radians.  inv_freq defaults to
     theta ** (-2 j / rotary_dim); pass it (rotary_dim / 2 values, kept in 64
     bits) for scaled variants.  interleaved: pairs (2j, 2j + 1) instead of
-    (j, j + rotary_dim / 2)."""
+    (j, j + rotary_dim / 2).  axes: for tokens with a position on several axes
+    (time, height, width), the axis that each pair turns by (rotary_dim / 2
+    numbers from 0), e.g. np.repeat([0, 1, 2], [16, 24, 24])."""
 
     def __init__(self, rotary_dim: int, theta: float = 10000.0, *, inv_freq=None,
-                 interleaved: bool = False):
+                 interleaved: bool = False, axes=None):
         if rotary_dim <= 0 or rotary_dim % 16:
             raise ValueError("rotary_dim must be a positive multiple of 16")
         if inv_freq is None:
@@ -872,6 +877,13 @@ class RotaryTable:
             raise ValueError(f"inv_freq must be {rotary_dim // 2} values of at most 2^32")
         self.rotary_dim = int(rotary_dim)
         self.interleaved = bool(interleaved)
+        self.axes = None
+        if axes is not None:
+            given = _host_i32(axes)
+            if given.shape != (rotary_dim // 2,) or (given < 0).any():
+                raise ValueError(f"axes must be {rotary_dim // 2} axis numbers from 0")
+            self.axes = given.copy()
+            self.num_axes = int(given.max()) + 1
 
 
 def append_workspace_size(batch: int, num_tokens: int) -> int:
@@ -884,7 +896,7 @@ def append_workspace_size(batch: int, num_tokens: int) -> int:
 
 class AppendPlan:
     """A planned append: where a batch's new tokens go in the paged cache.
-    Keeps the index tensor and the workspace alive."""
+    Keeps the index tensor, the positions and the workspace alive."""
 
     def __init__(self, handle, indices, workspace, q_dtype, kv_dtype, shape, num_tokens):
         self._h = handle
@@ -1036,12 +1048,15 @@ class AppendPlan:
 def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num_qo_heads: int,
                 num_kv_heads: int, head_dim: int, page_size: int, *, q_data_type=torch.bfloat16,
                 kv_data_type=None, rotary: RotaryTable | None = None, position_offset=None,
-                workspace: torch.Tensor | None = None, stream=None) -> AppendPlan:
+                positions: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                stream=None) -> AppendPlan:
     """Plan the append of append_indptr[i+1] - append_indptr[i] new tokens to
     request i.  indptr / indices / last_page_len describe the batch after the
     append, as plan takes them for the decode that follows; the new tokens are
     each request's last.  rotary: the rotation of k and q (None: none), at the
-    token's index in its request plus position_offset[i]."""
+    token's index in its request plus position_offset[i]; with rotary.axes, at
+    positions [axes, append_indptr[-1]], an int32 CUDA tensor that every run
+    reads (it may be written between runs)."""
     kv_data_type = q_data_type if kv_data_type is None else kv_data_type
     indptr_h, indptr_p, n_indptr = _host_i32_ptr(indptr)
     last_h, last_p, n_last = _host_i32_ptr(last_page_len)
@@ -1063,9 +1078,24 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
         if freq.shape != (rotary.rotary_dim // 2,):
             raise ValueError("rotary.inv_freq must have rotary_dim / 2 values")
     total = _i32_at(app_p, B) if B >= 0 else 0
+    axes = None if rotary is None else rotary.axes
+    if (axes is None) != (positions is None):
+        raise ValueError("positions go with a RotaryTable of several axes")
+    if axes is not None:
+        if position_offset is not None:
+            raise ValueError("positions are given: no position_offset")
+        if (positions.dtype != torch.int32 or not _reachable(positions)
+                or not positions.is_contiguous() or positions.dim() != 2
+                or positions.shape[0] < rotary.num_axes or positions.shape[1] != total):
+            raise ValueError(f"positions must be a contiguous int32 CUDA or page-locked tensor "
+                             f"[{rotary.num_axes}, {total}]")
+        axes = np.ascontiguousarray(axes, dtype=np.int32)
+        if axes.shape != (rotary.rotary_dim // 2,):
+            raise ValueError("rotary.axes must have rotary_dim / 2 values")
     device = torch.cuda.current_device()
-    if indices.is_cuda and indices.get_device() != device:
-        raise ValueError("indices must be on the current device")
+    for t in (indices, positions):
+        if t is not None and t.is_cuda and t.get_device() != device:
+            raise ValueError("indices and positions must be on the current device")
     if workspace is not None and (workspace.get_device() != device
                                   or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the current device")
@@ -1073,14 +1103,19 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
         workspace = _empty(append_workspace_size(max(B, 0), max(total, 0)), torch.uint8,
                            _cuda_device(indices), stream)
     handle = ctypes.c_void_p()
-    _check(_L().fa_append_plan(
-        indptr_p, indices.data_ptr() if indices.numel() else None, last_p if B else None, app_p,
-        off_p, B, num_qo_heads, num_kv_heads, head_dim, page_size, _dtype_code(q_data_type),
-        _dtype_code(kv_data_type), freq.ctypes.data if rotary else None,
-        rotary.rotary_dim if rotary else 0, int(rotary.interleaved) if rotary else 0,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream_handle(stream), ctypes.byref(handle)), "fa_append_plan")
-    return AppendPlan(handle.value, indices, workspace, q_data_type, kv_data_type,
+    first = (indptr_p, indices.data_ptr() if indices.numel() else None, last_p if B else None, app_p)
+    rest = (B, num_qo_heads, num_kv_heads, head_dim, page_size, _dtype_code(q_data_type),
+            _dtype_code(kv_data_type), freq.ctypes.data if rotary else None,
+            rotary.rotary_dim if rotary else 0, int(rotary.interleaved) if rotary else 0,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _stream_handle(stream), ctypes.byref(handle))
+    if axes is None:
+        _check(_L().fa_append_plan(*first, off_p, *rest), "fa_append_plan")
+    else:
+        _check(_L().fa_append_plan_axes(*first, positions.data_ptr() if total else None,
+                                        positions.shape[0], axes.ctypes.data, *rest),
+               "fa_append_plan_axes")
+    return AppendPlan(handle.value, (indices, positions), workspace, q_data_type, kv_data_type,
                       (B, num_qo_heads, num_kv_heads, head_dim, page_size), total)
 
 

@@ -97,7 +97,10 @@ struct AppendParams {
   const int32_t* indices;
   const AppendUnit* units;
   const unsigned long long* turns;  // [pairs] turns a position, 2^-64 units
+  const int32_t* positions;         // AXES: [axes, rows]
+  const int32_t* axis;              // [pairs] axis of each pair
   int* err;
+  int64_t num_rows;
   int64_t num_pages;
   int hq, hkv;
   int heads;  // kv heads of one CTA, kHeads per thread at most
@@ -390,7 +393,9 @@ struct Cfg {
 
 // INTERLEAVED as a constant: with both orders in one kernel, its code outgrew the
 // instruction cache (block-scaled prompts 155.9 us for 160.5, others 121.4 for 123.2).
-template <typename T, int D, int MODE, bool INTERLEAVED>
+// AXES (positions of several axes) as well: chosen in the kernel it cost prompts of
+// one axis 125.2 us for 121.6.
+template <typename T, int D, int MODE, bool INTERLEAVED, bool AXES>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
     fa_append_kernel(const __grid_constant__ AppendParams p) {
   using C = Cfg<D>;
@@ -435,8 +440,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, kCtasPerSm)
   for (int i = 2 * tid; i < n * p.pairs; i += 2 * C::THREADS) {
     const int t = i / p.pairs, j = i - t * p.pairs;
     const ulonglong2 turns = *reinterpret_cast<const ulonglong2*>(p.turns + j);
-    const unsigned long long at = (unsigned)(u.position + t);
-    *reinterpret_cast<float4*>(angle + t * kMaxPairs + j) = cos_sin(at * turns.x, at * turns.y);
+    unsigned long long at0 = (unsigned)(u.position + t), at1 = at0;
+    if constexpr (AXES) {  // a negative position turns the other way, modulo 2^64
+      const int2 axis = *reinterpret_cast<const int2*>(p.axis + j);
+      const int32_t* of_row = p.positions + u.row + t;
+      at0 = (unsigned long long)(long long)of_row[axis.x * p.num_rows];
+      at1 = (unsigned long long)(long long)of_row[axis.y * p.num_rows];
+    }
+    *reinterpret_cast<float4*>(angle + t * kMaxPairs + j) = cos_sin(at0 * turns.x, at1 * turns.y);
   }
   const int64_t scale_at = (int64_t)page * p.hkv + h0 + (tid < heads ? tid : tid - heads);
   float old_scale = 0.f;
@@ -583,30 +594,34 @@ struct AppendKernel {
 };
 
 template <typename T, int MODE>
-AppendKernel kernel_of(int head_dim, bool interleaved) {
+AppendKernel kernel_of(int head_dim, bool interleaved, bool axes) {
   auto of = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    const void* f = interleaved ? reinterpret_cast<const void*>(&fa_append_kernel<T, D, MODE, true>)
-                                : reinterpret_cast<const void*>(&fa_append_kernel<T, D, MODE, false>);
-    return AppendKernel{f, Cfg<D>::THREADS, Cfg<D>::ROWS};
+    using Kernel = void (*)(const AppendParams);
+    const Kernel f = interleaved ? (axes ? &fa_append_kernel<T, D, MODE, true, true>
+                                         : &fa_append_kernel<T, D, MODE, true, false>)
+                                 : (axes ? &fa_append_kernel<T, D, MODE, false, true>
+                                         : &fa_append_kernel<T, D, MODE, false, false>);
+    return AppendKernel{reinterpret_cast<const void*>(f), Cfg<D>::THREADS, Cfg<D>::ROWS};
   };
   return head_dim == 64 ? of(std::integral_constant<int, 64>{})
                         : of(std::integral_constant<int, 128>{});
 }
 
 // A kernel for q's type, the cache being E4M3 unless mode is kNative.
-AppendKernel find_append_kernel(fa_dtype q, int head_dim, Mode mode, bool interleaved) {
-  if (q == FA_DTYPE_F32) return kernel_of<float, kNative>(head_dim, interleaved);
+AppendKernel find_append_kernel(fa_dtype q, int head_dim, Mode mode, bool interleaved,
+                                bool axes) {
+  if (q == FA_DTYPE_F32) return kernel_of<float, kNative>(head_dim, interleaved, axes);
   if (q == FA_DTYPE_BF16) {
-    if (mode == kStatic) return kernel_of<__nv_bfloat16, kStatic>(head_dim, interleaved);
-    if (mode == kToken) return kernel_of<__nv_bfloat16, kToken>(head_dim, interleaved);
-    if (mode == kBlock) return kernel_of<__nv_bfloat16, kBlock>(head_dim, interleaved);
-    return kernel_of<__nv_bfloat16, kNative>(head_dim, interleaved);
+    if (mode == kStatic) return kernel_of<__nv_bfloat16, kStatic>(head_dim, interleaved, axes);
+    if (mode == kToken) return kernel_of<__nv_bfloat16, kToken>(head_dim, interleaved, axes);
+    if (mode == kBlock) return kernel_of<__nv_bfloat16, kBlock>(head_dim, interleaved, axes);
+    return kernel_of<__nv_bfloat16, kNative>(head_dim, interleaved, axes);
   }
-  if (mode == kStatic) return kernel_of<__half, kStatic>(head_dim, interleaved);
-  if (mode == kToken) return kernel_of<__half, kToken>(head_dim, interleaved);
-  if (mode == kBlock) return kernel_of<__half, kBlock>(head_dim, interleaved);
-  return kernel_of<__half, kNative>(head_dim, interleaved);
+  if (mode == kStatic) return kernel_of<__half, kStatic>(head_dim, interleaved, axes);
+  if (mode == kToken) return kernel_of<__half, kToken>(head_dim, interleaved, axes);
+  if (mode == kBlock) return kernel_of<__half, kBlock>(head_dim, interleaved, axes);
+  return kernel_of<__half, kNative>(head_dim, interleaved, axes);
 }
 
 // kv heads of one CTA, for runs of `longest` tokens at most, `tokens` in all:
@@ -635,15 +650,16 @@ int heads_of_cta(const AppendKernel& k, int64_t tokens, int64_t units, int longe
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
-// Device-check word, then the units, then the turns.
+// Device-check word, then the units, the turns and each pair's axis.
 struct AppendLayout {
-  size_t units, turns, total;
+  size_t units, turns, axis, total;
 };
 AppendLayout append_layout(int64_t n_units, int pairs) {
   AppendLayout L;
   L.units = kAlign;
   L.turns = align_up(L.units + sizeof(AppendUnit) * (size_t)n_units);
-  L.total = align_up(L.turns + 8 * (size_t)pairs);
+  L.axis = L.turns + 8 * (size_t)pairs;
+  L.total = align_up(L.axis + 4 * (size_t)pairs);
   return L;
 }
 
@@ -682,6 +698,8 @@ struct fa_append_plan_s {
   int longest = 0;  // tokens of the longest run
   int pairs = 0;
   bool interleaved = false;
+  bool pair_axes = false;              // positions of several axes
+  const int32_t* positions = nullptr;  // theirs, [axes, rows]
 };
 
 namespace {
@@ -727,12 +745,16 @@ int append_run(fa_append_plan_s* plan, Mode mode, const fa_rows* k, const fa_row
   p.indices = plan->indices;
   p.units = reinterpret_cast<const AppendUnit*>(plan->ws + plan->layout.units);
   p.turns = reinterpret_cast<const unsigned long long*>(plan->ws + plan->layout.turns);
+  p.positions = plan->positions;
+  p.axis = reinterpret_cast<const int32_t*>(plan->ws + plan->layout.axis);
+  p.num_rows = plan->num_rows;
   p.err = reinterpret_cast<int*>(plan->ws);
   p.num_pages = num_pages;
   p.hq = plan->hq;
   p.hkv = plan->hkv;
   p.pairs = plan->pairs;
-  const AppendKernel kern = find_append_kernel(plan->q_dtype, plan->d, mode, plan->interleaved);
+  const AppendKernel kern = find_append_kernel(plan->q_dtype, plan->d, mode, plan->interleaved,
+                                               plan->pair_axes);
   void* args[1] = {&p};
   p.heads = heads_of_cta(kern, plan->num_rows, plan->num_units, plan->longest, plan->hkv,
                          plan->hq / plan->hkv);
@@ -747,24 +769,16 @@ int append_run(fa_append_plan_s* plan, Mode mode, const fa_rows* k, const fa_row
              : FA_ERR_CUDA;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t fa_append_workspace_size(int batch, int64_t num_tokens) {
-  if (batch < 0 || num_tokens < 0 || num_tokens > std::numeric_limits<int32_t>::max()) return 0;
-  // a request's n tokens lie in at most n / 16 + 2 pages, and in at most n
-  const int64_t units = std::min(num_tokens, num_tokens / kPageSize + 2 * (int64_t)batch);
-  return append_layout(units, kMaxPairs).total;
-}
-
-int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
-                   const int32_t* last_page_len_host, const int32_t* append_indptr_host,
-                   const int32_t* position_offset_host, int batch, int num_qo_heads,
-                   int num_kv_heads, int head_dim, int page_size, fa_dtype q_dtype,
-                   fa_dtype kv_dtype, const double* inv_freq_host, int rotary_dim,
-                   int interleaved, void* workspace_dev, size_t workspace_bytes,
-                   void* cuda_stream, fa_append_plan_t* out_plan) {
+// fa_append_plan and fa_append_plan_axes: positions from the tokens' indices
+// (position_offset_host) or from positions_dev [num_axes, rows].
+int append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
+                const int32_t* last_page_len_host, const int32_t* append_indptr_host,
+                const int32_t* position_offset_host, const int32_t* positions_dev,
+                const int32_t* pair_axis_host, int batch, int num_qo_heads, int num_kv_heads,
+                int head_dim, int page_size, fa_dtype q_dtype, fa_dtype kv_dtype,
+                const double* inv_freq_host, int rotary_dim, int interleaved,
+                void* workspace_dev, size_t workspace_bytes, void* cuda_stream,
+                fa_append_plan_t* out_plan) {
   if (!out_plan) return FA_ERR_INVALID_ARG;
   *out_plan = nullptr;
   if (!indptr_host || !append_indptr_host || batch < 0 || num_qo_heads <= 0 ||
@@ -826,6 +840,8 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
   }
   unsigned long long* turns = reinterpret_cast<unsigned long long*>(meta.data() + L.turns);
   for (int i = 0; i < rotary_dim / 2; ++i) turns[i] = turns_of(inv_freq_host[i]);
+  if (pair_axis_host)
+    std::memcpy(meta.data() + L.axis, pair_axis_host, sizeof(int32_t) * (rotary_dim / 2));
 
   plan = new (std::nothrow) fa_append_plan_s();
   if (!plan) return FA_ERR_INVALID_ARG;
@@ -842,6 +858,8 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
   plan->longest = longest;
   plan->pairs = rotary_dim / 2;
   plan->interleaved = interleaved != 0;
+  plan->pair_axes = pair_axis_host != nullptr;
+  plan->positions = positions_dev;
   if (cudaGetDevice(&plan->device) != cudaSuccess ||
       upload_async(plan->ws, meta.data(), meta.size(), static_cast<cudaStream_t>(cuda_stream)) !=
           cudaSuccess) {
@@ -850,6 +868,53 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
   }
   *out_plan = plan;
   return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_append_workspace_size(int batch, int64_t num_tokens) {
+  if (batch < 0 || num_tokens < 0 || num_tokens > std::numeric_limits<int32_t>::max()) return 0;
+  // a request's n tokens lie in at most n / 16 + 2 pages, and in at most n
+  const int64_t units = std::min(num_tokens, num_tokens / kPageSize + 2 * (int64_t)batch);
+  return append_layout(units, kMaxPairs).total;
+}
+
+int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
+                   const int32_t* last_page_len_host, const int32_t* append_indptr_host,
+                   const int32_t* position_offset_host, int batch, int num_qo_heads,
+                   int num_kv_heads, int head_dim, int page_size, fa_dtype q_dtype,
+                   fa_dtype kv_dtype, const double* inv_freq_host, int rotary_dim,
+                   int interleaved, void* workspace_dev, size_t workspace_bytes,
+                   void* cuda_stream, fa_append_plan_t* out_plan) {
+  return append_plan(indptr_host, indices_dev, last_page_len_host, append_indptr_host,
+                     position_offset_host, nullptr, nullptr, batch, num_qo_heads, num_kv_heads,
+                     head_dim, page_size, q_dtype, kv_dtype, inv_freq_host, rotary_dim,
+                     interleaved, workspace_dev, workspace_bytes, cuda_stream, out_plan);
+}
+
+int fa_append_plan_axes(const int32_t* indptr_host, const int32_t* indices_dev,
+                        const int32_t* last_page_len_host, const int32_t* append_indptr_host,
+                        const int32_t* positions_dev, int num_axes, const int32_t* pair_axis_host,
+                        int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                        int page_size, fa_dtype q_dtype, fa_dtype kv_dtype,
+                        const double* inv_freq_host, int rotary_dim, int interleaved,
+                        void* workspace_dev, size_t workspace_bytes, void* cuda_stream,
+                        fa_append_plan_t* out_plan) {
+  if (!out_plan) return FA_ERR_INVALID_ARG;
+  *out_plan = nullptr;
+  if (num_axes < 1 || !pair_axis_host || rotary_dim <= 0 || rotary_dim > head_dim ||
+      !append_indptr_host || batch < 0 ||
+      (append_indptr_host[batch] > 0 && !positions_dev) ||
+      reinterpret_cast<uintptr_t>(positions_dev) % 4)
+    return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    if (pair_axis_host[i] < 0 || pair_axis_host[i] >= num_axes) return FA_ERR_INVALID_ARG;
+  return append_plan(indptr_host, indices_dev, last_page_len_host, append_indptr_host, nullptr,
+                     positions_dev, pair_axis_host, batch, num_qo_heads, num_kv_heads,
+                     head_dim, page_size, q_dtype, kv_dtype, inv_freq_host, rotary_dim,
+                     interleaved, workspace_dev, workspace_bytes, cuda_stream, out_plan);
 }
 
 int fa_append_run(fa_append_plan_t plan, const fa_rows* k, const fa_rows* v, const fa_rows* q,
