@@ -93,9 +93,10 @@ def read_bf16_peak():
 
 # Sources that are not part of the decode kernels or their launch: the
 # cascade's own kernels, the no-allocation entry point, fa_merge_states.
-NOT_DECODE_SOURCES = ("cascade.cu", "cascade_tc.cuh", "static_scratch.cu", "merge.cu")
-# Sources that no workload's kernels are in (the cache is written before).
-NOT_WORKLOAD_SOURCES = ("append.cu",)
+NOT_DECODE_SOURCES = ("cascade.cu", "cascade_tc.cuh", "tcgen05.cuh", "static_scratch.cu", "merge.cu")
+# Sources that no workload's kernels are in: what writes the cache, attends prompts,
+# accumulates weights and evicts around the decode steps.
+NOT_WORKLOAD_SOURCES = ("append.cu", "prefill.cu", "prefill.cuh", "weights.cu", "evict.cu")
 
 
 def kernel_source_hash(workload: str = "gqa_uniform") -> str:

@@ -709,6 +709,98 @@ int fa_append_check(fa_append_plan_t plan, void* cuda_stream, int* flags);
 
 int fa_append_plan_destroy(fa_append_plan_t plan);
 
+/* ---- attention of prompts ------------------------------------------------
+ *
+ * Causal attention of any number of query rows per request over its pages: whole
+ * prompts, chunks of prompts behind a cached context, and single tokens, packed
+ * in one batch - what fa_decode_plan_ragged_q computes, without its limit on
+ * rows.  Request i's query rows are rows qo_indptr[i] .. qo_indptr[i+1] of q and
+ * o, the last n_i positions of its cache (append them first); row j sees positions
+ * 0 .. len_i - n_i + j.  The products run on the tcgen05 tensor cores, 256 rows
+ * (tokens x the query heads of a kv head) against 128 tokens at a time.  A
+ * decode plan is the faster choice where all requests have a few rows: it reads
+ * an E4M3 cache as it is, and splits shorter contexts. */
+typedef struct fa_prefill_plan_s* fa_prefill_plan_t;
+
+/* Workspace that fa_prefill_plan needs for this batch (the same host arrays), on
+ * the current device: the work list, fp32 partial states of rows whose keys
+ * are split over SMs (few rows over long contexts), and, for an E4M3 cache, its
+ * pages in bf16 (twice the bytes of the requests' pages).  0 for invalid
+ * arguments. */
+size_t fa_prefill_workspace_size(const int32_t* indptr_host, const int32_t* last_page_len_host,
+                                 const int32_t* qo_indptr_host, int batch, int num_qo_heads,
+                                 int num_kv_heads, int head_dim, fa_dtype q_dtype,
+                                 fa_dtype kv_dtype);
+
+/* plan: arguments as fa_decode_plan_ragged_q, with any n_i from 0 to len_i and a
+ * workspace of fa_prefill_workspace_size.  indices_dev is kept by pointer; ids
+ * may repeat (shared prefixes).  Built for page_size 16, head_dim 64 and 128,
+ * groups 1, 2, 4, 8 and (q, kv) = (BF16, BF16), (F16, F16), (BF16, E4M3).
+ * Errors as fa_decode_plan. */
+int fa_prefill_plan(const int32_t* indptr_host, const int32_t* indices_dev,
+                    const int32_t* last_page_len_host, const int32_t* qo_indptr_host, int batch,
+                    int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
+                    fa_dtype q_dtype, fa_dtype kv_dtype, void* workspace_dev,
+                    size_t workspace_bytes, void* cuda_stream, fa_prefill_plan_t* out_plan);
+
+/* run: attention of the batch's query rows.
+ *
+ *  q          [rows, num_qo_heads, head_dim] by address and strides (fa_rows,
+ *             above; rows = qo_indptr[batch]), device: a slice of a fused
+ *             projection needs no copy.  Strides of dims longer than one are
+ *             positive.
+ *  paged_kv, num_pages, sm_scale: as fa_decode_run.
+ *  k_scale,   per-tensor scales of an E4M3 cache, 0 or positive; 1 for other kv
+ *  v_scale    types (FA_ERR_INVALID_ARG otherwise).
+ *  o          [rows, num_qo_heads, head_dim] contiguous, q dtype, device, 16-byte
+ *             aligned; not q itself.
+ *  lse        [rows, num_qo_heads] float32, device, or NULL.
+ * One to three kernels on cuda_stream, no allocation, no synchronisation: it can
+ * be captured into a CUDA graph.  Results are bitwise reproducible for a plan.
+ * Two runs that may be in flight together need two plans and workspaces.
+ * What slots behind a request's last token hold is ignored, NaN included.  A value
+ * that is not finite, of a token that a row does not see but another of the same
+ * 256 does, may reach that row as NaN.
+ * Errors: FA_ERR_INVALID_ARG (NULL or misaligned pointers and strides, scales, a
+ * current device that is not the plan's), FA_ERR_CUDA. */
+int fa_prefill_run(fa_prefill_plan_t plan, const fa_rows* q, const void* paged_kv,
+                   int64_t num_pages, float sm_scale, float k_scale, float v_scale, void* o,
+                   float* lse, void* cuda_stream);
+
+/* run over an E4M3 cache with scales per kv head, per token or per block, as
+ * fa_decode_run_head_scales, fa_decode_run_token_scales and
+ * fa_decode_run_block_scales read them (0 or positive).  Scales per tensor and per
+ * kv head multiply the logits and the output in fp32; those per token and per
+ * block multiply the elements, which are then rounded to bf16 (exactly where the
+ * scale is a power of two, as fa_append_run_block_scales writes them). */
+int fa_prefill_run_head_scales(fa_prefill_plan_t plan, const fa_rows* q, const void* paged_kv,
+                               int64_t num_pages, float sm_scale, const float* k_head_scales,
+                               const float* v_head_scales, void* o, float* lse,
+                               void* cuda_stream);
+int fa_prefill_run_token_scales(fa_prefill_plan_t plan, const fa_rows* q, const void* paged_kv,
+                                int64_t num_pages, float sm_scale, const float* k_scales,
+                                const float* v_scales, void* o, float* lse, void* cuda_stream);
+int fa_prefill_run_block_scales(fa_prefill_plan_t plan, const fa_rows* q, const void* paged_kv,
+                                int64_t num_pages, float sm_scale, const float* k_scales,
+                                const float* v_scales, void* o, float* lse, void* cuda_stream);
+
+/* As fa_decode_check, for a prefill plan. */
+int fa_prefill_check(fa_prefill_plan_t plan, void* cuda_stream, int* flags);
+
+int fa_prefill_plan_destroy(fa_prefill_plan_t plan);
+
+/* The work list fa_prefill_plan makes for max_ctas SMs, on the host (no GPU):
+ * cta_offsets [max_ctas + 1]; items [items_room, 8] = {first query token, tokens,
+ * position of the first, the request's first table entry, first and one past the
+ * last 128-token tile, partial slot or -1, kv head}; merge [merge_room, 8] = {first
+ * query token, tokens, first slot, pieces, kv head, 0, 0, 0}.  The four counts are
+ * written even where the room is too small (FA_ERR_WORKSPACE_TOO_SMALL). */
+int fa_plan_prefill_host(const int32_t* indptr_host, const int32_t* last_page_len_host,
+                         const int32_t* qo_indptr_host, int batch, int group, int num_kv_heads,
+                         int max_ctas, int32_t* cta_offsets, int32_t* items, int items_room,
+                         int32_t* merge, int merge_room, int* num_ctas, int* num_items,
+                         int* num_merge, int* num_slots);
+
 /* ---- cascade decode (shared prefix) ------------------------------------
  *
  * A batch whose requests all begin with the same shared prefix (whole pages,

@@ -24,6 +24,7 @@ __all__ = [
     "merge_states",
     "CascadePlan", "cascade_plan",
     "RotaryTable", "AppendPlan", "plan_append", "append_workspace_size",
+    "PrefillPlan", "plan_prefill", "plan_prefill_host",
     "workspace_size", "plan_work_host", "plan_work_host_buckets",
     "BatchDecodeWithPagedKVCacheWrapper",
     "LIB_PATH", "EXPORTED_SYMBOLS", "library", "library_stats",
@@ -49,6 +50,9 @@ EXPORTED_SYMBOLS = (
     "fa_append_workspace_size", "fa_append_plan", "fa_append_run", "fa_append_run_head_scales",
     "fa_append_run_token_scales", "fa_append_run_block_scales", "fa_append_check",
     "fa_append_plan_destroy", "fa_cascade_run_block_scales", "fa_append_plan_axes",
+    "fa_prefill_workspace_size", "fa_prefill_plan", "fa_prefill_run", "fa_prefill_run_head_scales",
+    "fa_prefill_run_token_scales", "fa_prefill_run_block_scales", "fa_prefill_check",
+    "fa_prefill_plan_destroy", "fa_plan_prefill_host",
 )
 
 FA_OK = 0
@@ -86,6 +90,7 @@ class PlanInfo(ctypes.Structure):
 
 # fa_rows of k, v and q in a row: {address, token stride, head stride} each
 _Rows3 = ctypes.c_int64 * 9
+_Rows = ctypes.c_int64 * 3
 _ROWS_BYTES = 24
 
 
@@ -138,6 +143,26 @@ def _load() -> ctypes.CDLL:
     lib.fa_append_plan_axes.argtypes = [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, i32,
                                         P, i32, i32, P, sz, P, ctypes.POINTER(P)]
     lib.fa_append_plan_axes.restype = i32
+    lib.fa_prefill_workspace_size.argtypes = [P, P, P, i32, i32, i32, i32, i32, i32]
+    lib.fa_prefill_workspace_size.restype = sz
+    lib.fa_prefill_plan.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, sz, P,
+                                    ctypes.POINTER(P)]
+    lib.fa_prefill_plan.restype = i32
+    lib.fa_prefill_run.argtypes = [P, P, P, i64, f32, f32, f32, P, P, P]
+    lib.fa_prefill_run.restype = i32
+    for name in ("fa_prefill_run_head_scales", "fa_prefill_run_token_scales",
+                 "fa_prefill_run_block_scales"):
+        f = getattr(lib, name)
+        f.argtypes = [P, P, P, i64, f32, P, P, P, P, P]
+        f.restype = i32
+    lib.fa_prefill_check.argtypes = [P, P, ctypes.POINTER(i32)]
+    lib.fa_prefill_check.restype = i32
+    lib.fa_prefill_plan_destroy.argtypes = [P]
+    lib.fa_prefill_plan_destroy.restype = i32
+    ip = ctypes.POINTER(i32)
+    lib.fa_plan_prefill_host.argtypes = [P, P, P, i32, i32, i32, i32, P, P, i32, P, i32, ip, ip,
+                                         ip, ip]
+    lib.fa_plan_prefill_host.restype = i32
     lib.fa_append_run.argtypes = [P, P, P, P, P, P, i64, f32, f32, P]
     lib.fa_append_run.restype = i32
     for name in ("fa_append_run_head_scales", "fa_append_run_token_scales",
@@ -1117,6 +1142,177 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
                "fa_append_plan_axes")
     return AppendPlan(handle.value, (indices, positions), workspace, q_data_type, kv_data_type,
                       (B, num_qo_heads, num_kv_heads, head_dim, page_size), total)
+
+
+class PrefillPlan:
+    """Planned attention of packed query rows (prompts, chunks of prompts, single
+    tokens) over their requests' pages.  Keeps the index tensor and the
+    workspace alive."""
+
+    def __init__(self, handle, indices, workspace, q_dtype, kv_dtype, shape, num_tokens):
+        self._h = handle
+        self._keep = (indices, workspace)
+        self.q_dtype = q_dtype
+        self.kv_dtype = kv_dtype
+        self.batch, self.num_qo_heads, self.num_kv_heads, self.head_dim, self.page_size = shape
+        self.num_tokens = num_tokens
+        self._device = workspace.get_device()
+        self._q_shape = (num_tokens, self.num_qo_heads, self.head_dim)
+        self._page_shape = (2, self.page_size, self.num_kv_heads, self.head_dim)
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h:
+            _L().fa_prefill_plan_destroy(h)
+            self._h = None
+
+    def run(self, q: torch.Tensor, paged_kv: torch.Tensor, *, sm_scale: float | None = None,
+            k_scale: float = 1.0, v_scale: float = 1.0, out: torch.Tensor | None = None,
+            lse: torch.Tensor | None = None, return_lse: bool = True, stream=None):
+        """Attention of q [qo_indptr[-1], Hq, D] (innermost dim contiguous, other
+        strides free); returns (o, lse) (lse None if return_lse is False).
+        k_scale / v_scale are an E4M3 cache's per-tensor scales."""
+        rows, out, lse = self._outputs(q, paged_kv, out, lse, return_lse, stream)
+        _check(_L().fa_prefill_run(
+            self._h, ctypes.addressof(rows), paged_kv.data_ptr(), paged_kv.shape[0],
+            0.0 if sm_scale is None else float(sm_scale), float(k_scale), float(v_scale),
+            out.data_ptr(), lse.data_ptr() if lse is not None else None,
+            _stream_handle(stream)), "fa_prefill_run")
+        return out, lse
+
+    def run_head_scales(self, q: torch.Tensor, paged_kv: torch.Tensor, k_scales: torch.Tensor,
+                        v_scales: torch.Tensor, **kw):
+        """As run, over an E4M3 cache with one scale per kv head: k_scales /
+        v_scales [num_kv_heads] float32."""
+        return self._run_scales("fa_prefill_run_head_scales", (self.num_kv_heads,), q, paged_kv,
+                                k_scales, v_scales, **kw)
+
+    def run_token_scales(self, q: torch.Tensor, paged_kv: torch.Tensor, k_scales: torch.Tensor,
+                         v_scales: torch.Tensor, **kw):
+        """As run, over an E4M3 cache with one scale per token and kv head:
+        k_scales / v_scales [num_pages, num_kv_heads, page_size] float32."""
+        shape = (paged_kv.shape[0], self.num_kv_heads, self.page_size)
+        return self._run_scales("fa_prefill_run_token_scales", shape, q, paged_kv, k_scales,
+                                v_scales, **kw)
+
+    def run_block_scales(self, q: torch.Tensor, paged_kv: torch.Tensor, k_scales: torch.Tensor,
+                         v_scales: torch.Tensor, **kw):
+        """As run, over an E4M3 cache with one scale per page and kv head:
+        k_scales / v_scales [num_pages, num_kv_heads] float32."""
+        return self._run_scales("fa_prefill_run_block_scales",
+                                (paged_kv.shape[0], self.num_kv_heads), q, paged_kv, k_scales,
+                                v_scales, **kw)
+
+    def _run_scales(self, name, shape, q, paged_kv, k_scales, v_scales, *, sm_scale=None, out=None,
+                    lse=None, return_lse=True, stream=None):
+        rows, out, lse = self._outputs(q, paged_kv, out, lse, return_lse, stream)
+        _check_scales((k_scales, v_scales), shape, paged_kv)
+        _check(getattr(_L(), name)(
+            self._h, ctypes.addressof(rows), paged_kv.data_ptr(), paged_kv.shape[0],
+            0.0 if sm_scale is None else float(sm_scale), k_scales.data_ptr(),
+            v_scales.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+            _stream_handle(stream)), name)
+        return out, lse
+
+    def _outputs(self, q, paged_kv, out, lse, return_lse, stream):
+        """Check q / paged_kv against the plan; allocate missing outputs."""
+        if q.dtype is not self.q_dtype or paged_kv.dtype is not self.kv_dtype:
+            raise TypeError("q / paged_kv dtype differs from the plan")
+        if q.shape != self._q_shape or q.get_device() != self._device:
+            raise ValueError(f"q must be a tensor {list(self._q_shape)} on the plan's device")
+        token, head, inner = q.stride()
+        if q.numel() and (inner != 1 or (q.shape[0] > 1 and (token <= 0 or token % 8))
+                          or (q.shape[1] > 1 and (head <= 0 or head % 8)) or q.data_ptr() % 16):
+            raise ValueError("q needs a contiguous innermost dim, and an address and strides in "
+                             "whole 16 bytes")
+        if (paged_kv.dim() != 5 or paged_kv.shape[1:] != self._page_shape
+                or not paged_kv.is_contiguous() or paged_kv.get_device() != self._device):
+            raise ValueError("paged_kv must be a contiguous tensor [num_pages, 2, page_size, "
+                             "num_kv_heads, head_dim] on the plan's device")
+        nbytes = q.numel() * q.element_size()
+        out = _empty(q.shape, q.dtype, q.device, stream) if out is None else _room(out, nbytes)
+        if lse is not None:
+            _room(lse, q.numel() // self.head_dim * 4)
+        elif return_lse:
+            lse = _empty(q.shape[:-1], torch.float32, q.device, stream)
+        for t in (out, lse):
+            if t is not None and (t.get_device() != self._device or not t.is_contiguous()):
+                raise ValueError("out / lse must be contiguous, on the plan's device")
+        if nbytes and out.data_ptr() < q.data_ptr() + nbytes and q.data_ptr() < out.data_ptr() + nbytes:
+            raise ValueError("out must not overlap q")
+        return _Rows(q.data_ptr(), token if q.shape[0] > 1 else 0, head if q.shape[1] > 1 else 0), \
+            out, lse
+
+    def check(self, stream=None) -> int:
+        """Synchronise and return the device-check flags (0 = clean)."""
+        flags = ctypes.c_int(0)
+        st = _L().fa_prefill_check(self._h, _stream_handle(stream), ctypes.byref(flags))
+        if st not in (FA_OK, -5):
+            _check(st, "fa_prefill_check")
+        return int(flags.value)
+
+
+def plan_prefill(indptr, indices: torch.Tensor, last_page_len, qo_indptr, num_qo_heads: int,
+                 num_kv_heads: int, head_dim: int, page_size: int, *, q_data_type=torch.bfloat16,
+                 kv_data_type=None, workspace: torch.Tensor | None = None,
+                 stream=None) -> PrefillPlan:
+    """Plan causal attention of qo_indptr[i+1] - qo_indptr[i] query rows for request
+    i, any number up to its length: the last positions of its cache (append them
+    first).  run() takes q [qo_indptr[-1], Hq, D]."""
+    kv_data_type = q_data_type if kv_data_type is None else kv_data_type
+    indptr_h, indptr_p, n_indptr = _host_i32_ptr(indptr)
+    last_h, last_p, n_last = _host_i32_ptr(last_page_len)
+    qo_h, qo_p, n_qo = _host_i32_ptr(qo_indptr)
+    B = n_indptr - 1
+    if B < 0 or n_last < B or n_qo != B + 1:
+        raise ValueError("last_page_len shorter than the batch, or qo_indptr not batch + 1 long")
+    _check_indices(indices, indptr_p, B)
+    device = torch.cuda.current_device()
+    if indices.is_cuda and indices.get_device() != device:
+        raise ValueError("indices must be on the current device")
+    q_code, kv_code = _dtype_code(q_data_type), _dtype_code(kv_data_type)
+    if workspace is None:
+        n = _L().fa_prefill_workspace_size(indptr_p, last_p if B else None, qo_p, B, num_qo_heads,
+                                           num_kv_heads, head_dim, q_code, kv_code)
+        # 0 for refused arguments, which the plan names
+        workspace = _empty(max(int(n), 256), torch.uint8, _cuda_device(indices), stream)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current device")
+    handle = ctypes.c_void_p()
+    _check(_L().fa_prefill_plan(
+        indptr_p, indices.data_ptr() if indices.numel() else None, last_p if B else None, qo_p, B,
+        num_qo_heads, num_kv_heads, head_dim, page_size, q_code, kv_code, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream),
+        ctypes.byref(handle)), "fa_prefill_plan")
+    return PrefillPlan(handle.value, indices, workspace, q_data_type, kv_data_type,
+                       (B, num_qo_heads, num_kv_heads, head_dim, page_size), _i32_at(qo_p, B))
+
+
+def plan_prefill_host(indptr, last_page_len, qo_indptr, group: int, num_kv_heads: int,
+                      max_ctas: int):
+    """Host-only work list of plan_prefill (fa_plan_prefill_host, no GPU): returns
+    (cta_offsets, items [n, 8], merge [m, 8], num_slots)."""
+    indptr_h, indptr_p, n_indptr = _host_i32_ptr(indptr)
+    last_h, last_p, n_last = _host_i32_ptr(last_page_len)
+    qo_h, qo_p, n_qo = _host_i32_ptr(qo_indptr)
+    B = n_indptr - 1
+    if B < 0 or n_last < B or n_qo != B + 1:
+        raise ValueError("last_page_len shorter than the batch, or qo_indptr not batch + 1 long")
+    cta = np.zeros(max_ctas + 1, np.int32)
+    counts = [ctypes.c_int() for _ in range(4)]
+    room = [0, 0]
+    while True:
+        items, merge = (np.zeros((n, 8), np.int32) for n in room)
+        rc = _L().fa_plan_prefill_host(indptr_p, last_p if B else None, qo_p, B, group, num_kv_heads,
+                                       max_ctas, cta.ctypes.data, items.ctypes.data, room[0],
+                                       merge.ctypes.data, room[1],
+                                       *(ctypes.byref(c) for c in counts))
+        need = [counts[1].value, counts[2].value]
+        if rc == -3 and need != room:
+            room = need
+            continue
+        _check(rc, "fa_plan_prefill_host")
+        return cta[:counts[0].value + 1], items[:need[0]], merge[:need[1]], counts[3].value
 
 
 class BatchDecodeWithPagedKVCacheWrapper:

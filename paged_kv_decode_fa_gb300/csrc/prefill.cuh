@@ -1,0 +1,497 @@
+// Causal attention of packed query rows over the paged KV cache, on the
+// fifth-generation tensor cores (tcgen05).
+//
+// The mathematics.  Row r of a request (its last n tokens are the query rows) at
+// position p = len - n + r sees the keys t <= p:
+//     o_r = sum_t w_t v_t / sum_t w_t,   w_t = 2^(c q_r . k_t - m),
+// c = sm_scale log2 e, with a running reference m: the largest score so far, moved
+// only when a tile's maximum passes it by more than 2^8 (an exact rescale of o and
+// of the sum), so that weights stay within 2^8 and the division at the end
+// removes m.  lse = (m + log2 sum) ln 2.
+//
+// Work.  An item is one kv head, up to 256 rows of one request and a range of
+// its 128-token tiles.  Rows are (token, query head of the group), a token's heads
+// together, so that a K/V tile serves the whole group and a tile of 128 rows
+// spans 128 / group tokens: two blocks A and B of 128 rows share every tile, and
+// while one block's softmax runs the tensor cores work for the other.  The grid
+// is persistent, one CTA per SM, with the plan's list of items for each CTA:
+//  - warp 9 loads K and V tiles into one ring, K(0) V(0) K(1) V(1) ..., by tensor
+//    copies of 16 tokens x 64 dims (one half of a page's rows of the head, 128-byte
+//    swizzled); its lanes issue a tile's copies side by side.  Pages behind the
+//    item's last visible token come from an out-of-range index: zeros.
+//  - warp 10 loads the blocks' Q (rows of a token's group adjacent in the tensor,
+//    so a block is one box of tokens x heads x 64 dims).
+//  - warp 8 issues the MMAs: S = Q K^T (M 128, N 128) into the block's score
+//    columns of TMEM, O += P V with P from TMEM and V MN-major from its slot.  Order:
+//    S_A(0) S_B(0), then per tile P V_A(j) S_A(j+1) P V_B(j) S_B(j+1).
+//    MMAs complete in order, so a block's scores of tile j+1 being there also means
+//    that its O holds the tiles up to j.
+//  - warps 0-3 and 4-7, the softmax of A and B: a thread per row = TMEM lane.  It
+//    reads its 128 scores, writes its weights as packed pairs over the first 64 of
+//    the score columns, rescales its row of O when its reference moves, and at the
+//    item's end writes the row: o and lse, or an fp32 partial state where the plan
+//    split the item's keys (folded by fa_prefill_merge_kernel).
+// Items follow each other without a barrier across the CTA: the loads and the first
+// scores of an item run under the softmax and the output of the one before.
+//
+// Slots behind the item's last visible token may hold anything: their scores are
+// replaced (select, not add), and their V rows are cleared in shared memory before
+// the tile's P V (0 * NaN would be NaN).
+//
+// Every wait is bounded (2 s); a wait that runs out sets bit 1 of the device-check
+// word and the CTA drains.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "decode_mma.cuh"
+#include "tcgen05.cuh"
+
+namespace fadecode {
+namespace pf {
+
+constexpr int kRows = 128;                       // rows of a block
+constexpr int kTok = 128;                        // tokens of a tile
+constexpr int kPages = kTok / kPageSize;         // 8
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleAbove = 8.f;             // log2 units
+constexpr int kItemInts = 8;
+
+struct Params {
+  const int32_t* cta_offsets;  // [CTAs + 1]
+  const int32_t* items;        // [n * 8], see Item
+  const int32_t* indices;      // page ids, or nullptr: entry i of the table is page i
+  void* o;                     // [rows, Hq, D]
+  float* lse;                  // [rows, Hq] or nullptr
+  float* part_o;               // [slots][256][D] normalised
+  float* part_lse;             // [slots][256] log2 units
+  int* err;
+  int64_t num_pages;
+  int num_qo_heads;
+  int group;
+  float scale;    // sm_scale * k_scale * log2(e) (> 0)
+  float v_scale;  // times o
+  const float* head_k_scales;  // [Hkv] times scale, or nullptr
+  const float* head_v_scales;  // [Hkv] times v_scale, or nullptr
+};
+
+// One item of a CTA's list.
+struct Item {
+  int row0;    // first query token (row of q)
+  int tokens;  // query tokens, 256 / group at most
+  int pos0;    // position of the first
+  int entry;   // the request's first entry of the page table
+  int t0, t1;  // its tiles
+  int slot;    // partial state, or -1: the whole range of keys is here
+  int head;    // kv head
+  __device__ __forceinline__ static Item load(const int32_t* items, int i) {
+    const int4 a = __ldg(reinterpret_cast<const int4*>(items) + 2 * i);
+    const int4 b = __ldg(reinterpret_cast<const int4*>(items) + 2 * i + 1);
+    return Item{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  }
+  // keys the block's last row sees, and the item's tiles that hold any
+  __device__ __forceinline__ int keys(int block, int block_tokens) const {
+    return pos0 + min(tokens, (block + 1) * block_tokens);
+  }
+  __device__ __forceinline__ int tiles(int block, int block_tokens) const {
+    if (block * block_tokens >= tokens) return 0;
+    return max(0, min(t1, (keys(block, block_tokens) + kTok - 1) / kTok) - t0);
+  }
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kHalf = kTok * 128;              // [128 tokens][64 dims]
+  static constexpr int kSlotBytes = kHalves * kHalf;    // one tile of K or V
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kQBytes = kHalves * kRows * 128;  // one block's Q
+  static constexpr int kOffRing = 2 * kQBytes;
+  static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
+  // kv_full[n], kv_empty[n]; q_full, q_empty, s_full, p_full, o_full, o_empty [2]
+  static constexpr int kNumBars = 2 * kSlots + 12;
+  static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
+  static constexpr int kBytes = kOffTmem + 16 + 1024;    // and the alignment to 1024
+  static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+};
+
+}  // namespace pf
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_plain(uint32_t dst, const CUtensorMap* map, int c0,
+                                                  int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(pf::kThreads, 1)
+    fa_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
+                      const __grid_constant__ CUtensorMap kv_map,
+                      const __grid_constant__ pf::Params p) {
+  using namespace pf;
+  using namespace tc;
+  using S = Smem<D>;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr uint32_t kIdescQK = instr_desc(kBf16, kRows, kTok, 0);
+  constexpr uint32_t kIdescPV = instr_desc(kBf16, kRows, D, 1);
+  constexpr int kSlots = S::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (dev::smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = dev::smem_addr(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
+  uint64_t* kv_full = bars;
+  uint64_t* kv_empty = bars + kSlots;
+  uint64_t* q_full = bars + 2 * kSlots;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_full + 4;
+  uint64_t* p_full = q_full + 6;
+  uint64_t* o_full = q_full + 8;
+  uint64_t* o_empty = q_full + 10;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffTmem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int first = p.cta_offsets[blockIdx.x], last = p.cta_offsets[blockIdx.x + 1];
+  const int block_tokens = kRows / p.group;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      dev::mbar_init(dev::smem_addr(&kv_full[s]), 1);
+      dev::mbar_init(dev::smem_addr(&kv_empty[s]), 1);
+    }
+    for (int X = 0; X < 2; ++X) {
+      dev::mbar_init(dev::smem_addr(&q_full[X]), 1);
+      dev::mbar_init(dev::smem_addr(&q_empty[X]), 1);
+      dev::mbar_init(dev::smem_addr(&s_full[X]), 1);
+      dev::mbar_init(dev::smem_addr(&p_full[X]), 4);
+      dev::mbar_init(dev::smem_addr(&o_full[X]), 1);
+      dev::mbar_init(dev::smem_addr(&o_empty[X]), 4);
+    }
+    dev::fence_barrier_init();
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     dev::smem_addr(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;  // S of block X at X * 128, O at 256 + X * 128
+  bool aborted = false;
+
+  if (warp == 9) {
+    // ------------------------------------------------------------ K and V loads
+    if (lane == 0) dev::prefetch_tensormap(&kv_map);
+    const int oob = (int)(2 * p.num_pages);  // beyond the last page: zeros
+    int n = 0;                               // slots filled
+    for (int it = first; it < last; ++it) {
+      const Item w = Item::load(p.items, it);
+      const int nblk = w.tokens > block_tokens ? 2 : 1;
+      const int keys = w.keys(nblk - 1, block_tokens), tiles = w.tiles(nblk - 1, block_tokens);
+      const int pages = (min(keys, w.t1 * kTok) + kPageSize - 1) / kPageSize;
+      int ids = 0;
+      for (int j = 0; j < tiles; ++j) {
+        const int page0 = (w.t0 + j) * kPages;
+        if (j % (32 / kPages) == 0) {  // the page ids of four tiles
+          const int at = page0 + lane;
+          ids = oob;
+          if (at < pages) {
+            const int id = p.indices ? __ldg(p.indices + w.entry + at) : w.entry + at;
+            if (id < 0 || (int64_t)id >= p.num_pages) {
+              atomicOr(p.err, 1);
+            } else {
+              ids = 2 * id;
+            }
+          }
+        }
+        // lane l: half l % kHalves of the tile's page l / kHalves
+        const int id = __shfl_sync(0xffffffffu, ids, (j * kPages) % 32 + (lane / S::kHalves) % kPages);
+        const uint32_t at = (uint32_t)(lane % S::kHalves) * S::kHalf +
+                            (uint32_t)(lane / S::kHalves) * (kPageSize * 128);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const int s = n % kSlots;
+          const uint32_t full = dev::smem_addr(&kv_full[s]);
+          dev::mbar_wait(dev::smem_addr(&kv_empty[s]), (uint32_t)(((n / kSlots) & 1) ^ 1), aborted,
+                         p.err);
+          if (lane == 0) dev::mbar_arrive_expect_tx(full, S::kSlotBytes);
+          __syncwarp();
+          if (lane < kPages * S::kHalves)
+            tma_load_4d_plain(sbase + S::kOffRing + s * S::kSlotBytes + at, &kv_map,
+                              (lane % S::kHalves) * 64, w.head, 0, id < oob ? id + kv : oob, full);
+        }
+      }
+      aborted = __any_sync(0xffffffffu, aborted);
+    }
+    // no copy may still be landing when the CTA exits
+    if (lane == 0)
+      for (int i = n > kSlots ? n - kSlots : 0; i < n; ++i)
+        if (!dev::mbar_wait_bounded(dev::smem_addr(&kv_full[i % kSlots]),
+                                    (uint32_t)((i / kSlots) & 1)))
+          atomicOr(p.err, 2);
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ Q loads
+    if (lane == 0) {
+      dev::prefetch_tensormap(&q_map);
+      int n[2] = {0, 0};
+      for (int it = first; it < last; ++it) {
+        const Item w = Item::load(p.items, it);
+        for (int X = 0; X < 2; ++X) {
+          if (w.tiles(X, block_tokens) == 0) continue;
+          const uint32_t full = dev::smem_addr(&q_full[X]);
+          dev::mbar_wait(dev::smem_addr(&q_empty[X]), (uint32_t)((n[X] & 1) ^ 1), aborted, p.err);
+          dev::mbar_arrive_expect_tx(full, S::kQBytes);
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_load_3d(sbase + X * S::kQBytes + h * (kRows * 128), &q_map, h * 64,
+                        w.head * p.group, w.row0 + X * block_tokens, full);
+          ++n[X];
+        }
+      }
+      for (int X = 0; X < 2; ++X)
+        if (n[X] > 0 &&
+            !dev::mbar_wait_bounded(dev::smem_addr(&q_full[X]), (uint32_t)((n[X] - 1) & 1)))
+          atomicOr(p.err, 2);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMAs
+    int n = 0;                    // ring slots consumed by earlier items
+    int q_n[2] = {0, 0};          // items so far, per block
+    int tile_n[2] = {0, 0};       // tiles so far, per block
+    for (int it = first; it < last; ++it) {
+      const Item w = Item::load(p.items, it);
+      const int tiles[2] = {w.tiles(0, block_tokens), w.tiles(1, block_tokens)};
+      const int last_block = w.tokens > block_tokens ? 1 : 0;  // sees the most tiles
+      const int keys = w.keys(last_block, block_tokens), all = tiles[last_block];
+      auto qk = [&](int X, int j) {
+        const int i = n + 2 * j, s = i % kSlots;
+        dev::mbar_wait(dev::smem_addr(&kv_full[s]), (uint32_t)((i / kSlots) & 1), aborted, p.err);
+        fence_after();
+        const uint32_t q_addr = sbase + X * S::kQBytes;
+        const uint32_t k_addr = sbase + S::kOffRing + s * S::kSlotBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {  // 16 dims an MMA, 64 a 128-byte half
+          const uint32_t off = (uint32_t)(k % 4) * 32;
+          umma(tmem + X * 128, smem_desc(q_addr + (k / 4) * (kRows * 128) + off, 16, 1024),
+               smem_desc(k_addr + (k / 4) * S::kHalf + off, 16, 1024), kIdescQK, k > 0);
+        }
+        commit(&s_full[X]);
+        if (X == last_block) commit(&kv_empty[s]);
+        if (j == tiles[X] - 1) commit(&q_empty[X]);
+      };
+      for (int X = 0; X < 2; ++X) {
+        if (tiles[X] == 0) continue;
+        dev::mbar_wait(dev::smem_addr(&q_full[X]), (uint32_t)(q_n[X] & 1), aborted, p.err);
+        qk(X, 0);
+      }
+      for (int j = 0; j < all; ++j) {
+        const int i = n + 2 * j + 1, s = i % kSlots;
+        const uint32_t v_addr = sbase + S::kOffRing + s * S::kSlotBytes;
+        dev::mbar_wait(dev::smem_addr(&kv_full[s]), (uint32_t)((i / kSlots) & 1), aborted, p.err);
+        // rows of the last page behind the last visible token
+        const int tail = keys - (w.t0 + j) * kTok;
+        if (tail < kTok && tail % kPageSize) {
+          const int rows = kPageSize - tail % kPageSize;
+          for (int e = lane; e < rows * 8 * S::kHalves; e += 32) {
+            const int r = tail + e / (8 * S::kHalves), c = e % (8 * S::kHalves);
+            const uint32_t a = v_addr + (c / 8) * S::kHalf + r * 128 + (c % 8) * 16;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+#pragma unroll
+        for (int X = 0; X < 2; ++X) {
+          if (j >= tiles[X]) continue;
+          dev::mbar_wait(dev::smem_addr(&p_full[X]), (uint32_t)(tile_n[X] & 1), aborted, p.err);
+          if (j == 0)  // the output of the block's item before has been read
+            dev::mbar_wait(dev::smem_addr(&o_empty[X]), (uint32_t)((q_n[X] & 1) ^ 1), aborted,
+                           p.err);
+          fence_after();
+          ++tile_n[X];
+#pragma unroll
+          for (int k = 0; k < kTok / 16; ++k)  // 16 tokens (8 columns of P) an MMA
+            umma_ts(tmem + 256 + X * 128, tmem + X * 128 + k * 8,
+                    smem_desc(v_addr + k * 16 * 128, S::kHalf, 1024), kIdescPV, j > 0 || k > 0);
+          if (X == last_block) commit(&kv_empty[s]);
+          if (j + 1 < tiles[X])
+            qk(X, j + 1);
+          else
+            commit(&o_full[X]);
+        }
+        aborted = __any_sync(0xffffffffu, aborted);
+      }
+      n += 2 * all;
+      for (int X = 0; X < 2; ++X) q_n[X] += tiles[X] > 0;
+    }
+    // TMEM is freed only after the last MMA completed
+    for (int X = 0; X < 2; ++X)
+      if (q_n[X] > 0 &&
+          !dev::mbar_wait_bounded(dev::smem_addr(&o_full[X]), (uint32_t)((q_n[X] - 1) & 1)) &&
+          lane == 0)
+        atomicOr(p.err, 2);
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax and output
+    const int X = warp / 4, r = threadIdx.x % kRows;
+    const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
+    const uint32_t tS = tmem + X * 128 + lane_off, tO = tmem + 256 + X * 128 + lane_off;
+    const int tok = X * block_tokens + r / p.group, g = r % p.group;
+    int tile_n = 0, item_n = 0;
+    for (int it = first; it < last; ++it) {
+      const Item w = Item::load(p.items, it);
+      if (X * block_tokens >= w.tokens) continue;
+      const int tiles = w.tiles(X, block_tokens);
+      // keys this row sees, from the item's first tile on; the warp's fewest
+      const int seen = w.pos0 + tok + 1 - w.t0 * kTok;
+      const int fewest = __shfl_sync(0xffffffffu, seen, 0);
+      // (kept above 0: 0 times a masked score's -inf would be NaN)
+      const float scale =
+          fmaxf(p.head_k_scales ? p.scale * __ldg(p.head_k_scales + w.head) : p.scale, 1.2e-38f);
+      float m = -INFINITY, d = 0.f;
+      for (int j = 0; j < tiles; ++j, ++tile_n) {
+        dev::mbar_wait(dev::smem_addr(&s_full[X]), (uint32_t)(tile_n & 1), aborted, p.err);
+        fence_after();
+        float s[kTok];
+#pragma unroll
+        for (int c = 0; c < kTok / 32; ++c) {
+          float v[32];
+          ld32(tS + c * 32, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[c * 32 + i] = v[i];
+        }
+        if (fewest < (j + 1) * kTok) {
+          const int valid = seen - j * kTok;
+#pragma unroll
+          for (int i = 0; i < kTok; ++i)
+            if (i >= valid) s[i] = -INFINITY;
+        }
+        float m8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float a = s[16 * k];
+#pragma unroll
+          for (int i = 1; i < 15; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
+          m8[k] = fmaxf(a, s[16 * k + 15]);
+        }
+        const float mt = scale * fmaxf(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[4]),
+                                       max3(m8[5], m8[6], m8[7]));
+        // the reference moves only when the maximum passes it by more than 2^8
+        const bool rebase = mt > m + kRescaleAbove;
+        const float m_new = rebase ? mt : m;
+        const float alpha = m == -INFINITY ? 0.f : dev::fast_exp2(m - m_new);
+        if (j > 0 && __any_sync(0xffffffffu, rebase)) {
+          // O holds the tiles before j
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            ld32(tO + c * 32, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = rebase ? (m == -INFINITY ? 0.f : v[i] * alpha) : v[i];
+            st32(tO + c * 32, v);
+          }
+        }
+        if (rebase) {
+          d *= alpha;
+          m = m_new;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const uint64_t scale2 = f2(scale, scale), neg_m2 = f2(-ref, -ref);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < kTok / 64; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x0, x1;
+            f2_split(fma2(f2(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), scale2, neg_m2), x0, x1);
+            const float a0 = dev::fast_exp2(x0), a1 = dev::fast_exp2(x1);
+            pk[i] = mma::pack2(a0, a1, kBf16);
+            acc[i % 4] = add2(acc[i % 4], f2(a0, a1));
+          }
+          st32u(tS + c * 32, pk);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(dev::smem_addr(&p_full[X]));
+        float lo, hi;
+        f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), lo, hi);
+        d += lo + hi;
+      }
+      // ---- the row's output
+      if (tiles > 0) {
+        dev::mbar_wait(dev::smem_addr(&o_full[X]), (uint32_t)(item_n & 1), aborted, p.err);
+        fence_after();
+      }
+      const bool ok = tok < w.tokens;
+      const float v_scale = p.head_v_scales ? p.v_scale * __ldg(p.head_v_scales + w.head) : p.v_scale;
+      const float inv = d > 0.f || d != d ? v_scale / d : 0.f;
+      const float lse = d > 0.f || d != d ? m + log2f(d) : -INFINITY;
+      const size_t row = (size_t)(w.row0 + tok) * p.num_qo_heads + (size_t)w.head * p.group + g;
+      const size_t part = (size_t)(w.slot < 0 ? 0 : w.slot) * 256 + X * kRows + r;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32];
+        if (tiles > 0) {
+          ld32(tO + c * 32, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        if (ok && w.slot < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * D + c * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(mma::pack2(v[8 * i] * inv, v[8 * i + 1] * inv, kBf16),
+                                mma::pack2(v[8 * i + 2] * inv, v[8 * i + 3] * inv, kBf16),
+                                mma::pack2(v[8 * i + 4] * inv, v[8 * i + 5] * inv, kBf16),
+                                mma::pack2(v[8 * i + 6] * inv, v[8 * i + 7] * inv, kBf16));
+        } else if (ok) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv,
+                                 v[4 * i + 3] * inv);
+        }
+        __syncwarp();
+      }
+      if (tiles > 0) {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(dev::smem_addr(&o_empty[X]));
+        ++item_n;
+      }
+      if (ok) {
+        if (w.slot >= 0)
+          p.part_lse[part] = lse;
+        else if (p.lse)
+          p.lse[row] = lse * dev::kLn2;
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+}  // namespace fadecode
