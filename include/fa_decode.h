@@ -801,6 +801,117 @@ int fa_plan_prefill_host(const int32_t* indptr_host, const int32_t* last_page_le
                          int32_t* merge, int merge_room, int* num_ctas, int* num_items,
                          int* num_merge, int* num_slots);
 
+/* ---- accumulated attention weights, and eviction by them -------------------
+ *
+ * A cache kept to a budget of tokens: fa_weights_run adds to every cached token, per
+ * kv head, the softmax weight that a batch of query rows gave it; fa_evict_run
+ * keeps each kv head's most attended and most recent tokens and moves them to
+ * the front of the request's pages.  weights [num_pages, num_kv_heads, page_size]
+ * float32, device, is the caller's: 0 for slots that hold no token yet. */
+typedef struct fa_weights_plan_s* fa_weights_plan_t;
+
+/* Upper bound of the workspace fa_weights_plan needs for a batch over total_pages
+ * entries of the page table (indptr[batch]); 0 for invalid arguments. */
+size_t fa_weights_workspace_size(int batch, int64_t total_pages);
+
+/* plan: arguments as fa_prefill_plan, with any n_i >= 0 (rows before a request's
+ * first token see nothing): one row a request after a decode step, or the rows
+ * of a prompt or of its last tokens.  Built for page_size 16, head_dim 64 and 128,
+ * groups 1, 2, 4, 8 and (q, kv) = (BF16, BF16), (F16, F16), (BF16, E4M3),
+ * (F16, E4M3).  Errors as fa_decode_plan. */
+int fa_weights_plan(const int32_t* indptr_host, const int32_t* indices_dev,
+                    const int32_t* last_page_len_host, const int32_t* qo_indptr_host, int batch,
+                    int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
+                    fa_dtype q_dtype, fa_dtype kv_dtype, void* workspace_dev,
+                    size_t workspace_bytes, void* cuda_stream, fa_weights_plan_t* out_plan);
+
+/* run: weights[p, h, s] += the sum over the rows that see the token at page p, slot
+ * s, and over the query heads of kv head h, of exp(sm_scale q . k - lse).
+ *
+ *  q         [rows, num_qo_heads, head_dim], as fa_prefill_run.
+ *  paged_kv, num_pages, sm_scale: as fa_decode_run; only K is read.  A page id
+ *            outside [0, num_pages) is skipped and sets the device-check word.
+ *  k_scale   per-tensor scale of an E4M3 cache's K; 1 for other kv types.
+ *  lse       [rows, num_qo_heads] float32, device: what the attention of these rows
+ *            returned (natural log); a row of -inf adds nothing.
+ *  weights   read and written, as above.
+ * One kernel on cuda_stream, no allocation, no synchronisation.  Each token gets one
+ * addition a run, so results are bitwise reproducible, but for pages that two
+ * requests (or two entries of one) share: they get all their requests' weights, in
+ * no fixed order of the fp32 additions.
+ * Errors as fa_prefill_run. */
+int fa_weights_run(fa_weights_plan_t plan, const fa_rows* q, const void* paged_kv,
+                   int64_t num_pages, float sm_scale, float k_scale, const float* lse,
+                   float* weights, void* cuda_stream);
+
+/* run over an E4M3 cache with K scales per kv head, per token or per block, as
+ * fa_decode_run_head_scales, fa_decode_run_token_scales and
+ * fa_decode_run_block_scales read them. */
+int fa_weights_run_head_scales(fa_weights_plan_t plan, const fa_rows* q, const void* paged_kv,
+                               int64_t num_pages, float sm_scale, const float* k_head_scales,
+                               const float* lse, float* weights, void* cuda_stream);
+int fa_weights_run_token_scales(fa_weights_plan_t plan, const fa_rows* q, const void* paged_kv,
+                                int64_t num_pages, float sm_scale, const float* k_scales,
+                                const float* lse, float* weights, void* cuda_stream);
+int fa_weights_run_block_scales(fa_weights_plan_t plan, const fa_rows* q, const void* paged_kv,
+                                int64_t num_pages, float sm_scale, const float* k_scales,
+                                const float* lse, float* weights, void* cuda_stream);
+
+/* As fa_decode_check, for a weights plan. */
+int fa_weights_check(fa_weights_plan_t plan, void* cuda_stream, int* flags);
+
+int fa_weights_plan_destroy(fa_weights_plan_t plan);
+
+typedef struct fa_evict_plan_s* fa_evict_plan_t;
+
+/* Upper bound of the workspace fa_evict_plan needs for a batch that keeps
+ * total_kept tokens; 0 for invalid arguments. */
+size_t fa_evict_workspace_size(int batch, int64_t total_kept, int num_kv_heads);
+
+/* plan: which requests lose tokens.
+ *
+ *  indptr_host, indices_dev, last_page_len_host, page_size, workspace, stream: as
+ *               fa_decode_plan.  indices_dev is kept by pointer.  A request's
+ *               pages are its own: the call writes them.
+ *  keep_host    [batch] int32, host, >= 0: tokens a request keeps, n_i = min(len_i,
+ *               keep_i).  A request of keep_i tokens or fewer is left alone.
+ *  recent_host  [batch] int32, host, >= 0, or NULL (0): of those, the last
+ *               min(recent_i, keep_i) tokens stay whatever their weight.
+ * Afterwards request i holds n_i tokens: ceil(n_i / page_size) pages of its list,
+ * the others are free.  Built for page_size 16, head_dim 64 and 128 and every kv
+ * type.  Errors as fa_decode_plan. */
+int fa_evict_plan(const int32_t* indptr_host, const int32_t* indices_dev,
+                  const int32_t* last_page_len_host, const int32_t* keep_host,
+                  const int32_t* recent_host, int batch, int num_kv_heads, int head_dim,
+                  int page_size, fa_dtype kv_dtype, void* workspace_dev, size_t workspace_bytes,
+                  void* cuda_stream, fa_evict_plan_t* out_plan);
+
+/* run: per kv head, the kept tokens (the recent ones and, of those before, the ones
+ * of largest weight; equal weights keep the earlier token, NaN counts as largest)
+ * move in their order to the request's first n_i slots, with their weights; the
+ * weights of slots n_i .. len_i - 1 become 0.  The kv heads of a request keep tokens
+ * of their own, all of them n_i.  K was rotated when it was appended, so tokens
+ * keep the positions they had; later tokens are appended with a position_offset
+ * (or positions) that counts the evicted ones.
+ *
+ *  paged_kv   as fa_append_run, read and written.  Tokens on a page id outside
+ *             [0, num_pages) are not moved, and set the device-check word.
+ *  weights    as above, read and written.
+ *  k_scales,  [num_pages, num_kv_heads, page_size] float32, device: the scales of an
+ *  v_scales   E4M3 cache that has one per token, moved with the tokens; NULL for
+ *             caches without (FA_ERR_UNSUPPORTED for other types).  A cache with
+ *             scales per block cannot be evicted from: its tokens share theirs.
+ * One kernel on cuda_stream, no allocation, no synchronisation.  Slots
+ * n_i .. len_i - 1 of the cache keep what they held.  Two runs that may be in flight together need two plans and workspaces.
+ * Errors: as fa_append_run. */
+int fa_evict_run(fa_evict_plan_t plan, void* paged_kv, int64_t num_pages, float* weights,
+                 float* k_scales, float* v_scales, void* cuda_stream);
+
+/* As fa_decode_check, for an evict plan. */
+int fa_evict_check(fa_evict_plan_t plan, void* cuda_stream, int* flags);
+
+int fa_evict_plan_destroy(fa_evict_plan_t plan);
+
 /* ---- cascade decode (shared prefix) ------------------------------------
  *
  * A batch whose requests all begin with the same shared prefix (whole pages,

@@ -25,6 +25,7 @@ __all__ = [
     "CascadePlan", "cascade_plan",
     "RotaryTable", "AppendPlan", "plan_append", "append_workspace_size",
     "PrefillPlan", "plan_prefill", "plan_prefill_host",
+    "WeightsPlan", "plan_weights", "EvictPlan", "plan_evict",
     "workspace_size", "plan_work_host", "plan_work_host_buckets",
     "BatchDecodeWithPagedKVCacheWrapper",
     "LIB_PATH", "EXPORTED_SYMBOLS", "library", "library_stats",
@@ -53,6 +54,10 @@ EXPORTED_SYMBOLS = (
     "fa_prefill_workspace_size", "fa_prefill_plan", "fa_prefill_run", "fa_prefill_run_head_scales",
     "fa_prefill_run_token_scales", "fa_prefill_run_block_scales", "fa_prefill_check",
     "fa_prefill_plan_destroy", "fa_plan_prefill_host",
+    "fa_weights_workspace_size", "fa_weights_plan", "fa_weights_run", "fa_weights_run_head_scales",
+    "fa_weights_run_token_scales", "fa_weights_run_block_scales", "fa_weights_check",
+    "fa_weights_plan_destroy", "fa_evict_workspace_size", "fa_evict_plan", "fa_evict_run",
+    "fa_evict_check", "fa_evict_plan_destroy",
 )
 
 FA_OK = 0
@@ -143,6 +148,32 @@ def _load() -> ctypes.CDLL:
     lib.fa_append_plan_axes.argtypes = [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, i32,
                                         P, i32, i32, P, sz, P, ctypes.POINTER(P)]
     lib.fa_append_plan_axes.restype = i32
+    lib.fa_weights_workspace_size.argtypes = [i32, i64]
+    lib.fa_weights_workspace_size.restype = sz
+    lib.fa_weights_plan.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, sz, P,
+                                    ctypes.POINTER(P)]
+    lib.fa_weights_plan.restype = i32
+    lib.fa_weights_run.argtypes = [P, P, P, i64, f32, f32, P, P, P]
+    lib.fa_weights_run.restype = i32
+    for name in ("fa_weights_run_head_scales", "fa_weights_run_token_scales",
+                 "fa_weights_run_block_scales"):
+        f = getattr(lib, name)
+        f.argtypes = [P, P, P, i64, f32, P, P, P, P]
+        f.restype = i32
+    lib.fa_evict_workspace_size.argtypes = [i32, i64, i32]
+    lib.fa_evict_workspace_size.restype = sz
+    lib.fa_evict_plan.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, P, sz, P,
+                                  ctypes.POINTER(P)]
+    lib.fa_evict_plan.restype = i32
+    lib.fa_evict_run.argtypes = [P, P, i64, P, P, P, P]
+    lib.fa_evict_run.restype = i32
+    for kind in ("weights", "evict"):
+        f = getattr(lib, f"fa_{kind}_check")
+        f.argtypes = [P, P, ctypes.POINTER(i32)]
+        f.restype = i32
+        f = getattr(lib, f"fa_{kind}_plan_destroy")
+        f.argtypes = [P]
+        f.restype = i32
     lib.fa_prefill_workspace_size.argtypes = [P, P, P, i32, i32, i32, i32, i32, i32]
     lib.fa_prefill_workspace_size.restype = sz
     lib.fa_prefill_plan.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, sz, P,
@@ -1144,6 +1175,19 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
                       (B, num_qo_heads, num_kv_heads, head_dim, page_size), total)
 
 
+def _q_rows(q: torch.Tensor):
+    """The fa_rows of a q [rows, heads, head_dim]."""
+    token, head, inner = q.stride()
+    # a stride that is never taken may be anything
+    token = token if q.shape[0] > 1 else 0
+    head = head if q.shape[1] > 1 else 0
+    if q.numel() and (inner != 1 or (q.data_ptr() | (token | head) * q.element_size()) & 15
+                      or (q.shape[0] > 1 and token <= 0) or (q.shape[1] > 1 and head <= 0)):
+        raise ValueError("q needs a contiguous innermost dim, and an address and strides in "
+                         "whole 16 bytes")
+    return _Rows(q.data_ptr(), token, head)
+
+
 class PrefillPlan:
     """Planned attention of packed query rows (prompts, chunks of prompts, single
     tokens) over their requests' pages.  Keeps the index tensor and the
@@ -1220,11 +1264,7 @@ class PrefillPlan:
             raise TypeError("q / paged_kv dtype differs from the plan")
         if q.shape != self._q_shape or q.get_device() != self._device:
             raise ValueError(f"q must be a tensor {list(self._q_shape)} on the plan's device")
-        token, head, inner = q.stride()
-        if q.numel() and (inner != 1 or (q.shape[0] > 1 and (token <= 0 or token % 8))
-                          or (q.shape[1] > 1 and (head <= 0 or head % 8)) or q.data_ptr() % 16):
-            raise ValueError("q needs a contiguous innermost dim, and an address and strides in "
-                             "whole 16 bytes")
+        rows = _q_rows(q)
         if (paged_kv.dim() != 5 or paged_kv.shape[1:] != self._page_shape
                 or not paged_kv.is_contiguous() or paged_kv.get_device() != self._device):
             raise ValueError("paged_kv must be a contiguous tensor [num_pages, 2, page_size, "
@@ -1240,8 +1280,7 @@ class PrefillPlan:
                 raise ValueError("out / lse must be contiguous, on the plan's device")
         if nbytes and out.data_ptr() < q.data_ptr() + nbytes and q.data_ptr() < out.data_ptr() + nbytes:
             raise ValueError("out must not overlap q")
-        return _Rows(q.data_ptr(), token if q.shape[0] > 1 else 0, head if q.shape[1] > 1 else 0), \
-            out, lse
+        return rows, out, lse
 
     def check(self, stream=None) -> int:
         """Synchronise and return the device-check flags (0 = clean)."""
@@ -1267,17 +1306,11 @@ def plan_prefill(indptr, indices: torch.Tensor, last_page_len, qo_indptr, num_qo
     if B < 0 or n_last < B or n_qo != B + 1:
         raise ValueError("last_page_len shorter than the batch, or qo_indptr not batch + 1 long")
     _check_indices(indices, indptr_p, B)
-    device = torch.cuda.current_device()
-    if indices.is_cuda and indices.get_device() != device:
-        raise ValueError("indices must be on the current device")
     q_code, kv_code = _dtype_code(q_data_type), _dtype_code(kv_data_type)
-    if workspace is None:
-        n = _L().fa_prefill_workspace_size(indptr_p, last_p if B else None, qo_p, B, num_qo_heads,
-                                           num_kv_heads, head_dim, q_code, kv_code)
-        # 0 for refused arguments, which the plan names
-        workspace = _empty(max(int(n), 256), torch.uint8, _cuda_device(indices), stream)
-    elif workspace.get_device() != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the current device")
+    workspace = _plan_workspace(
+        workspace, indices, lambda: _L().fa_prefill_workspace_size(
+            indptr_p, last_p if B else None, qo_p, B, num_qo_heads, num_kv_heads, head_dim, q_code,
+            kv_code), stream)
     handle = ctypes.c_void_p()
     _check(_L().fa_prefill_plan(
         indptr_p, indices.data_ptr() if indices.numel() else None, last_p if B else None, qo_p, B,
@@ -1313,6 +1346,258 @@ def plan_prefill_host(indptr, last_page_len, qo_indptr, group: int, num_kv_heads
             continue
         _check(rc, "fa_plan_prefill_host")
         return cta[:counts[0].value + 1], items[:need[0]], merge[:need[1]], counts[3].value
+
+
+class WeightsPlan:
+    """A planned accumulation of attention weights over a batch's cached tokens.
+    Keeps the index tensor and the workspace alive."""
+
+    def __init__(self, handle, indices, workspace, q_dtype, kv_dtype, shape, num_tokens):
+        self._h = handle
+        self._keep = (indices, workspace)
+        self.q_dtype = q_dtype
+        self.kv_dtype = kv_dtype
+        self.batch, self.num_qo_heads, self.num_kv_heads, self.head_dim, self.page_size = shape
+        self.num_tokens = num_tokens
+        self._device = workspace.get_device()
+        self._q_shape = (num_tokens, self.num_qo_heads, self.head_dim)
+        self._page_shape = (2, self.page_size, self.num_kv_heads, self.head_dim)
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h:
+            _L().fa_weights_plan_destroy(h)
+            self._h = None
+
+    def run(self, q: torch.Tensor, paged_kv: torch.Tensor, lse: torch.Tensor,
+            weights: torch.Tensor, *, sm_scale: float | None = None, k_scale: float = 1.0,
+            stream=None) -> torch.Tensor:
+        """Add to weights [num_pages, num_kv_heads, page_size] float32 what the rows
+        q [rows, Hq, D] gave each token; lse [rows, Hq] is what their attention
+        returned.  Returns weights."""
+        rows = self._checked(q, paged_kv, lse, weights)
+        _check(_L().fa_weights_run(
+            self._h, ctypes.addressof(rows), paged_kv.data_ptr(), paged_kv.shape[0],
+            0.0 if sm_scale is None else float(sm_scale), float(k_scale), lse.data_ptr(),
+            weights.data_ptr(), _stream_handle(stream)), "fa_weights_run")
+        return weights
+
+    def run_head_scales(self, q: torch.Tensor, paged_kv: torch.Tensor, lse: torch.Tensor,
+                        weights: torch.Tensor, k_scales: torch.Tensor, **kw) -> torch.Tensor:
+        """As run, over an E4M3 cache with one K scale per kv head [num_kv_heads]."""
+        return self._run_scales("fa_weights_run_head_scales", (self.num_kv_heads,), q, paged_kv,
+                                lse, weights, k_scales, **kw)
+
+    def run_token_scales(self, q: torch.Tensor, paged_kv: torch.Tensor, lse: torch.Tensor,
+                         weights: torch.Tensor, k_scales: torch.Tensor, **kw) -> torch.Tensor:
+        """As run, over an E4M3 cache with one K scale per token and kv head
+        [num_pages, num_kv_heads, page_size]."""
+        shape = (paged_kv.shape[0], self.num_kv_heads, self.page_size)
+        return self._run_scales("fa_weights_run_token_scales", shape, q, paged_kv, lse, weights,
+                                k_scales, **kw)
+
+    def run_block_scales(self, q: torch.Tensor, paged_kv: torch.Tensor, lse: torch.Tensor,
+                         weights: torch.Tensor, k_scales: torch.Tensor, **kw) -> torch.Tensor:
+        """As run, over an E4M3 cache with one K scale per page and kv head
+        [num_pages, num_kv_heads]."""
+        return self._run_scales("fa_weights_run_block_scales",
+                                (paged_kv.shape[0], self.num_kv_heads), q, paged_kv, lse, weights,
+                                k_scales, **kw)
+
+    def _run_scales(self, name, shape, q, paged_kv, lse, weights, k_scales, *, sm_scale=None,
+                    stream=None):
+        rows = self._checked(q, paged_kv, lse, weights)
+        _check_scales((k_scales,), shape, paged_kv)
+        _check(getattr(_L(), name)(
+            self._h, ctypes.addressof(rows), paged_kv.data_ptr(), paged_kv.shape[0],
+            0.0 if sm_scale is None else float(sm_scale), k_scales.data_ptr(), lse.data_ptr(),
+            weights.data_ptr(), _stream_handle(stream)), name)
+        return weights
+
+    def _checked(self, q, paged_kv, lse, weights):
+        if q.dtype is not self.q_dtype or paged_kv.dtype is not self.kv_dtype:
+            raise TypeError("q / paged_kv dtype differs from the plan")
+        if q.shape != self._q_shape or q.get_device() != self._device:
+            raise ValueError(f"q must be a tensor {list(self._q_shape)} on the plan's device")
+        if (paged_kv.dim() != 5 or paged_kv.shape[1:] != self._page_shape
+                or not paged_kv.is_contiguous() or paged_kv.get_device() != self._device):
+            raise ValueError("paged_kv must be a contiguous tensor [num_pages, 2, page_size, "
+                             "num_kv_heads, head_dim] on the plan's device")
+        if (lse.dtype is not torch.float32 or lse.shape != self._q_shape[:2]
+                or not lse.is_contiguous() or lse.get_device() != self._device):
+            raise ValueError(f"lse must be a contiguous float32 tensor {list(self._q_shape[:2])} "
+                             "on the plan's device")
+        _check_weights(weights, paged_kv)
+        return _q_rows(q)
+
+    def check(self, stream=None) -> int:
+        """Synchronise and return the device-check flags (0 = clean)."""
+        flags = ctypes.c_int(0)
+        st = _L().fa_weights_check(self._h, _stream_handle(stream), ctypes.byref(flags))
+        if st not in (FA_OK, -5):
+            _check(st, "fa_weights_check")
+        return int(flags.value)
+
+
+def _check_weights(weights, paged_kv) -> None:
+    shape = (paged_kv.shape[0], paged_kv.shape[3], paged_kv.shape[2])
+    if (weights.dtype is not torch.float32 or weights.shape != shape
+            or not weights.is_contiguous() or weights.get_device() != paged_kv.get_device()):
+        raise ValueError(f"weights must be a contiguous float32 tensor {list(shape)} on the device "
+                         "of paged_kv")
+
+
+def plan_weights(indptr, indices: torch.Tensor, last_page_len, qo_indptr, num_qo_heads: int,
+                 num_kv_heads: int, head_dim: int, page_size: int, *, q_data_type=torch.bfloat16,
+                 kv_data_type=None, workspace: torch.Tensor | None = None,
+                 stream=None) -> WeightsPlan:
+    """Plan the accumulation of the attention weights that qo_indptr[i+1] -
+    qo_indptr[i] query rows of request i (its last positions) give its cached
+    tokens; qo_indptr None: one row each, as after a decode step."""
+    kv_data_type = q_data_type if kv_data_type is None else kv_data_type
+    indptr_h, indptr_p, n_indptr = _host_i32_ptr(indptr)
+    last_h, last_p, n_last = _host_i32_ptr(last_page_len)
+    if qo_indptr is None:
+        qo_indptr = np.arange(n_indptr, dtype=np.int32)
+    qo_h, qo_p, n_qo = _host_i32_ptr(qo_indptr)
+    B = n_indptr - 1
+    if B < 0 or n_last < B or n_qo != B + 1:
+        raise ValueError("last_page_len shorter than the batch, or qo_indptr not batch + 1 long")
+    _check_indices(indices, indptr_p, B)
+    workspace = _plan_workspace(
+        workspace, indices, lambda: _L().fa_weights_workspace_size(B, max(_i32_at(indptr_p, B), 0)),
+        stream)
+    handle = ctypes.c_void_p()
+    _check(_L().fa_weights_plan(
+        indptr_p, indices.data_ptr() if indices.numel() else None, last_p if B else None, qo_p, B,
+        num_qo_heads, num_kv_heads, head_dim, page_size, _dtype_code(q_data_type),
+        _dtype_code(kv_data_type), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream),
+        ctypes.byref(handle)), "fa_weights_plan")
+    return WeightsPlan(handle.value, indices, workspace, q_data_type, kv_data_type,
+                       (B, num_qo_heads, num_kv_heads, head_dim, page_size), _i32_at(qo_p, B))
+
+
+def _plan_workspace(workspace, indices, size, stream) -> torch.Tensor:
+    """The caller's workspace, or one of size() bytes, on the current device."""
+    device = torch.cuda.current_device()
+    if indices.is_cuda and indices.get_device() != device:
+        raise ValueError("indices must be on the current device")
+    if workspace is None:
+        # 0 for refused arguments, which the plan names
+        return _empty(max(int(size()), 256), torch.uint8, _cuda_device(indices), stream)
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current device")
+    return workspace
+
+
+class EvictPlan:
+    """A planned eviction.  indptr, indices and last_page_len describe the batch
+    after it (indices where the plan's are), freed [n] the page ids that it no longer
+    needs.  Keeps the index tensor and the workspace alive."""
+
+    def __init__(self, handle, indices, workspace, kv_dtype, shape, after):
+        self._h = handle
+        self._keep = (indices, workspace)
+        self.kv_dtype = kv_dtype
+        self.batch, self.num_kv_heads, self.head_dim, self.page_size = shape
+        self._device = workspace.get_device()
+        self._page_shape = (2, self.page_size, self.num_kv_heads, self.head_dim)
+        self.indptr, self.indices, self.last_page_len, self.freed = after
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h:
+            _L().fa_evict_plan_destroy(h)
+            self._h = None
+
+    def run(self, paged_kv: torch.Tensor, weights: torch.Tensor, *,
+            k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
+            stream=None) -> None:
+        """Move each kv head's kept tokens to the front of its request's pages, in
+        place; weights [num_pages, num_kv_heads, page_size] float32 go with them
+        and are 0 behind them.  k_scales / v_scales: an E4M3 cache's scales per
+        token, moved too."""
+        if paged_kv.dtype is not self.kv_dtype:
+            raise TypeError("paged_kv dtype differs from the plan")
+        if (paged_kv.dim() != 5 or paged_kv.shape[1:] != self._page_shape
+                or not paged_kv.is_contiguous() or paged_kv.get_device() != self._device):
+            raise ValueError("paged_kv must be a contiguous tensor [num_pages, 2, page_size, "
+                             "num_kv_heads, head_dim] on the plan's device")
+        _check_weights(weights, paged_kv)
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("k_scales and v_scales go together")
+        if k_scales is not None:
+            _check_scales((k_scales, v_scales), weights.shape, paged_kv)
+        _check(_L().fa_evict_run(
+            self._h, paged_kv.data_ptr(), paged_kv.shape[0], weights.data_ptr(),
+            None if k_scales is None else k_scales.data_ptr(),
+            None if v_scales is None else v_scales.data_ptr(), _stream_handle(stream)),
+            "fa_evict_run")
+
+    def check(self, stream=None) -> int:
+        """Synchronise and return the device-check flags (0 = clean)."""
+        flags = ctypes.c_int(0)
+        st = _L().fa_evict_check(self._h, _stream_handle(stream), ctypes.byref(flags))
+        if st not in (FA_OK, -5):
+            _check(st, "fa_evict_check")
+        return int(flags.value)
+
+
+def _pages_after(indptr, last, kept, page_size):
+    """(indptr, last_page_len, entries that stay, entries that are freed) of a
+    batch of which request i keeps the first `kept[i]` slots at most."""
+    pages = np.diff(indptr).astype(np.int64)
+    length = np.where(pages > 0, (pages - 1) * page_size + last, 0)
+    length = np.minimum(length, kept)
+    stay = -(-length // page_size)
+    after = np.zeros(len(indptr), np.int64)
+    np.cumsum(stay, out=after[1:])
+    owner = np.repeat(np.arange(len(pages)), pages)
+    at = np.arange(int(pages.sum())) - indptr[:-1].astype(np.int64)[owner]
+    here = at < stay[owner]
+    last_after = np.where(stay > 0, length - (stay - 1) * page_size, page_size)
+    return (after.astype(np.int32), last_after.astype(np.int32), np.flatnonzero(here),
+            np.flatnonzero(~here))
+
+
+def plan_evict(indptr, indices: torch.Tensor, last_page_len, keep, num_kv_heads: int,
+               head_dim: int, page_size: int, *, recent=0, kv_data_type=torch.bfloat16,
+               workspace: torch.Tensor | None = None, stream=None) -> EvictPlan:
+    """Plan the eviction of each request's tokens beyond its budget: keep tokens stay
+    (a number, or one per request), the last `recent` of them whatever their
+    weight (likewise)."""
+    indptr_h, indptr_p, n_indptr = _host_i32_ptr(indptr)
+    last_h, last_p, n_last = _host_i32_ptr(last_page_len)
+    B = n_indptr - 1
+    if B < 0 or n_last < B:
+        raise ValueError("last_page_len shorter than the batch")
+    budgets = []
+    for v in (keep, recent):
+        a = np.full(B, v, np.int64) if np.ndim(v) == 0 else np.asarray(_host_i32(v), np.int64)
+        if a.shape != (B,) or (a < 0).any() or (a >= 2 ** 31).any():
+            raise ValueError("keep and recent must be one number, or one per request, from 0")
+        budgets.append(np.ascontiguousarray(a, np.int32))
+    _check_indices(indices, indptr_p, B)
+    total = max(_i32_at(indptr_p, B), 0) * page_size
+    workspace = _plan_workspace(
+        workspace, indices, lambda: _L().fa_evict_workspace_size(
+            B, min(int(budgets[0].sum(dtype=np.int64)), total), num_kv_heads), stream)
+    handle = ctypes.c_void_p()
+    _check(_L().fa_evict_plan(
+        indptr_p, indices.data_ptr() if indices.numel() else None, last_p if B else None,
+        budgets[0].ctypes.data if B else None, budgets[1].ctypes.data if B else None, B,
+        num_kv_heads, head_dim, page_size, _dtype_code(kv_data_type), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream),
+        ctypes.byref(handle)), "fa_evict_plan")
+    ptr, last, stay, free = _pages_after(np.asarray(indptr_h), np.asarray(last_h)[:B], budgets[0],
+                                         page_size)
+    pick = [indices[torch.from_numpy(e).to(indices.device)] for e in (stay, free)]
+    if not indices.is_cuda:
+        pick = [t.pin_memory() for t in pick]
+    return EvictPlan(handle.value, indices, workspace, kv_data_type,
+                     (B, num_kv_heads, head_dim, page_size),
+                     (torch.from_numpy(ptr), pick[0], torch.from_numpy(last), pick[1]))
 
 
 class BatchDecodeWithPagedKVCacheWrapper:

@@ -1,0 +1,471 @@
+// Eviction from a paged KV cache by accumulated attention weight: the calls
+// fa_evict_* (declared in include/fa_decode.h).
+//
+// The definition, per request of L tokens and kv head, n = min(L, keep): kept are the
+// last min(recent, n) tokens and, of those before, the n - recent of the largest
+// weight (equal weights: the earlier token).  They move, in their order, to the
+// request's first n slots: K, V, the weight and an E4M3 cache's scales per token;
+// the weights of slots n .. L-1 become 0, so that they can be appended to.
+//
+// Work.  A cluster of C CTAs (1 to 8) takes one (request, kv head):
+//  1. each CTA reads the weights of its share of the tokens, as 32-bit keys in
+//     the order of the floats (in shared memory where they fit);
+//  2. the key of the last kept token is found eight bits at a time: histograms in
+//     shared memory, summed over the cluster, four passes;
+//  3. counts of larger and equal keys, summed over the cluster's lower CTAs, give
+//     every kept token its rank; the list rank -> token goes to the workspace;
+//  4. the rows move a chunk of ranks at a time: all CTAs read the chunk's rows
+//     into shared memory, the cluster meets, all write.  A kept token's rank is at
+//     most its index, so the chunk's slots lie before every later chunk's rows:
+//     one barrier a chunk orders everything, in place, and each row is read
+//     and written once.  Rows already in their slots are left.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+#include <limits>
+#include <new>
+#include <vector>
+
+#include "decode_kernel.cuh"
+#include "fa_decode.h"
+#include "staging.h"
+
+namespace fadecode {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+constexpr int kThreads = 256;
+constexpr int kMostCtas = 8;              // of a cluster
+constexpr int kBuffer = 48 << 10;         // keys, then rows
+constexpr int kRankInfo = 512;            // ranks of a chunk at most
+
+struct EvictUnit {
+  int32_t entry, length, kept, recent;
+  int64_t list;  // its first kept token of head 0 in the workspace's lists
+  int32_t pad[2];
+};
+static_assert(sizeof(EvictUnit) == 32, "read as two int4");
+
+struct EvictParams {
+  uint8_t* kv;
+  float* weights;   // [pages, Hkv, 16]
+  float* k_scales;  // [pages, Hkv, 16] or nullptr
+  float* v_scales;
+  const int32_t* indices;
+  const EvictUnit* units;
+  int32_t* lists;
+  int* err;
+  int64_t num_pages;
+  int hkv;
+  int row_bytes;  // of K (or V) of one token and head
+};
+
+// Unsigned order = order of the floats, NaN above all, -0 = 0.
+__device__ __forceinline__ uint32_t key_of(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t b = __float_as_uint(w == 0.f ? 0.f : w);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+struct EvictShared {
+  int hist[2][256];
+  int counts[2];        // kept for sure / equal to the last key, of this CTA
+  int warp_counts[2][kThreads / 32];
+  int digit, above;     // of one pass
+  int64_t src[kRankInfo], dst[kRankInfo];  // page * 16 + slot; -1: nothing to move
+  float moved[3][kRankInfo];               // weight, K scale, V scale
+};
+
+__global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams p) {
+  extern __shared__ __align__(16) uint8_t buffer[];
+  __shared__ EvictShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), c = (int)cluster.block_rank();
+  const int job = blockIdx.x / C, h = job % p.hkv, tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
+  const EvictUnit u = p.units[job / p.hkv];
+  const int L = u.length, n = u.kept, cand = L - u.recent, want = n - u.recent;
+  int32_t* list = p.lists + u.list + (int64_t)h * n;
+
+  // a token's slot in the arrays per token; -1 for a page id outside the cache
+  auto place = [&](int t) -> int64_t {
+    const int page = __ldg(p.indices + u.entry + t / kPageSize);
+    if (page < 0 || (int64_t)page >= p.num_pages) {
+      atomicOr(p.err, 1);
+      return -1;
+    }
+    return (int64_t)page * kPageSize + t % kPageSize;
+  };
+  auto token_at = [&](int64_t at) -> int64_t {  // index into [pages, Hkv, 16]
+    return ((at / kPageSize) * p.hkv + h) * kPageSize + at % kPageSize;
+  };
+
+  // ---- 1. the keys of tokens t0 .. t1
+  const int t0 = (int)((int64_t)cand * c / C), t1 = (int)((int64_t)cand * (c + 1) / C);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(buffer);
+  const bool held = (t1 - t0) * 4 <= kBuffer;
+  auto read_key = [&](int t) -> uint32_t {
+    const int64_t at = place(t);
+    return at < 0 ? key_of(0.f) : key_of(p.weights[token_at(at)]);
+  };
+  if (held)
+    for (int t = t0 + tid; t < t1; t += kThreads) keys[t - t0] = read_key(t);
+  auto key = [&](int t) { return held ? keys[t - t0] : read_key(t); };
+  __syncthreads();
+
+  // ---- 2. the want-th largest key
+  uint32_t border = 0xffffffffu;  // keys above it are kept,
+  int ties = 0;                   // and the first `ties` of those equal to it
+  if (want > 0) {
+    uint32_t prefix = 0;
+    int left = want;
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+      int* hist = sh.hist[pass & 1];
+      hist[tid] = 0;
+      __syncthreads();
+      for (int i = t0; i < t1; i += kThreads) {
+        const int t = i + tid;
+        const uint32_t k = t < t1 ? key(t) : 0;
+        const bool in = t < t1 && (pass == 0 || (k >> (shift + 8)) == prefix);
+        const int digit = in ? (int)((k >> shift) & 0xff) : 256;
+        // equal digits of a warp are counted once (weights crowd few exponents)
+        const unsigned same = __match_any_sync(0xffffffffu, digit);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+      }
+      cluster.sync();
+      int sum = 0;
+      for (int r = 0; r < C; ++r) sum += cluster.map_shared_rank(hist, r)[tid];
+      // keys of larger digits: a suffix sum over the 256 threads
+      int suffix = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off *= 2) {
+        const int v = __shfl_down_sync(0xffffffffu, suffix, off);
+        if (lane + off < 32) suffix += v;
+      }
+      if (lane == 0) sh.warp_counts[0][warp] = suffix;
+      __syncthreads();
+      for (int w = warp + 1; w < kThreads / 32; ++w) suffix += sh.warp_counts[0][w];
+      if (suffix >= left && suffix - sum < left) {
+        sh.digit = tid;
+        sh.above = suffix - sum;
+      }
+      __syncthreads();
+      prefix = (prefix << 8) | (uint32_t)sh.digit;
+      left -= sh.above;
+      // (the other histogram is cleared next; this one only after the next meeting)
+    }
+    border = prefix;
+    ties = left;
+  }
+
+  // ---- 3. ranks
+  auto flags = [&](int t, bool* above, bool* equal) {
+    const uint32_t k = t < t1 && want > 0 ? key(t) : 0;
+    *above = t < t1 && want > 0 && k > border;
+    *equal = t < t1 && want > 0 && k == border;
+  };
+  {
+    int a = 0, e = 0;
+    for (int i = t0; i < t1; i += kThreads) {
+      bool above, equal;
+      flags(i + tid, &above, &equal);
+      a += __popc(__ballot_sync(0xffffffffu, above));
+      e += __popc(__ballot_sync(0xffffffffu, equal));
+    }
+    if (tid < 2) sh.counts[tid] = 0;
+    __syncthreads();
+    if (lane == 0) {
+      atomicAdd(&sh.counts[0], a);
+      atomicAdd(&sh.counts[1], e);
+    }
+  }
+  cluster.sync();
+  int above_before = 0, equal_before = 0;
+  for (int r = 0; r < c; ++r) {
+    const int* other = cluster.map_shared_rank(sh.counts, r);
+    above_before += other[0];
+    equal_before += other[1];
+  }
+  for (int i = t0; i < t1; i += kThreads) {
+    bool above, equal;
+    flags(i + tid, &above, &equal);
+    const unsigned ma = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, equal);
+    __syncthreads();
+    if (lane == 0) {
+      sh.warp_counts[0][warp] = __popc(ma);
+      sh.warp_counts[1][warp] = __popc(me);
+    }
+    __syncthreads();
+    int a = above_before, e = equal_before;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int wa = sh.warp_counts[0][w], we = sh.warp_counts[1][w];
+      if (w < warp) {
+        a += wa;
+        e += we;
+      }
+      above_before += wa;
+      equal_before += we;
+    }
+    const unsigned below = (1u << lane) - 1;
+    a += __popc(ma & below);
+    e += __popc(me & below);
+    if (above || (equal && e < ties)) list[a + min(e, ties)] = i + tid;
+  }
+  for (int i = c * kThreads + tid; i < u.recent; i += C * kThreads) list[want + i] = cand + i;
+  cluster.sync();  // the list is whole, and the keys are done with
+
+  // ---- 4. the rows, a chunk of ranks at a time
+  const int rb = p.row_bytes, pieces = 2 * rb / 16;  // 16-byte pieces of a token's K and V
+  const int chunk = min(kRankInfo, kBuffer / (2 * rb));
+  const int64_t token_bytes = (int64_t)p.hkv * rb, page_half = kPageSize * token_bytes;
+  const uint32_t sbase = dev::smem_addr(buffer);
+  auto address = [&](int64_t at, int piece) -> uint8_t* {
+    const int half = piece * 16 >= rb;
+    return p.kv + (at / kPageSize * 2 + half) * page_half + (at % kPageSize) * token_bytes +
+           (int64_t)h * rb + (piece * 16 - half * rb);
+  };
+  for (int r0 = 0; r0 < n; r0 += C * chunk) {
+    const int first = r0 + c * chunk, count = max(0, min(chunk, n - first));
+    for (int i = tid; i < count; i += kThreads) {
+      const int t = __ldcg(list + first + i);
+      int64_t src = -1, dst = -1;
+      if (t != first + i) {
+        src = place(t);
+        dst = place(first + i);
+        if (src < 0 || dst < 0) src = dst = -1;
+      }
+      sh.src[i] = src;
+      sh.dst[i] = dst;
+      if (src >= 0) {
+        const int64_t at = token_at(src);
+        sh.moved[0][i] = p.weights[at];
+        if (p.k_scales) {
+          sh.moved[1][i] = p.k_scales[at];
+          sh.moved[2][i] = p.v_scales[at];
+        }
+      }
+    }
+    __syncthreads();
+    for (int e = tid; e < count * pieces; e += kThreads) {
+      const int64_t src = sh.src[e / pieces];
+      if (src >= 0) dev::cp_async16(sbase + e * 16, address(src, e % pieces));
+    }
+    dev::cp_async_wait_all();
+    cluster.sync();
+    for (int e = tid; e < count * pieces; e += kThreads) {
+      const int64_t dst = sh.dst[e / pieces];
+      if (dst >= 0)
+        *reinterpret_cast<uint4*>(address(dst, e % pieces)) =
+            *reinterpret_cast<const uint4*>(buffer + e * 16);
+    }
+    for (int i = tid; i < count; i += kThreads) {
+      if (sh.dst[i] < 0) continue;
+      const int64_t at = token_at(sh.dst[i]);
+      p.weights[at] = sh.moved[0][i];
+      if (p.k_scales) {
+        p.k_scales[at] = sh.moved[1][i];
+        p.v_scales[at] = sh.moved[2][i];
+      }
+    }
+    __syncthreads();
+  }
+  // all weights have been read: those of the freed slots start again at 0
+  for (int t = n + c * kThreads + tid; t < L; t += C * kThreads) {
+    const int64_t at = place(t);
+    if (at >= 0) p.weights[token_at(at)] = 0.f;
+  }
+}
+
+struct EvictLayout {
+  size_t units, lists, total;
+};
+
+// Requests that lose tokens, counted or (with `out`) written; -1 for malformed
+// arguments.  *tokens: kept tokens of one kv head, in all; *longest: of one request.
+int64_t make_units(const int32_t* indptr, const int32_t* last_page_len, const int32_t* keep,
+                   const int32_t* recent, int batch, int heads, EvictUnit* out, int64_t* tokens,
+                   int64_t* longest) {
+  int64_t units = 0;
+  *tokens = *longest = 0;
+  for (int i = 0; i < batch; ++i) {
+    const int64_t pages = (int64_t)indptr[i + 1] - indptr[i];
+    if (pages < 0 || keep[i] < 0 || (recent && recent[i] < 0)) return -1;
+    if (pages > 0 && (last_page_len[i] < 1 || last_page_len[i] > kPageSize)) return -1;
+    const int64_t len = pages > 0 ? (pages - 1) * kPageSize + last_page_len[i] : 0;
+    if (len > std::numeric_limits<int32_t>::max() - kPageSize) return -1;
+    if (len <= keep[i]) continue;
+    if (out)
+      out[units] = EvictUnit{indptr[i], (int32_t)len, keep[i],
+                             recent ? std::min(recent[i], keep[i]) : 0, *tokens * heads, {0, 0}};
+    ++units;
+    *tokens += keep[i];
+    *longest = std::max(*longest, len);
+  }
+  return units;
+}
+
+EvictLayout evict_layout(int64_t units, int64_t tokens, int heads) {
+  EvictLayout L;
+  L.units = kAlign;
+  L.lists = align_up(L.units + sizeof(EvictUnit) * (size_t)units);
+  L.total = align_up(L.lists + 4 * (size_t)tokens * heads);
+  return L;
+}
+
+}  // namespace
+}  // namespace fadecode
+
+using namespace fadecode;
+
+struct fa_evict_plan_s {
+  int device = 0;
+  int hkv = 0, row_bytes = 0;
+  fa_dtype kv_dtype = FA_DTYPE_BF16;
+  const int32_t* indices = nullptr;
+  uint8_t* ws = nullptr;
+  EvictLayout layout{};
+  int64_t units = 0;
+  int cluster = 1;
+};
+
+extern "C" {
+
+size_t fa_evict_workspace_size(int batch, int64_t total_kept, int num_kv_heads) {
+  if (batch < 0 || total_kept < 0 || num_kv_heads <= 0 ||
+      total_kept > (int64_t)1 << 40)
+    return 0;
+  return evict_layout(batch, total_kept, num_kv_heads).total;
+}
+
+int fa_evict_plan(const int32_t* indptr_host, const int32_t* indices_dev,
+                  const int32_t* last_page_len_host, const int32_t* keep_host,
+                  const int32_t* recent_host, int batch, int num_kv_heads, int head_dim,
+                  int page_size, fa_dtype kv_dtype, void* workspace_dev, size_t workspace_bytes,
+                  void* cuda_stream, fa_evict_plan_t* out_plan) {
+  if (!out_plan) return FA_ERR_INVALID_ARG;
+  *out_plan = nullptr;
+  if (!indptr_host || batch < 0 || num_kv_heads <= 0 || head_dim <= 0 || page_size <= 0 ||
+      (batch > 0 && (!last_page_len_host || !keep_host)) || !workspace_dev ||
+      reinterpret_cast<uintptr_t>(workspace_dev) % kAlign)
+    return FA_ERR_INVALID_ARG;
+  const int es = kv_dtype == FA_DTYPE_F32                                 ? 4
+                 : kv_dtype == FA_DTYPE_BF16 || kv_dtype == FA_DTYPE_F16 ? 2
+                 : kv_dtype == FA_DTYPE_E4M3                             ? 1
+                                                                          : 0;
+  if (page_size != kPageSize || (head_dim != 64 && head_dim != 128) || es == 0)
+    return FA_ERR_UNSUPPORTED;
+  if (indptr_host[0] != 0 || (indptr_host[batch] > 0 && !indices_dev)) return FA_ERR_INVALID_ARG;
+  int64_t tokens = 0, longest = 0;
+  const int64_t units = make_units(indptr_host, last_page_len_host, keep_host, recent_host, batch,
+                                   num_kv_heads, nullptr, &tokens, &longest);
+  if (units < 0) return FA_ERR_INVALID_ARG;
+  const EvictLayout L = evict_layout(units, tokens, num_kv_heads);
+  if (L.total > workspace_bytes) return FA_ERR_WORKSPACE_TOO_SMALL;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FA_ERR_CUDA;
+  // as many CTAs to a (request, kv head) as fill the SMs four times, none with
+  // under a thousand tokens
+  int cluster = 1;
+  while (cluster < kMostCtas && units * num_kv_heads * cluster * 2 <= 4 * (int64_t)sms &&
+         longest >= 1024 * 2 * (int64_t)cluster)
+    cluster *= 2;
+  if (units * num_kv_heads * cluster > std::numeric_limits<int32_t>::max())
+    return FA_ERR_UNSUPPORTED;
+  try {
+    std::vector<uint8_t> meta(L.lists, 0);
+    make_units(indptr_host, last_page_len_host, keep_host, recent_host, batch, num_kv_heads,
+               reinterpret_cast<EvictUnit*>(meta.data() + L.units), &tokens, &longest);
+    fa_evict_plan_s* plan = new fa_evict_plan_s();
+    plan->device = dev;
+    plan->hkv = num_kv_heads;
+    plan->row_bytes = head_dim * es;
+    plan->kv_dtype = kv_dtype;
+    plan->indices = indices_dev;
+    plan->ws = static_cast<uint8_t*>(workspace_dev);
+    plan->layout = L;
+    plan->units = units;
+    plan->cluster = cluster;
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(&fa_evict_kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBuffer) !=
+            cudaSuccess ||
+        upload_async(plan->ws, meta.data(), meta.size(),
+                     static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
+      delete plan;
+      return FA_ERR_CUDA;
+    }
+    *out_plan = plan;
+  } catch (const std::bad_alloc&) {
+    return FA_ERR_INVALID_ARG;
+  }
+  return FA_OK;
+}
+
+int fa_evict_run(fa_evict_plan_t plan, void* paged_kv, int64_t num_pages, float* weights,
+                 float* k_scales, float* v_scales, void* cuda_stream) {
+  if (!plan) return FA_ERR_INVALID_ARG;
+  if (plan->units == 0) return FA_OK;
+  if (!paged_kv || !weights || num_pages <= 0 || reinterpret_cast<uintptr_t>(paged_kv) % 16 ||
+      reinterpret_cast<uintptr_t>(weights) % 4 || reinterpret_cast<uintptr_t>(k_scales) % 4 ||
+      reinterpret_cast<uintptr_t>(v_scales) % 4 || (k_scales == nullptr) != (v_scales == nullptr))
+    return FA_ERR_INVALID_ARG;
+  if (k_scales && plan->kv_dtype != FA_DTYPE_E4M3) return FA_ERR_UNSUPPORTED;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  if (dev != plan->device) return FA_ERR_INVALID_ARG;
+  EvictParams p;
+  std::memset(&p, 0, sizeof p);
+  p.kv = static_cast<uint8_t*>(paged_kv);
+  p.weights = weights;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.indices = plan->indices;
+  p.units = reinterpret_cast<const EvictUnit*>(plan->ws + plan->layout.units);
+  p.lists = reinterpret_cast<int32_t*>(plan->ws + plan->layout.lists);
+  p.err = reinterpret_cast<int*>(plan->ws);
+  p.num_pages = num_pages;
+  p.hkv = plan->hkv;
+  p.row_bytes = plan->row_bytes;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3((unsigned)(plan->units * plan->hkv * plan->cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kBuffer;
+  cfg.stream = static_cast<cudaStream_t>(cuda_stream);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)plan->cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void* args[1] = {&p};
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&fa_evict_kernel), args) ==
+                 cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+int fa_evict_check(fa_evict_plan_t plan, void* cuda_stream, int* flags) {
+  if (!plan || !flags) return FA_ERR_INVALID_ARG;
+  int word = 0;
+  if (take_word(reinterpret_cast<int*>(plan->ws), &word, static_cast<cudaStream_t>(cuda_stream)) !=
+      cudaSuccess)
+    return FA_ERR_CUDA;
+  *flags = word;
+  return word ? FA_ERR_DEVICE_CHECK : FA_OK;
+}
+
+int fa_evict_plan_destroy(fa_evict_plan_t plan) {
+  delete plan;
+  return FA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,464 @@
+// Attention weights accumulated per cached token: the calls fa_weights_* (declared
+// in include/fa_decode.h).
+//
+// The mathematics.  A cached token t of a request gains, in its kv head,
+//     w_t += sum over query rows r that see t and the group's heads g of
+//            2^(c q_rg . k_t - lse_rg log2 e),   c = sm_scale log2 e,
+// the weight that the softmax of those rows gave it; lse is what the attention
+// of the same rows returned.  One pass over K, none over V.
+//
+// Work.  A CTA takes a kv head and a run of a request's pages, a warp one page at
+// a time: its 16 tokens are the MMA's M side (m16n8k16, mma.sync), eight columns
+// (query row x head of the group) its N side.  The dot product does not mind the order
+// of dims, so a lane's fragments are whole 16-byte pieces of a K row and of a q
+// row: lane c of a row's four holds dims 8c .. 8c+7 of every 32 (16 of every 64 codes of
+// an E4M3 cache), straight from global memory into registers.  A page's K stays in
+// registers while all columns pass by; the sums over columns stay in two
+// registers a lane until the page is done, so every token's weight is one addition
+// to memory a call, and the result does not depend on the schedule.
+// (Pages that two requests share receive two.)
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <limits>
+#include <new>
+#include <type_traits>
+#include <vector>
+
+#include "decode_mma.cuh"
+#include "fa_decode.h"
+#include "staging.h"
+
+namespace fadecode {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+// A run of a request's pages.
+struct WeightsUnit {
+  int32_t row0, rows;    // query rows of the request
+  int32_t entry, pages;  // table entries of the run
+  int32_t pos0;          // position of its first token
+  int32_t before;        // length - rows: row r sees positions up to before + r
+  int32_t pad[2];
+};
+static_assert(sizeof(WeightsUnit) == 32, "read as two int4");
+
+struct WeightsParams {
+  const void* q;  // [rows, Hq, D], by strides in elements
+  int64_t q_token, q_head;
+  const void* kv;
+  const float* lse;           // [rows, Hq]
+  float* weights;             // [pages, Hkv, 16]
+  const float* k_scales;      // kScalePerToken [pages, Hkv, 16], kScalePerBlock [pages, Hkv]
+  const float* head_k_scales; // [Hkv] times scale, or nullptr
+  const int32_t* indices;
+  const WeightsUnit* units;
+  int* err;
+  int64_t num_pages;
+  int hq, hkv;
+  float scale;  // sm_scale * k_scale * log2(e)
+};
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1, bool bf16) {
+  if (bf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two E4M3 codes as a pair of T (exact in both 16-bit types).
+template <typename T>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  if constexpr (std::is_same<T, __half>::value) {
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+  } else {
+    const float2 f = __half22float2(__half2(h));
+    return mma::pack2(f.x, f.y, true);
+  }
+}
+
+template <typename T, typename KVT, int D, int SC>
+__global__ void __launch_bounds__(kWarps * 32, 2) fa_weights_kernel(const WeightsParams p) {
+  constexpr bool kE4m3 = !std::is_same<T, KVT>::value;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int kPiece = 16 / sizeof(KVT);       // elements of a lane's 16 bytes of K
+  constexpr int kPieces = D / (4 * kPiece);      // of them in a row
+  constexpr int kQPieces = D / 32;
+  const int4* up = reinterpret_cast<const int4*>(p.units + blockIdx.x / p.hkv);
+  const int4 ua = __ldg(up), ub = __ldg(up + 1);
+  const int row0 = ua.x, rows = ua.y, entry = ua.z, pages = ua.w, pos0 = ub.x, before = ub.y;
+  const int h = blockIdx.x % p.hkv, G = p.hq / p.hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = lane % 4, n = lane / 4;  // piece of a row; token and column of the fragments
+  const int columns = rows * G;
+  const KVT* kv = static_cast<const KVT*>(p.kv);
+  const int64_t token_stride = (int64_t)p.hkv * D;
+
+  auto load_page = [&](int i, uint4 (&k)[2][kPieces]) -> int {
+    int page = i < pages ? __ldg(p.indices + entry + i) : -1;
+    if (page < 0 || (int64_t)page >= p.num_pages) {
+      if (i < pages && lane == 0) atomicOr(p.err, 1);
+      page = -1;
+    }
+    const KVT* base = kv + (int64_t)max(page, 0) * 2 * kPageSize * token_stride + (int64_t)h * D;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+        k[t][j] = page < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                           : __ldg(reinterpret_cast<const uint4*>(
+                                 base + (n + 8 * t) * token_stride + (4 * j + c) * kPiece));
+    return page;
+  };
+  // column x = (row, head): its q row as B fragments, its log2 lse and last position
+  auto load_column = [&](int x, uint4 (&b)[kQPieces]) {
+    const T* q = static_cast<const T*>(p.q) + (row0 + x / G) * p.q_token +
+                 (int64_t)(h * G + x % G) * p.q_head;
+#pragma unroll
+    for (int j = 0; j < kQPieces; ++j) {
+      // the dims that this lane's piece of K holds
+      const int d = kE4m3 ? (j / 2) * 64 + c * 16 + (j % 2) * 8 : (4 * j + c) * 8;
+      b[j] = x < columns ? __ldg(reinterpret_cast<const uint4*>(q + d)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+
+  uint4 held[kQPieces];  // the only columns, where there are eight at most
+  const bool single = columns <= 8;
+  if (single) load_column(n, held);
+  const float head_scale = p.head_k_scales ? p.scale * __ldg(p.head_k_scales + h) : p.scale;
+
+  uint4 raw[2][kPieces];
+  int page = load_page(warp, raw);
+  for (int i = warp; i < pages; i += kWarps) {
+    uint4 k[2][kPieces];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) k[t][j] = raw[t][j];
+    const int this_page = page;
+    page = load_page(i + kWarps, raw);
+    if (this_page < 0) continue;
+    const int64_t at = ((int64_t)this_page * p.hkv + h) * kPageSize;
+    float scale[2] = {head_scale, head_scale};  // of tokens n and n + 8
+    if constexpr (SC == kScalePerToken) {
+      scale[0] *= __ldg(p.k_scales + at + n);
+      scale[1] *= __ldg(p.k_scales + at + n + 8);
+    } else if constexpr (SC == kScalePerBlock) {
+      scale[0] = scale[1] = head_scale * __ldg(p.k_scales + at / kPageSize);
+    }
+    const int pos = pos0 + i * kPageSize + n;
+    float sum[2] = {0.f, 0.f};
+    for (int x0 = 0; x0 < columns; x0 += 8) {
+      uint4 b[kQPieces];
+      if (single) {
+#pragma unroll
+        for (int j = 0; j < kQPieces; ++j) b[j] = held[j];
+      } else {
+        load_column(x0 + n, b);
+      }
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < kQPieces; ++j) {
+        uint32_t a[2][4];  // two MMAs of a 16-byte piece of q
+        if constexpr (kE4m3) {
+          const uint4 lo = k[0][j / 2], hi = k[1][j / 2];
+          const uint32_t l0 = j % 2 ? lo.z : lo.x, l1 = j % 2 ? lo.w : lo.y;
+          const uint32_t h0 = j % 2 ? hi.z : hi.x, h1 = j % 2 ? hi.w : hi.y;
+          a[0][0] = widen2<T>(l0 & 0xffffu);
+          a[0][1] = widen2<T>(h0 & 0xffffu);
+          a[0][2] = widen2<T>(l0 >> 16);
+          a[0][3] = widen2<T>(h0 >> 16);
+          a[1][0] = widen2<T>(l1 & 0xffffu);
+          a[1][1] = widen2<T>(h1 & 0xffffu);
+          a[1][2] = widen2<T>(l1 >> 16);
+          a[1][3] = widen2<T>(h1 >> 16);
+        } else {
+          a[0][0] = k[0][j].x;
+          a[0][1] = k[1][j].x;
+          a[0][2] = k[0][j].y;
+          a[0][3] = k[1][j].y;
+          a[1][0] = k[0][j].z;
+          a[1][1] = k[1][j].z;
+          a[1][2] = k[0][j].w;
+          a[1][3] = k[1][j].w;
+        }
+        mma_16816(s, a[0], b[j].x, b[j].y, kBf16);
+        mma_16816(s, a[1], b[j].z, b[j].w, kBf16);
+      }
+      // s[0], s[1]: token n, columns x0 + 2c, + 1; s[2], s[3]: token n + 8
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int x = x0 + 2 * c + e;
+        if (x >= columns) continue;
+        const int row = x / G;
+        float lse = __ldg(p.lse + (int64_t)(row0 + row) * p.hq + h * G + x % G) * 1.4426950408889634f;
+        lse = lse == -INFINITY ? INFINITY : lse;  // a row that saw nothing
+        const int last = before + row;
+        if (pos <= last) sum[0] += dev::fast_exp2(fmaf(s[e], scale[0], -lse));
+        if (pos + 8 <= last) sum[1] += dev::fast_exp2(fmaf(s[2 + e], scale[1], -lse));
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], 1);
+      sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], 2);
+    }
+    // tokens that no row sees (slots behind the request's last) stay
+    if (c < 2 && pos + 8 * c <= before + rows - 1) atomicAdd(p.weights + at + n + 8 * c, sum[c]);
+  }
+}
+
+using WeightsFn = void (*)(const WeightsParams);
+
+template <typename T, typename KVT, int D>
+WeightsFn weights_kernel(int sc) {
+  if constexpr (std::is_same<T, KVT>::value) {
+    return &fa_weights_kernel<T, KVT, D, kScaleNone>;
+  } else {
+    return sc == kScalePerToken   ? &fa_weights_kernel<T, KVT, D, kScalePerToken>
+           : sc == kScalePerBlock ? &fa_weights_kernel<T, KVT, D, kScalePerBlock>
+                                  : &fa_weights_kernel<T, KVT, D, kScaleNone>;
+  }
+}
+
+template <int D>
+WeightsFn find_weights_kernel(fa_dtype q, bool e4m3, int sc) {
+  if (q == FA_DTYPE_BF16)
+    return e4m3 ? weights_kernel<__nv_bfloat16, uint8_t, D>(sc)
+                : weights_kernel<__nv_bfloat16, __nv_bfloat16, D>(sc);
+  return e4m3 ? weights_kernel<__half, uint8_t, D>(sc) : weights_kernel<__half, __half, D>(sc);
+}
+
+bool weights_pair_built(fa_dtype q, fa_dtype kv) {
+  return (q == FA_DTYPE_BF16 || q == FA_DTYPE_F16) && (kv == q || kv == FA_DTYPE_E4M3);
+}
+
+// Pages of a run: 64 (eight a warp), halved while that leaves under four CTAs an SM.
+constexpr int kMostPages = 64;
+int run_pages(int64_t total_pages, int heads, int sms) {
+  int n = kMostPages;
+  while (n > kWarps && total_pages * heads < (int64_t)n * 4 * sms) n /= 2;
+  return n;
+}
+
+// Runs of a batch; -1 for malformed arguments.
+int64_t make_units(const int32_t* indptr, const int32_t* last_page_len, const int32_t* qo_indptr,
+                   int batch, int run, WeightsUnit* out) {
+  int64_t units = 0;
+  for (int i = 0; i < batch; ++i) {
+    const int64_t n = (int64_t)qo_indptr[i + 1] - qo_indptr[i];
+    const int64_t pages = (int64_t)indptr[i + 1] - indptr[i];
+    if (n < 0 || pages < 0) return -1;
+    if (pages > 0 && (last_page_len[i] < 1 || last_page_len[i] > kPageSize)) return -1;
+    const int64_t len = pages > 0 ? (pages - 1) * kPageSize + last_page_len[i] : 0;
+    if (len > std::numeric_limits<int32_t>::max() - kPageSize) return -1;
+    if (n == 0) continue;
+    for (int64_t e = 0; e < pages; e += run, ++units)
+      if (out)
+        out[units] = WeightsUnit{qo_indptr[i],
+                                 (int32_t)n,
+                                 (int32_t)(indptr[i] + e),
+                                 (int32_t)std::min<int64_t>(run, pages - e),
+                                 (int32_t)(e * kPageSize),
+                                 (int32_t)(len - n),
+                                 {0, 0}};
+  }
+  return units;
+}
+
+}  // namespace
+}  // namespace fadecode
+
+using namespace fadecode;
+
+struct fa_weights_plan_s {
+  int device = 0;
+  int hq = 0, hkv = 0, d = 0;
+  fa_dtype q_dtype = FA_DTYPE_BF16, kv_dtype = FA_DTYPE_BF16;
+  const int32_t* indices = nullptr;
+  uint8_t* ws = nullptr;
+  int64_t units = 0, rows = 0;
+};
+
+namespace {
+
+int weights_run(fa_weights_plan_s* plan, int sc, const fa_rows* q, const void* paged_kv,
+                int64_t num_pages, float sm_scale, const float* lse, float k_scale,
+                const float* head_k, const float* k_scales, float* weights, void* cuda_stream) {
+  if (plan->units == 0) return FA_OK;
+  if (!q || !q->data || !paged_kv || !lse || !weights || num_pages <= 0 ||
+      reinterpret_cast<uintptr_t>(paged_kv) % 16 || reinterpret_cast<uintptr_t>(q->data) % 16 ||
+      reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(weights) % 4 ||
+      q->token_stride < 0 || q->head_stride < 0 || q->token_stride % 8 || q->head_stride % 8)
+    return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(k_scale)) return FA_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  if (dev != plan->device) return FA_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f)) sm_scale = 1.0f / std::sqrt((float)plan->d);
+  WeightsParams p;
+  std::memset(&p, 0, sizeof p);
+  p.q = q->data;
+  p.q_token = q->token_stride;
+  p.q_head = q->head_stride;
+  p.kv = paged_kv;
+  p.lse = lse;
+  p.weights = weights;
+  p.k_scales = k_scales;
+  p.head_k_scales = head_k;
+  p.indices = plan->indices;
+  p.units = reinterpret_cast<const WeightsUnit*>(plan->ws + kAlign);
+  p.err = reinterpret_cast<int*>(plan->ws);
+  p.num_pages = num_pages;
+  p.hq = plan->hq;
+  p.hkv = plan->hkv;
+  p.scale = sm_scale * k_scale * 1.4426950408889634f;
+  const bool e4m3 = plan->kv_dtype == FA_DTYPE_E4M3;
+  const WeightsFn f = plan->d == 128 ? find_weights_kernel<128>(plan->q_dtype, e4m3, sc)
+                                     : find_weights_kernel<64>(plan->q_dtype, e4m3, sc);
+  void* args[1] = {&p};
+  return cudaLaunchKernel(reinterpret_cast<const void*>(f),
+                          dim3((unsigned)(plan->units * plan->hkv)), dim3(kWarps * 32), args, 0,
+                          static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_weights_workspace_size(int batch, int64_t total_pages) {
+  if (batch < 0 || total_pages < 0 || total_pages > std::numeric_limits<int32_t>::max()) return 0;
+  // runs of eight pages at least
+  return kAlign + align_up(sizeof(WeightsUnit) * (size_t)(total_pages / kWarps + batch));
+}
+
+int fa_weights_plan(const int32_t* indptr_host, const int32_t* indices_dev,
+                    const int32_t* last_page_len_host, const int32_t* qo_indptr_host, int batch,
+                    int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
+                    fa_dtype q_dtype, fa_dtype kv_dtype, void* workspace_dev,
+                    size_t workspace_bytes, void* cuda_stream, fa_weights_plan_t* out_plan) {
+  if (!out_plan) return FA_ERR_INVALID_ARG;
+  *out_plan = nullptr;
+  if (!indptr_host || !qo_indptr_host || batch < 0 || num_qo_heads <= 0 || num_kv_heads <= 0 ||
+      head_dim <= 0 || page_size <= 0 || num_qo_heads % num_kv_heads ||
+      (batch > 0 && !last_page_len_host) || !workspace_dev ||
+      reinterpret_cast<uintptr_t>(workspace_dev) % kAlign)
+    return FA_ERR_INVALID_ARG;
+  const int G = num_qo_heads / num_kv_heads;
+  if (page_size != kPageSize || (head_dim != 64 && head_dim != 128) ||
+      (G != 1 && G != 2 && G != 4 && G != 8) || !weights_pair_built(q_dtype, kv_dtype))
+    return FA_ERR_UNSUPPORTED;
+  if (indptr_host[0] != 0 || qo_indptr_host[0] != 0) return FA_ERR_INVALID_ARG;
+  if (indptr_host[batch] > 0 && !indices_dev) return FA_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  // the arguments are checked before any CUDA call
+  if (make_units(indptr_host, last_page_len_host, qo_indptr_host, batch, kMostPages, nullptr) < 0)
+    return FA_ERR_INVALID_ARG;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FA_ERR_CUDA;
+  const int run = run_pages(indptr_host[batch], num_kv_heads, sms);
+  const int64_t units =
+      make_units(indptr_host, last_page_len_host, qo_indptr_host, batch, run, nullptr);
+  const size_t bytes = kAlign + sizeof(WeightsUnit) * (size_t)units;
+  if (bytes > workspace_bytes) return FA_ERR_WORKSPACE_TOO_SMALL;
+  if (units * num_kv_heads > std::numeric_limits<int32_t>::max()) return FA_ERR_UNSUPPORTED;
+  try {
+    std::vector<uint8_t> meta(bytes, 0);
+    make_units(indptr_host, last_page_len_host, qo_indptr_host, batch, run,
+               reinterpret_cast<WeightsUnit*>(meta.data() + kAlign));
+    fa_weights_plan_s* plan = new fa_weights_plan_s();
+    plan->device = dev;
+    plan->hq = num_qo_heads;
+    plan->hkv = num_kv_heads;
+    plan->d = head_dim;
+    plan->q_dtype = q_dtype;
+    plan->kv_dtype = kv_dtype;
+    plan->indices = indices_dev;
+    plan->ws = static_cast<uint8_t*>(workspace_dev);
+    plan->units = units;
+    plan->rows = qo_indptr_host[batch];
+    if (upload_async(plan->ws, meta.data(), bytes, static_cast<cudaStream_t>(cuda_stream)) !=
+        cudaSuccess) {
+      delete plan;
+      return FA_ERR_CUDA;
+    }
+    *out_plan = plan;
+  } catch (const std::bad_alloc&) {
+    return FA_ERR_INVALID_ARG;
+  }
+  return FA_OK;
+}
+
+int fa_weights_run(fa_weights_plan_t plan, const fa_rows* q, const void* paged_kv,
+                   int64_t num_pages, float sm_scale, float k_scale, const float* lse,
+                   float* weights, void* cuda_stream) {
+  if (!plan) return FA_ERR_INVALID_ARG;
+  if (plan->kv_dtype != FA_DTYPE_E4M3 && k_scale != 1.f) return FA_ERR_INVALID_ARG;
+  return weights_run(plan, kScaleNone, q, paged_kv, num_pages, sm_scale, lse, k_scale, nullptr,
+                     nullptr, weights, cuda_stream);
+}
+
+static int weights_run_scales(fa_weights_plan_t plan, int sc, bool heads, const fa_rows* q,
+                              const void* paged_kv, int64_t num_pages, float sm_scale,
+                              const float* k_scales, const float* lse, float* weights,
+                              void* cuda_stream) {
+  if (!plan) return FA_ERR_INVALID_ARG;
+  if (plan->kv_dtype != FA_DTYPE_E4M3) return FA_ERR_UNSUPPORTED;
+  if (!k_scales || reinterpret_cast<uintptr_t>(k_scales) % 4) return FA_ERR_INVALID_ARG;
+  return weights_run(plan, sc, q, paged_kv, num_pages, sm_scale, lse, 1.f,
+                     heads ? k_scales : nullptr, heads ? nullptr : k_scales, weights, cuda_stream);
+}
+
+int fa_weights_run_head_scales(fa_weights_plan_t plan, const fa_rows* q, const void* paged_kv,
+                               int64_t num_pages, float sm_scale, const float* k_head_scales,
+                               const float* lse, float* weights, void* cuda_stream) {
+  return weights_run_scales(plan, kScaleNone, true, q, paged_kv, num_pages, sm_scale,
+                            k_head_scales, lse, weights, cuda_stream);
+}
+
+int fa_weights_run_token_scales(fa_weights_plan_t plan, const fa_rows* q, const void* paged_kv,
+                                int64_t num_pages, float sm_scale, const float* k_scales,
+                                const float* lse, float* weights, void* cuda_stream) {
+  return weights_run_scales(plan, kScalePerToken, false, q, paged_kv, num_pages, sm_scale,
+                            k_scales, lse, weights, cuda_stream);
+}
+
+int fa_weights_run_block_scales(fa_weights_plan_t plan, const fa_rows* q, const void* paged_kv,
+                                int64_t num_pages, float sm_scale, const float* k_scales,
+                                const float* lse, float* weights, void* cuda_stream) {
+  return weights_run_scales(plan, kScalePerBlock, false, q, paged_kv, num_pages, sm_scale,
+                            k_scales, lse, weights, cuda_stream);
+}
+
+int fa_weights_check(fa_weights_plan_t plan, void* cuda_stream, int* flags) {
+  if (!plan || !flags) return FA_ERR_INVALID_ARG;
+  int word = 0;
+  if (take_word(reinterpret_cast<int*>(plan->ws), &word, static_cast<cudaStream_t>(cuda_stream)) !=
+      cudaSuccess)
+    return FA_ERR_CUDA;
+  *flags = word;
+  return word ? FA_ERR_DEVICE_CHECK : FA_OK;
+}
+
+int fa_weights_plan_destroy(fa_weights_plan_t plan) {
+  delete plan;
+  return FA_OK;
+}
+
+}  // extern "C"
