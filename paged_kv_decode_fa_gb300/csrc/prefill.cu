@@ -625,6 +625,13 @@ int fa_prefill_plan(const int32_t* indptr_host, const int32_t* indices_dev,
     plan->ctas = (int)w.cta_offsets.size() - 1;
     plan->merge_units = (int)(w.merge.size() / 8);
     plan->kernel = find_prefill_kernel(q_dtype, head_dim);
+    // the kernel's warpgroups share out the registers it is launched with
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, plan->kernel.attend) != cudaSuccess ||
+        attr.numRegs < pf::kLaunchRegs) {
+      delete plan;
+      return FA_ERR_CUDA;
+    }
     if (cudaFuncSetAttribute(plan->kernel.attend, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              plan->kernel.smem) != cudaSuccess ||
         upload_async(plan->ws, meta.data(), meta.size(),

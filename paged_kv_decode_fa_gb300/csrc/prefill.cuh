@@ -57,6 +57,11 @@ constexpr int kRows = 128;                       // rows of a block
 constexpr int kTok = 128;                        // tokens of a tile
 constexpr int kPages = kTok / kPageSize;         // 8
 constexpr int kThreads = 384;
+// Registers a thread: as launched, and as the warpgroups split them (the softmax's
+// two take what the third, which loads and issues, gives back).
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kIssueRegs = 104;
+static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs,
+              "a larger share would be waited for without end");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleAbove = 8.f;             // log2 units
 constexpr int kItemInts = 8;
@@ -101,6 +106,10 @@ struct Item {
     if (block * block_tokens >= tokens) return 0;
     return max(0, min(t1, (keys(block, block_tokens) + kTok - 1) / kTok) - t0);
   }
+  // the last of its `all` tiles ends inside a page
+  __device__ __forceinline__ bool ragged(int keys, int all) const {
+    return keys < (t0 + all) * kTok && keys % kPageSize;
+  }
 };
 
 template <int D>
@@ -112,8 +121,9 @@ struct Smem {
   static constexpr int kQBytes = kHalves * kRows * 128;  // one block's Q
   static constexpr int kOffRing = 2 * kQBytes;
   static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-  // kv_full[n], kv_empty[n]; q_full, q_empty, s_full, p_full, o_full, o_empty [2]
-  static constexpr int kNumBars = 2 * kSlots + 12;
+  // kv_full[n], kv_empty[n]; q_full, q_empty, s_full [2], p_full [2][2], o_full, o_empty [2],
+  // v_there, v_clean
+  static constexpr int kNumBars = 2 * kSlots + 16;
   static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
   static constexpr int kBytes = kOffTmem + 16 + 1024;    // and the alignment to 1024
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
@@ -160,8 +170,10 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_full = q_full + 4;
   uint64_t* p_full = q_full + 6;
-  uint64_t* o_full = q_full + 8;
-  uint64_t* o_empty = q_full + 10;
+  uint64_t* o_full = q_full + 10;  // (p_full: [block][half])
+  uint64_t* o_empty = q_full + 12;
+  uint64_t* v_there = q_full + 14;
+  uint64_t* v_clean = q_full + 15;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffTmem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int first = p.cta_offsets[blockIdx.x], last = p.cta_offsets[blockIdx.x + 1];
@@ -176,10 +188,13 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
       dev::mbar_init(dev::smem_addr(&q_full[X]), 1);
       dev::mbar_init(dev::smem_addr(&q_empty[X]), 1);
       dev::mbar_init(dev::smem_addr(&s_full[X]), 1);
-      dev::mbar_init(dev::smem_addr(&p_full[X]), 4);
+      dev::mbar_init(dev::smem_addr(&p_full[2 * X]), 4);
+      dev::mbar_init(dev::smem_addr(&p_full[2 * X + 1]), 4);
       dev::mbar_init(dev::smem_addr(&o_full[X]), 1);
       dev::mbar_init(dev::smem_addr(&o_empty[X]), 4);
     }
+    dev::mbar_init(dev::smem_addr(v_there), 1);
+    dev::mbar_init(dev::smem_addr(v_clean), 1);
     dev::fence_barrier_init();
   }
   if (warp == 8) {
@@ -194,159 +209,206 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
   fence_after();
   const uint32_t tmem = *tmem_slot;  // S of block X at X * 128, O at 256 + X * 128
   bool aborted = false;
-
-  if (warp == 9) {
-    // ------------------------------------------------------------ K and V loads
-    if (lane == 0) dev::prefetch_tensormap(&kv_map);
-    const int oob = (int)(2 * p.num_pages);  // beyond the last page: zeros
-    int n = 0;                               // slots filled
-    for (int it = first; it < last; ++it) {
-      const Item w = Item::load(p.items, it);
-      const int nblk = w.tokens > block_tokens ? 2 : 1;
-      const int keys = w.keys(nblk - 1, block_tokens), tiles = w.tiles(nblk - 1, block_tokens);
-      const int pages = (min(keys, w.t1 * kTok) + kPageSize - 1) / kPageSize;
-      int ids = 0;
-      for (int j = 0; j < tiles; ++j) {
-        const int page0 = (w.t0 + j) * kPages;
-        if (j % (32 / kPages) == 0) {  // the page ids of four tiles
-          const int at = page0 + lane;
-          ids = oob;
-          if (at < pages) {
-            const int id = p.indices ? __ldg(p.indices + w.entry + at) : w.entry + at;
-            if (id < 0 || (int64_t)id >= p.num_pages) {
-              atomicOr(p.err, 1);
-            } else {
-              ids = 2 * id;
-            }
-          }
-        }
-        // lane l: half l % kHalves of the tile's page l / kHalves
-        const int id = __shfl_sync(0xffffffffu, ids, (j * kPages) % 32 + (lane / S::kHalves) % kPages);
-        const uint32_t at = (uint32_t)(lane % S::kHalves) * S::kHalf +
-                            (uint32_t)(lane / S::kHalves) * (kPageSize * 128);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const int s = n % kSlots;
-          const uint32_t full = dev::smem_addr(&kv_full[s]);
-          dev::mbar_wait(dev::smem_addr(&kv_empty[s]), (uint32_t)(((n / kSlots) & 1) ^ 1), aborted,
-                         p.err);
-          if (lane == 0) dev::mbar_arrive_expect_tx(full, S::kSlotBytes);
-          __syncwarp();
-          if (lane < kPages * S::kHalves)
-            tma_load_4d_plain(sbase + S::kOffRing + s * S::kSlotBytes + at, &kv_map,
-                              (lane % S::kHalves) * 64, w.head, 0, id < oob ? id + kv : oob, full);
-        }
-      }
-      aborted = __any_sync(0xffffffffu, aborted);
-    }
-    // no copy may still be landing when the CTA exits
-    if (lane == 0)
-      for (int i = n > kSlots ? n - kSlots : 0; i < n; ++i)
-        if (!dev::mbar_wait_bounded(dev::smem_addr(&kv_full[i % kSlots]),
-                                    (uint32_t)((i / kSlots) & 1)))
-          atomicOr(p.err, 2);
-  } else if (warp == 10) {
-    // ------------------------------------------------------------ Q loads
-    if (lane == 0) {
-      dev::prefetch_tensormap(&q_map);
-      int n[2] = {0, 0};
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 9) {
+      // ------------------------------------------------------------ K and V loads
+      if (lane == 0) dev::prefetch_tensormap(&kv_map);
+      const int oob = (int)(2 * p.num_pages);  // beyond the last page: zeros
+      int n = 0;                               // slots filled
       for (int it = first; it < last; ++it) {
         const Item w = Item::load(p.items, it);
-        for (int X = 0; X < 2; ++X) {
-          if (w.tiles(X, block_tokens) == 0) continue;
-          const uint32_t full = dev::smem_addr(&q_full[X]);
-          dev::mbar_wait(dev::smem_addr(&q_empty[X]), (uint32_t)((n[X] & 1) ^ 1), aborted, p.err);
-          dev::mbar_arrive_expect_tx(full, S::kQBytes);
-          for (int h = 0; h < S::kHalves; ++h)
-            tma_load_3d(sbase + X * S::kQBytes + h * (kRows * 128), &q_map, h * 64,
-                        w.head * p.group, w.row0 + X * block_tokens, full);
-          ++n[X];
-        }
-      }
-      for (int X = 0; X < 2; ++X)
-        if (n[X] > 0 &&
-            !dev::mbar_wait_bounded(dev::smem_addr(&q_full[X]), (uint32_t)((n[X] - 1) & 1)))
-          atomicOr(p.err, 2);
-    }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ MMAs
-    int n = 0;                    // ring slots consumed by earlier items
-    int q_n[2] = {0, 0};          // items so far, per block
-    int tile_n[2] = {0, 0};       // tiles so far, per block
-    for (int it = first; it < last; ++it) {
-      const Item w = Item::load(p.items, it);
-      const int tiles[2] = {w.tiles(0, block_tokens), w.tiles(1, block_tokens)};
-      const int last_block = w.tokens > block_tokens ? 1 : 0;  // sees the most tiles
-      const int keys = w.keys(last_block, block_tokens), all = tiles[last_block];
-      auto qk = [&](int X, int j) {
-        const int i = n + 2 * j, s = i % kSlots;
-        dev::mbar_wait(dev::smem_addr(&kv_full[s]), (uint32_t)((i / kSlots) & 1), aborted, p.err);
-        fence_after();
-        const uint32_t q_addr = sbase + X * S::kQBytes;
-        const uint32_t k_addr = sbase + S::kOffRing + s * S::kSlotBytes;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {  // 16 dims an MMA, 64 a 128-byte half
-          const uint32_t off = (uint32_t)(k % 4) * 32;
-          umma(tmem + X * 128, smem_desc(q_addr + (k / 4) * (kRows * 128) + off, 16, 1024),
-               smem_desc(k_addr + (k / 4) * S::kHalf + off, 16, 1024), kIdescQK, k > 0);
-        }
-        commit(&s_full[X]);
-        if (X == last_block) commit(&kv_empty[s]);
-        if (j == tiles[X] - 1) commit(&q_empty[X]);
-      };
-      for (int X = 0; X < 2; ++X) {
-        if (tiles[X] == 0) continue;
-        dev::mbar_wait(dev::smem_addr(&q_full[X]), (uint32_t)(q_n[X] & 1), aborted, p.err);
-        qk(X, 0);
-      }
-      for (int j = 0; j < all; ++j) {
-        const int i = n + 2 * j + 1, s = i % kSlots;
-        const uint32_t v_addr = sbase + S::kOffRing + s * S::kSlotBytes;
-        dev::mbar_wait(dev::smem_addr(&kv_full[s]), (uint32_t)((i / kSlots) & 1), aborted, p.err);
-        // rows of the last page behind the last visible token
-        const int tail = keys - (w.t0 + j) * kTok;
-        if (tail < kTok && tail % kPageSize) {
-          const int rows = kPageSize - tail % kPageSize;
-          for (int e = lane; e < rows * 8 * S::kHalves; e += 32) {
-            const int r = tail + e / (8 * S::kHalves), c = e % (8 * S::kHalves);
-            const uint32_t a = v_addr + (c / 8) * S::kHalf + r * 128 + (c % 8) * 16;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+        const int nblk = w.tokens > block_tokens ? 2 : 1;
+        const int keys = w.keys(nblk - 1, block_tokens), tiles = w.tiles(nblk - 1, block_tokens);
+        const int pages = (min(keys, w.t1 * kTok) + kPageSize - 1) / kPageSize;
+        int ids = 0;
+        for (int j = 0; j < tiles; ++j) {
+          const int page0 = (w.t0 + j) * kPages;
+          if (j % (32 / kPages) == 0) {  // the page ids of four tiles
+            const int at = page0 + lane;
+            ids = oob;
+            if (at < pages) {
+              const int id = p.indices ? __ldg(p.indices + w.entry + at) : w.entry + at;
+              if (id < 0 || (int64_t)id >= p.num_pages) {
+                atomicOr(p.err, 1);
+              } else {
+                ids = 2 * id;
+              }
+            }
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
+          // lane l: half l % kHalves of the tile's page l / kHalves
+          const int id = __shfl_sync(0xffffffffu, ids,
+                                     (j * kPages) % 32 + (lane / S::kHalves) % kPages);
+          const uint32_t at = (uint32_t)(lane % S::kHalves) * S::kHalf +
+                              (uint32_t)(lane / S::kHalves) * (kPageSize * 128);
 #pragma unroll
-        for (int X = 0; X < 2; ++X) {
-          if (j >= tiles[X]) continue;
-          dev::mbar_wait(dev::smem_addr(&p_full[X]), (uint32_t)(tile_n[X] & 1), aborted, p.err);
-          if (j == 0)  // the output of the block's item before has been read
-            dev::mbar_wait(dev::smem_addr(&o_empty[X]), (uint32_t)((q_n[X] & 1) ^ 1), aborted,
-                           p.err);
-          fence_after();
-          ++tile_n[X];
-#pragma unroll
-          for (int k = 0; k < kTok / 16; ++k)  // 16 tokens (8 columns of P) an MMA
-            umma_ts(tmem + 256 + X * 128, tmem + X * 128 + k * 8,
-                    smem_desc(v_addr + k * 16 * 128, S::kHalf, 1024), kIdescPV, j > 0 || k > 0);
-          if (X == last_block) commit(&kv_empty[s]);
-          if (j + 1 < tiles[X])
-            qk(X, j + 1);
-          else
-            commit(&o_full[X]);
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const int s = n % kSlots;
+            const uint32_t full = dev::smem_addr(&kv_full[s]);
+            dev::mbar_wait(dev::smem_addr(&kv_empty[s]), (uint32_t)(((n / kSlots) & 1) ^ 1),
+                           aborted, p.err);
+            if (lane == 0) dev::mbar_arrive_expect_tx(full, S::kSlotBytes);
+            __syncwarp();
+            if (lane < kPages * S::kHalves)
+              tma_load_4d_plain(sbase + S::kOffRing + s * S::kSlotBytes + at, &kv_map,
+                                (lane % S::kHalves) * 64, w.head, 0, id < oob ? id + kv : oob,
+                                full);
+          }
         }
         aborted = __any_sync(0xffffffffu, aborted);
       }
-      n += 2 * all;
-      for (int X = 0; X < 2; ++X) q_n[X] += tiles[X] > 0;
+      // no copy may still be landing when the CTA exits
+      if (lane == 0)
+        for (int i = n > kSlots ? n - kSlots : 0; i < n; ++i)
+          if (!dev::mbar_wait_bounded(dev::smem_addr(&kv_full[i % kSlots]),
+                                      (uint32_t)((i / kSlots) & 1)))
+            atomicOr(p.err, 2);
+    } else if (warp == 11) {
+      // ------------------------------------------------------------ Q loads
+      if (lane == 0) {
+        dev::prefetch_tensormap(&q_map);
+        int n[2] = {0, 0};
+        for (int it = first; it < last; ++it) {
+          const Item w = Item::load(p.items, it);
+          for (int X = 0; X < 2; ++X) {
+            if (w.tiles(X, block_tokens) == 0) continue;
+            const uint32_t full = dev::smem_addr(&q_full[X]);
+            dev::mbar_wait(dev::smem_addr(&q_empty[X]), (uint32_t)((n[X] & 1) ^ 1), aborted, p.err);
+            dev::mbar_arrive_expect_tx(full, S::kQBytes);
+            for (int h = 0; h < S::kHalves; ++h)
+              tma_load_3d(sbase + X * S::kQBytes + h * (kRows * 128), &q_map, h * 64,
+                          w.head * p.group, w.row0 + X * block_tokens, full);
+            ++n[X];
+          }
+        }
+        for (int X = 0; X < 2; ++X)
+          if (n[X] > 0 &&
+              !dev::mbar_wait_bounded(dev::smem_addr(&q_full[X]), (uint32_t)((n[X] - 1) & 1)))
+            atomicOr(p.err, 2);
+      }
+    } else if (warp == 10) {
+      // ------------------------------------------------------------ ragged ends
+      // V rows of the item's last page behind its last visible token are cleared
+      // once the MMA lane has seen the tile arrive (a wait of this warp's own on the
+      // ring could not tell a fill from the one two before)
+      int n = 0;       // ring slots up to the item's end
+      int ragged = 0;  // such items so far
+      for (int it = first; it < last; ++it) {
+        const Item w = Item::load(p.items, it);
+        const int last_block = w.tokens > block_tokens ? 1 : 0;
+        const int keys = w.keys(last_block, block_tokens), all = w.tiles(last_block, block_tokens);
+        n += 2 * all;
+        if (!w.ragged(keys, all)) continue;
+        const int tail = keys % kTok, rows = kPageSize - tail % kPageSize;
+        const uint32_t v_addr = sbase + S::kOffRing + (n - 1) % kSlots * S::kSlotBytes;
+        dev::mbar_wait(dev::smem_addr(v_there), (uint32_t)(ragged++ & 1), aborted, p.err);
+        for (int e = lane; e < rows * 8 * S::kHalves; e += 32) {
+          const int r = tail + e / (8 * S::kHalves), c = e % (8 * S::kHalves);
+          const uint32_t a = v_addr + (c / 8) * S::kHalf + r * 128 + (c % 8) * 16;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(dev::smem_addr(v_clean));
+      }
+    } else if (elect_one()) {
+      // ------------------------------------------------------------ MMAs
+      // One lane alone.  Between a block's last MMA and the other's first stands one
+      // wait, for the weights; the waits for K and V come behind issued MMAs.
+      int n = 0;                                 // ring slots consumed by earlier items
+      int cleared = 0;                           // ragged items so far
+      int item_n[2] = {0, 0}, tile_n[2] = {0, 0};  // items and tiles so far, per block
+      const uint64_t q_desc[2] = {smem_desc(sbase, 16, 1024),
+                                  smem_desc(sbase + S::kQBytes, 16, 1024)};
+      for (int it = first; it < last; ++it) {
+        const Item w = Item::load(p.items, it);
+        const int tiles[2] = {w.tiles(0, block_tokens), w.tiles(1, block_tokens)};
+        const int last_block = w.tokens > block_tokens ? 1 : 0;  // sees the most tiles
+        const int keys = w.keys(last_block, block_tokens), all = tiles[last_block];
+        const bool ragged = w.ragged(keys, all);
+        int slot = n % kSlots, phase = (n / kSlots) & 1;  // of K(j), then V(j), ...
+        auto full = [&](int s, int ph) {
+          dev::mbar_wait(dev::smem_addr(&kv_full[s]), (uint32_t)ph, aborted, p.err);
+        };
+        auto qk = [&](int X, int j, int s) {
+          const uint64_t k_desc = smem_desc(sbase + S::kOffRing + s * S::kSlotBytes, 16, 1024);
+#pragma unroll
+          for (int h = 0; h < S::kHalves; ++h)
+            umma4(tmem + X * 128, q_desc[X] + h * (kRows * 128 / 16),
+                  k_desc + h * (S::kHalf / 16), kIdescQK, h > 0);
+          commit_one(&s_full[X]);
+          if (X == last_block) commit_one(&kv_empty[s]);
+          if (j == tiles[X] - 1) commit_one(&q_empty[X]);
+        };
+        full(slot, phase);
+#pragma unroll
+        for (int X = 0; X < 2; ++X) {
+          if (tiles[X] == 0) continue;
+          dev::mbar_wait(dev::smem_addr(&q_full[X]), (uint32_t)(item_n[X] & 1), aborted, p.err);
+          fence_after();
+          qk(X, 0, slot);
+        }
+        auto advance = [&] {
+          if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
+        };
+        auto v_full = [&](int j) {
+          full(slot, phase);
+          if (ragged && j == all - 1) dev::mbar_arrive(dev::smem_addr(v_there));
+        };
+        advance();
+        v_full(0);
+        for (int j = 0; j < all; ++j) {
+          const int v_slot = slot;
+          const uint64_t v_desc =
+              smem_desc(sbase + S::kOffRing + v_slot * S::kSlotBytes, S::kHalf, 1024);
+          if (ragged && j == all - 1)
+            dev::mbar_wait(dev::smem_addr(v_clean), (uint32_t)(cleared++ & 1), aborted, p.err);
+          advance();  // to K(j + 1)
+          const int k_slot = slot, k_phase = phase;
+          advance();  // to V(j + 1)
+#pragma unroll
+          for (int X = 0; X < 2; ++X) {
+            if (j >= tiles[X]) continue;
+            if (j == 0)  // the output of the block's item before has been read
+              dev::mbar_wait(dev::smem_addr(&o_empty[X]), (uint32_t)((item_n[X] & 1) ^ 1), aborted,
+                             p.err);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // 64 tokens: 32 columns of P
+              dev::mbar_wait(dev::smem_addr(&p_full[2 * X + half]), (uint32_t)(tile_n[X] & 1),
+                             aborted, p.err);
+              fence_after();
+              umma4_ts(tmem + 256 + X * 128, tmem + X * 128 + half * 32,
+                       v_desc + half * (64 * 128 / 16), kIdescPV, j > 0 || half > 0);
+            }
+            ++tile_n[X];
+            if (X == last_block) {
+              commit_one(&kv_empty[v_slot]);
+              if (j + 1 < all) v_full(j + 1);
+            }
+            if (j + 1 < tiles[X]) {
+              full(k_slot, k_phase);
+              qk(X, j + 1, k_slot);
+            } else {
+              commit_one(&o_full[X]);
+            }
+          }
+        }
+        n += 2 * all;
+        for (int X = 0; X < 2; ++X) item_n[X] += tiles[X] > 0;
+      }
+      // TMEM is freed only after the last MMA completed
+      for (int X = 0; X < 2; ++X)
+        if (item_n[X] > 0 &&
+            !dev::mbar_wait_bounded(dev::smem_addr(&o_full[X]), (uint32_t)((item_n[X] - 1) & 1)))
+          atomicOr(p.err, 2);
     }
-    // TMEM is freed only after the last MMA completed
-    for (int X = 0; X < 2; ++X)
-      if (q_n[X] > 0 &&
-          !dev::mbar_wait_bounded(dev::smem_addr(&o_full[X]), (uint32_t)((q_n[X] - 1) & 1)) &&
-          lane == 0)
-        atomicOr(p.err, 2);
-  } else if (warp < 8) {
+    __syncwarp();
+  } else {
     // ------------------------------------------------------------ softmax and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int X = warp / 4, r = threadIdx.x % kRows;
     const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
     const uint32_t tS = tmem + X * 128 + lane_off, tO = tmem + 256 + X * 128 + lane_off;
@@ -367,12 +429,17 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         dev::mbar_wait(dev::smem_addr(&s_full[X]), (uint32_t)(tile_n & 1), aborted, p.err);
         fence_after();
         float s[kTok];
+        {
+          uint32_t raw[kTok / 32][32];  // all in flight before the one wait
 #pragma unroll
-        for (int c = 0; c < kTok / 32; ++c) {
-          float v[32];
-          ld32(tS + c * 32, v);
+          for (int c = 0; c < kTok / 32; ++c) ld32_start(tS + c * 32, raw[c]);
+          ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[c * 32 + i] = v[i];
+          for (int c = 0; c < kTok / 32; ++c) {
+            ld32_use(raw[c]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(raw[c][i]);
+          }
         }
         if (fewest < (j + 1) * kTok) {
           const int valid = seen - j * kTok;
@@ -396,13 +463,16 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         const float alpha = m == -INFINITY ? 0.f : dev::fast_exp2(m - m_new);
         if (j > 0 && __any_sync(0xffffffffu, rebase)) {
           // O holds the tiles before j
+          const float f = rebase ? alpha : 1.f;
+          const bool clear = rebase && m == -INFINITY;  // nothing seen so far
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float v[32];
-            ld32(tO + c * 32, v);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16];
+            ld16u(tO + c * 16, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = rebase ? (m == -INFINITY ? 0.f : v[i] * alpha) : v[i];
-            st32(tO + c * 32, v);
+            for (int i = 0; i < 16; ++i)
+              v[i] = clear ? 0u : __float_as_uint(__uint_as_float(v[i]) * f);
+            st16u(tO + c * 16, v);
           }
         }
         if (rebase) {
@@ -413,22 +483,24 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         const uint64_t scale2 = f2(scale, scale), neg_m2 = f2(-ref, -ref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < kTok / 64; ++c) {
-          uint32_t pk[32];
+        for (int c = 0; c < kTok / 32; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 16; ++i) {
             float x0, x1;
-            f2_split(fma2(f2(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), scale2, neg_m2), x0, x1);
+            f2_split(fma2(f2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), scale2, neg_m2), x0, x1);
             const float a0 = dev::fast_exp2(x0), a1 = dev::fast_exp2(x1);
             pk[i] = mma::pack2(a0, a1, kBf16);
             acc[i % 4] = add2(acc[i % 4], f2(a0, a1));
           }
-          st32u(tS + c * 32, pk);
+          st16u(tS + c * 16, pk);
+          if (c % 2) {  // half of the weights: P V may begin on them
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            fence_before();
+            __syncwarp();
+            if (lane == 0) dev::mbar_arrive(dev::smem_addr(&p_full[2 * X + c / 2]));
+          }
         }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        fence_before();
-        __syncwarp();
-        if (lane == 0) dev::mbar_arrive(dev::smem_addr(&p_full[X]));
         float lo, hi;
         f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), lo, hi);
         d += lo + hi;
@@ -439,7 +511,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         fence_after();
       }
       const bool ok = tok < w.tokens;
-      const float v_scale = p.head_v_scales ? p.v_scale * __ldg(p.head_v_scales + w.head) : p.v_scale;
+      const float v_scale =
+          p.head_v_scales ? p.v_scale * __ldg(p.head_v_scales + w.head) : p.v_scale;
       const float inv = d > 0.f || d != d ? v_scale / d : 0.f;
       const float lse = d > 0.f || d != d ? m + log2f(d) : -INFINITY;
       const size_t row = (size_t)(w.row0 + tok) * p.num_qo_heads + (size_t)w.head * p.group + g;

@@ -82,6 +82,32 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// The same without waiting: the registers hold the columns after ld_wait, and
+// are handed to it before their use.
+__device__ __forceinline__ void ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      :
+        "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void ld_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Ties registers of ld32_start to the wait before it.
+__device__ __forceinline__ void ld32_use(uint32_t (&r)[32]) {
+  asm volatile(""
+               :
+                 "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
 __device__ __forceinline__ void st32(uint32_t taddr, const float (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
@@ -137,6 +163,54 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(e));
+  return e != 0;
+}
+
+// The forms for a warp of which one lane runs alone: four MMAs of one accumulator,
+// K 16 each.  (An election and fresh descriptors for each MMA took the issuing
+// warp 80 cycles an MMA of 64.)  A and B K-major in shared memory, 16 elements (32
+// bytes) a step.
+__device__ __forceinline__ void umma4(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                      bool accumulate) {
+  asm volatile(
+      "{\n.reg .pred p, t;\n.reg .b64 x, y;\n"
+      "setp.ne.b32 p, %4, 0;\nsetp.eq.b32 t, 0, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "add.s64 x, %1, 2;\nadd.s64 y, %2, 2;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n"
+      "add.s64 x, %1, 4;\nadd.s64 y, %2, 4;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n"
+      "add.s64 x, %1, 6;\nadd.s64 y, %2, 6;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+}
+// A in TMEM (8 columns a step), B MN-major in shared memory (16 rows of 128 bytes).
+__device__ __forceinline__ void umma4_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                         uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n.reg .pred p, t;\n.reg .b32 x;\n.reg .b64 y;\n"
+      "setp.ne.b32 p, %4, 0;\nsetp.eq.b32 t, 0, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      "add.s32 x, %1, 8;\nadd.s64 y, %2, 128;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n"
+      "add.s32 x, %1, 16;\nadd.s64 y, %2, 256;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n"
+      "add.s32 x, %1, 24;\nadd.s64 y, %2, 384;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          dev::smem_addr(bar))
+      : "memory");
+}
+
 // 32 consecutive 32-bit columns of this thread's TMEM lane from packed words
 __device__ __forceinline__ void st32u(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
@@ -148,6 +222,26 @@ __device__ __forceinline__ void st32u(uint32_t taddr, const uint32_t (&v)[32]) {
       "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
       "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
       "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+// 16 columns, as they are
+__device__ __forceinline__ void ld16u(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      :
+        "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 
