@@ -752,7 +752,7 @@ int fa_prefill_plan(const int32_t* indptr_host, const int32_t* indices_dev,
  *  paged_kv, num_pages, sm_scale: as fa_decode_run.
  *  k_scale,   per-tensor scales of an E4M3 cache, 0 or positive; 1 for other kv
  *  v_scale    types (FA_ERR_INVALID_ARG otherwise).
- *  o          [rows, num_qo_heads, head_dim] contiguous, q dtype, device, 16-byte
+ *  o          [rows, num_qo_heads, head_dim] contiguous, q dtype, device, 32-byte
  *             aligned; not q itself.
  *  lse        [rows, num_qo_heads] float32, device, or NULL.
  * One to three kernels on cuda_stream, no allocation, no synchronisation: it can

@@ -419,7 +419,7 @@ int prefill_run(fa_prefill_plan_s* plan, int sc, const fa_rows* q, const void* p
   if (plan->rows == 0) return FA_OK;
   if (!q || !q->data || !paged_kv || !o || num_pages <= 0 || num_pages >= (1 << 30) ||
       reinterpret_cast<uintptr_t>(paged_kv) % 16 || reinterpret_cast<uintptr_t>(q->data) % 16 ||
-      reinterpret_cast<uintptr_t>(o) % 16 || reinterpret_cast<uintptr_t>(lse) % 4 ||
+      reinterpret_cast<uintptr_t>(o) % 32 || reinterpret_cast<uintptr_t>(lse) % 4 ||
       q->token_stride % 8 || q->head_stride % 8 || (plan->rows > 1 && q->token_stride <= 0) ||
       (plan->hq > 1 && q->head_stride <= 0))
     return FA_ERR_INVALID_ARG;

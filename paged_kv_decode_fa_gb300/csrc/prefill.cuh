@@ -148,6 +148,13 @@ __device__ __forceinline__ void tma_load_4d_plain(uint32_t dst, const CUtensorMa
       : "memory");
 }
 
+// 32 bytes in one store, a whole sector (32-byte aligned).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(pf::kThreads, 1)
     fa_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
@@ -517,38 +524,45 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
       const float lse = d > 0.f || d != d ? m + log2f(d) : -INFINITY;
       const size_t row = (size_t)(w.row0 + tok) * p.num_qo_heads + (size_t)w.head * p.group + g;
       const size_t part = (size_t)(w.slot < 0 ? 0 : w.slot) * 256 + X * kRows + r;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        float v[32];
-        if (tiles > 0) {
-          ld32(tO + c * 32, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
-        if (ok && w.slot < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * D + c * 32);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(mma::pack2(v[8 * i] * inv, v[8 * i + 1] * inv, kBf16),
-                                mma::pack2(v[8 * i + 2] * inv, v[8 * i + 3] * inv, kBf16),
-                                mma::pack2(v[8 * i + 4] * inv, v[8 * i + 5] * inv, kBf16),
-                                mma::pack2(v[8 * i + 6] * inv, v[8 * i + 7] * inv, kBf16));
-        } else if (ok) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv,
-                                 v[4 * i + 3] * inv);
-        }
-        __syncwarp();
-      }
+      uint32_t raw[D / 32][32];
       if (tiles > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) ld32_start(tO + c * 32, raw[c]);
+        ld_wait();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) ld32_use(raw[c]);
         fence_before();
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(dev::smem_addr(&o_empty[X]));
         ++item_n;
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) raw[c][i] = 0u;
       }
+      auto value = [&](int i) { return __uint_as_float(raw[i / 32][i % 32]) * inv; };
+      if (ok && w.slot < 0) {
+        T* dst = static_cast<T*>(p.o) + row * D;
+#pragma unroll
+        for (int i = 0; i < D; i += 16) {
+          uint32_t x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            x[e] = mma::pack2(value(i + 2 * e), value(i + 2 * e + 1), kBf16);
+          store32(dst + i, x);
+        }
+      } else if (ok) {
+        float* dst = p.part_o + part * D;
+#pragma unroll
+        for (int i = 0; i < D; i += 8) {
+          uint32_t x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(value(i + e));
+          store32(dst + i, x);
+        }
+      }
+      __syncwarp();
       if (ok) {
         if (w.slot >= 0)
           p.part_lse[part] = lse;

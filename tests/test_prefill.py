@@ -433,6 +433,7 @@ def test_run_refusals(lib, cuda):
                 lambda: p.run(b.q, b.kv, k_scale=-1.0), lambda: p.run(b.q, b.kv, v_scale=float("nan")),
                 lambda: p.run(b.q, b.kv, out=b.q), lambda: p.run(b.q, b.kv, out=torch.empty_like(b.q)[:9]),
                 lambda: p.run(b.q, b.kv, lse=torch.empty(4, device=cuda)),
+                lambda: p.run(b.q, b.kv, out=torch.empty(b.q.numel() + 8, dtype=BF16, device=cuda)[8:]),
                 lambda: p.run(b.q, b.kv, out=torch.empty(b.q.shape, dtype=BF16)),
                 lambda: p.run_head_scales(b.q, b.kv, sb, sb), lambda: p.run_block_scales(b.q, b.kv, sh, sh),
                 lambda: p.run_token_scales(b.q, b.kv, sb, sb),
