@@ -35,6 +35,7 @@ namespace fadecode {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kMostPages = 64;  // of a run
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
@@ -61,6 +62,7 @@ struct WeightsParams {
   int* err;
   int64_t num_pages;
   int hq, hkv;
+  int group_log2;
   float scale;  // sm_scale * k_scale * log2(e)
 };
 
@@ -90,30 +92,89 @@ __device__ __forceinline__ uint32_t widen2(uint32_t codes) {
   }
 }
 
-template <typename T, typename KVT, int D, int SC>
-__global__ void __launch_bounds__(kWarps * 32, 2) fa_weights_kernel(const WeightsParams p) {
-  constexpr bool kE4m3 = !std::is_same<T, KVT>::value;
-  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int kPiece = 16 / sizeof(KVT);       // elements of a lane's 16 bytes of K
-  constexpr int kPieces = D / (4 * kPiece);      // of them in a row
-  constexpr int kQPieces = D / 32;
-  const int4* up = reinterpret_cast<const int4*>(p.units + blockIdx.x / p.hkv);
-  const int4 ua = __ldg(up), ub = __ldg(up + 1);
-  const int row0 = ua.x, rows = ua.y, entry = ua.z, pages = ua.w, pos0 = ub.x, before = ub.y;
-  const int h = blockIdx.x % p.hkv, G = p.hq / p.hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = lane % 4, n = lane / 4;  // piece of a row; token and column of the fragments
-  const int columns = rows * G;
-  const KVT* kv = static_cast<const KVT*>(p.kv);
-  const int64_t token_stride = (int64_t)p.hkv * D;
+// Fragments of a page's K: two MMAs' A operands (rows n and n + 8, 16 dims each) for each
+// 16-byte piece of a q row.
+template <int D>
+struct Fragments {
+  uint32_t a[D / 32][2][4];
+};
 
-  auto load_page = [&](int i, uint4 (&k)[2][kPieces]) -> int {
-    int page = i < pages ? __ldg(p.indices + entry + i) : -1;
-    if (page < 0 || (int64_t)page >= p.num_pages) {
-      if (i < pages && lane == 0) atomicOr(p.err, 1);
-      page = -1;
+template <typename T, typename KVT, int D>
+__device__ __forceinline__ void widen_page(const uint4 (&k)[2][D * sizeof(KVT) / 64],
+                                           Fragments<D>* f) {
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    if constexpr (!std::is_same<T, KVT>::value) {
+      const uint4 lo = k[0][j / 2], hi = k[1][j / 2];
+      const uint32_t l[2] = {j % 2 ? lo.z : lo.x, j % 2 ? lo.w : lo.y};
+      const uint32_t h[2] = {j % 2 ? hi.z : hi.x, j % 2 ? hi.w : hi.y};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f->a[j][i][0] = widen2<T>(l[i] & 0xffffu);
+        f->a[j][i][1] = widen2<T>(h[i] & 0xffffu);
+        f->a[j][i][2] = widen2<T>(l[i] >> 16);
+        f->a[j][i][3] = widen2<T>(h[i] >> 16);
+      }
+    } else {
+      const uint4 lo = k[0][j], hi = k[1][j];
+      const uint32_t w[2][4] = {{lo.x, hi.x, lo.y, hi.y}, {lo.z, hi.z, lo.w, hi.w}};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f->a[j][i][e] = w[i][e];
     }
-    const KVT* base = kv + (int64_t)max(page, 0) * 2 * kPageSize * token_stride + (int64_t)h * D;
+  }
+}
+
+// What a CTA works on, and the loads of both kernels.
+template <typename T, typename KVT, int D, int SC>
+struct Worker {
+  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr bool kE4m3 = !std::is_same<T, KVT>::value;
+  static constexpr int kPiece = 16 / sizeof(KVT);  // elements of a lane's 16 bytes of K
+  static constexpr int kPieces = D / (4 * kPiece);  // of them in a row
+  static constexpr int kQPieces = D / 32;
+  const WeightsParams& p;
+  int row0, rows, entry, pages, pos0, before;  // see WeightsUnit
+  int h, lane, c, n;  // c: piece of a row; n: token and column of the fragments
+  int columns;
+  int ids[2];  // of the run's pages lane and lane + 32, -1 for none
+  float head_scale;
+
+  __device__ __forceinline__ explicit Worker(const WeightsParams& params) : p(params) {
+    const int4* up = reinterpret_cast<const int4*>(p.units + blockIdx.x / p.hkv);
+    const int4 a = __ldg(up), b = __ldg(up + 1);
+    row0 = a.x;
+    rows = a.y;
+    entry = a.z;
+    pages = a.w;
+    pos0 = b.x;
+    before = b.y;
+    h = blockIdx.x % p.hkv;
+    lane = threadIdx.x & 31;
+    c = lane % 4;
+    n = lane / 4;
+    columns = rows << p.group_log2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = lane + 32 * i;
+      ids[i] = at < pages ? __ldg(p.indices + entry + at) : -1;
+      if (ids[i] < 0 || (int64_t)ids[i] >= p.num_pages) {
+        if (at < pages) atomicOr(p.err, 1);
+        ids[i] = -1;
+      }
+    }
+    head_scale = p.head_k_scales ? p.scale * __ldg(p.head_k_scales + h) : p.scale;
+  }
+  // K of the run's page i; -1 if there is none
+  __device__ __forceinline__ int load_page(int i, uint4 (&k)[2][kPieces]) const {
+    static_assert(kMostPages <= 64, "the run's page ids are held two a lane");
+    const int lo = __shfl_sync(0xffffffffu, ids[0], i % 32);
+    const int hi = __shfl_sync(0xffffffffu, ids[1], i % 32);
+    const int page = i < 32 ? lo : i < 64 ? hi : -1;
+    const int64_t token_stride = (int64_t)p.hkv * D;
+    const KVT* base = static_cast<const KVT*>(p.kv) +
+                      (int64_t)max(page, 0) * 2 * kPageSize * token_stride + (int64_t)h * D;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -122,103 +183,143 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fa_weights_kernel(const Weight
                            : __ldg(reinterpret_cast<const uint4*>(
                                  base + (n + 8 * t) * token_stride + (4 * j + c) * kPiece));
     return page;
-  };
-  // column x = (row, head): its q row as B fragments, its log2 lse and last position
-  auto load_column = [&](int x, uint4 (&b)[kQPieces]) {
-    const T* q = static_cast<const T*>(p.q) + (row0 + x / G) * p.q_token +
-                 (int64_t)(h * G + x % G) * p.q_head;
+  }
+  // column x = (row, head of the group): its q row as B fragments
+  __device__ __forceinline__ void load_column(int x, uint4 (&b)[kQPieces]) const {
+    const T* q = static_cast<const T*>(p.q) + (row0 + (x >> p.group_log2)) * p.q_token +
+                 (int64_t)((h << p.group_log2) + (x & ((1 << p.group_log2) - 1))) * p.q_head;
 #pragma unroll
     for (int j = 0; j < kQPieces; ++j) {
       // the dims that this lane's piece of K holds
       const int d = kE4m3 ? (j / 2) * 64 + c * 16 + (j % 2) * 8 : (4 * j + c) * 8;
       b[j] = x < columns ? __ldg(reinterpret_cast<const uint4*>(q + d)) : make_uint4(0u, 0u, 0u, 0u);
     }
-  };
-
-  uint4 held[kQPieces];  // the only columns, where there are eight at most
-  const bool single = columns <= 8;
-  if (single) load_column(n, held);
-  const float head_scale = p.head_k_scales ? p.scale * __ldg(p.head_k_scales + h) : p.scale;
-
-  uint4 raw[2][kPieces];
-  int page = load_page(warp, raw);
-  for (int i = warp; i < pages; i += kWarps) {
-    uint4 k[2][kPieces];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j) k[t][j] = raw[t][j];
-    const int this_page = page;
-    page = load_page(i + kWarps, raw);
-    if (this_page < 0) continue;
-    const int64_t at = ((int64_t)this_page * p.hkv + h) * kPageSize;
-    float scale[2] = {head_scale, head_scale};  // of tokens n and n + 8
+  }
+  // its lse in log2 units; +inf (weight 0) behind the last column and where the row
+  // saw nothing
+  __device__ __forceinline__ float load_lse(int x) const {
+    const int row = x >> p.group_log2, g = x & ((1 << p.group_log2) - 1);
+    const float lse = x < columns ? __ldg(p.lse + (int64_t)(row0 + row) * p.hq +
+                                          (h << p.group_log2) + g) * 1.4426950408889634f
+                                  : INFINITY;
+    return lse == -INFINITY ? INFINITY : lse;
+  }
+  // the logit scales of tokens n and n + 8 of a page
+  __device__ __forceinline__ void load_scales(int page, float (&scale)[2]) const {
+    const int64_t at = ((int64_t)page * p.hkv + h) * kPageSize;
+    scale[0] = scale[1] = head_scale;
     if constexpr (SC == kScalePerToken) {
       scale[0] *= __ldg(p.k_scales + at + n);
       scale[1] *= __ldg(p.k_scales + at + n + 8);
     } else if constexpr (SC == kScalePerBlock) {
       scale[0] = scale[1] = head_scale * __ldg(p.k_scales + at / kPageSize);
     }
-    const int pos = pos0 + i * kPageSize + n;
-    float sum[2] = {0.f, 0.f};
-    for (int x0 = 0; x0 < columns; x0 += 8) {
-      uint4 b[kQPieces];
-      if (single) {
+  }
+  // Eight columns from x0 on against a page whose token n is at position pos:
+  // their weights' sums for tokens n and n + 8, this lane's two columns
+  __device__ __forceinline__ void add_columns(const Fragments<D>& k, const uint4 (&b)[kQPieces],
+                                              int x0, const float (&lse)[2],
+                                              const float (&scale)[2], int pos,
+                                              float (&sum)[2]) const {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < kQPieces; ++j) b[j] = held[j];
-      } else {
-        load_column(x0 + n, b);
-      }
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < kQPieces; ++j) {
-        uint32_t a[2][4];  // two MMAs of a 16-byte piece of q
-        if constexpr (kE4m3) {
-          const uint4 lo = k[0][j / 2], hi = k[1][j / 2];
-          const uint32_t l0 = j % 2 ? lo.z : lo.x, l1 = j % 2 ? lo.w : lo.y;
-          const uint32_t h0 = j % 2 ? hi.z : hi.x, h1 = j % 2 ? hi.w : hi.y;
-          a[0][0] = widen2<T>(l0 & 0xffffu);
-          a[0][1] = widen2<T>(h0 & 0xffffu);
-          a[0][2] = widen2<T>(l0 >> 16);
-          a[0][3] = widen2<T>(h0 >> 16);
-          a[1][0] = widen2<T>(l1 & 0xffffu);
-          a[1][1] = widen2<T>(h1 & 0xffffu);
-          a[1][2] = widen2<T>(l1 >> 16);
-          a[1][3] = widen2<T>(h1 >> 16);
-        } else {
-          a[0][0] = k[0][j].x;
-          a[0][1] = k[1][j].x;
-          a[0][2] = k[0][j].y;
-          a[0][3] = k[1][j].y;
-          a[1][0] = k[0][j].z;
-          a[1][1] = k[1][j].z;
-          a[1][2] = k[0][j].w;
-          a[1][3] = k[1][j].w;
-        }
-        mma_16816(s, a[0], b[j].x, b[j].y, kBf16);
-        mma_16816(s, a[1], b[j].z, b[j].w, kBf16);
-      }
-      // s[0], s[1]: token n, columns x0 + 2c, + 1; s[2], s[3]: token n + 8
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int x = x0 + 2 * c + e;
-        if (x >= columns) continue;
-        const int row = x / G;
-        float lse = __ldg(p.lse + (int64_t)(row0 + row) * p.hq + h * G + x % G) * 1.4426950408889634f;
-        lse = lse == -INFINITY ? INFINITY : lse;  // a row that saw nothing
-        const int last = before + row;
-        if (pos <= last) sum[0] += dev::fast_exp2(fmaf(s[e], scale[0], -lse));
-        if (pos + 8 <= last) sum[1] += dev::fast_exp2(fmaf(s[2 + e], scale[1], -lse));
-      }
+    for (int j = 0; j < kQPieces; ++j) {
+      mma_16816(s, k.a[j][0], b[j].x, b[j].y, kBf16);
+      mma_16816(s, k.a[j][1], b[j].z, b[j].w, kBf16);
     }
+    // s[0], s[1]: token n, columns x0 + 2c, + 1; s[2], s[3]: token n + 8
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int last = before + ((x0 + 2 * c + e) >> p.group_log2);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (pos + 8 * t <= last) sum[t] += dev::fast_exp2(fmaf(s[2 * t + e], scale[t], -lse[e]));
+    }
+  }
+  // A page's sums over its columns, added to the weights; tokens that no row sees
+  // (slots behind the request's last) stay
+  __device__ __forceinline__ void store(int page, int pos, float (&sum)[2]) const {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], 1);
       sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], 2);
     }
-    // tokens that no row sees (slots behind the request's last) stay
-    if (c < 2 && pos + 8 * c <= before + rows - 1) atomicAdd(p.weights + at + n + 8 * c, sum[c]);
+    if (page >= 0 && c < 2 && pos + 8 * c <= before + rows - 1)
+      atomicAdd(p.weights + ((int64_t)page * p.hkv + h) * kPageSize + n + 8 * c, sum[c]);
   }
+};
+
+// Eight columns at most (a decode step): they stay in registers while the pages
+// pass, each loaded while the one before is worked on.
+template <typename T, typename KVT, int D, int SC>
+__device__ __forceinline__ void weights_of_few(const Worker<T, KVT, D, SC>& w) {
+  using W = Worker<T, KVT, D, SC>;
+  uint4 q[W::kQPieces];
+  w.load_column(w.n, q);
+  const float lse[2] = {w.load_lse(2 * w.c), w.load_lse(2 * w.c + 1)};
+  uint4 raw[2][W::kPieces];
+  const int warp = threadIdx.x >> 5;
+  int page = w.load_page(warp, raw);
+  for (int i = warp; i < w.pages; i += kWarps) {
+    Fragments<D> k;
+    widen_page<T, KVT, D>(raw, &k);
+    const int this_page = page;
+    page = w.load_page(i + kWarps, raw);
+    if (this_page < 0) continue;
+    float scale[2], sum[2] = {0.f, 0.f};
+    w.load_scales(this_page, scale);
+    const int pos = w.pos0 + i * kPageSize + w.n;
+    w.add_columns(k, q, 0, lse, scale, pos, sum);
+    w.store(this_page, pos, sum);
+  }
+}
+
+// More columns: a warp holds the K of two pages while all columns pass, eight at a
+// time, the next eight's q on their way.
+template <typename T, typename KVT, int D, int SC>
+__device__ __forceinline__ void weights_of_many(const Worker<T, KVT, D, SC>& w) {
+  using W = Worker<T, KVT, D, SC>;
+  const int warp = threadIdx.x >> 5;
+  for (int i = 2 * warp; i < w.pages; i += 2 * kWarps) {
+    Fragments<D> k[2];
+    int page[2], pos[2];
+    float scale[2][2], sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint4 raw[2][W::kPieces];
+      page[t] = w.load_page(i + t, raw);
+      widen_page<T, KVT, D>(raw, &k[t]);
+      w.load_scales(max(page[t], 0), scale[t]);
+      pos[t] = w.pos0 + (i + t) * kPageSize + w.n;
+    }
+    uint4 next[W::kQPieces];
+    float next_lse[2] = {w.load_lse(2 * w.c), w.load_lse(2 * w.c + 1)};
+    w.load_column(w.n, next);
+    for (int x0 = 0; x0 < w.columns; x0 += 8) {
+      uint4 q[W::kQPieces];
+#pragma unroll
+      for (int j = 0; j < W::kQPieces; ++j) q[j] = next[j];
+      const float lse[2] = {next_lse[0], next_lse[1]};
+      if (x0 + 8 < w.columns) {
+        w.load_column(x0 + 8 + w.n, next);
+        next_lse[0] = w.load_lse(x0 + 8 + 2 * w.c);
+        next_lse[1] = w.load_lse(x0 + 9 + 2 * w.c);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) w.add_columns(k[t], q, x0, lse, scale[t], pos[t], sum[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) w.store(page[t], pos[t], sum[t]);
+  }
+}
+
+template <typename T, typename KVT, int D, int SC>
+__global__ void __launch_bounds__(kWarps * 32, 2) fa_weights_kernel(const WeightsParams p) {
+  const Worker<T, KVT, D, SC> w(p);
+  if (w.columns <= 8)
+    weights_of_few(w);
+  else
+    weights_of_many(w);
 }
 
 using WeightsFn = void (*)(const WeightsParams);
@@ -247,7 +348,6 @@ bool weights_pair_built(fa_dtype q, fa_dtype kv) {
 }
 
 // Pages of a run: 64 (eight a warp), halved while that leaves under four CTAs an SM.
-constexpr int kMostPages = 64;
 int run_pages(int64_t total_pages, int heads, int sms) {
   int n = kMostPages;
   while (n > kWarps && total_pages * heads < (int64_t)n * 4 * sms) n /= 2;
@@ -325,6 +425,7 @@ int weights_run(fa_weights_plan_s* plan, int sc, const fa_rows* q, const void* p
   p.num_pages = num_pages;
   p.hq = plan->hq;
   p.hkv = plan->hkv;
+  while ((plan->hkv << p.group_log2) < plan->hq) ++p.group_log2;
   p.scale = sm_scale * k_scale * 1.4426950408889634f;
   const bool e4m3 = plan->kv_dtype == FA_DTYPE_E4M3;
   const WeightsFn f = plan->d == 128 ? find_weights_kernel<128>(plan->q_dtype, e4m3, sc)
