@@ -896,7 +896,7 @@ int fa_evict_plan(const int32_t* indptr_host, const int32_t* indices_dev,
  *
  *  paged_kv   as fa_append_run, read and written.  Tokens on a page id outside
  *             [0, num_pages) are not moved, and set the device-check word.
- *  weights    as above, read and written.
+ *  weights    as above, 16-byte aligned, read and written.
  *  k_scales,  [num_pages, num_kv_heads, page_size] float32, device: the scales of an
  *  v_scales   E4M3 cache that has one per token, moved with the tokens; NULL for
  *             caches without (FA_ERR_UNSUPPORTED for other types).  A cache with

@@ -41,9 +41,13 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;              // of a cluster
-constexpr int kBuffer = 48 << 10;         // keys, then rows
-constexpr int kRankInfo = 512;            // ranks of a chunk at most
+// Dynamic shared memory: keys, then two stages of rows.  Four CTAs an SM, or two
+// with twice as much each where there are no more.
+constexpr int kBuffer = 40 << 10, kBigBuffer = 96 << 10;
+constexpr int kRankInfo = 192;            // ranks of a chunk at most
+constexpr int kBatch = 4;                 // loads of a thread in flight
 
 struct EvictUnit {
   int32_t entry, length, kept, recent;
@@ -64,6 +68,7 @@ struct EvictParams {
   int64_t num_pages;
   int hkv;
   int row_bytes;  // of K (or V) of one token and head
+  int buffer;     // bytes of dynamic shared memory
 };
 
 // Unsigned order = order of the floats, NaN above all, -0 = 0.
@@ -76,10 +81,12 @@ __device__ __forceinline__ uint32_t key_of(float w) {
 struct EvictShared {
   int hist[2][256];
   int counts[2];        // kept for sure / equal to the last key, of this CTA
-  int warp_counts[2][kThreads / 32];
+  int warp_counts[2][kWarps];
   int digit, above;     // of one pass
-  int64_t src[kRankInfo], dst[kRankInfo];  // page * 16 + slot; -1: nothing to move
-  float moved[3][kRankInfo];               // weight, K scale, V scale
+  // a chunk's ranks: from and to page * 16 + slot (from -1: nothing to move), and
+  // what moves beside the rows: weight, K scale, V scale
+  int64_t src[2][kRankInfo], dst[2][kRankInfo];
+  float moved[2][3][kRankInfo];
 };
 
 __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams p) {
@@ -106,16 +113,37 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
     return ((at / kPageSize) * p.hkv + h) * kPageSize + at % kPageSize;
   };
 
-  // ---- 1. the keys of tokens t0 .. t1
-  const int t0 = (int)((int64_t)cand * c / C), t1 = (int)((int64_t)cand * (c + 1) / C);
+  // ---- 1. the keys of tokens t0 .. t1 (t0 at a page's start: four tokens a load)
+  const int share = ((cand + C - 1) / C + kPageSize - 1) / kPageSize * kPageSize;
+  const int t0 = min(c * share, cand), t1 = min(t0 + share, cand);
   uint32_t* keys = reinterpret_cast<uint32_t*>(buffer);
-  const bool held = (t1 - t0) * 4 <= kBuffer;
+  const bool held = (t1 - t0 + 3) / 4 * 16 <= p.buffer;
   auto read_key = [&](int t) -> uint32_t {
     const int64_t at = place(t);
     return at < 0 ? key_of(0.f) : key_of(p.weights[token_at(at)]);
   };
-  if (held)
-    for (int t = t0 + tid; t < t1; t += kThreads) keys[t - t0] = read_key(t);
+  if (held) {
+    for (int i = t0 + 4 * tid; i < t1; i += 4 * kThreads * kBatch) {
+      int64_t at[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int t = i + 4 * kThreads * k;
+        at[k] = t < t1 ? place(t) : -1;
+      }
+      float4 w[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        w[k] = at[k] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                         : *reinterpret_cast<const float4*>(p.weights + token_at(at[k]));
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int t = i + 4 * kThreads * k;
+        if (t < t1)  // keys behind t1, of the same page, are not looked at
+          *reinterpret_cast<uint4*>(keys + (t - t0)) =
+              make_uint4(key_of(w[k].x), key_of(w[k].y), key_of(w[k].z), key_of(w[k].w));
+      }
+    }
+  }
   auto key = [&](int t) { return held ? keys[t - t0] : read_key(t); };
   __syncthreads();
 
@@ -134,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
         const int t = i + tid;
         const uint32_t k = t < t1 ? key(t) : 0;
         const bool in = t < t1 && (pass == 0 || (k >> (shift + 8)) == prefix);
+        if (!__any_sync(0xffffffffu, in)) continue;
         const int digit = in ? (int)((k >> shift) & 0xff) : 256;
         // equal digits of a warp are counted once (weights crowd few exponents)
         const unsigned same = __match_any_sync(0xffffffffu, digit);
@@ -165,121 +194,152 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
     ties = left;
   }
 
-  // ---- 3. ranks
-  auto flags = [&](int t, bool* above, bool* equal) {
-    const uint32_t k = t < t1 && want > 0 ? key(t) : 0;
-    *above = t < t1 && want > 0 && k > border;
-    *equal = t < t1 && want > 0 && k == border;
+  // ---- 3. ranks: a warp takes a run of the CTA's tokens
+  auto flags = [&](int t, int end, bool* above, bool* equal) {
+    const uint32_t k = t < end && want > 0 ? key(t) : 0;
+    *above = t < end && want > 0 && k > border;
+    *equal = t < end && want > 0 && k == border;
   };
+  const int per_warp = ((t1 - t0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+  const int w0 = min(t0 + warp * per_warp, t1), w1 = min(w0 + per_warp, t1);
   {
     int a = 0, e = 0;
-    for (int i = t0; i < t1; i += kThreads) {
+    for (int i = w0; i < w1; i += 32) {
       bool above, equal;
-      flags(i + tid, &above, &equal);
+      flags(i + lane, w1, &above, &equal);
       a += __popc(__ballot_sync(0xffffffffu, above));
       e += __popc(__ballot_sync(0xffffffffu, equal));
     }
-    if (tid < 2) sh.counts[tid] = 0;
-    __syncthreads();
     if (lane == 0) {
-      atomicAdd(&sh.counts[0], a);
-      atomicAdd(&sh.counts[1], e);
+      sh.warp_counts[0][warp] = a;
+      sh.warp_counts[1][warp] = e;
+    }
+    __syncthreads();
+    if (tid < 2) {
+      int sum = 0;
+      for (int w = 0; w < kWarps; ++w) sum += sh.warp_counts[tid][w];
+      sh.counts[tid] = sum;
     }
   }
   cluster.sync();
-  int above_before = 0, equal_before = 0;
-  for (int r = 0; r < c; ++r) {
-    const int* other = cluster.map_shared_rank(sh.counts, r);
-    above_before += other[0];
-    equal_before += other[1];
-  }
-  for (int i = t0; i < t1; i += kThreads) {
-    bool above, equal;
-    flags(i + tid, &above, &equal);
-    const unsigned ma = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, equal);
-    __syncthreads();
-    if (lane == 0) {
-      sh.warp_counts[0][warp] = __popc(ma);
-      sh.warp_counts[1][warp] = __popc(me);
+  {
+    int a = 0, e = 0;  // kept for sure, and equal to the border, before this warp
+    for (int r = 0; r < c; ++r) {
+      const int* other = cluster.map_shared_rank(sh.counts, r);
+      a += other[0];
+      e += other[1];
     }
-    __syncthreads();
-    int a = above_before, e = equal_before;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const int wa = sh.warp_counts[0][w], we = sh.warp_counts[1][w];
-      if (w < warp) {
-        a += wa;
-        e += we;
-      }
-      above_before += wa;
-      equal_before += we;
+    for (int w = 0; w < warp; ++w) {
+      a += sh.warp_counts[0][w];
+      e += sh.warp_counts[1][w];
     }
     const unsigned below = (1u << lane) - 1;
-    a += __popc(ma & below);
-    e += __popc(me & below);
-    if (above || (equal && e < ties)) list[a + min(e, ties)] = i + tid;
+    for (int i = w0; i < w1; i += 32) {
+      bool above, equal;
+      flags(i + lane, w1, &above, &equal);
+      const unsigned ma = __ballot_sync(0xffffffffu, above);
+      const unsigned me = __ballot_sync(0xffffffffu, equal);
+      const int mine = e + __popc(me & below);
+      if (above || (equal && mine < ties))
+        list[a + __popc(ma & below) + min(mine, ties)] = i + lane;
+      a += __popc(ma);
+      e += __popc(me);
+    }
   }
   for (int i = c * kThreads + tid; i < u.recent; i += C * kThreads) list[want + i] = cand + i;
   cluster.sync();  // the list is whole, and the keys are done with
 
-  // ---- 4. the rows, a chunk of ranks at a time
+  // ---- 4. the rows, a chunk of ranks at a time, the next chunk's on their way
   const int rb = p.row_bytes, pieces = 2 * rb / 16;  // 16-byte pieces of a token's K and V
-  const int chunk = min(kRankInfo, kBuffer / (2 * rb));
+  const int chunk = min(kRankInfo, p.buffer / 2 / (2 * rb));
   const int64_t token_bytes = (int64_t)p.hkv * rb, page_half = kPageSize * token_bytes;
-  const uint32_t sbase = dev::smem_addr(buffer);
   auto address = [&](int64_t at, int piece) -> uint8_t* {
     const int half = piece * 16 >= rb;
     return p.kv + (at / kPageSize * 2 + half) * page_half + (at % kPageSize) * token_bytes +
            (int64_t)h * rb + (piece * 16 - half * rb);
   };
-  for (int r0 = 0; r0 < n; r0 += C * chunk) {
-    const int first = r0 + c * chunk, count = max(0, min(chunk, n - first));
+  const int steps = (n + C * chunk - 1) / (C * chunk);
+  auto count_of = [&](int step) {
+    return max(0, min(chunk, n - (step * C + c) * chunk));
+  };
+  // where a chunk's ranks come from and go to, and what moves beside their rows
+  auto look_up = [&](int step) {
+    const int first = (step * C + c) * chunk, count = count_of(step), s = step & 1;
     for (int i = tid; i < count; i += kThreads) {
       const int t = __ldcg(list + first + i);
       int64_t src = -1, dst = -1;
       if (t != first + i) {
         src = place(t);
         dst = place(first + i);
-        if (src < 0 || dst < 0) src = dst = -1;
+        if (dst < 0) src = -1;
       }
-      sh.src[i] = src;
-      sh.dst[i] = dst;
+      sh.src[s][i] = src;
+      sh.dst[s][i] = dst;
       if (src >= 0) {
         const int64_t at = token_at(src);
-        sh.moved[0][i] = p.weights[at];
+        sh.moved[s][0][i] = p.weights[at];
         if (p.k_scales) {
-          sh.moved[1][i] = p.k_scales[at];
-          sh.moved[2][i] = p.v_scales[at];
+          sh.moved[s][1][i] = p.k_scales[at];
+          sh.moved[s][2][i] = p.v_scales[at];
         }
       }
     }
-    __syncthreads();
+  };
+  auto fetch = [&](int step) {
+    const int count = count_of(step), s = step & 1;
+    const uint32_t to = dev::smem_addr(buffer) + s * (p.buffer / 2);
     for (int e = tid; e < count * pieces; e += kThreads) {
-      const int64_t src = sh.src[e / pieces];
-      if (src >= 0) dev::cp_async16(sbase + e * 16, address(src, e % pieces));
+      const int64_t src = sh.src[s][e / pieces];
+      if (src >= 0) dev::cp_async16(to + e * 16, address(src, e % pieces));
     }
-    dev::cp_async_wait_all();
-    cluster.sync();
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (steps > 0) {
+    look_up(0);
+    __syncthreads();
+    fetch(0);
+  }
+  for (int step = 0; step < steps; ++step) {
+    if (step + 1 < steps) {
+      look_up(step + 1);
+      __syncthreads();
+      fetch(step + 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    cluster.sync();  // all of the chunk's rows have been read
+    const int count = count_of(step), s = step & 1;
+    const uint8_t* from = buffer + s * (p.buffer / 2);
     for (int e = tid; e < count * pieces; e += kThreads) {
-      const int64_t dst = sh.dst[e / pieces];
-      if (dst >= 0)
-        *reinterpret_cast<uint4*>(address(dst, e % pieces)) =
-            *reinterpret_cast<const uint4*>(buffer + e * 16);
+      const int i = e / pieces;
+      if (sh.src[s][i] >= 0)
+        *reinterpret_cast<uint4*>(address(sh.dst[s][i], e % pieces)) =
+            *reinterpret_cast<const uint4*>(from + e * 16);
     }
     for (int i = tid; i < count; i += kThreads) {
-      if (sh.dst[i] < 0) continue;
-      const int64_t at = token_at(sh.dst[i]);
-      p.weights[at] = sh.moved[0][i];
+      if (sh.src[s][i] < 0) continue;
+      const int64_t at = token_at(sh.dst[s][i]);
+      p.weights[at] = sh.moved[s][0][i];
       if (p.k_scales) {
-        p.k_scales[at] = sh.moved[1][i];
-        p.v_scales[at] = sh.moved[2][i];
+        p.k_scales[at] = sh.moved[s][1][i];
+        p.v_scales[at] = sh.moved[s][2][i];
       }
     }
-    __syncthreads();
+    __syncthreads();  // the stage is free
   }
   // all weights have been read: those of the freed slots start again at 0
-  for (int t = n + c * kThreads + tid; t < L; t += C * kThreads) {
-    const int64_t at = place(t);
-    if (at >= 0) p.weights[token_at(at)] = 0.f;
+  for (int i = n / 4 * 4 + 4 * (c * kThreads + tid); i < L; i += 4 * C * kThreads) {
+    const int64_t at = place(i);
+    if (at < 0) continue;
+    float* w = p.weights + token_at(at);
+    if (i >= n && i + 4 <= L) {
+      *reinterpret_cast<float4*>(w) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k >= n && i + k < L) w[k] = 0.f;
+    }
   }
 }
 
@@ -332,7 +392,7 @@ struct fa_evict_plan_s {
   uint8_t* ws = nullptr;
   EvictLayout layout{};
   int64_t units = 0;
-  int cluster = 1;
+  int cluster = 1, buffer = kBuffer;
 };
 
 extern "C" {
@@ -394,8 +454,9 @@ int fa_evict_plan(const int32_t* indptr_host, const int32_t* indices_dev,
     plan->layout = L;
     plan->units = units;
     plan->cluster = cluster;
+    if (units * num_kv_heads * cluster <= 2 * (int64_t)sms) plan->buffer = kBigBuffer;
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(&fa_evict_kernel),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBuffer) !=
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBigBuffer) !=
             cudaSuccess ||
         upload_async(plan->ws, meta.data(), meta.size(),
                      static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
@@ -414,7 +475,7 @@ int fa_evict_run(fa_evict_plan_t plan, void* paged_kv, int64_t num_pages, float*
   if (!plan) return FA_ERR_INVALID_ARG;
   if (plan->units == 0) return FA_OK;
   if (!paged_kv || !weights || num_pages <= 0 || reinterpret_cast<uintptr_t>(paged_kv) % 16 ||
-      reinterpret_cast<uintptr_t>(weights) % 4 || reinterpret_cast<uintptr_t>(k_scales) % 4 ||
+      reinterpret_cast<uintptr_t>(weights) % 16 || reinterpret_cast<uintptr_t>(k_scales) % 4 ||
       reinterpret_cast<uintptr_t>(v_scales) % 4 || (k_scales == nullptr) != (v_scales == nullptr))
     return FA_ERR_INVALID_ARG;
   if (k_scales && plan->kv_dtype != FA_DTYPE_E4M3) return FA_ERR_UNSUPPORTED;
@@ -434,11 +495,12 @@ int fa_evict_run(fa_evict_plan_t plan, void* paged_kv, int64_t num_pages, float*
   p.num_pages = num_pages;
   p.hkv = plan->hkv;
   p.row_bytes = plan->row_bytes;
+  p.buffer = plan->buffer;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3((unsigned)(plan->units * plan->hkv * plan->cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kBuffer;
+  cfg.dynamicSmemBytes = (size_t)plan->buffer;
   cfg.stream = static_cast<cudaStream_t>(cuda_stream);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
