@@ -83,9 +83,9 @@ struct EvictShared {
   int counts[2];        // kept for sure / equal to the last key, of this CTA
   int warp_counts[2][kWarps];
   int digit, above;     // of one pass
-  // a chunk's ranks: from and to page * 16 + slot (from -1: nothing to move), and
-  // what moves beside the rows: weight, K scale, V scale
-  int64_t src[2][kRankInfo], dst[2][kRankInfo];
+  // ranks looked up: the byte offsets of their K rows, from (-1: nothing to move) and
+  // to; the slot in the arrays per token; and what moves there: weight, K and V scale
+  int64_t src[2][kRankInfo], dst[2][kRankInfo], slot[2][kRankInfo];
   float moved[2][3][kRankInfo];
 };
 
@@ -253,44 +253,53 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
   const int rb = p.row_bytes, pieces = 2 * rb / 16;  // 16-byte pieces of a token's K and V
   const int chunk = min(kRankInfo, p.buffer / 2 / (2 * rb));
   const int64_t token_bytes = (int64_t)p.hkv * rb, page_half = kPageSize * token_bytes;
-  auto address = [&](int64_t at, int piece) -> uint8_t* {
-    const int half = piece * 16 >= rb;
-    return p.kv + (at / kPageSize * 2 + half) * page_half + (at % kPageSize) * token_bytes +
-           (int64_t)h * rb + (piece * 16 - half * rb);
+  // a thread moves one piece (a power of two of them) of every so many ranks
+  const int piece = tid & (pieces - 1), first_rank = tid / pieces, ranks = kThreads / pieces;
+  uint8_t* const base = p.kv + (int64_t)h * rb +
+                        (piece * 16 < rb ? piece * 16 : page_half + piece * 16 - rb);
+  auto row_of = [&](int64_t at) {
+    return at / kPageSize * 2 * page_half + at % kPageSize * token_bytes;
   };
   const int steps = (n + C * chunk - 1) / (C * chunk);
+  // The ranks of a few steps are looked up at once: the chain list -> page -> weight
+  // took longer than a chunk's rows.
+  const int group = kRankInfo / chunk;
   auto count_of = [&](int step) {
-    return max(0, min(chunk, n - (step * C + c) * chunk));
+    return step < steps ? max(0, min(chunk, n - (step * C + c) * chunk)) : 0;
   };
-  // where a chunk's ranks come from and go to, and what moves beside their rows
-  auto look_up = [&](int step) {
-    const int first = (step * C + c) * chunk, count = count_of(step), s = step & 1;
-    for (int i = tid; i < count; i += kThreads) {
-      const int t = __ldcg(list + first + i);
+  // where the ranks of steps g * group .. come from and go to, and what moves
+  // beside their rows
+  auto look_up = [&](int g) {
+    const int s = g & 1;
+    for (int e = tid; e < group * chunk; e += kThreads) {
+      const int step = g * group + e / chunk, i = e % chunk;
+      if (i >= count_of(step)) continue;
+      const int rank = (step * C + c) * chunk + i, t = __ldcg(list + rank);
       int64_t src = -1, dst = -1;
-      if (t != first + i) {
+      if (t != rank) {
         src = place(t);
-        dst = place(first + i);
+        dst = place(rank);
         if (dst < 0) src = -1;
       }
-      sh.src[s][i] = src;
-      sh.dst[s][i] = dst;
+      sh.src[s][e] = src < 0 ? -1 : row_of(src);
       if (src >= 0) {
+        sh.dst[s][e] = row_of(dst);
+        sh.slot[s][e] = token_at(dst);
         const int64_t at = token_at(src);
-        sh.moved[s][0][i] = p.weights[at];
+        sh.moved[s][0][e] = p.weights[at];
         if (p.k_scales) {
-          sh.moved[s][1][i] = p.k_scales[at];
-          sh.moved[s][2][i] = p.v_scales[at];
+          sh.moved[s][1][e] = p.k_scales[at];
+          sh.moved[s][2][e] = p.v_scales[at];
         }
       }
     }
   };
   auto fetch = [&](int step) {
-    const int count = count_of(step), s = step & 1;
-    const uint32_t to = dev::smem_addr(buffer) + s * (p.buffer / 2);
-    for (int e = tid; e < count * pieces; e += kThreads) {
-      const int64_t src = sh.src[s][e / pieces];
-      if (src >= 0) dev::cp_async16(to + e * 16, address(src, e % pieces));
+    const int count = count_of(step), s = step / group & 1, first = step % group * chunk;
+    const uint32_t to = dev::smem_addr(buffer) + (step & 1) * (p.buffer / 2) + piece * 16;
+    for (int i = first_rank; i < count; i += ranks) {
+      const int64_t src = sh.src[s][first + i];
+      if (src >= 0) dev::cp_async16(to + i * 2 * rb, base + src);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -301,25 +310,25 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
   }
   for (int step = 0; step < steps; ++step) {
     if (step + 1 < steps) {
-      look_up(step + 1);
-      __syncthreads();
+      if ((step + 1) % group == 0) {
+        look_up((step + 1) / group);
+        __syncthreads();
+      }
       fetch(step + 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
     } else {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     cluster.sync();  // all of the chunk's rows have been read
-    const int count = count_of(step), s = step & 1;
-    const uint8_t* from = buffer + s * (p.buffer / 2);
-    for (int e = tid; e < count * pieces; e += kThreads) {
-      const int i = e / pieces;
-      if (sh.src[s][i] >= 0)
-        *reinterpret_cast<uint4*>(address(sh.dst[s][i], e % pieces)) =
-            *reinterpret_cast<const uint4*>(from + e * 16);
-    }
-    for (int i = tid; i < count; i += kThreads) {
+    const int count = count_of(step), s = step / group & 1, first = step % group * chunk;
+    const uint8_t* from = buffer + (step & 1) * (p.buffer / 2) + piece * 16;
+    for (int i = first_rank; i < count; i += ranks)
+      if (sh.src[s][first + i] >= 0)
+        *reinterpret_cast<uint4*>(base + sh.dst[s][first + i]) =
+            *reinterpret_cast<const uint4*>(from + i * 2 * rb);
+    for (int i = first + tid; i < first + count; i += kThreads) {
       if (sh.src[s][i] < 0) continue;
-      const int64_t at = token_at(sh.dst[s][i]);
+      const int64_t at = sh.slot[s][i];
       p.weights[at] = sh.moved[s][0][i];
       if (p.k_scales) {
         p.k_scales[at] = sh.moved[s][1][i];
