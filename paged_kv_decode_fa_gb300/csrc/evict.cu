@@ -40,13 +40,13 @@ namespace cg = cooperative_groups;
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// Threads of a CTA: many where the CTAs are few.
+constexpr int kThreads = 256, kManyThreads = 1024;
 constexpr int kMostCtas = 8;              // of a cluster
-// Dynamic shared memory: keys, then two stages of rows.  Four CTAs an SM, or two
-// with twice as much each where there are no more.
-constexpr int kBuffer = 40 << 10, kBigBuffer = 96 << 10;
-constexpr int kRankInfo = 192;            // ranks of a chunk at most
+// Shared memory beside EvictShared: keys, then two stages of rows.  Four CTAs an SM, or
+// one with more where there are no more.  And ranks looked up at once.
+constexpr int kBuffer = 40 << 10, kBigBuffer = 160 << 10;
+constexpr int kRanks = 128, kManyRanks = 512;
 constexpr int kBatch = 4;                 // loads of a thread in flight
 
 struct EvictUnit {
@@ -78,20 +78,26 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+template <int kRankInfo>
 struct EvictShared {
   int hist[2][256];
   int counts[2];        // kept for sure / equal to the last key, of this CTA
-  int warp_counts[2][kWarps];
+  int warp_counts[2][kManyThreads / 32];
   int digit, above;     // of one pass
   // ranks looked up: the byte offsets of their K rows, from (-1: nothing to move) and
   // to; the slot in the arrays per token; and what moves there: weight, K and V scale
-  int64_t src[2][kRankInfo], dst[2][kRankInfo], slot[2][kRankInfo];
-  float moved[2][3][kRankInfo];
+  int64_t src[3][kRankInfo], dst[3][kRankInfo], slot[3][kRankInfo];
+  float moved[3][3][kRankInfo];
 };
 
-__global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams p) {
-  extern __shared__ __align__(16) uint8_t buffer[];
-  __shared__ EvictShared sh;
+template <int kThreads, int kRankInfo>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+    fa_evict_kernel(const EvictParams p) {
+  constexpr int kWarps = kThreads / 32;
+  using Shared = EvictShared<kRankInfo>;
+  extern __shared__ __align__(16) uint8_t shared[];
+  Shared& sh = *reinterpret_cast<Shared*>(shared);
+  uint8_t* const buffer = shared + (sizeof(Shared) + 15) / 16 * 16;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), c = (int)cluster.block_rank();
   const int job = blockIdx.x / C, h = job % p.hkv, tid = threadIdx.x;
@@ -156,34 +162,44 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
     for (int pass = 0; pass < 4; ++pass) {
       const int shift = 24 - 8 * pass;
       int* hist = sh.hist[pass & 1];
-      hist[tid] = 0;
+      if (tid < 256) hist[tid] = 0;
       __syncthreads();
-      for (int i = t0; i < t1; i += kThreads) {
-        const int t = i + tid;
-        const uint32_t k = t < t1 ? key(t) : 0;
-        const bool in = t < t1 && (pass == 0 || (k >> (shift + 8)) == prefix);
-        if (!__any_sync(0xffffffffu, in)) continue;
-        const int digit = in ? (int)((k >> shift) & 0xff) : 256;
-        // equal digits of a warp are counted once (weights crowd few exponents)
-        const unsigned same = __match_any_sync(0xffffffffu, digit);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+      for (int i = t0; i < t1; i += kThreads * kBatch) {
+        uint32_t k[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int t = i + b * kThreads + tid;
+          k[b] = t < t1 ? key(t) : 0;
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const bool in = i + b * kThreads + tid < t1 &&
+                          (pass == 0 || (k[b] >> (shift + 8)) == prefix);
+          if (!__any_sync(0xffffffffu, in)) continue;
+          const int digit = in ? (int)((k[b] >> shift) & 0xff) : 256;
+          // equal digits of a warp are counted once (weights crowd few exponents)
+          const unsigned same = __match_any_sync(0xffffffffu, digit);
+          if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+        }
       }
       cluster.sync();
-      int sum = 0;
-      for (int r = 0; r < C; ++r) sum += cluster.map_shared_rank(hist, r)[tid];
-      // keys of larger digits: a suffix sum over the 256 threads
-      int suffix = sum;
+      if (tid < 256) {
+        int sum = 0;
+        for (int r = 0; r < C; ++r) sum += cluster.map_shared_rank(hist, r)[tid];
+        // with the keys of larger digits: a suffix sum over the 256 threads
+        int suffix = sum;
 #pragma unroll
-      for (int off = 1; off < 32; off *= 2) {
-        const int v = __shfl_down_sync(0xffffffffu, suffix, off);
-        if (lane + off < 32) suffix += v;
-      }
-      if (lane == 0) sh.warp_counts[0][warp] = suffix;
-      __syncthreads();
-      for (int w = warp + 1; w < kThreads / 32; ++w) suffix += sh.warp_counts[0][w];
-      if (suffix >= left && suffix - sum < left) {
-        sh.digit = tid;
-        sh.above = suffix - sum;
+        for (int off = 1; off < 32; off *= 2) {
+          const int v = __shfl_down_sync(0xffffffffu, suffix, off);
+          if (lane + off < 32) suffix += v;
+        }
+        if (lane == 0) sh.warp_counts[0][warp] = suffix;
+        dev::named_barrier(1, 256);
+        for (int w = warp + 1; w < 8; ++w) suffix += sh.warp_counts[0][w];
+        if (suffix >= left && suffix - sum < left) {
+          sh.digit = tid;
+          sh.above = suffix - sum;
+        }
       }
       __syncthreads();
       prefix = (prefix << 8) | (uint32_t)sh.digit;
@@ -261,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
     return at / kPageSize * 2 * page_half + at % kPageSize * token_bytes;
   };
   const int steps = (n + C * chunk - 1) / (C * chunk);
-  // The ranks of a few steps are looked up at once: the chain list -> page -> weight
-  // took longer than a chunk's rows.
+  // The ranks of a few steps are looked up at once, two such groups ahead: the chain
+  // list -> page -> weight takes longer than a chunk's rows.
   const int group = kRankInfo / chunk;
   auto count_of = [&](int step) {
     return step < steps ? max(0, min(chunk, n - (step * C + c) * chunk)) : 0;
@@ -270,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
   // where the ranks of steps g * group .. come from and go to, and what moves
   // beside their rows
   auto look_up = [&](int g) {
-    const int s = g & 1;
+    const int s = g % 3;
     for (int e = tid; e < group * chunk; e += kThreads) {
       const int step = g * group + e / chunk, i = e % chunk;
       if (i >= count_of(step)) continue;
@@ -295,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
     }
   };
   auto fetch = [&](int step) {
-    const int count = count_of(step), s = step / group & 1, first = step % group * chunk;
+    const int count = count_of(step), s = step / group % 3, first = step % group * chunk;
     const uint32_t to = dev::smem_addr(buffer) + (step & 1) * (p.buffer / 2) + piece * 16;
     for (int i = first_rank; i < count; i += ranks) {
       const int64_t src = sh.src[s][first + i];
@@ -303,24 +319,16 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (steps > 0) {
-    look_up(0);
-    __syncthreads();
-    fetch(0);
-  }
+  look_up(0);
+  look_up(1);
+  __syncthreads();
+  fetch(0);
   for (int step = 0; step < steps; ++step) {
-    if (step + 1 < steps) {
-      if ((step + 1) % group == 0) {
-        look_up((step + 1) / group);
-        __syncthreads();
-      }
-      fetch(step + 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    }
+    fetch(step + 1);
+    if (step % group == 0) look_up(step / group + 2);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     cluster.sync();  // all of the chunk's rows have been read
-    const int count = count_of(step), s = step / group & 1, first = step % group * chunk;
+    const int count = count_of(step), s = step / group % 3, first = step % group * chunk;
     const uint8_t* from = buffer + (step & 1) * (p.buffer / 2) + piece * 16;
     for (int i = first_rank; i < count; i += ranks)
       if (sh.src[s][first + i] >= 0)
@@ -351,6 +359,13 @@ __global__ void __launch_bounds__(kThreads, 4) fa_evict_kernel(const EvictParams
     }
   }
 }
+
+template <int kRankInfo>
+constexpr int evict_shared() {
+  return (int)((sizeof(EvictShared<kRankInfo>) + 15) / 16 * 16);
+}
+static_assert(4 * (evict_shared<kRanks>() + kBuffer + 1024) <= 228 << 10, "four CTAs an SM");
+static_assert(evict_shared<kManyRanks>() + kBigBuffer <= 227 << 10, "shared memory per CTA");
 
 struct EvictLayout {
   size_t units, lists, total;
@@ -401,7 +416,9 @@ struct fa_evict_plan_s {
   uint8_t* ws = nullptr;
   EvictLayout layout{};
   int64_t units = 0;
-  int cluster = 1, buffer = kBuffer;
+  int cluster = 1, buffer = kBuffer, threads = kThreads;
+  int shared = evict_shared<kRanks>();
+  const void* kernel = reinterpret_cast<const void*>(&fa_evict_kernel<kThreads, kRanks>);
 };
 
 extern "C" {
@@ -463,9 +480,14 @@ int fa_evict_plan(const int32_t* indptr_host, const int32_t* indices_dev,
     plan->layout = L;
     plan->units = units;
     plan->cluster = cluster;
-    if (units * num_kv_heads * cluster <= 2 * (int64_t)sms) plan->buffer = kBigBuffer;
-    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(&fa_evict_kernel),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBigBuffer) !=
+    if (units * num_kv_heads * cluster <= sms) {
+      plan->buffer = kBigBuffer;
+      plan->threads = kManyThreads;
+      plan->shared = evict_shared<kManyRanks>();
+      plan->kernel = reinterpret_cast<const void*>(&fa_evict_kernel<kManyThreads, kManyRanks>);
+    }
+    if (cudaFuncSetAttribute(plan->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             plan->shared + plan->buffer) !=
             cudaSuccess ||
         upload_async(plan->ws, meta.data(), meta.size(),
                      static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
@@ -508,8 +530,8 @@ int fa_evict_run(fa_evict_plan_t plan, void* paged_kv, int64_t num_pages, float*
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3((unsigned)(plan->units * plan->hkv * plan->cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)plan->buffer;
+  cfg.blockDim = dim3((unsigned)plan->threads);
+  cfg.dynamicSmemBytes = (size_t)(plan->shared + plan->buffer);
   cfg.stream = static_cast<cudaStream_t>(cuda_stream);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -518,10 +540,7 @@ int fa_evict_run(fa_evict_plan_t plan, void* paged_kv, int64_t num_pages, float*
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   void* args[1] = {&p};
-  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&fa_evict_kernel), args) ==
-                 cudaSuccess
-             ? FA_OK
-             : FA_ERR_CUDA;
+  return cudaLaunchKernelExC(&cfg, plan->kernel, args) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_evict_check(fa_evict_plan_t plan, void* cuda_stream, int* flags) {
