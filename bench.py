@@ -96,7 +96,8 @@ def read_bf16_peak():
 NOT_DECODE_SOURCES = ("cascade.cu", "cascade_tc.cuh", "tcgen05.cuh", "static_scratch.cu", "merge.cu")
 # Sources that no workload's kernels are in: what writes the cache, attends prompts,
 # accumulates weights and evicts around the decode steps.
-NOT_WORKLOAD_SOURCES = ("append.cu", "prefill.cu", "prefill.cuh", "weights.cu", "evict.cu")
+NOT_WORKLOAD_SOURCES = ("append.cu", "prefill.cu", "prefill.cuh", "weights.cu",
+                        "weights_tc.cuh", "tensor_map.h", "evict.cu")
 
 
 def kernel_source_hash(workload: str = "gqa_uniform") -> str:

@@ -3,19 +3,17 @@
 // planner, and the kernels around fa_prefill_kernel (prefill.cuh).
 #include "prefill.cuh"
 
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <limits>
-#include <mutex>
 #include <new>
 #include <queue>
 #include <vector>
 
 #include "fa_decode.h"
 #include "staging.h"
+#include "tensor_map.h"
 
 namespace fadecode {
 namespace {
@@ -298,32 +296,6 @@ __global__ void __launch_bounds__(256) fa_prefill_widen_kernel(const WidenParams
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-bool encode(CUtensorMap* map, fa_dtype dt, int rank, const void* base, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box) {
-  const auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return fn(map, dt == FA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-            (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 struct PrefillKernel {
   const void* attend = nullptr;
   const void* merge = nullptr;
@@ -436,23 +408,9 @@ int prefill_run(fa_prefill_plan_s* plan, int sc, const fa_rows* q, const void* p
   const int64_t pages = wide ? plan->table : num_pages;
 
   CUtensorMap maps[2];
-  {
-    // a single head or token may have any stride: one whose steps are never taken
-    const cuuint64_t token = plan->rows > 1 ? (cuuint64_t)q->token_stride * 2 : (cuuint64_t)D * 2;
-    const cuuint64_t head = plan->hq > 1 ? (cuuint64_t)q->head_stride * 2 : (cuuint64_t)D * 2;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)plan->hq, (cuuint64_t)plan->rows};
-    const cuuint64_t strides[2] = {head, token};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)(pf::kRows / G)};
-    if (!encode(&maps[0], plan->q_dtype, 3, q->data, dims, strides, box)) return FA_ERR_CUDA;
-  }
-  {
-    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)hkv, (cuuint64_t)kPageSize,
-                                (cuuint64_t)(2 * pages)};
-    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)hkv * D * 2,
-                                   (cuuint64_t)kPageSize * hkv * D * 2};
-    const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)kPageSize, 1u};
-    if (!encode(&maps[1], plan->q_dtype, 4, kv, dims, strides, box)) return FA_ERR_CUDA;
-  }
+  if (!encode_q_rows(&maps[0], plan->q_dtype, *q, plan->rows, plan->hq, D, G) ||
+      !encode_pages(&maps[1], plan->q_dtype, kv, pages, hkv, D))
+    return FA_ERR_CUDA;
   pf::Params p;
   std::memset(&p, 0, sizeof p);
   p.cta_offsets = reinterpret_cast<const int32_t*>(plan->ws + plan->layout.offsets);

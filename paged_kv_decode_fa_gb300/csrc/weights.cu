@@ -30,14 +30,9 @@
 #include "decode_mma.cuh"
 #include "fa_decode.h"
 #include "staging.h"
+#include "tensor_map.h"
 
 namespace fadecode {
-namespace {
-
-constexpr int kWarps = 8;
-constexpr int kMostPages = 64;  // of a run
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // A run of a request's pages.
 struct WeightsUnit {
@@ -66,6 +61,30 @@ struct WeightsParams {
   float scale;  // sm_scale * k_scale * log2(e)
 };
 
+// Two E4M3 codes as a pair of T (exact in both 16-bit types).
+template <typename T>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  if constexpr (std::is_same<T, __half>::value) {
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+  } else {
+    const float2 f = __half22float2(__half2(h));
+    return mma::pack2(f.x, f.y, true);
+  }
+}
+
+}  // namespace fadecode
+
+#include "weights_tc.cuh"
+
+namespace fadecode {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kMostPages = 64;  // of a run
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1, bool bf16) {
   if (bf16)
@@ -78,18 +97,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Two E4M3 codes as a pair of T (exact in both 16-bit types).
-template <typename T>
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-  if constexpr (std::is_same<T, __half>::value) {
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
-  } else {
-    const float2 f = __half22float2(__half2(h));
-    return mma::pack2(f.x, f.y, true);
-  }
 }
 
 // Fragments of a page's K: two MMAs' A operands (rows n and n + 8, 16 dims each) for each
@@ -343,6 +350,27 @@ WeightsFn find_weights_kernel(fa_dtype q, bool e4m3, int sc) {
   return e4m3 ? weights_kernel<__half, uint8_t, D>(sc) : weights_kernel<__half, __half, D>(sc);
 }
 
+template <typename T, typename KVT, int D>
+const void* weights_tc_kernel(int sc) {
+  const auto f = [](auto k) { return reinterpret_cast<const void*>(k); };
+  if constexpr (std::is_same<T, KVT>::value) {
+    return f(&fa_weights_tc_kernel<T, KVT, D, kScaleNone>);
+  } else {
+    return sc == kScalePerToken   ? f(&fa_weights_tc_kernel<T, KVT, D, kScalePerToken>)
+           : sc == kScalePerBlock ? f(&fa_weights_tc_kernel<T, KVT, D, kScalePerBlock>)
+                                  : f(&fa_weights_tc_kernel<T, KVT, D, kScaleNone>);
+  }
+}
+
+template <int D>
+const void* find_weights_tc_kernel(fa_dtype q, bool e4m3, int sc) {
+  if (q == FA_DTYPE_BF16)
+    return e4m3 ? weights_tc_kernel<__nv_bfloat16, uint8_t, D>(sc)
+                : weights_tc_kernel<__nv_bfloat16, __nv_bfloat16, D>(sc);
+  return e4m3 ? weights_tc_kernel<__half, uint8_t, D>(sc)
+              : weights_tc_kernel<__half, __half, D>(sc);
+}
+
 bool weights_pair_built(fa_dtype q, fa_dtype kv) {
   return (q == FA_DTYPE_BF16 || q == FA_DTYPE_F16) && (kv == q || kv == FA_DTYPE_E4M3);
 }
@@ -354,9 +382,15 @@ int run_pages(int64_t total_pages, int heads, int sms) {
   return n;
 }
 
-// Runs of a batch; -1 for malformed arguments.
+// Requests of more columns than this go through the tcgen05 kernel, in runs of
+// kTcPages.
+constexpr int kFewColumns = 16;
+constexpr int kTcPages = 2 * wt::kPages;
+
+// Runs of a batch's requests of many columns (`many`) or of the others; -1 for
+// malformed arguments.
 int64_t make_units(const int32_t* indptr, const int32_t* last_page_len, const int32_t* qo_indptr,
-                   int batch, int run, WeightsUnit* out) {
+                   int batch, int group, bool many, int run, WeightsUnit* out) {
   int64_t units = 0;
   for (int i = 0; i < batch; ++i) {
     const int64_t n = (int64_t)qo_indptr[i + 1] - qo_indptr[i];
@@ -364,8 +398,10 @@ int64_t make_units(const int32_t* indptr, const int32_t* last_page_len, const in
     if (n < 0 || pages < 0) return -1;
     if (pages > 0 && (last_page_len[i] < 1 || last_page_len[i] > kPageSize)) return -1;
     const int64_t len = pages > 0 ? (pages - 1) * kPageSize + last_page_len[i] : 0;
-    if (len > std::numeric_limits<int32_t>::max() - kPageSize) return -1;
-    if (n == 0) continue;
+    if (len > std::numeric_limits<int32_t>::max() - 2 * wt::kTok ||
+        n * group > std::numeric_limits<int32_t>::max() - wt::kTok)
+      return -1;
+    if (n == 0 || (n * group > kFewColumns) != many) continue;
     for (int64_t e = 0; e < pages; e += run, ++units)
       if (out)
         out[units] = WeightsUnit{qo_indptr[i],
@@ -390,7 +426,9 @@ struct fa_weights_plan_s {
   fa_dtype q_dtype = FA_DTYPE_BF16, kv_dtype = FA_DTYPE_BF16;
   const int32_t* indices = nullptr;
   uint8_t* ws = nullptr;
-  int64_t units = 0, rows = 0;
+  int64_t few = 0, many = 0;  // units of few columns, then of many
+  int64_t rows = 0;
+  int sms = 0;
 };
 
 namespace {
@@ -398,11 +436,12 @@ namespace {
 int weights_run(fa_weights_plan_s* plan, int sc, const fa_rows* q, const void* paged_kv,
                 int64_t num_pages, float sm_scale, const float* lse, float k_scale,
                 const float* head_k, const float* k_scales, float* weights, void* cuda_stream) {
-  if (plan->units == 0) return FA_OK;
+  if (plan->few + plan->many == 0) return FA_OK;
   if (!q || !q->data || !paged_kv || !lse || !weights || num_pages <= 0 ||
       reinterpret_cast<uintptr_t>(paged_kv) % 16 || reinterpret_cast<uintptr_t>(q->data) % 16 ||
       reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(weights) % 4 ||
-      q->token_stride < 0 || q->head_stride < 0 || q->token_stride % 8 || q->head_stride % 8)
+      q->token_stride % 8 || q->head_stride % 8 || num_pages >= (1 << 30) ||
+      (plan->rows > 1 && q->token_stride <= 0) || (plan->hq > 1 && q->head_stride <= 0))
     return FA_ERR_INVALID_ARG;
   if (!std::isfinite(k_scale)) return FA_ERR_INVALID_ARG;
   int dev = 0;
@@ -428,14 +467,36 @@ int weights_run(fa_weights_plan_s* plan, int sc, const fa_rows* q, const void* p
   while ((plan->hkv << p.group_log2) < plan->hq) ++p.group_log2;
   p.scale = sm_scale * k_scale * 1.4426950408889634f;
   const bool e4m3 = plan->kv_dtype == FA_DTYPE_E4M3;
-  const WeightsFn f = plan->d == 128 ? find_weights_kernel<128>(plan->q_dtype, e4m3, sc)
-                                     : find_weights_kernel<64>(plan->q_dtype, e4m3, sc);
-  void* args[1] = {&p};
-  return cudaLaunchKernel(reinterpret_cast<const void*>(f),
-                          dim3((unsigned)(plan->units * plan->hkv)), dim3(kWarps * 32), args, 0,
-                          static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
-             ? FA_OK
-             : FA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (plan->few > 0) {
+    const WeightsFn f = plan->d == 128 ? find_weights_kernel<128>(plan->q_dtype, e4m3, sc)
+                                       : find_weights_kernel<64>(plan->q_dtype, e4m3, sc);
+    void* args[1] = {&p};
+    if (cudaLaunchKernel(reinterpret_cast<const void*>(f),
+                         dim3((unsigned)(plan->few * plan->hkv)), dim3(kWarps * 32), args, 0,
+                         st) != cudaSuccess)
+      return FA_ERR_CUDA;
+  }
+  if (plan->many > 0) {
+    p.units += plan->few;
+    const int G = plan->hq / plan->hkv;
+    CUtensorMap maps[2];
+    std::memset(maps, 0, sizeof maps);
+    if (!encode_q_rows(&maps[0], plan->q_dtype, *q, plan->rows, plan->hq, plan->d, G) ||
+        (!e4m3 && !encode_pages(&maps[1], plan->q_dtype, paged_kv, num_pages, plan->hkv, plan->d)))
+      return FA_ERR_CUDA;
+    const void* f = plan->d == 128 ? find_weights_tc_kernel<128>(plan->q_dtype, e4m3, sc)
+                                   : find_weights_tc_kernel<64>(plan->q_dtype, e4m3, sc);
+    const int smem = plan->d == 128 ? wt::Smem<128>::kBytes : wt::Smem<64>::kBytes;
+    int jobs = (int)(plan->many * plan->hkv);
+    void* args[4] = {&maps[0], &maps[1], &p, &jobs};
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess ||
+        cudaLaunchKernel(f, dim3((unsigned)std::min(jobs, plan->sms)), dim3(wt::threads(e4m3)),
+                         args, (size_t)smem, st) != cudaSuccess)
+      return FA_ERR_CUDA;
+  }
+  return FA_OK;
 }
 
 }  // namespace
@@ -467,22 +528,26 @@ int fa_weights_plan(const int32_t* indptr_host, const int32_t* indices_dev,
   if (indptr_host[0] != 0 || qo_indptr_host[0] != 0) return FA_ERR_INVALID_ARG;
   if (indptr_host[batch] > 0 && !indices_dev) return FA_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
+  auto units = [&](bool many, int run, WeightsUnit* out) {
+    return make_units(indptr_host, last_page_len_host, qo_indptr_host, batch, G, many, run, out);
+  };
   // the arguments are checked before any CUDA call
-  if (make_units(indptr_host, last_page_len_host, qo_indptr_host, batch, kMostPages, nullptr) < 0)
-    return FA_ERR_INVALID_ARG;
+  const int64_t many = units(true, kTcPages, nullptr);
+  if (many < 0) return FA_ERR_INVALID_ARG;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FA_ERR_CUDA;
   const int run = run_pages(indptr_host[batch], num_kv_heads, sms);
-  const int64_t units =
-      make_units(indptr_host, last_page_len_host, qo_indptr_host, batch, run, nullptr);
-  const size_t bytes = kAlign + sizeof(WeightsUnit) * (size_t)units;
+  const int64_t few = units(false, run, nullptr);
+  const size_t bytes = kAlign + sizeof(WeightsUnit) * (size_t)(few + many);
   if (bytes > workspace_bytes) return FA_ERR_WORKSPACE_TOO_SMALL;
-  if (units * num_kv_heads > std::numeric_limits<int32_t>::max()) return FA_ERR_UNSUPPORTED;
+  if (std::max(few, many) * num_kv_heads > std::numeric_limits<int32_t>::max() - 1024)
+    return FA_ERR_UNSUPPORTED;
   try {
     std::vector<uint8_t> meta(bytes, 0);
-    make_units(indptr_host, last_page_len_host, qo_indptr_host, batch, run,
-               reinterpret_cast<WeightsUnit*>(meta.data() + kAlign));
+    WeightsUnit* out = reinterpret_cast<WeightsUnit*>(meta.data() + kAlign);
+    units(false, run, out);
+    units(true, kTcPages, out + few);
     fa_weights_plan_s* plan = new fa_weights_plan_s();
     plan->device = dev;
     plan->hq = num_qo_heads;
@@ -492,7 +557,9 @@ int fa_weights_plan(const int32_t* indptr_host, const int32_t* indices_dev,
     plan->kv_dtype = kv_dtype;
     plan->indices = indices_dev;
     plan->ws = static_cast<uint8_t*>(workspace_dev);
-    plan->units = units;
+    plan->few = few;
+    plan->many = many;
+    plan->sms = sms;
     plan->rows = qo_indptr_host[batch];
     if (upload_async(plan->ws, meta.data(), bytes, static_cast<cudaStream_t>(cuda_stream)) !=
         cudaSuccess) {
