@@ -433,6 +433,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         }
         if (fewest < (j + 1) * kTok) {
           const int valid = seen - j * kTok;
+          asm volatile("" ::: "memory");  // a branch: most tiles need no select
 #pragma unroll
           for (int i = 0; i < kTok; ++i)
             if (i >= valid) s[i] = -INFINITY;

@@ -127,15 +127,15 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
       const Job w = load_job(j);
       for (int t = w.t0; t < w.t1; ++t, ++n) {
         const int s = n % kQSlots;
-        float lse[4];  // of columns lane, lane + 32, ...: before the wait
+        float lse[4];  // -lse of columns lane, lane + 32, ...: before the wait
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int x = t * kTok + lane + 32 * i;
           const int row = x >> p.group_log2, g = x & ((1 << p.group_log2) - 1);
           lse[i] = x < w.columns ? __ldg(p.lse + (int64_t)(w.row0 + row) * p.hq +
-                                         (w.h << p.group_log2) + g) * 1.4426950408889634f
-                                 : INFINITY;
-          if (lse[i] == -INFINITY) lse[i] = INFINITY;  // a row that saw nothing: weight 0
+                                         (w.h << p.group_log2) + g) * -1.4426950408889634f
+                                 : -INFINITY;
+          if (lse[i] == INFINITY) lse[i] = -INFINITY;  // a row that saw nothing: weight 0
         }
         dev::mbar_wait(dev::smem_addr(&q_empty[s]), (uint32_t)(((n / kQSlots) & 1) ^ 1), aborted,
                        p.err);
@@ -184,51 +184,73 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
           atomicOr(p.err, 2);
   } else if (kE4m3 && warp >= 12) {
     // -------------------------------------------------------------- K, widened
-    const int r = threadIdx.x % kTok;  // a token of each block
-    constexpr int kPieces = D / 16;    // 16 codes each
+    // A thread widens a token of each block.  A job's codes are loaded into
+    // registers while the job before is widened and its buffer waited for; the unit
+    // and the page ids one job earlier still.
+    const int r = threadIdx.x % kTok, step = gridDim.x;
+    constexpr int kPieces = D / 16;  // 16 codes each
     const int64_t token_bytes = (int64_t)p.hkv * D;
+    uint4 codes[2][kPieces];
+    auto ids_of = [&](const Job& w, int j, int (&id)[2]) {
+#pragma unroll
+      for (int X = 0; X < 2; ++X) {
+        const int i = X * kPages + r / kPageSize;
+        id[X] = j < jobs && i < w.pages ? __ldg(p.indices + w.entry + i) : -1;
+      }
+    };
+    auto load = [&](int id, int h, uint4 (&to)[kPieces]) {
+      const bool ok = id >= 0 && (int64_t)id < p.num_pages;
+      const uint8_t* row = static_cast<const uint8_t*>(p.kv) +
+                           ((int64_t)(ok ? id : 0) * 2 * kPageSize + r % kPageSize) * token_bytes +
+                           (int64_t)h * D;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        to[i] = ok ? __ldg(reinterpret_cast<const uint4*>(row) + i) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    int ids[2];
+    Job w = load_job(blockIdx.x), w1 = load_job(min((int)blockIdx.x + step, jobs - 1));
+    ids_of(w, blockIdx.x, ids);
+#pragma unroll
+    for (int X = 0; X < 2; ++X) load(ids[X], w.h, codes[X]);
+    ids_of(w1, blockIdx.x + step, ids);
     int n = 0;
-    for (int j = blockIdx.x; j < jobs; j += gridDim.x, ++n) {
-      const Job w = load_job(j);
+    for (int j = blockIdx.x; j < jobs; j += step, ++n) {
       const int s = n & 1;
-      for (int X = 0; X < w.blocks; ++X) {
-        const int page = page_of(w, X * kPages + r / kPageSize);
-        const uint8_t* row = static_cast<const uint8_t*>(p.kv) +
-                             ((int64_t)max(page, 0) * 2 * kPageSize + r % kPageSize) * token_bytes +
-                             (int64_t)w.h * D;
-        uint4 codes[kPieces];
+      const Job w2 = load_job(min(j + 2 * step, jobs - 1));
+      dev::mbar_wait(dev::smem_addr(&k_empty[s]), (uint32_t)(((n >> 1) & 1) ^ 1), aborted, p.err);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          codes[i] = page < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                              : __ldg(reinterpret_cast<const uint4*>(row) + i);
-        if (X == 0)
-          dev::mbar_wait(dev::smem_addr(&k_empty[s]), (uint32_t)(((n >> 1) & 1) ^ 1), aborted,
-                         p.err);
-        const uint32_t tile = sbase + S::kOffK + (2 * s + X) * S::kTile + r * 128;
+      for (int X = 0; X < 2; ++X) {
+        if (X < w.blocks) {
+          const uint32_t tile = sbase + S::kOffK + (2 * s + X) * S::kTile + r * 128;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const uint32_t in[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-          uint32_t out[8];
+          for (int i = 0; i < kPieces; ++i) {
+            const uint32_t in[4] = {codes[X][i].x, codes[X][i].y, codes[X][i].z, codes[X][i].w};
+            uint32_t out[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            out[2 * e] = widen2<T>(in[e] & 0xffffu);
-            out[2 * e + 1] = widen2<T>(in[e] >> 16);
-          }
-          // granule g (8 dims) of row r stands at g ^ (r % 8) of its half's 128 bytes
+            for (int e = 0; e < 4; ++e) {
+              out[2 * e] = widen2<T>(in[e] & 0xffffu);
+              out[2 * e + 1] = widen2<T>(in[e] >> 16);
+            }
+            // granule g (8 dims) of row r stands at g ^ (r % 8) of its half's 128 bytes
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int g = 2 * i + k;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             tile + (g / 8) * (kTok * 128) + ((g % 8) ^ (r & 7)) * 16),
-                         "r"(out[4 * k]), "r"(out[4 * k + 1]), "r"(out[4 * k + 2]),
-                         "r"(out[4 * k + 3])
-                         : "memory");
+            for (int k = 0; k < 2; ++k) {
+              const int g = 2 * i + k;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               tile + (g / 8) * (kTok * 128) + ((g % 8) ^ (r & 7)) * 16),
+                           "r"(out[4 * k]), "r"(out[4 * k + 1]), "r"(out[4 * k + 2]),
+                           "r"(out[4 * k + 3])
+                           : "memory");
+            }
           }
         }
+        load(ids[X], w1.h, codes[X]);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(dev::smem_addr(&k_full[s]));
+      ids_of(w2, j + 2 * step, ids);
+      w = w1;
+      w1 = w2;
     }
   } else if (warp == 8) {
     // -------------------------------------------------------------- MMAs
@@ -274,17 +296,37 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
     const int X = warp / 4, r = threadIdx.x % kTok;
     const uint32_t tS = tmem + X * 256 + ((uint32_t)(32 * (warp % 4)) << 16);
     int q_n = 0, cnt = 0;
-    for (int j = blockIdx.x; j < jobs; j += gridDim.x) {
-      const Job w = load_job(j);
+    // A job's page id and scale are loaded during the jobs before: the chain unit ->
+    // page -> scale would stand in front of every tile.
+    const int at = X * kTok + r;
+    auto id_of = [&](const Job& w, int j) {
+      return j < jobs && at / kPageSize < w.pages ? __ldg(p.indices + w.entry + at / kPageSize)
+                                                  : -1;
+    };
+    auto slot_of = [&](int page, int h) {
+      return ((int64_t)max(page, 0) * p.hkv + h) * kPageSize + at % kPageSize;
+    };
+    auto scale_of = [&](int page, int h) {
+      if constexpr (SC == kScalePerToken) return __ldg(p.k_scales + slot_of(page, h));
+      if constexpr (SC == kScalePerBlock) return __ldg(p.k_scales + slot_of(page, h) / kPageSize);
+      return 1.f;
+    };
+    auto checked = [&](int page) { return (int64_t)page < p.num_pages ? max(page, -1) : -1; };
+    const int step = gridDim.x;
+    Job w = load_job(blockIdx.x), w1 = load_job(min((int)blockIdx.x + step, jobs - 1));
+    int id = id_of(w, blockIdx.x), id1 = id_of(w1, blockIdx.x + step);
+    float token_scale = scale_of(checked(id), w.h);
+    for (int j = blockIdx.x; j < jobs; j += step) {
+      const float scale1 = scale_of(checked(id1), w1.h);
+      const Job w2 = load_job(min(j + 2 * step, jobs - 1));
+      const int id2 = id_of(w2, j + 2 * step);
       const bool active = X < w.blocks;
-      const int at = X * kTok + r, pos = w.pos0 + at;
-      const int page = active ? page_of(w, at / kPageSize) : -1;
+      const int pos = w.pos0 + at, page = active ? checked(id) : -1;
       if (active && page < 0 && at / kPageSize < w.pages && r % kPageSize == 0)
         atomicOr(p.err, 1);
-      float scale = p.head_k_scales ? p.scale * __ldg(p.head_k_scales + w.h) : p.scale;
-      const int64_t slot = ((int64_t)max(page, 0) * p.hkv + w.h) * kPageSize + at % kPageSize;
-      if constexpr (SC == kScalePerToken) scale *= __ldg(p.k_scales + slot);
-      if constexpr (SC == kScalePerBlock) scale *= __ldg(p.k_scales + slot / kPageSize);
+      const float scale =
+          token_scale * (p.head_k_scales ? p.scale * __ldg(p.head_k_scales + w.h) : p.scale);
+      const int64_t slot = slot_of(page, w.h);
       // columns that see this token: from `seen` on (the warp's last token: `warp_seen`)
       const int seen = max(0, pos - w.before) << p.group_log2;
       const int warp_seen = __shfl_sync(0xffffffffu, seen, 31);
@@ -302,35 +344,50 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
           ++cnt;
           const int lo = seen - t * kTok, hi = w.columns - t * kTok;
           const bool whole = warp_seen <= t * kTok && hi >= kTok;
-          const float4* lse =
-              reinterpret_cast<const float4*>(smem + S::kOffLse) + qs * (kTok / 4);
-          uint32_t raw[2][32];
-          ld32_start(tS + b * 128, raw[0]);
+          // 16 columns at a time: the next ones' scores and lse on their way
+          const uint32_t lse_at = sbase + S::kOffLse + qs * (kTok * 4);
+          const int steps = min(kTok / 16, (hi + 15) / 16);
+          uint32_t raw[2][16];
+          uint64_t neg[2][8];  // -lse, in pairs
+          auto start = [&](int c, int to) {
+            ld16_start(tS + b * 128 + c * 16, raw[to]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            ld_wait();
-            ld32_use(raw[c & 1]);
-            if (c < 3) ld32_start(tS + b * 128 + (c + 1) * 32, raw[(c + 1) & 1]);
-            if (32 * c >= hi) continue;
+            for (int i = 0; i < 4; ++i)
+              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                           : "=l"(neg[to][2 * i]), "=l"(neg[to][2 * i + 1])
+                           : "r"(lse_at + (c * 16 + 4 * i) * 4));
+          };
+          start(0, 0);
+          // (two loops: with the test inside one, every column paid for its compares)
+          auto add_up = [&](auto every) {
+            constexpr bool all = decltype(every)::value;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 l = lse[8 * c + i];
-              float x[4];
-              f2_split(fma2(f2(__uint_as_float(raw[c & 1][4 * i]),
-                               __uint_as_float(raw[c & 1][4 * i + 1])),
-                            scale2, f2(-l.x, -l.y)), x[0], x[1]);
-              f2_split(fma2(f2(__uint_as_float(raw[c & 1][4 * i + 2]),
-                               __uint_as_float(raw[c & 1][4 * i + 3])),
-                            scale2, f2(-l.z, -l.w)), x[2], x[3]);
+            for (int c = 0; c < kTok / 16; ++c) {
+              if (!all && c >= steps) break;
+              ld_wait();
+              ld16_use(raw[c & 1]);
+              if (c + 1 < kTok / 16 && (all || c + 1 < steps)) start(c + 1, (c + 1) & 1);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                x[e] = dev::fast_exp2(x[e]);
-                const int col = 32 * c + 4 * i + e;
-                if (!whole) x[e] = col >= lo && col < hi ? x[e] : 0.f;
+              for (int i = 0; i < 8; ++i) {
+                float x0, x1;
+                f2_split(fma2(f2(__uint_as_float(raw[c & 1][2 * i]),
+                                 __uint_as_float(raw[c & 1][2 * i + 1])),
+                              scale2, neg[c & 1][i]), x0, x1);
+                x0 = dev::fast_exp2(x0);
+                x1 = dev::fast_exp2(x1);
+                if (!all) {
+                  const int col = 16 * c + 2 * i;
+                  x0 = col >= lo && col < hi ? x0 : 0.f;
+                  x1 = col + 1 >= lo && col + 1 < hi ? x1 : 0.f;
+                }
+                acc[i % 4] = add2(acc[i % 4], f2(x0, x1));
               }
-              acc[i % 4] = add2(acc[i % 4], add2(f2(x[0], x[1]), f2(x[2], x[3])));
             }
-          }
+          };
+          if (whole)
+            add_up(std::true_type{});
+          else
+            add_up(std::false_type{});
           fence_before();
           __syncwarp();
           if (lane == 0) dev::mbar_arrive(dev::smem_addr(&s_empty[2 * X + b]));
@@ -342,6 +399,11 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
       f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), lo, hi);
       // tokens that no row sees (slots behind the request's last) stay
       if (page >= 0 && pos <= w.before + w.rows - 1) atomicAdd(p.weights + slot, lo + hi);
+      w = w1;
+      w1 = w2;
+      id = id1;
+      id1 = id2;
+      token_scale = scale1;
     }
   }
   fence_before();
