@@ -1,5 +1,5 @@
 // TMA descriptors of query rows and cache pages for the tcgen05 kernels: boxes of 64
-// 16-bit elements (128 bytes, swizzled) in rows of a K-major operand.
+// 16-bit elements (128 bytes, swizzled), the rows of a K-major operand, or of codes.
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -13,7 +13,8 @@
 namespace fadecode {
 
 inline bool encode_map(CUtensorMap* map, fa_dtype dt, int rank, const void* base,
-                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                       bool swizzle64 = false) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -27,10 +28,12 @@ inline bool encode_map(CUtensorMap* map, fa_dtype dt, int rank, const void* base
   if (!fn) return false;
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   return fn(map,
-            dt == FA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            dt == FA_DTYPE_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+            : dt == FA_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
             (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -56,6 +59,17 @@ inline bool encode_pages(CUtensorMap* map, fa_dtype dt, const void* kv, int64_t 
                                  (cuuint64_t)kPageSize * heads * D * 2};
   const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)kPageSize, 1u};
   return encode_map(map, dt, 4, kv, dims, strides, box);
+}
+
+// The pages of an E4M3 cache: a box is one head's rows of one page's K or V, D codes
+// (64 or 128 bytes, swizzled in spans of as many).
+inline bool encode_codes(CUtensorMap* map, const void* kv, int64_t pages, int heads, int D) {
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)kPageSize,
+                              (cuuint64_t)(2 * pages)};
+  const cuuint64_t strides[3] = {(cuuint64_t)D, (cuuint64_t)heads * D,
+                                 (cuuint64_t)kPageSize * heads * D};
+  const cuuint32_t box[4] = {(cuuint32_t)D, 1u, (cuuint32_t)kPageSize, 1u};
+  return encode_map(map, FA_DTYPE_E4M3, 4, kv, dims, strides, box, D == 64);
 }
 
 }  // namespace fadecode

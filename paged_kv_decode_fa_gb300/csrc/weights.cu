@@ -483,7 +483,8 @@ int weights_run(fa_weights_plan_s* plan, int sc, const fa_rows* q, const void* p
     CUtensorMap maps[2];
     std::memset(maps, 0, sizeof maps);
     if (!encode_q_rows(&maps[0], plan->q_dtype, *q, plan->rows, plan->hq, plan->d, G) ||
-        (!e4m3 && !encode_pages(&maps[1], plan->q_dtype, paged_kv, num_pages, plan->hkv, plan->d)))
+        !(e4m3 ? encode_codes(&maps[1], paged_kv, num_pages, plan->hkv, plan->d)
+               : encode_pages(&maps[1], plan->q_dtype, paged_kv, num_pages, plan->hkv, plan->d)))
       return FA_ERR_CUDA;
     const void* f = plan->d == 128 ? find_weights_tc_kernel<128>(plan->q_dtype, e4m3, sc)
                                    : find_weights_tc_kernel<64>(plan->q_dtype, e4m3, sc);

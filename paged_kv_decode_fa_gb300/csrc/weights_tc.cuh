@@ -7,9 +7,8 @@
 // (TMEM lane), so the sum over the columns stays in its registers, and only the
 // columns' lse come from shared memory, four a load for the whole warp.
 //  - warp 9 loads Q tiles (tensor copies, as fa_prefill_kernel's) and their lse;
-//  - K, two stages of two tiles: from a 16-bit cache by warp 10's tensor copies, from
-//    an E4M3 cache by warps 12-15, which widen the codes (exactly) into the same
-//    swizzled layout;
+//  - K, two stages of two tiles, by warp 10's tensor copies; an E4M3 cache's codes are
+//    copied aside, and warps 12-19 widen them (exactly) into the same layout;
 //  - warp 8, one lane, issues the MMAs into two score buffers a block;
 //  - warps 0-3 and 4-7 turn the scores of the two blocks into sums.
 // The grid is persistent and nothing waits for a whole CTA between jobs.  Waits are
@@ -35,16 +34,18 @@ struct Smem {
   static constexpr int kQSlots = D == 128 ? 2 : 4;
   static constexpr int kOffK = 0;                      // [stage][block]
   static constexpr int kOffQ = 4 * kTile;
-  static constexpr int kOffLse = kOffQ + kQSlots * kTile;
+  static constexpr int kOffRaw = kOffQ + kQSlots * kTile;  // a job's codes (E4M3)
+  static constexpr int kOffLse = kOffRaw + 2 * kTok * D;
   static constexpr int kOffBar = kOffLse + kQSlots * kTok * 4;
-  // q_full, q_empty [slots]; k_full, k_empty [2]; s_full, s_empty [block][buffer]
-  static constexpr int kNumBars = 2 * kQSlots + 4 + 8;
+  // q_full, q_empty [slots]; k_full, k_empty [2]; s_full, s_empty [block][buffer];
+  // raw_full, raw_empty
+  static constexpr int kNumBars = 2 * kQSlots + 4 + 8 + 2;
   static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
   static constexpr int kBytes = kOffTmem + 16 + 1024;
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
-constexpr int threads(bool e4m3) { return e4m3 ? 512 : 384; }
+constexpr int threads(bool e4m3) { return e4m3 ? 640 : 384; }
 
 }  // namespace wt
 
@@ -69,6 +70,8 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
   uint64_t* k_empty = k_full + 2;
   uint64_t* s_full = k_full + 4;   // [block][buffer]
   uint64_t* s_empty = k_full + 8;
+  uint64_t* raw_full = k_full + 12;
+  uint64_t* raw_empty = k_full + 13;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffTmem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool aborted = false;
@@ -79,13 +82,15 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
       dev::mbar_init(dev::smem_addr(&q_empty[s]), 9);  // the MMAs and eight warps' lse
     }
     for (int s = 0; s < 2; ++s) {
-      dev::mbar_init(dev::smem_addr(&k_full[s]), kE4m3 ? 4 : 1);
+      dev::mbar_init(dev::smem_addr(&k_full[s]), kE4m3 ? 8 : 1);
       dev::mbar_init(dev::smem_addr(&k_empty[s]), 1);
     }
     for (int s = 0; s < 4; ++s) {
       dev::mbar_init(dev::smem_addr(&s_full[s]), 1);
       dev::mbar_init(dev::smem_addr(&s_empty[s]), 4);
     }
+    dev::mbar_init(dev::smem_addr(raw_full), 1);
+    dev::mbar_init(dev::smem_addr(raw_empty), 8);
     dev::fence_barrier_init();
   }
   if (warp == 8) {
@@ -158,99 +163,90 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
         if (!dev::mbar_wait_bounded(dev::smem_addr(&q_full[i % kQSlots]),
                                     (uint32_t)((i / kQSlots) & 1)))
           atomicOr(p.err, 2);
-  } else if (!kE4m3 && warp == 10) {
-    // -------------------------------------------------------------- K, 16 bits
+  } else if (warp == 10) {
+    // -------------------------------------------------------------- K
+    // from a 16-bit cache into the tiles, from an E4M3 cache its codes
     const int oob = (int)(2 * p.num_pages);  // beyond the last page: zeros
+    constexpr int kStages = kE4m3 ? 1 : 2;
+    uint64_t* full_bar = kE4m3 ? raw_full : k_full;
+    uint64_t* empty_bar = kE4m3 ? raw_empty : k_empty;
     int n = 0;
     for (int j = blockIdx.x; j < jobs; j += gridDim.x, ++n) {
       const Job w = load_job(j);
-      const int s = n & 1;
-      const uint32_t full = dev::smem_addr(&k_full[s]);
-      const int page = page_of(w, lane % (2 * kPages));
+      const int s = n % kStages;
+      const uint32_t full = dev::smem_addr(&full_bar[s]);
       // lane l: half l / 16 of page l % 16
       const int half = lane / (2 * kPages), at = lane % (2 * kPages);
-      dev::mbar_wait(dev::smem_addr(&k_empty[s]), (uint32_t)(((n >> 1) & 1) ^ 1), aborted, p.err);
-      if (lane == 0) dev::mbar_arrive_expect_tx(full, w.blocks * S::kTile);
+      const int page = page_of(w, at), c3 = page < 0 ? oob : 2 * page;
+      dev::mbar_wait(dev::smem_addr(&empty_bar[s]), (uint32_t)(((n / kStages) & 1) ^ 1), aborted,
+                     p.err);
+      if (lane == 0)
+        dev::mbar_arrive_expect_tx(full, w.blocks * (kE4m3 ? kTok * D : S::kTile));
       __syncwarp();
-      if (half < S::kHalves && at < w.blocks * kPages)
-        tma_load_4d_plain(sbase + S::kOffK + (2 * s + at / kPages) * S::kTile +
-                              half * (kTok * 128) + at % kPages * (kPageSize * 128),
-                          &kv_map, half * 64, w.h, 0, page < 0 ? oob : 2 * page, full);
+      if (at < w.blocks * kPages) {
+        if (kE4m3 && half == 0)
+          tma_load_4d_plain(sbase + S::kOffRaw + at * (kPageSize * D), &kv_map, 0, w.h, 0, c3,
+                            full);
+        if (!kE4m3 && half < S::kHalves)
+          tma_load_4d_plain(sbase + S::kOffK + (2 * s + at / kPages) * S::kTile +
+                                half * (kTok * 128) + at % kPages * (kPageSize * 128),
+                            &kv_map, half * 64, w.h, 0, c3, full);
+      }
       __syncwarp();
     }
     if (lane == 0)
-      for (int i = n > 2 ? n - 2 : 0; i < n; ++i)
-        if (!dev::mbar_wait_bounded(dev::smem_addr(&k_full[i & 1]), (uint32_t)((i >> 1) & 1)))
+      for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
+        if (!dev::mbar_wait_bounded(dev::smem_addr(&full_bar[i % kStages]),
+                                    (uint32_t)((i / kStages) & 1)))
           atomicOr(p.err, 2);
   } else if (kE4m3 && warp >= 12) {
     // -------------------------------------------------------------- K, widened
-    // A thread widens a token of each block.  A job's codes are loaded into
-    // registers while the job before is widened and its buffer waited for; the unit
-    // and the page ids one job earlier still.
-    const int r = threadIdx.x % kTok, step = gridDim.x;
+    // A thread widens one token's row of codes.  They stand in shared memory by tensor
+    // copy (read straight from global memory, a thread a row, they missed L1 at
+    // every piece: 55-65 us for 128 columns), and the next job's are on their way
+    // once this job's are in registers.
+    const int row = threadIdx.x - 12 * 32, X = row / kTok, r = row % kTok;
     constexpr int kPieces = D / 16;  // 16 codes each
-    const int64_t token_bytes = (int64_t)p.hkv * D;
-    uint4 codes[2][kPieces];
-    auto ids_of = [&](const Job& w, int j, int (&id)[2]) {
-#pragma unroll
-      for (int X = 0; X < 2; ++X) {
-        const int i = X * kPages + r / kPageSize;
-        id[X] = j < jobs && i < w.pages ? __ldg(p.indices + w.entry + i) : -1;
-      }
-    };
-    auto load = [&](int id, int h, uint4 (&to)[kPieces]) {
-      const bool ok = id >= 0 && (int64_t)id < p.num_pages;
-      const uint8_t* row = static_cast<const uint8_t*>(p.kv) +
-                           ((int64_t)(ok ? id : 0) * 2 * kPageSize + r % kPageSize) * token_bytes +
-                           (int64_t)h * D;
+    // piece i of a row stands at i ^ (r % 8), or ^ (r / 2 % 4) in rows of 64 bytes
+    const int mix = D == 128 ? r & 7 : r >> 1 & 3;
+    int n = 0;
+    for (int j = blockIdx.x; j < jobs; j += gridDim.x, ++n) {
+      const int s = n & 1;
+      const bool active = X < load_job(j).blocks;
+      dev::mbar_wait(dev::smem_addr(raw_full), (uint32_t)(n & 1), aborted, p.err);
+      uint4 codes[kPieces];
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)
-        to[i] = ok ? __ldg(reinterpret_cast<const uint4*>(row) + i) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    int ids[2];
-    Job w = load_job(blockIdx.x), w1 = load_job(min((int)blockIdx.x + step, jobs - 1));
-    ids_of(w, blockIdx.x, ids);
-#pragma unroll
-    for (int X = 0; X < 2; ++X) load(ids[X], w.h, codes[X]);
-    ids_of(w1, blockIdx.x + step, ids);
-    int n = 0;
-    for (int j = blockIdx.x; j < jobs; j += step, ++n) {
-      const int s = n & 1;
-      const Job w2 = load_job(min(j + 2 * step, jobs - 1));
+        if (active)
+          codes[i] = *reinterpret_cast<const uint4*>(smem + S::kOffRaw + row * D + (i ^ mix) * 16);
+      dev::release_stage(dev::smem_addr(raw_empty), lane);
       dev::mbar_wait(dev::smem_addr(&k_empty[s]), (uint32_t)(((n >> 1) & 1) ^ 1), aborted, p.err);
+      if (active) {
+        const uint32_t tile = sbase + S::kOffK + (2 * s + X) * S::kTile + r * 128;
 #pragma unroll
-      for (int X = 0; X < 2; ++X) {
-        if (X < w.blocks) {
-          const uint32_t tile = sbase + S::kOffK + (2 * s + X) * S::kTile + r * 128;
+        for (int i = 0; i < kPieces; ++i) {
+          const uint32_t in[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+          uint32_t out[8];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) {
-            const uint32_t in[4] = {codes[X][i].x, codes[X][i].y, codes[X][i].z, codes[X][i].w};
-            uint32_t out[8];
+          for (int e = 0; e < 4; ++e) {
+            out[2 * e] = widen2<T>(in[e] & 0xffffu);
+            out[2 * e + 1] = widen2<T>(in[e] >> 16);
+          }
+          // granule g (8 dims) of row r stands at g ^ (r % 8) of its half's 128 bytes
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              out[2 * e] = widen2<T>(in[e] & 0xffffu);
-              out[2 * e + 1] = widen2<T>(in[e] >> 16);
-            }
-            // granule g (8 dims) of row r stands at g ^ (r % 8) of its half's 128 bytes
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int g = 2 * i + k;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                               tile + (g / 8) * (kTok * 128) + ((g % 8) ^ (r & 7)) * 16),
-                           "r"(out[4 * k]), "r"(out[4 * k + 1]), "r"(out[4 * k + 2]),
-                           "r"(out[4 * k + 3])
-                           : "memory");
-            }
+          for (int k = 0; k < 2; ++k) {
+            const int g = 2 * i + k;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             tile + (g / 8) * (kTok * 128) + ((g % 8) ^ (r & 7)) * 16),
+                         "r"(out[4 * k]), "r"(out[4 * k + 1]), "r"(out[4 * k + 2]),
+                         "r"(out[4 * k + 3])
+                         : "memory");
           }
         }
-        load(ids[X], w1.h, codes[X]);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(dev::smem_addr(&k_full[s]));
-      ids_of(w2, j + 2 * step, ids);
-      w = w1;
-      w1 = w2;
     }
   } else if (warp == 8) {
     // -------------------------------------------------------------- MMAs
