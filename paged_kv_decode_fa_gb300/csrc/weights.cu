@@ -68,8 +68,9 @@ __device__ __forceinline__ uint32_t widen2(uint32_t codes) {
   if constexpr (std::is_same<T, __half>::value) {
     return (uint32_t)h.x | ((uint32_t)h.y << 16);
   } else {
+    // four significant bits at most: the upper halves of the floats are exact
     const float2 f = __half22float2(__half2(h));
-    return mma::pack2(f.x, f.y, true);
+    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
   }
 }
 

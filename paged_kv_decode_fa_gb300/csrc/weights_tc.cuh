@@ -8,7 +8,7 @@
 // columns' lse come from shared memory, four a load for the whole warp.
 //  - warp 9 loads Q tiles (tensor copies, as fa_prefill_kernel's) and their lse;
 //  - K, two stages of two tiles, by warp 10's tensor copies; an E4M3 cache's codes are
-//    copied aside, and warps 12-19 widen them (exactly) into the same layout;
+//    copied aside, and warps 12-15 widen them (exactly) into the same layout;
 //  - warp 8, one lane, issues the MMAs into two score buffers a block;
 //  - warps 0-3 and 4-7 turn the scores of the two blocks into sums.
 // The grid is persistent and nothing waits for a whole CTA between jobs.  Waits are
@@ -45,7 +45,7 @@ struct Smem {
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
-constexpr int threads(bool e4m3) { return e4m3 ? 640 : 384; }
+constexpr int threads(bool e4m3) { return e4m3 ? 512 : 384; }
 
 }  // namespace wt
 
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
       dev::mbar_init(dev::smem_addr(&q_empty[s]), 9);  // the MMAs and eight warps' lse
     }
     for (int s = 0; s < 2; ++s) {
-      dev::mbar_init(dev::smem_addr(&k_full[s]), kE4m3 ? 8 : 1);
+      dev::mbar_init(dev::smem_addr(&k_full[s]), kE4m3 ? 4 : 1);
       dev::mbar_init(dev::smem_addr(&k_empty[s]), 1);
     }
     for (int s = 0; s < 4; ++s) {
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
       dev::mbar_init(dev::smem_addr(&s_empty[s]), 4);
     }
     dev::mbar_init(dev::smem_addr(raw_full), 1);
-    dev::mbar_init(dev::smem_addr(raw_empty), 8);
+    dev::mbar_init(dev::smem_addr(raw_empty), 4);
     dev::fence_barrier_init();
   }
   if (warp == 8) {
@@ -201,28 +201,28 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
           atomicOr(p.err, 2);
   } else if (kE4m3 && warp >= 12) {
     // -------------------------------------------------------------- K, widened
-    // A thread widens one token's row of codes.  They stand in shared memory by tensor
-    // copy (read straight from global memory, a thread a row, they missed L1 at
-    // every piece: 55-65 us for 128 columns), and the next job's are on their way
-    // once this job's are in registers.
-    const int row = threadIdx.x - 12 * 32, X = row / kTok, r = row % kTok;
+    // A thread widens the codes of a token of each block.  They stand in shared memory
+    // by tensor copy: read straight from global memory, a thread a row, they missed
+    // L1 at every piece.  (Eight warps left the sums 96 registers and spills.)
+    const int r = threadIdx.x % kTok;
     constexpr int kPieces = D / 16;  // 16 codes each
     // piece i of a row stands at i ^ (r % 8), or ^ (r / 2 % 4) in rows of 64 bytes
     const int mix = D == 128 ? r & 7 : r >> 1 & 3;
     int n = 0;
     for (int j = blockIdx.x; j < jobs; j += gridDim.x, ++n) {
       const int s = n & 1;
-      const bool active = X < load_job(j).blocks;
+      const int blocks = load_job(j).blocks;
       dev::mbar_wait(dev::smem_addr(raw_full), (uint32_t)(n & 1), aborted, p.err);
-      uint4 codes[kPieces];
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i)
-        if (active)
-          codes[i] = *reinterpret_cast<const uint4*>(smem + S::kOffRaw + row * D + (i ^ mix) * 16);
-      dev::release_stage(dev::smem_addr(raw_empty), lane);
       dev::mbar_wait(dev::smem_addr(&k_empty[s]), (uint32_t)(((n >> 1) & 1) ^ 1), aborted, p.err);
-      if (active) {
+#pragma unroll 1
+      for (int X = 0; X < blocks; ++X) {
         const uint32_t tile = sbase + S::kOffK + (2 * s + X) * S::kTile + r * 128;
+        const uint8_t* row = smem + S::kOffRaw + (X * kTok + r) * D;
+        uint4 codes[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          codes[i] = *reinterpret_cast<const uint4*>(row + (i ^ mix) * 16);
+        if (X + 1 == blocks) dev::release_stage(dev::smem_addr(raw_empty), lane);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
           const uint32_t in[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
