@@ -7,16 +7,19 @@
 // the weight that the softmax of those rows gave it; lse is what the attention
 // of the same rows returned.  One pass over K, none over V.
 //
-// Work.  A CTA takes a kv head and a run of a request's pages, a warp one page at
-// a time: its 16 tokens are the MMA's M side (m16n8k16, mma.sync), eight columns
-// (query row x head of the group) its N side.  The dot product does not mind the order
-// of dims, so a lane's fragments are whole 16-byte pieces of a K row and of a q
-// row: lane c of a row's four holds dims 8c .. 8c+7 of every 32 (16 of every 64 codes of
-// an E4M3 cache), straight from global memory into registers.  A page's K stays in
-// registers while all columns pass by; the sums over columns stay in two
-// registers a lane until the page is done, so every token's weight is one addition
-// to memory a call, and the result does not depend on the schedule.
-// (Pages that two requests share receive two.)
+// Work.  Requests of more than eight columns (query row x head of the group) go
+// through weights_tc.cuh.  Of the others a CTA takes a kv head and a run of pages, a
+// warp one page at a time: its 16 tokens are the MMA's M side (m16n8k16, mma.sync), the
+// columns its N side.  The dot product does not mind the order of dims, so a lane's
+// fragments are whole 16-byte pieces of a K row and of a q row: lane c of a row's four
+// holds dims 8c .. 8c+7 of every 32 (16 of every 64 codes of an E4M3 cache), straight
+// from global memory into registers.  Every token's weight is one addition to
+// memory a call, so the result does not depend on the schedule.  (Pages that two
+// requests share receive two.)
+//
+// What bounds it: HBM.  128 requests of 1024-8192 tokens, 64 / 8 heads, bf16, 1.28 GB:
+// 209 us = 6.1 TB/s, 0.91 of the copy rate (246 us with each page's id loaded in front
+// of its rows).  Few short requests: the launch and one chain of loads, 8 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -134,7 +137,7 @@ __device__ __forceinline__ void widen_page(const uint4 (&k)[2][D * sizeof(KVT) /
   }
 }
 
-// What a CTA works on, and the loads of both kernels.
+// What a CTA works on, and its loads.
 template <typename T, typename KVT, int D, int SC>
 struct Worker {
   static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -200,7 +203,8 @@ struct Worker {
     for (int j = 0; j < kQPieces; ++j) {
       // the dims that this lane's piece of K holds
       const int d = kE4m3 ? (j / 2) * 64 + c * 16 + (j % 2) * 8 : (4 * j + c) * 8;
-      b[j] = x < columns ? __ldg(reinterpret_cast<const uint4*>(q + d)) : make_uint4(0u, 0u, 0u, 0u);
+      b[j] = x < columns ? __ldg(reinterpret_cast<const uint4*>(q + d))
+                         : make_uint4(0u, 0u, 0u, 0u);
     }
   }
   // its lse in log2 units; +inf (weight 0) behind the last column and where the row
@@ -223,22 +227,21 @@ struct Worker {
       scale[0] = scale[1] = head_scale * __ldg(p.k_scales + at / kPageSize);
     }
   }
-  // Eight columns from x0 on against a page whose token n is at position pos:
-  // their weights' sums for tokens n and n + 8, this lane's two columns
+  // The columns against a page whose token n is at position pos: their weights' sums
+  // for tokens n and n + 8, this lane's two columns
   __device__ __forceinline__ void add_columns(const Fragments<D>& k, const uint4 (&b)[kQPieces],
-                                              int x0, const float (&lse)[2],
-                                              const float (&scale)[2], int pos,
-                                              float (&sum)[2]) const {
+                                              const float (&lse)[2], const float (&scale)[2],
+                                              int pos, float (&sum)[2]) const {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < kQPieces; ++j) {
       mma_16816(s, k.a[j][0], b[j].x, b[j].y, kBf16);
       mma_16816(s, k.a[j][1], b[j].z, b[j].w, kBf16);
     }
-    // s[0], s[1]: token n, columns x0 + 2c, + 1; s[2], s[3]: token n + 8
+    // s[0], s[1]: token n, columns 2c, + 1; s[2], s[3]: token n + 8
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int last = before + ((x0 + 2 * c + e) >> p.group_log2);
+      const int last = before + ((2 * c + e) >> p.group_log2);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         if (pos + 8 * t <= last) sum[t] += dev::fast_exp2(fmaf(s[2 * t + e], scale[t], -lse[e]));
@@ -260,8 +263,9 @@ struct Worker {
 // Eight columns at most (a decode step): they stay in registers while the pages
 // pass, each loaded while the one before is worked on.
 template <typename T, typename KVT, int D, int SC>
-__device__ __forceinline__ void weights_of_few(const Worker<T, KVT, D, SC>& w) {
+__global__ void __launch_bounds__(kWarps * 32, 2) fa_weights_kernel(const WeightsParams p) {
   using W = Worker<T, KVT, D, SC>;
+  const W w(p);
   uint4 q[W::kQPieces];
   w.load_column(w.n, q);
   const float lse[2] = {w.load_lse(2 * w.c), w.load_lse(2 * w.c + 1)};
@@ -277,57 +281,9 @@ __device__ __forceinline__ void weights_of_few(const Worker<T, KVT, D, SC>& w) {
     float scale[2], sum[2] = {0.f, 0.f};
     w.load_scales(this_page, scale);
     const int pos = w.pos0 + i * kPageSize + w.n;
-    w.add_columns(k, q, 0, lse, scale, pos, sum);
+    w.add_columns(k, q, lse, scale, pos, sum);
     w.store(this_page, pos, sum);
   }
-}
-
-// More columns: a warp holds the K of two pages while all columns pass, eight at a
-// time, the next eight's q on their way.
-template <typename T, typename KVT, int D, int SC>
-__device__ __forceinline__ void weights_of_many(const Worker<T, KVT, D, SC>& w) {
-  using W = Worker<T, KVT, D, SC>;
-  const int warp = threadIdx.x >> 5;
-  for (int i = 2 * warp; i < w.pages; i += 2 * kWarps) {
-    Fragments<D> k[2];
-    int page[2], pos[2];
-    float scale[2][2], sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      uint4 raw[2][W::kPieces];
-      page[t] = w.load_page(i + t, raw);
-      widen_page<T, KVT, D>(raw, &k[t]);
-      w.load_scales(max(page[t], 0), scale[t]);
-      pos[t] = w.pos0 + (i + t) * kPageSize + w.n;
-    }
-    uint4 next[W::kQPieces];
-    float next_lse[2] = {w.load_lse(2 * w.c), w.load_lse(2 * w.c + 1)};
-    w.load_column(w.n, next);
-    for (int x0 = 0; x0 < w.columns; x0 += 8) {
-      uint4 q[W::kQPieces];
-#pragma unroll
-      for (int j = 0; j < W::kQPieces; ++j) q[j] = next[j];
-      const float lse[2] = {next_lse[0], next_lse[1]};
-      if (x0 + 8 < w.columns) {
-        w.load_column(x0 + 8 + w.n, next);
-        next_lse[0] = w.load_lse(x0 + 8 + 2 * w.c);
-        next_lse[1] = w.load_lse(x0 + 9 + 2 * w.c);
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) w.add_columns(k[t], q, x0, lse, scale[t], pos[t], sum[t]);
-    }
-#pragma unroll
-    for (int t = 0; t < 2; ++t) w.store(page[t], pos[t], sum[t]);
-  }
-}
-
-template <typename T, typename KVT, int D, int SC>
-__global__ void __launch_bounds__(kWarps * 32, 2) fa_weights_kernel(const WeightsParams p) {
-  const Worker<T, KVT, D, SC> w(p);
-  if (w.columns <= 8)
-    weights_of_few(w);
-  else
-    weights_of_many(w);
 }
 
 using WeightsFn = void (*)(const WeightsParams);
@@ -384,8 +340,10 @@ int run_pages(int64_t total_pages, int heads, int sms) {
 }
 
 // Requests of more columns than this go through the tcgen05 kernel, in runs of
-// kTcPages.
-constexpr int kFewColumns = 16;
+// kTcPages.  (16 requests of 4096 tokens, 32 / 8 heads, us there and with the columns
+// eight at a time on mma.sync: 12 columns 31 and 38, 32 columns 31 and 52, 64
+// columns 33 and 83; over an E4M3 cache 29 and 29, 30 and 42, 35 and 70.)
+constexpr int kFewColumns = 8;
 constexpr int kTcPages = 2 * wt::kPages;
 
 // Runs of a batch's requests of many columns (`many`) or of the others; -1 for
