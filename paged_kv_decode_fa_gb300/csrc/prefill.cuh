@@ -310,8 +310,10 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
       int item_n[2] = {0, 0}, tile_n[2] = {0, 0};  // items and tiles so far, per block
       const uint64_t q_desc[2] = {smem_desc(sbase, 16, 1024),
                                   smem_desc(sbase + S::kQBytes, 16, 1024)};
+      Item next = Item::load(p.items, first);
       for (int it = first; it < last; ++it) {
-        const Item w = Item::load(p.items, it);
+        const Item w = next;
+        next = Item::load(p.items, min(it + 1, last - 1));
         const int tiles[2] = {w.tiles(0, block_tokens), w.tiles(1, block_tokens)};
         const int last_block = w.tokens > block_tokens ? 1 : 0;  // sees the most tiles
         const int keys = w.keys(last_block, block_tokens), all = tiles[last_block];
@@ -526,27 +528,56 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           for (int i = 0; i < 32; ++i) raw[c][i] = 0u;
       }
       auto value = [&](int i) { return __uint_as_float(raw[i / 32][i % 32]) * inv; };
-      if (ok && w.slot < 0) {
-        T* dst = static_cast<T*>(p.o) + row * D;
+      // Four lanes trade the 32-byte chunks of their rows, so that a store of theirs
+      // fills 128 bytes of one row: a row a lane, every store touched 32 lines.
+      const int q4 = lane & 3;
+      auto put = [&](uint32_t (&x)[4][8], char* base, int64_t pitch, int at) {
 #pragma unroll
-        for (int i = 0; i < D; i += 16) {
-          uint32_t x[8];
+        for (int bit = 1; bit <= 2; ++bit)
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[e] = mma::pack2(value(i + 2 * e), value(i + 2 * e + 1), kBf16);
-          store32(dst + i, x);
+          for (int i = 0; i < 2; ++i) {
+            const int lo = bit == 1 ? 2 * i : i, hi = lo + bit;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t t =
+                  __shfl_xor_sync(0xffffffffu, (q4 & bit) ? x[lo][e] : x[hi][e], bit);
+              if (q4 & bit)
+                x[lo][e] = t;
+              else
+                x[hi][e] = t;
+            }
+          }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {  // chunk q4 of lane r's row
+          const int row = __shfl_sync(0xffffffffu, at, (lane & ~3) | r);
+          if (row >= 0) store32(base + row * pitch + q4 * 32, x[r]);
         }
-      } else if (ok) {
-        float* dst = p.part_o + part * D;
+      };
+      if (w.slot < 0) {
+        // rows of o from the item's first head on, counted in heads
+        char* base = reinterpret_cast<char*>(
+            static_cast<T*>(p.o) +
+            ((size_t)w.row0 * p.num_qo_heads + (size_t)w.head * p.group) * D);
+        const int at = ok ? tok * p.num_qo_heads + g : -1;
 #pragma unroll
-        for (int i = 0; i < D; i += 8) {
-          uint32_t x[8];
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t x[4][8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(value(i + e));
-          store32(dst + i, x);
+          for (int e = 0; e < 32; ++e)
+            x[e / 8][e % 8] = mma::pack2(value(64 * c + 2 * e), value(64 * c + 2 * e + 1), kBf16);
+          put(x, base + c * 128, (int64_t)D * 2, at);
+        }
+      } else {
+        char* base = reinterpret_cast<char*>(p.part_o + ((size_t)w.slot * 256 + X * kRows) * D);
+        const int at = ok ? r : -1;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[4][8];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e / 8][e % 8] = __float_as_uint(value(32 * c + e));
+          put(x, base + c * 128, (int64_t)D * 4, at);
         }
       }
-      __syncwarp();
       if (ok) {
         if (w.slot >= 0)
           p.part_lse[part] = lse;
