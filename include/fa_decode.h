@@ -758,9 +758,9 @@ int fa_prefill_plan(const int32_t* indptr_host, const int32_t* indices_dev,
  * One to three kernels on cuda_stream, no allocation, no synchronisation: it can
  * be captured into a CUDA graph.  Results are bitwise reproducible for a plan.
  * Two runs that may be in flight together need two plans and workspaces.
- * What slots behind a request's last token hold is ignored, NaN included.  A value
- * that is not finite, of a token that a row does not see but another of the same
- * 256 does, may reach that row as NaN.
+ * What slots behind a request's last token hold is ignored, NaN included; so is a
+ * value that is not finite at a token that a row does not see (rows next to such
+ * tokens are computed a second time, slowly).
  * Errors: FA_ERR_INVALID_ARG (NULL or misaligned pointers and strides, scales, a
  * current device that is not the plan's), FA_ERR_CUDA. */
 int fa_prefill_run(fa_prefill_plan_t plan, const fa_rows* q, const void* paged_kv,

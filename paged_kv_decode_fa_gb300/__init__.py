@@ -1177,15 +1177,17 @@ def plan_append(indptr, indices: torch.Tensor, last_page_len, append_indptr, num
 
 def _q_rows(q: torch.Tensor):
     """The fa_rows of a q [rows, heads, head_dim]."""
-    token, head, inner = q.stride()
+    address, (n, heads, _), (token, head, inner) = q.data_ptr(), q.shape, q.stride()
     # a stride that is never taken may be anything
-    token = token if q.shape[0] > 1 else 0
-    head = head if q.shape[1] > 1 else 0
-    if q.numel() and (inner != 1 or (q.data_ptr() | (token | head) * q.element_size()) & 15
-                      or (q.shape[0] > 1 and token <= 0) or (q.shape[1] > 1 and head <= 0)):
+    if n <= 1:
+        token = 8
+    if heads == 1:
+        head = 8
+    if n and (inner != 1 or (address | (token | head) * q.element_size()) & 15 or token <= 0
+              or head <= 0):
         raise ValueError("q needs a contiguous innermost dim, and an address and strides in "
                          "whole 16 bytes")
-    return _Rows(q.data_ptr(), token, head)
+    return _Rows(address, token, head)
 
 
 class PrefillPlan:
@@ -1202,6 +1204,8 @@ class PrefillPlan:
         self.num_tokens = num_tokens
         self._device = workspace.get_device()
         self._q_shape = (num_tokens, self.num_qo_heads, self.head_dim)
+        self._nbytes = num_tokens * self.num_qo_heads * self.head_dim * q_dtype.itemsize
+        self._lse_bytes = num_tokens * self.num_qo_heads * 4
         self._page_shape = (2, self.page_size, self.num_kv_heads, self.head_dim)
 
     def __del__(self):
@@ -1260,27 +1264,39 @@ class PrefillPlan:
 
     def _outputs(self, q, paged_kv, out, lse, return_lse, stream):
         """Check q / paged_kv against the plan; allocate missing outputs."""
+        device = self._device
         if q.dtype is not self.q_dtype or paged_kv.dtype is not self.kv_dtype:
             raise TypeError("q / paged_kv dtype differs from the plan")
-        if q.shape != self._q_shape or q.get_device() != self._device:
+        if q.shape != self._q_shape or q.get_device() != device:
             raise ValueError(f"q must be a tensor {list(self._q_shape)} on the plan's device")
         rows = _q_rows(q)
         if (paged_kv.dim() != 5 or paged_kv.shape[1:] != self._page_shape
-                or not paged_kv.is_contiguous() or paged_kv.get_device() != self._device):
+                or not paged_kv.is_contiguous() or paged_kv.get_device() != device):
             raise ValueError("paged_kv must be a contiguous tensor [num_pages, 2, page_size, "
                              "num_kv_heads, head_dim] on the plan's device")
-        nbytes = q.numel() * q.element_size()
-        out = _empty(q.shape, q.dtype, q.device, stream) if out is None else _room(out, nbytes)
+        if out is None:
+            out = (torch.empty_like(q) if stream is None and q.is_contiguous()
+                   else _empty(self._q_shape, q.dtype, q.device, stream))
+        else:
+            nbytes, at, to = self._nbytes, q.data_ptr(), _room(out, self._nbytes).data_ptr()
+            if out.get_device() != device or not out.is_contiguous():
+                raise ValueError("out must be contiguous, on the plan's device")
+            end = at + self._span(q)
+            if nbytes and to < end and at < to + nbytes:
+                raise ValueError("out must not overlap q")
         if lse is not None:
-            _room(lse, q.numel() // self.head_dim * 4)
+            _room(lse, self._lse_bytes)
+            if lse.get_device() != device or not lse.is_contiguous():
+                raise ValueError("lse must be contiguous, on the plan's device")
         elif return_lse:
-            lse = _empty(q.shape[:-1], torch.float32, q.device, stream)
-        for t in (out, lse):
-            if t is not None and (t.get_device() != self._device or not t.is_contiguous()):
-                raise ValueError("out / lse must be contiguous, on the plan's device")
-        if nbytes and out.data_ptr() < q.data_ptr() + nbytes and q.data_ptr() < out.data_ptr() + nbytes:
-            raise ValueError("out must not overlap q")
+            lse = _empty(self._q_shape[:2], torch.float32, q.device, stream)
         return rows, out, lse
+
+    @staticmethod
+    def _span(q) -> int:
+        """Bytes from q's first element to past its last."""
+        last = sum((n - 1) * st for n, st in zip(q.shape, q.stride()) if n)
+        return (last + 1) * q.element_size()
 
     def check(self, stream=None) -> int:
         """Synchronise and return the device-check flags (0 = clean)."""
@@ -1494,7 +1510,8 @@ def _plan_workspace(workspace, indices, size, stream) -> torch.Tensor:
 class EvictPlan:
     """A planned eviction.  indptr, indices and last_page_len describe the batch
     after it (indices where the plan's are), freed [n] the page ids that it no longer
-    needs.  Keeps the index tensor and the workspace alive."""
+    needs; indices and freed are gathered from the plan's when first asked for.
+    Keeps the index tensor and the workspace alive."""
 
     def __init__(self, handle, indices, workspace, kv_dtype, shape, after):
         self._h = handle
@@ -1503,7 +1520,23 @@ class EvictPlan:
         self.batch, self.num_kv_heads, self.head_dim, self.page_size = shape
         self._device = workspace.get_device()
         self._page_shape = (2, self.page_size, self.num_kv_heads, self.head_dim)
-        self.indptr, self.indices, self.last_page_len, self.freed = after
+        self.indptr, self.last_page_len, *self._entries = after
+        self._gathered = [None, None]
+
+    def _pages(self, which):
+        if self._gathered[which] is None:
+            table = self._keep[0]
+            t = table[torch.from_numpy(self._entries[which]).to(table.device)]
+            self._gathered[which] = t if t.is_cuda else t.pin_memory()
+        return self._gathered[which]
+
+    @property
+    def indices(self) -> torch.Tensor:
+        return self._pages(0)
+
+    @property
+    def freed(self) -> torch.Tensor:
+        return self._pages(1)
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -1592,12 +1625,9 @@ def plan_evict(indptr, indices: torch.Tensor, last_page_len, keep, num_kv_heads:
         ctypes.byref(handle)), "fa_evict_plan")
     ptr, last, stay, free = _pages_after(np.asarray(indptr_h), np.asarray(last_h)[:B], budgets[0],
                                          page_size)
-    pick = [indices[torch.from_numpy(e).to(indices.device)] for e in (stay, free)]
-    if not indices.is_cuda:
-        pick = [t.pin_memory() for t in pick]
     return EvictPlan(handle.value, indices, workspace, kv_data_type,
                      (B, num_kv_heads, head_dim, page_size),
-                     (torch.from_numpy(ptr), pick[0], torch.from_numpy(last), pick[1]))
+                     (torch.from_numpy(ptr), torch.from_numpy(last), stay, free))
 
 
 class BatchDecodeWithPagedKVCacheWrapper:

@@ -416,6 +416,11 @@ int prefill_run(fa_prefill_plan_s* plan, int sc, const fa_rows* q, const void* p
   p.cta_offsets = reinterpret_cast<const int32_t*>(plan->ws + plan->layout.offsets);
   p.items = reinterpret_cast<const int32_t*>(plan->ws + plan->layout.items);
   p.indices = wide ? nullptr : plan->indices;
+  p.q = q->data;
+  p.q_token = q->token_stride;
+  p.q_head = q->head_stride;
+  p.kv = kv;
+  p.num_kv_heads = hkv;
   p.o = o;
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(plan->ws + plan->layout.part_o);

@@ -70,6 +70,10 @@ struct Params {
   const int32_t* cta_offsets;  // [CTAs + 1]
   const int32_t* items;        // [n * 8], see Item
   const int32_t* indices;      // page ids, or nullptr: entry i of the table is page i
+  const void* q;               // [rows, Hq, D], by strides in elements
+  int64_t q_token, q_head;
+  const void* kv;
+  int num_kv_heads;
   void* o;                     // [rows, Hq, D]
   float* lse;                  // [rows, Hq] or nullptr
   float* part_o;               // [slots][256][D] normalised
@@ -136,6 +140,69 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
                "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                : "memory");
+}
+
+// A value of V that is not finite, at a token that some rows of a block see and
+// others do not, reaches those others through a weight of 0 (0 * inf is NaN).  So a
+// row whose output is not finite is computed again by its warp, over the tokens it
+// sees alone (the first `seen` from the item's first tile on, whose entry is
+// `entry`), from its reference m and inv = 1 / sum - if such a value stands among
+// the others of the block's tiles, up to token `end`.  to: its D outputs, T or fp32.
+template <typename T, int D>
+__device__ __forceinline__ void fix_row(const pf::Params& p, int entry, int seen, int end, int head,
+                                     int64_t q_row, float scale, float m, float inv, char* to,
+                                     bool part) {
+  constexpr int V = D / 32;  // dims of a lane
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  const int lane = threadIdx.x & 31;
+  const int64_t token = (int64_t)p.num_kv_heads * D;
+  auto row_of = [&](int t) -> const T* {  // K of token t, its V a half page on
+    const int e = entry + t / kPageSize, id = p.indices ? __ldg(p.indices + e) : e;
+    if (id < 0 || (int64_t)id >= p.num_pages) return nullptr;
+    return static_cast<const T*>(p.kv) +
+           ((int64_t)id * 2 * kPageSize + t % kPageSize) * token + (int64_t)head * D + lane * V;
+  };
+  auto read = [&](const T* x, float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = dev::to_float(x[i]);
+  };
+  float x[V];
+  bool hidden = false;
+#pragma unroll 1
+  for (int t = seen; t < end; ++t) {
+    const T* k = row_of(t);
+    if (k == nullptr) continue;
+    read(k + kPageSize * token, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) hidden |= !(fabsf(x[i]) < INFINITY);
+  }
+  if (!__any_sync(0xffffffffu, hidden)) return;
+  float q[V], o[V] = {};
+  read(static_cast<const T*>(p.q) + q_row + lane * V, q);
+#pragma unroll 1
+  for (int t = 0; t < seen; ++t) {
+    const T* k = row_of(t);
+    float s = 0.f, v[V] = {};
+    if (k != nullptr) {
+      read(k, x);
+      read(k + kPageSize * token, v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s = fmaf(q[i], x[i], s);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    const float w = dev::fast_exp2(fmaf(s, scale, -m));
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = fmaf(w, v[i], o[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    if (part)
+      *reinterpret_cast<float2*>(to + (lane * V + i) * 4) = make_float2(o[i] * inv, o[i + 1] * inv);
+    else
+      *reinterpret_cast<uint32_t*>(to + (lane * V + i) * 2) =
+          mma::pack2(o[i] * inv, o[i + 1] * inv, kBf16);
+  }
 }
 
 template <typename T, int D>
@@ -553,6 +620,15 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           if (row >= 0) store32(base + row * pitch + q4 * 32, x[r]);
         }
       };
+      uint64_t odd2 = 0;  // NaN where the row's output is not finite
+#pragma unroll
+      for (int i = 0; i < D; i += 2)
+        odd2 = fma2(f2(__uint_as_float(raw[i / 32][i % 32]),
+                       __uint_as_float(raw[i / 32][i % 32 + 1])),
+                    0ull, odd2);
+      float odd, odd_hi;
+      f2_split(odd2, odd, odd_hi);
+      odd += odd_hi;
       if (w.slot < 0) {
         // rows of o from the item's first head on, counted in heads
         char* base = reinterpret_cast<char*>(
@@ -576,6 +652,30 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[e / 8][e % 8] = __float_as_uint(value(32 * c + e));
           put(x, base + c * 128, (int64_t)D * 4, at);
+        }
+      }
+      unsigned again = __ballot_sync(0xffffffffu, ok && odd != odd);
+      if (again) {  // (rare: rows are taken one after the other)
+        asm volatile("" ::: "memory");
+        __syncwarp();
+        // the block's tiles may hold tokens that only the other block sees
+        const int end = min(w.keys(w.tokens > block_tokens, block_tokens) - w.t0 * kTok,
+                            tiles * kTok);
+#pragma unroll 1
+        while (again) {
+          const int l = __ffs(again) - 1;
+          again &= again - 1;
+          const int t = __shfl_sync(0xffffffffu, tok, l), gl = __shfl_sync(0xffffffffu, g, l);
+          const float ml = __shfl_sync(0xffffffffu, m, l), il = __shfl_sync(0xffffffffu, inv, l);
+          const int64_t row_l = w.row0 + t, head = (int64_t)w.head * p.group + gl;
+          const size_t part_l = (size_t)w.slot * 256 + X * kRows + warp % 4 * 32 + l;
+          char* to = w.slot < 0 ? reinterpret_cast<char*>(static_cast<T*>(p.o) +
+                                                          (row_l * p.num_qo_heads + head) * D)
+                                : reinterpret_cast<char*>(p.part_o + part_l * D);
+          fix_row<T, D>(p, w.entry + w.t0 * kPages,
+                        max(0, min(w.pos0 + t + 1 - w.t0 * kTok, end)), end, w.head,
+                        row_l * p.q_token + head * p.q_head, scale, ml == -INFINITY ? 0.f : ml, il,
+                        to, w.slot >= 0);
         }
       }
       if (ok) {

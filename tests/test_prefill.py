@@ -320,6 +320,34 @@ def test_infinite_logits_are_nan_as_by_definition(lib, cuda):
     assert torch.isfinite(o[:, 1]).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype,d,hq,hkv,ctx,new", [
+    (BF16, 128, 8, 2, 40, 90), (F16, 64, 3, 3, 0, 300), (BF16, 64, 8, 1, 200, 60),
+    (BF16, 128, 4, 4, 20000, 40)])  # (the last: keys split over SMs)
+def test_values_that_a_row_does_not_see(lib, cuda, dtype, d, hq, hkv, ctx, new, value):
+    """V of one token of the prompt is not finite: rows before it have their finite
+    results, rows from it on have none in that dim.  K not finite: likewise."""
+    b = Batch([ctx], [new], hq, hkv, d, dtype, seed=15)
+    clean, lse = b.plan(lib).run(b.q, b.kv)
+    at = new // 2
+    page, slot = int(b.indices[(ctx + at) // 16]), (ctx + at) % 16
+    kv = b.kv.clone()
+    kv[page, 1, slot, 0, 5] = value
+    p = b.plan(lib)
+    o, l = p.run(b.q, kv)
+    assert p.check() == 0 and torch.equal(l, lse)
+    G = hq // hkv
+    assert not torch.isfinite(o[at:, :G, 5]).any()
+    o[at:, :G, 5] = clean[at:, :G, 5]
+    b.check(o, l, rows=30)
+    assert torch.equal(o[at:], clean[at:]) and torch.equal(o[:, G:], clean[:, G:])
+    kv = b.kv.clone()
+    kv[page, 0, slot, 0, 5] = value
+    o, l = p.run(b.q, kv)
+    assert torch.equal(o[:at], clean[:at]) and torch.equal(l[:at], lse[:at])
+
+
 # ---------------------------------------------------------------- the planner (CPU)
 
 def lay(total):
