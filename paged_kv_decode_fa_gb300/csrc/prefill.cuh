@@ -19,24 +19,43 @@
 //    copies of 16 tokens x 64 dims (one half of a page's rows of the head, 128-byte
 //    swizzled); its lanes issue a tile's copies side by side.  Pages behind the
 //    item's last visible token come from an out-of-range index: zeros.
-//  - warp 10 loads the blocks' Q (rows of a token's group adjacent in the tensor,
+//  - warp 11 loads the blocks' Q (rows of a token's group adjacent in the tensor,
 //    so a block is one box of tokens x heads x 64 dims).
-//  - warp 8 issues the MMAs: S = Q K^T (M 128, N 128) into the block's score
-//    columns of TMEM, O += P V with P from TMEM and V MN-major from its slot.  Order:
-//    S_A(0) S_B(0), then per tile P V_A(j) S_A(j+1) P V_B(j) S_B(j+1).
-//    MMAs complete in order, so a block's scores of tile j+1 being there also means
-//    that its O holds the tiles up to j.
+//  - warp 8, one lane, issues the MMAs: S = Q K^T (M 128, N 128) into the block's
+//    score columns of TMEM, O += P V with P from TMEM and V MN-major from its slot.
+//    Order: S_A(0) S_B(0), then per tile P V_A(j) S_A(j+1) P V_B(j) S_B(j+1), which
+//    holds the blocks half a period apart.  MMAs complete in order, so a block's
+//    scores of tile j+1 being there also means that its O holds the tiles up to j.
 //  - warps 0-3 and 4-7, the softmax of A and B: a thread per row = TMEM lane.  It
 //    reads its 128 scores, writes its weights as packed pairs over the first 64 of
-//    the score columns, rescales its row of O when its reference moves, and at the
-//    item's end writes the row: o and lse, or an fp32 partial state where the plan
-//    split the item's keys (folded by fa_prefill_merge_kernel).
+//    the score columns, in two halves, each handed to the MMAs as it is there;
+//    rescales its row of O when its reference moves; and at the item's end writes
+//    the row: o and lse, or an fp32 partial state where the plan split the item's keys
+//    (folded by fa_prefill_merge_kernel).
+//  - warp 10 clears the V rows behind an item's last visible token.
 // Items follow each other without a barrier across the CTA: the loads and the first
 // scores of an item run under the softmax and the output of the one before.
 //
 // Slots behind the item's last visible token may hold anything: their scores are
 // replaced (select, not add), and their V rows are cleared in shared memory before
-// the tile's P V (0 * NaN would be NaN).
+// the tile's P V (0 * NaN would be NaN).  For tokens that only some of the rows see
+// there is fix_row.
+//
+// What bounds it.  Long prompts: the tensor cores under the power limit.  8192 rows on a
+// context of 24576 (32 / 8 heads, head_dim 128, bf16): 2.48-2.53 ms = 1.52-1.55
+// PFLOP/s, 0.87 of what cuBLAS holds for seconds (0.77 of its burst).  A
+// tile of both blocks takes 2100-2600 cycles: 2048 of MMAs at head_dim 128 (1024 at
+// 64, where the two softmaxes, 1250 cycles each and half overlapped, set it).  Whole
+// prompts of 2048-6144 tokens 1.06-1.16 ms (1.40-1.52): an item's output and the next
+// one's first scores cost about two tiles, of 17 on average.
+// On the way (8192 rows on 24576): 4.52 ms with the MMAs issued by a whole warp and
+// 514 bytes of spills in the softmax; 2.65 with the registers split by warpgroup; 2.58
+// with four MMAs an election; 2.53 with one lane and the waits behind issued MMAs.
+// Slower and not kept: a warp for each block's MMAs (the blocks fall in step, 3.11 ms);
+// the first half's weights against the old reference while the maximum is found (3 %);
+// the next item's first scores before the other block's last tile (1 %, the issuing
+// lane waits for its Q); K and V loaded by a warp each, boxes of 4 KB, half the
+// bytes (no change: the copies are not what it waits for).
 //
 // Every wait is bounded (2 s); a wait that runs out sets bit 1 of the device-check
 // word and the CTA drains.
