@@ -1279,15 +1279,16 @@ class PrefillPlan:
                    else _empty(self._q_shape, q.dtype, q.device, stream))
         else:
             nbytes, at, to = self._nbytes, q.data_ptr(), _room(out, self._nbytes).data_ptr()
-            if out.get_device() != device or not out.is_contiguous():
-                raise ValueError("out must be contiguous, on the plan's device")
+            if out.dtype is not q.dtype or out.get_device() != device or not out.is_contiguous():
+                raise ValueError("out must be contiguous, of q's dtype, on the plan's device")
             end = at + self._span(q)
             if nbytes and to < end and at < to + nbytes:
                 raise ValueError("out must not overlap q")
         if lse is not None:
             _room(lse, self._lse_bytes)
-            if lse.get_device() != device or not lse.is_contiguous():
-                raise ValueError("lse must be contiguous, on the plan's device")
+            if (lse.dtype is not torch.float32 or lse.get_device() != device
+                    or not lse.is_contiguous()):
+                raise ValueError("lse must be contiguous float32, on the plan's device")
         elif return_lse:
             lse = _empty(self._q_shape[:2], torch.float32, q.device, stream)
         return rows, out, lse

@@ -388,6 +388,7 @@ struct fa_weights_plan_s {
   int64_t few = 0, many = 0;  // units of few columns, then of many
   int64_t rows = 0;
   int sms = 0;
+  bool ready[3] = {false, false, false};  // the tcgen05 kernel, by kScale...
 };
 
 namespace {
@@ -450,9 +451,17 @@ int weights_run(fa_weights_plan_s* plan, int sc, const fa_rows* q, const void* p
     const int smem = plan->d == 128 ? wt::Smem<128>::kBytes : wt::Smem<64>::kBytes;
     int jobs = (int)(plan->many * plan->hkv);
     void* args[4] = {&maps[0], &maps[1], &p, &jobs};
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess ||
-        cudaLaunchKernel(f, dim3((unsigned)std::min(jobs, plan->sms)), dim3(wt::threads(e4m3)),
+    if (!plan->ready[sc]) {
+      // the kernel's warpgroups share out the registers it is launched with
+      cudaFuncAttributes attr;
+      if (cudaFuncGetAttributes(&attr, f) != cudaSuccess ||
+          (e4m3 && attr.numRegs < wt::kLaunchRegs) ||
+          cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+              cudaSuccess)
+        return FA_ERR_CUDA;
+      plan->ready[sc] = true;
+    }
+    if (cudaLaunchKernel(f, dim3((unsigned)std::min(jobs, plan->sms)), dim3(wt::threads(e4m3)),
                          args, (size_t)smem, st) != cudaSuccess)
       return FA_ERR_CUDA;
   }

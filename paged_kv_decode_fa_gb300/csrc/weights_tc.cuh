@@ -8,7 +8,7 @@
 // columns' lse come from shared memory, four a load for the whole warp.
 //  - warp 9 loads Q tiles (tensor copies, as fa_prefill_kernel's) and their lse;
 //  - K, two stages of two tiles, by warp 10's tensor copies; an E4M3 cache's codes are
-//    copied aside, and warps 12-15 widen them (exactly) into the same layout;
+//    copied aside, and warps 12-19 widen them (exactly) into the same layout;
 //  - warp 8, one lane, issues the MMAs into two score buffers a block;
 //  - warps 0-3 and 4-7 turn the scores of the two blocks into sums.
 // The grid is persistent and nothing waits for a whole CTA between jobs.  Waits are
@@ -54,7 +54,13 @@ struct Smem {
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
-constexpr int threads(bool e4m3) { return e4m3 ? 512 : 384; }
+// Warps: 0-7 sums, 8-11 MMAs and loads, 12-19 widening (E4M3).
+constexpr int threads(bool e4m3) { return e4m3 ? 640 : 384; }
+// Registers a thread with twenty warps: as launched, and as the sums and the others
+// share them out.
+constexpr int kLaunchRegs = 96, kSumRegs = 136, kOtherRegs = 64;
+static_assert(256 * kSumRegs + 384 * kOtherRegs <= 640 * kLaunchRegs,
+              "a larger share would be waited for without end");
 
 }  // namespace wt
 
@@ -91,7 +97,7 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
       dev::mbar_init(dev::smem_addr(&q_empty[s]), 9);  // the MMAs and eight warps' lse
     }
     for (int s = 0; s < 2; ++s) {
-      dev::mbar_init(dev::smem_addr(&k_full[s]), kE4m3 ? 4 : 1);
+      dev::mbar_init(dev::smem_addr(&k_full[s]), kE4m3 ? 8 : 1);
       dev::mbar_init(dev::smem_addr(&k_empty[s]), 1);
     }
     for (int s = 0; s < 4; ++s) {
@@ -99,7 +105,7 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
       dev::mbar_init(dev::smem_addr(&s_empty[s]), 4);
     }
     dev::mbar_init(dev::smem_addr(raw_full), 1);
-    dev::mbar_init(dev::smem_addr(raw_empty), 4);
+    dev::mbar_init(dev::smem_addr(raw_empty), 8);
     dev::fence_barrier_init();
   }
   if (warp == 8) {
@@ -133,171 +139,176 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
     return page < 0 || (int64_t)page >= p.num_pages ? -1 : page;
   };
 
-  if (warp == 9) {
-    // -------------------------------------------------------------- Q and lse
-    const int tile_tokens = kTok >> p.group_log2;
-    int n = 0;
-    for (int j = blockIdx.x; j < jobs; j += gridDim.x) {
-      const Job w = load_job(j);
-      for (int t = w.t0; t < w.t1; ++t, ++n) {
-        const int s = n % kQSlots;
-        float lse[4];  // -lse of columns lane, lane + 32, ...: before the wait
+  if (warp >= 8) {
+    if constexpr (kE4m3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 9) {
+      // -------------------------------------------------------------- Q and lse
+      const int tile_tokens = kTok >> p.group_log2;
+      int n = 0;
+      for (int j = blockIdx.x; j < jobs; j += gridDim.x) {
+        const Job w = load_job(j);
+        for (int t = w.t0; t < w.t1; ++t, ++n) {
+          const int s = n % kQSlots;
+          float lse[4];  // -lse of columns lane, lane + 32, ...: before the wait
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = t * kTok + lane + 32 * i;
-          const int row = x >> p.group_log2, g = x & ((1 << p.group_log2) - 1);
-          lse[i] = x < w.columns ? __ldg(p.lse + (int64_t)(w.row0 + row) * p.hq +
-                                         (w.h << p.group_log2) + g) * -1.4426950408889634f
-                                 : -INFINITY;
-          if (lse[i] == INFINITY) lse[i] = -INFINITY;  // a row that saw nothing: weight 0
+          for (int i = 0; i < 4; ++i) {
+            const int x = t * kTok + lane + 32 * i;
+            const int row = x >> p.group_log2, g = x & ((1 << p.group_log2) - 1);
+            lse[i] = x < w.columns ? __ldg(p.lse + (int64_t)(w.row0 + row) * p.hq +
+                                           (w.h << p.group_log2) + g) * -1.4426950408889634f
+                                   : -INFINITY;
+            if (lse[i] == INFINITY) lse[i] = -INFINITY;  // a row that saw nothing: weight 0
+          }
+          dev::mbar_wait(dev::smem_addr(&q_empty[s]), (uint32_t)(((n / kQSlots) & 1) ^ 1), aborted,
+                         p.err);
+          float* to = reinterpret_cast<float*>(smem + S::kOffLse) + s * kTok;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) to[lane + 32 * i] = lse[i];
+          __syncwarp();
+          if (lane == 0) {
+            const uint32_t full = dev::smem_addr(&q_full[s]);
+            dev::mbar_arrive_expect_tx(full, S::kTile);
+            for (int h = 0; h < S::kHalves; ++h)
+              tma_load_3d(sbase + S::kOffQ + s * S::kTile + h * (kTok * 128), &q_map, h * 64,
+                          w.h << p.group_log2, w.row0 + t * tile_tokens, full);
+          }
+          __syncwarp();
         }
-        dev::mbar_wait(dev::smem_addr(&q_empty[s]), (uint32_t)(((n / kQSlots) & 1) ^ 1), aborted,
+      }
+      if (lane == 0)  // no copy may still be landing when the CTA exits
+        for (int i = n > kQSlots ? n - kQSlots : 0; i < n; ++i)
+          if (!dev::mbar_wait_bounded(dev::smem_addr(&q_full[i % kQSlots]),
+                                      (uint32_t)((i / kQSlots) & 1)))
+            atomicOr(p.err, 2);
+    } else if (warp == 10) {
+      // -------------------------------------------------------------- K
+      // from a 16-bit cache into the tiles, from an E4M3 cache its codes
+      const int oob = (int)(2 * p.num_pages);  // beyond the last page: zeros
+      constexpr int kStages = kE4m3 ? 1 : 2;
+      uint64_t* full_bar = kE4m3 ? raw_full : k_full;
+      uint64_t* empty_bar = kE4m3 ? raw_empty : k_empty;
+      int n = 0;
+      for (int j = blockIdx.x; j < jobs; j += gridDim.x, ++n) {
+        const Job w = load_job(j);
+        const int s = n % kStages;
+        const uint32_t full = dev::smem_addr(&full_bar[s]);
+        // lane l: half l / 16 of page l % 16
+        const int half = lane / (2 * kPages), at = lane % (2 * kPages);
+        const int page = page_of(w, at), c3 = page < 0 ? oob : 2 * page;
+        dev::mbar_wait(dev::smem_addr(&empty_bar[s]), (uint32_t)(((n / kStages) & 1) ^ 1), aborted,
                        p.err);
-        float* to = reinterpret_cast<float*>(smem + S::kOffLse) + s * kTok;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) to[lane + 32 * i] = lse[i];
+        if (lane == 0)
+          dev::mbar_arrive_expect_tx(full, w.blocks * (kE4m3 ? kTok * D : S::kTile));
         __syncwarp();
-        if (lane == 0) {
-          const uint32_t full = dev::smem_addr(&q_full[s]);
-          dev::mbar_arrive_expect_tx(full, S::kTile);
-          for (int h = 0; h < S::kHalves; ++h)
-            tma_load_3d(sbase + S::kOffQ + s * S::kTile + h * (kTok * 128), &q_map, h * 64,
-                        w.h << p.group_log2, w.row0 + t * tile_tokens, full);
+        if (at < w.blocks * kPages) {
+          if (kE4m3 && half == 0)
+            tma_load_4d_plain(sbase + S::kOffRaw + at * (kPageSize * D), &kv_map, 0, w.h, 0, c3,
+                              full);
+          if (!kE4m3 && half < S::kHalves)
+            tma_load_4d_plain(sbase + S::kOffK + (2 * s + at / kPages) * S::kTile +
+                                  half * (kTok * 128) + at % kPages * (kPageSize * 128),
+                              &kv_map, half * 64, w.h, 0, c3, full);
         }
         __syncwarp();
       }
-    }
-    if (lane == 0)  // no copy may still be landing when the CTA exits
-      for (int i = n > kQSlots ? n - kQSlots : 0; i < n; ++i)
-        if (!dev::mbar_wait_bounded(dev::smem_addr(&q_full[i % kQSlots]),
-                                    (uint32_t)((i / kQSlots) & 1)))
-          atomicOr(p.err, 2);
-  } else if (warp == 10) {
-    // -------------------------------------------------------------- K
-    // from a 16-bit cache into the tiles, from an E4M3 cache its codes
-    const int oob = (int)(2 * p.num_pages);  // beyond the last page: zeros
-    constexpr int kStages = kE4m3 ? 1 : 2;
-    uint64_t* full_bar = kE4m3 ? raw_full : k_full;
-    uint64_t* empty_bar = kE4m3 ? raw_empty : k_empty;
-    int n = 0;
-    for (int j = blockIdx.x; j < jobs; j += gridDim.x, ++n) {
-      const Job w = load_job(j);
-      const int s = n % kStages;
-      const uint32_t full = dev::smem_addr(&full_bar[s]);
-      // lane l: half l / 16 of page l % 16
-      const int half = lane / (2 * kPages), at = lane % (2 * kPages);
-      const int page = page_of(w, at), c3 = page < 0 ? oob : 2 * page;
-      dev::mbar_wait(dev::smem_addr(&empty_bar[s]), (uint32_t)(((n / kStages) & 1) ^ 1), aborted,
-                     p.err);
       if (lane == 0)
-        dev::mbar_arrive_expect_tx(full, w.blocks * (kE4m3 ? kTok * D : S::kTile));
-      __syncwarp();
-      if (at < w.blocks * kPages) {
-        if (kE4m3 && half == 0)
-          tma_load_4d_plain(sbase + S::kOffRaw + at * (kPageSize * D), &kv_map, 0, w.h, 0, c3,
-                            full);
-        if (!kE4m3 && half < S::kHalves)
-          tma_load_4d_plain(sbase + S::kOffK + (2 * s + at / kPages) * S::kTile +
-                                half * (kTok * 128) + at % kPages * (kPageSize * 128),
-                            &kv_map, half * 64, w.h, 0, c3, full);
-      }
-      __syncwarp();
-    }
-    if (lane == 0)
-      for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
-        if (!dev::mbar_wait_bounded(dev::smem_addr(&full_bar[i % kStages]),
-                                    (uint32_t)((i / kStages) & 1)))
-          atomicOr(p.err, 2);
-  } else if (kE4m3 && warp >= 12) {
-    // -------------------------------------------------------------- K, widened
-    // A thread widens the codes of a token of each block.  They stand in shared memory
-    // by tensor copy: read straight from global memory, a thread a row, they missed
-    // L1 at every piece.  (Eight warps left the sums 96 registers and spills.)
-    const int r = threadIdx.x % kTok;
-    constexpr int kPieces = D / 16;  // 16 codes each
-    // piece i of a row stands at i ^ (r % 8), or ^ (r / 2 % 4) in rows of 64 bytes
-    const int mix = D == 128 ? r & 7 : r >> 1 & 3;
-    int n = 0;
-    for (int j = blockIdx.x; j < jobs; j += gridDim.x, ++n) {
-      const int s = n & 1;
-      const int blocks = load_job(j).blocks;
-      dev::mbar_wait(dev::smem_addr(raw_full), (uint32_t)(n & 1), aborted, p.err);
-      dev::mbar_wait(dev::smem_addr(&k_empty[s]), (uint32_t)(((n >> 1) & 1) ^ 1), aborted, p.err);
-#pragma unroll 1
-      for (int X = 0; X < blocks; ++X) {
-        const uint32_t tile = sbase + S::kOffK + (2 * s + X) * S::kTile + r * 128;
-        const uint8_t* row = smem + S::kOffRaw + (X * kTok + r) * D;
+        for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
+          if (!dev::mbar_wait_bounded(dev::smem_addr(&full_bar[i % kStages]),
+                                      (uint32_t)((i / kStages) & 1)))
+            atomicOr(p.err, 2);
+    } else if (kE4m3 && warp >= 12) {
+      // -------------------------------------------------------------- K, widened
+      // A thread widens the codes of one token.  They stand in shared memory by
+      // tensor copy: read straight from global memory, a thread a row, they missed L1
+      // at every piece.
+      const int row = threadIdx.x - 12 * 32, X = row / kTok, r = row % kTok;
+      constexpr int kPieces = D / 16;  // 16 codes each
+      // piece i of a row stands at i ^ (r % 8), or ^ (r / 2 % 4) in rows of 64 bytes
+      const int mix = D == 128 ? r & 7 : r >> 1 & 3;
+      int n = 0;
+      for (int j = blockIdx.x; j < jobs; j += gridDim.x, ++n) {
+        const int s = n & 1;
+        const bool active = X < load_job(j).blocks;
+        dev::mbar_wait(dev::smem_addr(raw_full), (uint32_t)(n & 1), aborted, p.err);
         uint4 codes[kPieces];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-          codes[i] = *reinterpret_cast<const uint4*>(row + (i ^ mix) * 16);
-        if (X + 1 == blocks) dev::release_stage(dev::smem_addr(raw_empty), lane);
+          if (active)
+            codes[i] =
+                *reinterpret_cast<const uint4*>(smem + S::kOffRaw + row * D + (i ^ mix) * 16);
+        dev::release_stage(dev::smem_addr(raw_empty), lane);
+        dev::mbar_wait(dev::smem_addr(&k_empty[s]), (uint32_t)(((n >> 1) & 1) ^ 1), aborted,
+                       p.err);
+        if (active) {
+          const uint32_t tile = sbase + S::kOffK + (2 * s + X) * S::kTile + r * 128;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const uint32_t in[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-          uint32_t out[8];
+          for (int i = 0; i < kPieces; ++i) {
+            const uint32_t in[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+            uint32_t out[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            out[2 * e] = widen2<T>(in[e] & 0xffffu);
-            out[2 * e + 1] = widen2<T>(in[e] >> 16);
-          }
-          // granule g (8 dims) of row r stands at g ^ (r % 8) of its half's 128 bytes
+            for (int e = 0; e < 4; ++e) {
+              out[2 * e] = widen2<T>(in[e] & 0xffffu);
+              out[2 * e + 1] = widen2<T>(in[e] >> 16);
+            }
+            // granule g (8 dims) of row r stands at g ^ (r % 8) of its half's 128 bytes
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int g = 2 * i + k;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             tile + (g / 8) * (kTok * 128) + ((g % 8) ^ (r & 7)) * 16),
-                         "r"(out[4 * k]), "r"(out[4 * k + 1]), "r"(out[4 * k + 2]),
-                         "r"(out[4 * k + 3])
-                         : "memory");
+            for (int k = 0; k < 2; ++k) {
+              const int g = 2 * i + k;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               tile + (g / 8) * (kTok * 128) + ((g % 8) ^ (r & 7)) * 16),
+                           "r"(out[4 * k]), "r"(out[4 * k + 1]), "r"(out[4 * k + 2]),
+                           "r"(out[4 * k + 3])
+                           : "memory");
+            }
           }
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(dev::smem_addr(&k_full[s]));
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    } else if (warp == 8) {
+      // -------------------------------------------------------------- MMAs
+      if (elect_one()) {
+        int n = 0, q_n = 0, cnt[2] = {0, 0};
+        for (int j = blockIdx.x; j < jobs; j += gridDim.x, ++n) {
+          const Job w = load_job(j);
+          dev::mbar_wait(dev::smem_addr(&k_full[n & 1]), (uint32_t)((n >> 1) & 1), aborted, p.err);
+          for (int t = w.t0; t < w.t1; ++t, ++q_n) {
+            const int qs = q_n % kQSlots;
+            dev::mbar_wait(dev::smem_addr(&q_full[qs]), (uint32_t)((q_n / kQSlots) & 1), aborted,
+                           p.err);
+            const uint64_t q_desc = smem_desc(sbase + S::kOffQ + qs * S::kTile, 16, 1024);
+#pragma unroll
+            for (int X = 0; X < 2; ++X) {
+              if (X >= w.blocks) continue;
+              const int b = cnt[X] & 1;
+              dev::mbar_wait(dev::smem_addr(&s_empty[2 * X + b]),
+                             (uint32_t)(((cnt[X] >> 1) & 1) ^ 1), aborted, p.err);
+              fence_after();
+              ++cnt[X];
+              const uint64_t k_desc =
+                  smem_desc(sbase + S::kOffK + (2 * (n & 1) + X) * S::kTile, 16, 1024);
+#pragma unroll
+              for (int h = 0; h < S::kHalves; ++h)
+                umma4(tmem + X * 256 + b * 128, k_desc + h * (kTok * 128 / 16),
+                      q_desc + h * (kTok * 128 / 16), kIdesc, h > 0);
+              commit_one(&s_full[2 * X + b]);
+            }
+            commit_one(&q_empty[qs]);
+          }
+          commit_one(&k_empty[n & 1]);
+        }
+        // TMEM is freed only after the last MMA completed
+        if (n > 0 &&
+            !dev::mbar_wait_bounded(dev::smem_addr(&k_empty[(n - 1) & 1]),
+                                    (uint32_t)(((n - 1) >> 1) & 1)))
+          atomicOr(p.err, 2);
+      }
       __syncwarp();
-      if (lane == 0) dev::mbar_arrive(dev::smem_addr(&k_full[s]));
     }
-  } else if (warp == 8) {
-    // -------------------------------------------------------------- MMAs
-    if (elect_one()) {
-      int n = 0, q_n = 0, cnt[2] = {0, 0};
-      for (int j = blockIdx.x; j < jobs; j += gridDim.x, ++n) {
-        const Job w = load_job(j);
-        dev::mbar_wait(dev::smem_addr(&k_full[n & 1]), (uint32_t)((n >> 1) & 1), aborted, p.err);
-        for (int t = w.t0; t < w.t1; ++t, ++q_n) {
-          const int qs = q_n % kQSlots;
-          dev::mbar_wait(dev::smem_addr(&q_full[qs]), (uint32_t)((q_n / kQSlots) & 1), aborted,
-                         p.err);
-          const uint64_t q_desc = smem_desc(sbase + S::kOffQ + qs * S::kTile, 16, 1024);
-#pragma unroll
-          for (int X = 0; X < 2; ++X) {
-            if (X >= w.blocks) continue;
-            const int b = cnt[X] & 1;
-            dev::mbar_wait(dev::smem_addr(&s_empty[2 * X + b]),
-                           (uint32_t)(((cnt[X] >> 1) & 1) ^ 1), aborted, p.err);
-            fence_after();
-            ++cnt[X];
-            const uint64_t k_desc =
-                smem_desc(sbase + S::kOffK + (2 * (n & 1) + X) * S::kTile, 16, 1024);
-#pragma unroll
-            for (int h = 0; h < S::kHalves; ++h)
-              umma4(tmem + X * 256 + b * 128, k_desc + h * (kTok * 128 / 16),
-                    q_desc + h * (kTok * 128 / 16), kIdesc, h > 0);
-            commit_one(&s_full[2 * X + b]);
-          }
-          commit_one(&q_empty[qs]);
-        }
-        commit_one(&k_empty[n & 1]);
-      }
-      // TMEM is freed only after the last MMA completed
-      if (n > 0 &&
-          !dev::mbar_wait_bounded(dev::smem_addr(&k_empty[(n - 1) & 1]),
-                                  (uint32_t)(((n - 1) >> 1) & 1)))
-        atomicOr(p.err, 2);
-    }
-    __syncwarp();
-  } else if (warp < 8) {
+  } else {
     // -------------------------------------------------------------- sums
+    if constexpr (kE4m3) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     const int X = warp / 4, r = threadIdx.x % kTok;
     const uint32_t tS = tmem + X * 256 + ((uint32_t)(32 * (warp % 4)) << 16);
     int q_n = 0, cnt = 0;

@@ -463,6 +463,9 @@ def test_run_refusals(lib, cuda):
                 lambda: p.run(b.q, b.kv, lse=torch.empty(4, device=cuda)),
                 lambda: p.run(b.q, b.kv, out=torch.empty(b.q.numel() + 8, dtype=BF16, device=cuda)[8:]),
                 lambda: p.run(b.q, b.kv, out=torch.empty(b.q.shape, dtype=BF16)),
+                lambda: p.run(b.q, b.kv, out=torch.empty(b.q.shape, device=cuda)),
+                lambda: p.run(b.q, b.kv, lse=torch.empty((40, 8), device=cuda).double()),
+                lambda: p.run(b.q, b.kv, lse=torch.empty((40, 8))),
                 lambda: p.run_head_scales(b.q, b.kv, sb, sb), lambda: p.run_block_scales(b.q, b.kv, sh, sh),
                 lambda: p.run_token_scales(b.q, b.kv, sb, sb),
                 lambda: p.run_block_scales(b.q, b.kv, sb, sb.double()),
