@@ -114,6 +114,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   const int L = u.length, n = u.kept, cand = L - u.recent, want = n - u.recent;
   int32_t* list = p.lists + u.list + (int64_t)h * n;
 
+  // The cluster meets: memory written before is seen after.  (A cluster's own barrier
+  // waits for every store in flight, also of a cluster of one.)
+  auto meet = [&] {
+    if (C == 1)
+      __syncthreads();
+    else
+      cluster.sync();
+  };
   // a token's slot in the arrays per token; -1 for a page id outside the cache
   auto place = [&](int t) -> int64_t {
     const int page = __ldg(p.indices + u.entry + t / kPageSize);
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
           if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
         }
       }
-      cluster.sync();
+      meet();
       if (tid < 256) {
         int sum = 0;
         for (int r = 0; r < C; ++r) sum += cluster.map_shared_rank(hist, r)[tid];
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       sh.counts[tid] = sum;
     }
   }
-  cluster.sync();
+  meet();
   {
     int a = 0, e = 0;  // kept for sure, and equal to the border, before this warp
     for (int r = 0; r < c; ++r) {
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     }
   }
   for (int i = c * kThreads + tid; i < u.recent; i += C * kThreads) list[want + i] = cand + i;
-  cluster.sync();  // the list is whole, and the keys are done with
+  meet();  // the list is whole, and the keys are done with
 
   // ---- 4. the rows, a chunk of ranks at a time, the next chunk's on their way
   const int rb = p.row_bytes, pieces = 2 * rb / 16;  // 16-byte pieces of a token's K and V
@@ -335,7 +343,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     fetch(step + 1);
     if (step % group == 0) look_up(step / group + 2);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
-    cluster.sync();  // all of the chunk's rows have been read
+    // all of the chunk's rows have been read (nothing else is handed over: a
+    // thread writes the pieces that it fetched itself)
+    if (C == 1)
+      __syncthreads();
+    else
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::
+                       : "memory");
     const int count = count_of(step), s = step / group % 3, first = step % group * chunk;
     const uint8_t* from = buffer + (step & 1) * (p.buffer / 2) + piece * 16;
     for (int i = first_rank; i < count; i += ranks)
