@@ -16,12 +16,13 @@
 //
 // What bounds it.  32 rows of 4 heads over 16 prompts of 2048-8192 tokens, 8 kv heads:
 // 36 us from a 16-bit cache (168 MB: 25 us at the copy rate), where a job of one
-// tile waits for its K; 48 us from an E4M3 cache (84 MB), where the four warps that
-// widen set the pace (4600 cycles a job of 256 tokens, the conversions alone 2000 a
-// block).  Widening in integer steps and a bf16 product took longer (58-92 us), as
-// did reading codes straight from global memory, a row a thread (55-67) or a piece a
-// lane (65), and eight warps (53: 96 registers, the sums spill).  Columns' masks inside
-// the sums' one loop doubled it (2460 cycles a tile, 1140 with two loops).
+// tile waits for its K; 45 us from an E4M3 cache (84 MB), 4300 cycles a job of 256
+// tokens in which codes, widening, MMAs and sums follow each other.  On the way: 67 us
+// with a thread a row reading its codes straight from global memory, 48 with four
+// warps widening from shared memory (4600 cycles a job), 53 with eight of 96
+// registers (the sums spill).  Widening in integer steps and a bf16 product took
+// longer (58-92 us).  Columns' masks inside the sums' one loop doubled it (2460
+// cycles a tile, 1140 with two loops).
 #pragma once
 
 #include <cuda.h>
