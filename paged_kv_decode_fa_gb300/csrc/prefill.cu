@@ -178,10 +178,12 @@ void make_work(const std::vector<Block>& blocks, int heads, int max_ctas, Prefil
 // Device-check word, the work list, the table entries to widen, then the partial
 // states and, for an E4M3 cache, its pages in q's type.
 struct PrefillLayout {
-  size_t offsets, items, merge, entries, meta, part_o, part_lse, wide, total;
+  size_t offsets, items, merge, entries, meta, part_o, part_lse, scales, wide, total;
 };
 
-PrefillLayout layout_of(const PrefillWork& w, size_t entries, size_t wide_bytes, int D) {
+// scale_bytes, wide_bytes: of an E4M3 cache's K scales by token and its pages.
+PrefillLayout layout_of(const PrefillWork& w, size_t entries, size_t scale_bytes,
+                        size_t wide_bytes, int D) {
   PrefillLayout L;
   L.offsets = kAlign;
   L.items = align_up(L.offsets + 4 * w.cta_offsets.size());
@@ -190,7 +192,8 @@ PrefillLayout layout_of(const PrefillWork& w, size_t entries, size_t wide_bytes,
   L.meta = align_up(L.entries + 4 * entries);
   L.part_o = L.meta;
   L.part_lse = align_up(L.part_o + 4 * (size_t)w.slots * 256 * D);
-  L.wide = align_up(L.part_lse + 4 * (size_t)w.slots * 256);
+  L.scales = align_up(L.part_lse + 4 * (size_t)w.slots * 256);
+  L.wide = align_up(L.scales + scale_bytes);
   L.total = align_up(L.wide + wide_bytes);
   return L;
 }
@@ -255,15 +258,17 @@ struct WidenParams {
   const int32_t* entries;   // table entries to widen
   const float* k_scales;    // kScalePerToken [pages, Hkv, 16], kScalePerBlock [pages, Hkv]
   const float* v_scales;
+  float* out_scales;        // the K scales by table entry: [entries, Hkv(, 16)]
   int* err;
   int64_t num_pages;
   int hkv;
 };
 
 // One page of an E4M3 cache in bf16: the codes as they are (4 significant bits:
-// exact), times a token's or a block's scale where the cache has one (exact for
-// powers of two; otherwise one rounding of 2^-9, as the weights' own).  A streaming
-// pass over the cache, read once here and as bf16 by every block of rows.
+// exact).  Scales per token or block: V's multiply its elements (exact for powers of
+// two; otherwise one rounding of 2^-9, as the weights' own); K's are laid out by table
+// entry, for the scores, whose precision lse has.  A streaming pass over the cache, read
+// once here and as bf16 by every block of rows.
 template <int D, int SC>
 __global__ void __launch_bounds__(256) fa_prefill_widen_kernel(const WidenParams p) {
   const int entry = p.entries[blockIdx.x];
@@ -273,14 +278,19 @@ __global__ void __launch_bounds__(256) fa_prefill_widen_kernel(const WidenParams
   const int groups = 2 * kPageSize * p.hkv * (D / 16);  // of 16 codes
   const uint4* src = reinterpret_cast<const uint4*>(p.kv) + (ok ? (int64_t)page * groups : 0);
   uint4* dst = p.out + (int64_t)entry * groups * 2;
+  if constexpr (SC != kScaleNone) {
+    const int n = p.hkv * (SC == kScalePerToken ? kPageSize : 1);
+    for (int i = threadIdx.x; i < n; i += 256)
+      p.out_scales[(int64_t)entry * n + i] = ok ? __ldg(p.k_scales + (int64_t)page * n + i) : 0.f;
+  }
   for (int i = threadIdx.x; i < groups; i += 256) {
     const uint4 c = ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
     float scale = 1.f;
     if constexpr (SC != kScaleNone) {
       const int row = i / (D / 16), head = row % p.hkv, slot = row / p.hkv % kPageSize;
-      const float* s = row < kPageSize * p.hkv ? p.k_scales : p.v_scales;
       const int64_t at = (int64_t)page * p.hkv + head;
-      if (ok) scale = __ldg(s + (SC == kScalePerToken ? at * kPageSize + slot : at));
+      if (ok && row >= kPageSize * p.hkv)
+        scale = __ldg(p.v_scales + (SC == kScalePerToken ? at * kPageSize + slot : at));
     }
     const uint32_t in[4] = {c.x, c.y, c.z, c.w};
     uint32_t out[8];
@@ -297,16 +307,23 @@ __global__ void __launch_bounds__(256) fa_prefill_widen_kernel(const WidenParams
 }
 
 struct PrefillKernel {
-  const void* attend = nullptr;
+  const void* attend[3] = {nullptr, nullptr, nullptr};  // by kScale... (E4M3: bf16 only)
   const void* merge = nullptr;
   int smem = 0;
 };
 
 template <typename T, int D>
 PrefillKernel kernel_for() {
-  return PrefillKernel{reinterpret_cast<const void*>(&fa_prefill_kernel<T, D>),
-                       reinterpret_cast<const void*>(&fa_prefill_merge_kernel<T, D>),
-                       pf::Smem<D>::kBytes};
+  PrefillKernel k;
+  const auto f = [](auto kernel) { return reinterpret_cast<const void*>(kernel); };
+  k.attend[kScaleNone] = f(&fa_prefill_kernel<T, D, kScaleNone>);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    k.attend[kScalePerToken] = f(&fa_prefill_kernel<T, D, kScalePerToken>);
+    k.attend[kScalePerBlock] = f(&fa_prefill_kernel<T, D, kScalePerBlock>);
+  }
+  k.merge = reinterpret_cast<const void*>(&fa_prefill_merge_kernel<T, D>);
+  k.smem = pf::Smem<D>::kBytes;
+  return k;
 }
 
 PrefillKernel find_prefill_kernel(fa_dtype q, int D) {
@@ -421,6 +438,7 @@ int prefill_run(fa_prefill_plan_s* plan, int sc, const fa_rows* q, const void* p
   p.q_head = q->head_stride;
   p.kv = kv;
   p.num_kv_heads = hkv;
+  p.k_scales = reinterpret_cast<const float*>(plan->ws + plan->layout.scales);
   p.o = o;
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(plan->ws + plan->layout.part_o);
@@ -442,6 +460,7 @@ int prefill_run(fa_prefill_plan_s* plan, int sc, const fa_rows* q, const void* p
     w.entries = reinterpret_cast<const int32_t*>(plan->ws + plan->layout.entries);
     w.k_scales = k_scales;
     w.v_scales = v_scales;
+    w.out_scales = reinterpret_cast<float*>(plan->ws + plan->layout.scales);
     w.err = p.err;
     w.num_pages = num_pages;
     w.hkv = hkv;
@@ -451,8 +470,8 @@ int prefill_run(fa_prefill_plan_s* plan, int sc, const fa_rows* q, const void* p
       return FA_ERR_CUDA;
   }
   void* args[3] = {&maps[0], &maps[1], &p};
-  if (cudaLaunchKernel(plan->kernel.attend, dim3((unsigned)plan->ctas), dim3(pf::kThreads), args,
-                       (size_t)plan->kernel.smem, st) != cudaSuccess)
+  if (cudaLaunchKernel(plan->kernel.attend[sc], dim3((unsigned)plan->ctas), dim3(pf::kThreads),
+                       args, (size_t)plan->kernel.smem, st) != cudaSuccess)
     return FA_ERR_CUDA;
   if (plan->merge_units > 0) {
     PrefillMergeParams m;
@@ -491,12 +510,13 @@ size_t fa_prefill_workspace_size(const int32_t* indptr_host, const int32_t* last
       return 0;
     PrefillWork w;
     make_work(blocks, num_kv_heads, sms, &w);
-    size_t entries = 0, wide = 0;
+    size_t entries = 0, scales = 0, wide = 0;
     if (kv_dtype == FA_DTYPE_E4M3) {
       entries = wide_entries(indptr_host, qo_indptr_host, batch, nullptr);
-      wide = (size_t)indptr_host[batch] * 2 * kPageSize * num_kv_heads * head_dim * 2;
+      scales = (size_t)indptr_host[batch] * kPageSize * num_kv_heads * 4;
+      wide = scales * head_dim;  // K and V, two bytes each
     }
-    return layout_of(w, entries, wide, head_dim).total;
+    return layout_of(w, entries, scales, wide, head_dim).total;
   } catch (const std::bad_alloc&) {
     return 0;
   }
@@ -557,12 +577,13 @@ int fa_prefill_plan(const int32_t* indptr_host, const int32_t* indices_dev,
     PrefillWork w;
     make_work(blocks, num_kv_heads, sms, &w);
     std::vector<int32_t> entries;
-    size_t wide = 0;
+    size_t scales = 0, wide = 0;
     if (kv_dtype == FA_DTYPE_E4M3) {
       wide_entries(indptr_host, qo_indptr_host, batch, &entries);
-      wide = (size_t)indptr_host[batch] * 2 * kPageSize * num_kv_heads * head_dim * 2;
+      scales = (size_t)indptr_host[batch] * kPageSize * num_kv_heads * 4;
+      wide = scales * head_dim;  // K and V, two bytes each
     }
-    const PrefillLayout L = layout_of(w, entries.size(), wide, head_dim);
+    const PrefillLayout L = layout_of(w, entries.size(), scales, wide, head_dim);
     if (L.total > workspace_bytes) return FA_ERR_WORKSPACE_TOO_SMALL;
     std::vector<uint8_t> meta(L.meta, 0);
     auto put = [&](size_t at, const std::vector<int32_t>& v) {
@@ -588,17 +609,19 @@ int fa_prefill_plan(const int32_t* indptr_host, const int32_t* indices_dev,
     plan->ctas = (int)w.cta_offsets.size() - 1;
     plan->merge_units = (int)(w.merge.size() / 8);
     plan->kernel = find_prefill_kernel(q_dtype, head_dim);
-    // the kernel's warpgroups share out the registers it is launched with
-    cudaFuncAttributes attr;
-    if (cudaFuncGetAttributes(&attr, plan->kernel.attend) != cudaSuccess ||
-        attr.numRegs < pf::kLaunchRegs) {
-      delete plan;
-      return FA_ERR_CUDA;
+    // the kernels' warpgroups share out the registers they are launched with
+    cudaError_t e = cudaSuccess;
+    for (int sc = 0; sc < (kv_dtype == FA_DTYPE_E4M3 ? 3 : 1); ++sc) {
+      const void* f = plan->kernel.attend[sc];
+      cudaFuncAttributes attr;
+      if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, f);
+      if (e == cudaSuccess && attr.numRegs < pf::kLaunchRegs) e = cudaErrorInvalidDeviceFunction;
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 plan->kernel.smem);
     }
-    if (cudaFuncSetAttribute(plan->kernel.attend, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             plan->kernel.smem) != cudaSuccess ||
-        upload_async(plan->ws, meta.data(), meta.size(),
-                     static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
+    if (e != cudaSuccess || upload_async(plan->ws, meta.data(), meta.size(),
+                                         static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
       delete plan;
       return FA_ERR_CUDA;
     }

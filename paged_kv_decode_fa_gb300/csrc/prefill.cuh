@@ -92,6 +92,8 @@ struct Params {
   const void* q;               // [rows, Hq, D], by strides in elements
   int64_t q_token, q_head;
   const void* kv;
+  const float* k_scales;       // SC: times scores; [table entries, Hkv, 16] by token or
+                               // [table entries, Hkv] by block
   int num_kv_heads;
   void* o;                     // [rows, Hq, D]
   float* lse;                  // [rows, Hq] or nullptr
@@ -145,10 +147,13 @@ struct Smem {
   static constexpr int kOffRing = 2 * kQBytes;
   static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
   // kv_full[n], kv_empty[n]; q_full, q_empty, s_full [2], p_full [2][2], o_full, o_empty [2],
-  // v_there, v_clean
-  static constexpr int kNumBars = 2 * kSlots + 16;
+  // v_there, v_clean; sc_full, sc_empty [kScaleSlots]
+  static constexpr int kScaleSlots = 3;
+  static constexpr int kNumBars = 2 * kSlots + 16 + 2 * kScaleSlots;
   static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
-  static constexpr int kBytes = kOffTmem + 16 + 1024;    // and the alignment to 1024
+  static constexpr int kOffScales = kOffTmem + 16;       // SC: K scales of a tile's tokens
+  static constexpr int kBytes = kOffScales + kScaleSlots * kTok * 4 + 1024;  // and alignment
+  static_assert(kOffScales % 16 == 0, "bulk copies");
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -167,7 +172,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
 // sees alone (the first `seen` from the item's first tile on, whose entry is
 // `entry`), from its reference m and inv = 1 / sum - if such a value stands among
 // the others of the block's tiles, up to token `end`.  to: its D outputs, T or fp32.
-template <typename T, int D>
+template <typename T, int D, int SC>
 __device__ __forceinline__ void fix_row(const pf::Params& p, int entry, int seen, int end, int head,
                                      int64_t q_row, float scale, float m, float inv, char* to,
                                      bool part) {
@@ -210,6 +215,10 @@ __device__ __forceinline__ void fix_row(const pf::Params& p, int entry, int seen
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if constexpr (SC != kScaleNone) {
+      const int64_t at = (int64_t)(entry + t / kPageSize) * p.num_kv_heads + head;
+      s *= __ldg(p.k_scales + (SC == kScalePerToken ? at * kPageSize + t % kPageSize : at));
+    }
     const float w = dev::fast_exp2(fmaf(s, scale, -m));
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = fmaf(w, v[i], o[i]);
@@ -224,7 +233,14 @@ __device__ __forceinline__ void fix_row(const pf::Params& p, int entry, int seen
   }
 }
 
-template <typename T, int D>
+// SC: K's elements are their scales short (an E4M3 cache's, kScalePerToken or
+// kScalePerBlock): the scales multiply the scores, whose precision lse has.  Per token
+// they come through a ring of their own; per block, a group of 16 columns, they join
+// the factors of its maximum and exponents, read a tile ahead.  (16 requests of 500
+// rows behind 1024-8192, 64 / 8 heads: 1236 us per token, 1104 per block, for 1070
+// with the scales multiplied into K's elements, whose rounding to bf16 then cost
+// lse 2^-9 of the logits unless they were powers of two.)
+template <typename T, int D, int SC>
 __global__ void __launch_bounds__(pf::kThreads, 1)
     fa_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap kv_map,
@@ -250,6 +266,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
   uint64_t* o_empty = q_full + 12;
   uint64_t* v_there = q_full + 14;
   uint64_t* v_clean = q_full + 15;
+  uint64_t* sc_full = q_full + 16;
+  uint64_t* sc_empty = sc_full + S::kScaleSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffTmem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int first = p.cta_offsets[blockIdx.x], last = p.cta_offsets[blockIdx.x + 1];
@@ -271,6 +289,10 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     }
     dev::mbar_init(dev::smem_addr(v_there), 1);
     dev::mbar_init(dev::smem_addr(v_clean), 1);
+    for (int i = 0; i < S::kScaleSlots; ++i) {
+      dev::mbar_init(dev::smem_addr(&sc_full[i]), 1);
+      dev::mbar_init(dev::smem_addr(&sc_empty[i]), 8);
+    }
     dev::fence_barrier_init();
   }
   if (warp == 8) {
@@ -369,11 +391,30 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
       // ring could not tell a fill from the one two before)
       int n = 0;       // ring slots up to the item's end
       int ragged = 0;  // such items so far
+      int sn = 0;      // SC: tiles so far
       for (int it = first; it < last; ++it) {
         const Item w = Item::load(p.items, it);
         const int last_block = w.tokens > block_tokens ? 1 : 0;
         const int keys = w.keys(last_block, block_tokens), all = w.tiles(last_block, block_tokens);
         n += 2 * all;
+        if constexpr (SC == kScalePerToken) {  // the item's K scales, a tile a slot
+          const int pages = (min(keys, w.t1 * kTok) + kPageSize - 1) / kPageSize;
+          for (int j = 0; j < all; ++j, ++sn) {
+            const int slot = sn % S::kScaleSlots, page = (w.t0 + j) * kPages + lane;
+            const uint32_t full = dev::smem_addr(&sc_full[slot]);
+            dev::mbar_wait(dev::smem_addr(&sc_empty[slot]),
+                           (uint32_t)(((sn / S::kScaleSlots) & 1) ^ 1), aborted, p.err);
+            const int there = min(kPages, pages - (w.t0 + j) * kPages);
+            if (lane == 0) dev::mbar_arrive_expect_tx(full, there * kPageSize * 4);
+            __syncwarp();
+            if (lane < there)
+              dev::bulk_load(sbase + S::kOffScales + slot * (kTok * 4) + lane * (kPageSize * 4),
+                             p.k_scales + ((int64_t)(w.entry + page) * p.num_kv_heads + w.head) *
+                                              kPageSize,
+                             kPageSize * 4, full);
+            __syncwarp();
+          }
+        }
         if (!w.ragged(keys, all)) continue;
         const int tail = keys % kTok, rows = kPageSize - tail % kPageSize;
         const uint32_t v_addr = sbase + S::kOffRing + (n - 1) % kSlots * S::kSlotBytes;
@@ -492,9 +533,30 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     const uint32_t tS = tmem + X * 128 + lane_off, tO = tmem + 256 + X * 128 + lane_off;
     const int tok = X * block_tokens + r / p.group, g = r % p.group;
     int tile_n = 0, item_n = 0;
+    int sn = 0;  // SC: tiles so far, of all blocks
+    auto scales_full = [&] {
+      dev::mbar_wait(dev::smem_addr(&sc_full[sn % S::kScaleSlots]),
+                     (uint32_t)((sn / S::kScaleSlots) & 1), aborted, p.err);
+    };
+    auto scales_read = [&] {
+      dev::release_stage(dev::smem_addr(&sc_empty[sn % S::kScaleSlots]), lane);
+      ++sn;
+    };
+    // SC: slots of tiles that this block has no part in are given back unread
+    auto skip_scales = [&](const Item& w, int from) {
+      const int all =
+          SC == kScalePerToken ? w.tiles(w.tokens > block_tokens ? 1 : 0, block_tokens) : 0;
+      for (int j = from; j < all; ++j) {
+        scales_full();
+        scales_read();
+      }
+    };
     for (int it = first; it < last; ++it) {
       const Item w = Item::load(p.items, it);
-      if (X * block_tokens >= w.tokens) continue;
+      if (X * block_tokens >= w.tokens) {
+        skip_scales(w, 0);
+        continue;
+      }
       const int tiles = w.tiles(X, block_tokens);
       // keys this row sees, from the item's first tile on; the warp's fewest
       const int seen = w.pos0 + tok + 1 - w.t0 * kTok;
@@ -503,7 +565,17 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
       const float scale =
           fmaxf(p.head_k_scales ? p.scale * __ldg(p.head_k_scales + w.head) : p.scale, 1.2e-38f);
       float m = -INFINITY, d = 0.f;
+      // per block: lane l holds the scale of the tile's page l % 8, read a tile ahead
+      auto block_scale = [&](int j) {
+        const int page = (w.t0 + j) * kPages + lane % kPages;
+        return j < tiles && page * kPageSize < w.keys(X, block_tokens)
+                   ? __ldg(p.k_scales + (int64_t)(w.entry + page) * p.num_kv_heads + w.head)
+                   : 1.f;
+      };
+      float next_scale = SC == kScalePerBlock ? block_scale(0) : 1.f;
       for (int j = 0; j < tiles; ++j, ++tile_n) {
+        const float page_scale = next_scale;
+        if constexpr (SC == kScalePerBlock) next_scale = block_scale(j + 1);
         dev::mbar_wait(dev::smem_addr(&s_full[X]), (uint32_t)(tile_n & 1), aborted, p.err);
         fence_after();
         float s[kTok];
@@ -518,6 +590,20 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(raw[c][i]);
           }
+        }
+        if constexpr (SC == kScalePerToken) {
+          scales_full();
+          const uint32_t at = sbase + S::kOffScales + sn % S::kScaleSlots * (kTok * 4);
+#pragma unroll
+          for (int i = 0; i < kTok / 4; ++i) {
+            float k[4];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(k[0]), "=f"(k[1]), "=f"(k[2]), "=f"(k[3])
+                         : "r"(at + i * 16));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[4 * i + e] *= k[e];
+          }
+          scales_read();
         }
         if (fewest < (j + 1) * kTok) {
           const int valid = seen - j * kTok;
@@ -534,8 +620,18 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           for (int i = 1; i < 15; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
           m8[k] = fmaxf(a, s[16 * k + 15]);
         }
-        const float mt = scale * fmaxf(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[4]),
-                                       max3(m8[5], m8[6], m8[7]));
+        float by_page[8];  // factors of the 16-column groups
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          by_page[k] = scale;
+          if constexpr (SC == kScalePerBlock) {
+            by_page[k] = fmaxf(scale * __shfl_sync(0xffffffffu, page_scale, k), 1.2e-38f);
+            m8[k] *= by_page[k];
+          }
+        }
+        const float mt = (SC == kScalePerBlock ? 1.f : scale) *
+                         fmaxf(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[4]),
+                               max3(m8[5], m8[6], m8[7]));
         // the reference moves only when the maximum passes it by more than 2^8
         const bool rebase = mt > m + kRescaleAbove;
         const float m_new = rebase ? mt : m;
@@ -559,7 +655,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           m = m_new;
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        const uint64_t scale2 = f2(scale, scale), neg_m2 = f2(-ref, -ref);
+        const uint64_t neg_m2 = f2(-ref, -ref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < kTok / 32; ++c) {
@@ -567,7 +663,9 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float x0, x1;
-            f2_split(fma2(f2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), scale2, neg_m2), x0, x1);
+            const float factor = by_page[2 * c + i / 8];
+            f2_split(fma2(f2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), f2(factor, factor),
+                          neg_m2), x0, x1);
             const float a0 = dev::fast_exp2(x0), a1 = dev::fast_exp2(x1);
             pk[i] = mma::pack2(a0, a1, kBf16);
             acc[i % 4] = add2(acc[i % 4], f2(a0, a1));
@@ -584,6 +682,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), lo, hi);
         d += lo + hi;
       }
+      skip_scales(w, tiles);
       // ---- the row's output
       if (tiles > 0) {
         dev::mbar_wait(dev::smem_addr(&o_full[X]), (uint32_t)(item_n & 1), aborted, p.err);
@@ -691,7 +790,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           char* to = w.slot < 0 ? reinterpret_cast<char*>(static_cast<T*>(p.o) +
                                                           (row_l * p.num_qo_heads + head) * D)
                                 : reinterpret_cast<char*>(p.part_o + part_l * D);
-          fix_row<T, D>(p, w.entry + w.t0 * kPages,
+          fix_row<T, D, SC>(p, w.entry + w.t0 * kPages,
                         max(0, min(w.pos0 + t + 1 - w.t0 * kTok, end)), end, w.head,
                         row_l * p.q_token + head * p.q_head, scale, ml == -INFINITY ? 0.f : ml, il,
                         to, w.slot >= 0);

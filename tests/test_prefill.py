@@ -9,9 +9,9 @@ exact products in fp32, in the tensor cores' order: its error is held to
 D 2^-23 times the sum of the products' magnitudes (2^-24 an addition, twice that where
 additions truncate), plus 2^-21 |logit| for the scaling, the exponential (2^-22)
 and the sum; that moves every weight by twice its value relative (numerator and
-denominator), and lse once.  An E4M3 cache's elements are exact under a scale per
-tensor, head or power of two; otherwise bf16's half step on K moves a logit by HALF
-times the sum of magnitudes, and one on V adds HALF sum_t w_t |v_t|.
+denominator), and lse once.  An E4M3 cache's codes are exact in bf16 and K's scales
+multiply the logits; V's elements under a scale per token or block that is no power of
+two are rounded: HALF sum_t w_t |v_t| more.
 """
 import ctypes
 
@@ -65,7 +65,7 @@ class Batch:
 
     def check(self, o, lse, scale_of=None, inexact=False, sm_scale=None, rows=None):
         """o and lse against the definition; scale_of(half, pages, slots): [tokens,
-        hkv] factors of the elements; inexact: elements rounded to bf16."""
+        hkv] factors of the elements; inexact: V's elements rounded to bf16."""
         half, d, G = HALF[self.q_dtype], self.d, self.hq // self.hkv
         sm = d ** -0.5 if sm_scale is None else sm_scale
         kv = self.kv.double()
@@ -91,7 +91,7 @@ class Batch:
                 ref = torch.logsumexp(s, -1)
                 w = (s - ref[:, None]).exp()
                 want, mag = w @ vh, w @ vh.abs()
-                err = size * (d * 2.0 ** -23 + (half if inexact else 0)) + 2.0 ** -21 * (1 + size)
+                err = size * d * 2.0 ** -23 + 2.0 ** -21 * (1 + size)
                 bound = (half * (2 if inexact else 1) + 2 * err)[:, None] * mag + half * want.abs()
                 bound = bound * 1.001 + 1e-30
                 if self.q_dtype == F16:
