@@ -122,7 +122,8 @@ def test_types(lib, cuda, dtype, d, scales):
     ([5000, 4100], 8, 700, 700, "ties"),     # the last tokens alone
     ([70000], 1, 2000, 1, "ties"),
     ([130000], 1, 100000, 5, "random"),      # keys beyond a CTA's shared memory
-    ([3000] * 40, 8, 1000, 64, "zeros")])    # a CTA each
+    ([3000] * 40, 8, 1000, 64, "zeros"),     # a CTA each
+    ([12000] + [40] * 79, 8, 30, 3, "ties")])  # a CTA each, keys beyond its shared memory
 def test_long(lib, cuda, lengths, hkv, keep, recent, weights):
     Cache(lengths, hkv, 64, BF16, seed=3, weights=weights).check(lib, keep, recent)
 
@@ -268,6 +269,32 @@ def test_a_request_within_a_budget(lib, cuda, kv_dtype):
         n.q = ap.run(k, v, n.kv, q=q)
         o, lse = dec.run(n.q, n.kv)
     n.check(o, None, of, inexact=True)  # the decode kernel rounds weights and their sum
+
+
+@pytest.mark.gpu
+def test_cache_beyond_32_bits(lib, cuda):
+    """Prefill, weights and eviction over pages behind 2^31 elements: bit for bit what
+    they give in a small cache."""
+    b = Batch([300], [70], 8, 8, 128, seed=31, garbage=0.0)
+    few = torch.tensor([0, 1], dtype=torch.int32)
+    pages = 70_000
+    big = torch.empty((pages, 2, 16, 8, 128), dtype=BF16, device=cuda)
+    assert big.numel() > 2 ** 31
+    high = pages - 1 - torch.arange(len(b.ids), dtype=torch.int32, device=cuda)
+    big[high.long()] = b.kv[b.indices.long()]
+    w = [torch.rand((n, 8, 16), device=cuda) for n in (b.num_pages, pages)]
+    w[1][high.long()] = w[0][b.indices.long()]
+    out = []
+    for kv, ids, wt in ((b.kv.clone(), b.indices, w[0]), (big, high, w[1])):
+        o, lse = lib.plan_prefill(b.indptr, ids, b.last, b.qo, 8, 8, 128, 16).run(b.q, kv)
+        for rows in (b.qo, few):  # the tcgen05 kernel, and the one of few columns
+            n = int(rows[-1])
+            lib.plan_weights(b.indptr, ids, b.last, rows, 8, 8, 128, 16).run(
+                b.q[b.T - n:].contiguous(), kv, lse[b.T - n:].contiguous(), wt)
+        lib.plan_evict(b.indptr, ids, b.last, 100, 8, 128, 16, recent=9).run(kv, wt)
+        out.append((o, lse, kv[ids.long()], wt[ids.long()]))
+    for x, y in zip(*out):
+        assert torch.equal(x, y)
 
 
 # ---------------------------------------------------------------- refusals

@@ -272,6 +272,24 @@ def test_stream_and_graph(lib, cuda):
 
 
 @pytest.mark.gpu
+def test_two_plans_on_two_streams(lib, cuda):
+    """Runs in flight together, each with a plan (and workspace) of its own; outputs and
+    workspaces made for those streams."""
+    b = [Batch([9000, 40], [5, 300], 8, 2, 128, seed=20), Batch([0, 7000], [700, 3], 8, 2, 128, seed=21)]
+    want = [x.plan(lib).run(x.q, x.kv) for x in b]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in b]
+    plans = [x.plan(lib, stream=st) for x, st in zip(b, streams)]
+    got = []
+    for _ in range(5):
+        got.append([p.run(x.q, x.kv, stream=st) for x, p, st in zip(b, plans, streams)])
+    torch.cuda.synchronize()
+    for pair in got:
+        for (o, lse), (ow, lw) in zip(pair, want):
+            assert torch.equal(o, ow) and torch.equal(lse, lw)
+
+
+@pytest.mark.gpu
 def test_bad_page_ids_read_zeros(lib, cuda):
     b = Batch([0, 200], [40, 150], 8, 2, 128, seed=13)
     good, _ = b.plan(lib).run(b.q, b.kv)
