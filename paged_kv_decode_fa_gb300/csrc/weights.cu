@@ -241,7 +241,8 @@ struct Worker {
     // s[0], s[1]: token n, columns 2c, + 1; s[2], s[3]: token n + 8
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int last = before + ((2 * c + e) >> p.group_log2);
+      // (a column behind the last sees nothing: its zeros times an infinite K are NaN)
+      const int last = 2 * c + e < columns ? before + ((2 * c + e) >> p.group_log2) : -1;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         if (pos + 8 * t <= last) sum[t] += dev::fast_exp2(fmaf(s[2 * t + e], scale[t], -lse[e]));

@@ -196,6 +196,19 @@ def test_e4m3(lib, cuda, mode, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_behind_the_last_token_are_ignored(lib, cuda, d):
+    b = Batch([0, 40, 300], [70, 1, 130], 16, 4, d, BF16, E4M3, seed=9)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    s = [torch.rand((b.num_pages, 4, 16), generator=g, device="cuda") * 0.2 + 0.001 for _ in range(2)]
+    unused = (b.kv.view(torch.uint8)[:, 0, :, :, 0] == 127).transpose(1, 2)
+    for x in s:
+        x[unused] = float("nan")
+    o, lse = b.plan(lib).run_token_scales(b.q, b.kv, *s)
+    b.check(o, lse, lambda half, page, slot: s[half].double()[page, :, slot], True)
+
+
+@pytest.mark.gpu
 def test_scales_of_zero(lib, cuda):
     """A scale of 0: all logits equal (K), all values 0 (V)."""
     b = Batch([20], [30], 4, 1, 128, BF16, E4M3, seed=8)

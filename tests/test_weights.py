@@ -153,6 +153,39 @@ def test_rows_before_the_first_token_and_rows_of_minus_infinity(lib, cuda):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("hq,hkv,d,ctx,new", [(1, 1, 64, 50, 1), (4, 2, 128, 50, 1), (8, 2, 64, 37, 1),
+                                              (8, 2, 128, 100, 5), (4, 4, 64, 300, 33)])
+def test_logits_of_minus_infinity_weigh_nothing(lib, cuda, dtype, hq, hkv, d, ctx, new):
+    """An infinite element of K against negative elements of q: the token's weights are
+    0, whatever number of columns a tile is filled up with."""
+    b = Batch([ctx], [new], hq, hkv, d, dtype, seed=31)
+    b.q[..., 3] = -1
+    page = b.indices.long()[1]
+    b.kv[page, 0, 5, :, 3] = float("inf")
+    lse, w = exact_lse(b), fresh(b)
+    assert torch.isfinite(lse).all()
+    before = w.clone()
+    plan(b, lib).run(b.q, b.kv, lse, w)
+    assert torch.equal(w[page, :, 5], before[page, :, 5])
+    check(b, w, before, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [[1, 1, 1], [70, 2, 130]])
+def test_scales_behind_the_last_token_are_ignored(lib, cuda, new):
+    b = Batch([0, 40, 300], new, 8, 2, 128, BF16, E4M3, seed=32)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    s = torch.rand((b.num_pages, 2, 16), generator=g, device="cuda") * 0.1 + 0.001
+    s[(b.kv.view(torch.uint8)[:, 0, :, :, 0] == 127).transpose(1, 2)] = float("nan")
+    of = lambda page, slot: s.double()[page, :, slot]  # noqa: E731
+    lse, w = exact_lse(b, of), fresh(b)
+    before = w.clone()
+    plan(b, lib).run_token_scales(b.q, b.kv, lse, w, s)
+    check(b, w, before, lse, of)
+
+
+@pytest.mark.gpu
 def test_strides_stream_and_graph(lib, cuda):
     b = Batch([0, 500], [30, 20], 16, 4, 128, seed=6)
     lse = exact_lse(b, sm=0.1)
