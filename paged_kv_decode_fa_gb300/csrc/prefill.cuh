@@ -41,6 +41,12 @@
 // the tile's P V (0 * NaN would be NaN).  For tokens that only some of the rows see
 // there is fix_row.
 //
+// Roundings.  Scores, sums, O and partial states are fp32; the weights are rounded to
+// q's 16 bits, the operand type that P V takes, while their sum takes them unrounded
+// (lse has fp32's precision).  Half a step a weight, independent: over 9000 keys the
+// output is 2.9e-4 off in f16 (rms; 2.1e-4 by its own rounding alone), 2.3e-3 in bf16
+// (1.7e-3).  Weights in two terms would halve the rate of P V.
+//
 // What bounds it.  Long prompts: the tensor cores under the power limit.  8192 rows on a
 // context of 24576 (32 / 8 heads, head_dim 128, bf16): 2.48-2.53 ms = 1.52-1.55
 // PFLOP/s, 0.87 of what cuBLAS holds for seconds (0.77 of its burst).  A
