@@ -294,6 +294,14 @@ def _stream_handle(stream) -> int | None:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _as_stream(stream) -> torch.cuda.Stream:
+    """A torch stream, or one of a raw handle."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    # (an ExternalStream of the null handle would be a new stream)
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+
+
 def _empty(shape, dtype, device, stream, **kw) -> torch.Tensor:
     """A tensor that a call running on `stream` (None: the current one) writes.
     It comes from that stream's memory: what the current stream has freed may
@@ -301,10 +309,7 @@ def _empty(shape, dtype, device, stream, **kw) -> torch.Tensor:
     caller gets it, is done with it too."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device, **kw)
-    if not isinstance(stream, torch.cuda.Stream):
-        # (an ExternalStream of the null handle would be a new stream)
-        stream = (torch.cuda.ExternalStream(int(stream)) if int(stream)
-                  else torch.cuda.default_stream())
+    stream = _as_stream(stream)
     current = torch.cuda.current_stream()
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device, **kw)
@@ -1511,8 +1516,9 @@ def _plan_workspace(workspace, indices, size, stream) -> torch.Tensor:
 class EvictPlan:
     """A planned eviction.  indptr, indices and last_page_len describe the batch
     after it (indices where the plan's are), freed [n] the page ids that it no longer
-    needs; indices and freed are gathered from the plan's when first asked for.
-    Keeps the index tensor and the workspace alive."""
+    needs.  Both were taken from the page table as it was planned, on the plan's
+    stream: writing the table later does not change them.  Keeps the index tensor
+    and the workspace alive."""
 
     def __init__(self, handle, indices, workspace, kv_dtype, shape, after):
         self._h = handle
@@ -1521,23 +1527,7 @@ class EvictPlan:
         self.batch, self.num_kv_heads, self.head_dim, self.page_size = shape
         self._device = workspace.get_device()
         self._page_shape = (2, self.page_size, self.num_kv_heads, self.head_dim)
-        self.indptr, self.last_page_len, *self._entries = after
-        self._gathered = [None, None]
-
-    def _pages(self, which):
-        if self._gathered[which] is None:
-            table = self._keep[0]
-            t = table[torch.from_numpy(self._entries[which]).to(table.device)]
-            self._gathered[which] = t if t.is_cuda else t.pin_memory()
-        return self._gathered[which]
-
-    @property
-    def indices(self) -> torch.Tensor:
-        return self._pages(0)
-
-    @property
-    def freed(self) -> torch.Tensor:
-        return self._pages(1)
+        self.indptr, self.last_page_len = after
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -1595,6 +1585,22 @@ def _pages_after(indptr, last, kept, page_size):
             np.flatnonzero(~here))
 
 
+def _take_pages(table, stay, free, stream):
+    """The page ids at the entries that stay and at those that are freed, where `table`
+    is, as they stand when the work before on `stream` is done."""
+    order = torch.from_numpy(np.concatenate([stay, free]).astype(np.int32))
+    if not table.is_cuda:
+        ids = table[order.long()].pin_memory()
+    elif stream is None:
+        ids = table.index_select(0, order.to(table.device))
+    else:
+        stream = _as_stream(stream)
+        ids = _empty(order.shape, table.dtype, table.device, stream)
+        with torch.cuda.stream(stream):
+            torch.index_select(table, 0, order.to(table.device), out=ids)
+    return ids[:len(stay)], ids[len(stay):]
+
+
 def plan_evict(indptr, indices: torch.Tensor, last_page_len, keep, num_kv_heads: int,
                head_dim: int, page_size: int, *, recent=0, kv_data_type=torch.bfloat16,
                workspace: torch.Tensor | None = None, stream=None) -> EvictPlan:
@@ -1626,9 +1632,11 @@ def plan_evict(indptr, indices: torch.Tensor, last_page_len, keep, num_kv_heads:
         ctypes.byref(handle)), "fa_evict_plan")
     ptr, last, stay, free = _pages_after(np.asarray(indptr_h), np.asarray(last_h)[:B], budgets[0],
                                          page_size)
-    return EvictPlan(handle.value, indices, workspace, kv_data_type,
+    plan = EvictPlan(handle.value, indices, workspace, kv_data_type,
                      (B, num_kv_heads, head_dim, page_size),
-                     (torch.from_numpy(ptr), torch.from_numpy(last), stay, free))
+                     (torch.from_numpy(ptr), torch.from_numpy(last)))
+    plan.indices, plan.freed = _take_pages(indices.view(-1), stay, free, stream)
+    return plan
 
 
 class BatchDecodeWithPagedKVCacheWrapper:
