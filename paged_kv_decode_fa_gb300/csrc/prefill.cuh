@@ -63,8 +63,12 @@
 // lane waits for its Q); K and V loaded by a warp each, boxes of 4 KB, half the
 // bytes (no change: the copies are not what it waits for).
 //
-// Every wait is bounded (2 s); a wait that runs out sets bit 1 of the device-check
-// word and the CTA drains.
+// Every wait is bounded: it runs out where for 2 s no softmax warp has got on (each
+// counts its tiles, and the tokens of a row that it computes again, in shared memory),
+// sets bit 1 of the device-check word and the CTA drains.  (A bound on the time alone
+// would also end waits that are merely long: 32 rows computed again over 150000 tokens
+// each, or a block or the ragged-end warp without work through millions of tokens of
+// other items.)
 #pragma once
 
 #include <cuda.h>
@@ -157,11 +161,42 @@ struct Smem {
   static constexpr int kScaleSlots = 3;
   static constexpr int kNumBars = 2 * kSlots + 16 + 2 * kScaleSlots;
   static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
+  static constexpr int kOffProgress = kOffTmem + 4;      // what the softmax warps count
   static constexpr int kOffScales = kOffTmem + 16;       // SC: K scales of a tile's tokens
   static constexpr int kBytes = kOffScales + kScaleSlots * kTok * 4 + 1024;  // and alignment
   static_assert(kOffScales % 16 == 0, "bulk copies");
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
+
+// What the CTA's softmax warps have counted in all (kOffProgress), and one more.
+__device__ __forceinline__ uint32_t progress_of(uint32_t count) {
+  uint32_t n;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(n) : "r"(count) : "memory");
+  return n;
+}
+__device__ __forceinline__ void count_on(uint32_t count) {
+  asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(count) : "memory");
+}
+
+// dev::mbar_wait with a bound on standstill instead of time: it runs out where
+// kWaitTimeoutNs pass and no softmax warp has counted on.
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, bool& aborted, int* err,
+                                          uint32_t count) {
+  if (aborted || dev::mbar_try_wait(bar, parity)) return;
+  unsigned long long t0 = dev::global_timer_ns();
+  uint32_t before = progress_of(count);
+  while (!dev::mbar_try_wait(bar, parity)) {
+    if (dev::global_timer_ns() - t0 <= dev::kWaitTimeoutNs) continue;
+    const uint32_t now = progress_of(count);
+    if (now == before) {
+      aborted = true;
+      atomicOr(err, 2);
+      return;
+    }
+    before = now;
+    t0 = dev::global_timer_ns();
+  }
+}
 
 }  // namespace pf
 
@@ -181,7 +216,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
 template <typename T, int D, int SC>
 __device__ __forceinline__ void fix_row(const pf::Params& p, int entry, int seen, int end, int head,
                                      int64_t q_row, float scale, float m, float inv, char* to,
-                                     bool part) {
+                                     bool part, uint32_t count) {
   constexpr int V = D / 32;  // dims of a lane
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   const int lane = threadIdx.x & 31;
@@ -211,6 +246,7 @@ __device__ __forceinline__ void fix_row(const pf::Params& p, int entry, int seen
   read(static_cast<const T*>(p.q) + q_row + lane * V, q);
 #pragma unroll 1
   for (int t = 0; t < seen; ++t) {
+    if (t % 64 == 0 && lane == 0) pf::count_on(count);  // others wait for this warp
     const T* k = row_of(t);
     float s = 0.f, v[V] = {};
     if (k != nullptr) {
@@ -260,7 +296,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
   constexpr int kSlots = S::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (dev::smem_addr(smem_raw) & 1023u)) & 1023u);
-  const uint32_t sbase = dev::smem_addr(smem);
+  const uint32_t sbase = dev::smem_addr(smem), count = sbase + S::kOffProgress;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = bars + kSlots;
@@ -299,6 +335,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
       dev::mbar_init(dev::smem_addr(&sc_full[i]), 1);
       dev::mbar_init(dev::smem_addr(&sc_empty[i]), 8);
     }
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(count), "r"(0) : "memory");
     dev::fence_barrier_init();
   }
   if (warp == 8) {
@@ -349,8 +386,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const int s = n % kSlots;
             const uint32_t full = dev::smem_addr(&kv_full[s]);
-            dev::mbar_wait(dev::smem_addr(&kv_empty[s]), (uint32_t)(((n / kSlots) & 1) ^ 1),
-                           aborted, p.err);
+            pf::mbar_wait(dev::smem_addr(&kv_empty[s]), (uint32_t)(((n / kSlots) & 1) ^ 1),
+                          aborted, p.err, count);
             if (lane == 0) dev::mbar_arrive_expect_tx(full, S::kSlotBytes);
             __syncwarp();
             if (lane < kPages * S::kHalves)
@@ -377,7 +414,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           for (int X = 0; X < 2; ++X) {
             if (w.tiles(X, block_tokens) == 0) continue;
             const uint32_t full = dev::smem_addr(&q_full[X]);
-            dev::mbar_wait(dev::smem_addr(&q_empty[X]), (uint32_t)((n[X] & 1) ^ 1), aborted, p.err);
+            pf::mbar_wait(dev::smem_addr(&q_empty[X]), (uint32_t)((n[X] & 1) ^ 1), aborted, p.err,
+                          count);
             dev::mbar_arrive_expect_tx(full, S::kQBytes);
             for (int h = 0; h < S::kHalves; ++h)
               tma_load_3d(sbase + X * S::kQBytes + h * (kRows * 128), &q_map, h * 64,
@@ -408,8 +446,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           for (int j = 0; j < all; ++j, ++sn) {
             const int slot = sn % S::kScaleSlots, page = (w.t0 + j) * kPages + lane;
             const uint32_t full = dev::smem_addr(&sc_full[slot]);
-            dev::mbar_wait(dev::smem_addr(&sc_empty[slot]),
-                           (uint32_t)(((sn / S::kScaleSlots) & 1) ^ 1), aborted, p.err);
+            pf::mbar_wait(dev::smem_addr(&sc_empty[slot]),
+                          (uint32_t)(((sn / S::kScaleSlots) & 1) ^ 1), aborted, p.err, count);
             const int there = min(kPages, pages - (w.t0 + j) * kPages);
             if (lane == 0) dev::mbar_arrive_expect_tx(full, there * kPageSize * 4);
             __syncwarp();
@@ -424,7 +462,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         if (!w.ragged(keys, all)) continue;
         const int tail = keys % kTok, rows = kPageSize - tail % kPageSize;
         const uint32_t v_addr = sbase + S::kOffRing + (n - 1) % kSlots * S::kSlotBytes;
-        dev::mbar_wait(dev::smem_addr(v_there), (uint32_t)(ragged++ & 1), aborted, p.err);
+        pf::mbar_wait(dev::smem_addr(v_there), (uint32_t)(ragged++ & 1), aborted, p.err, count);
         for (int e = lane; e < rows * 8 * S::kHalves; e += 32) {
           const int r = tail + e / (8 * S::kHalves), c = e % (8 * S::kHalves);
           const uint32_t a = v_addr + (c / 8) * S::kHalf + r * 128 + (c % 8) * 16;
@@ -453,7 +491,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         const bool ragged = w.ragged(keys, all);
         int slot = n % kSlots, phase = (n / kSlots) & 1;  // of K(j), then V(j), ...
         auto full = [&](int s, int ph) {
-          dev::mbar_wait(dev::smem_addr(&kv_full[s]), (uint32_t)ph, aborted, p.err);
+          pf::mbar_wait(dev::smem_addr(&kv_full[s]), (uint32_t)ph, aborted, p.err, count);
         };
         auto qk = [&](int X, int j, int s) {
           const uint64_t k_desc = smem_desc(sbase + S::kOffRing + s * S::kSlotBytes, 16, 1024);
@@ -469,7 +507,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
 #pragma unroll
         for (int X = 0; X < 2; ++X) {
           if (tiles[X] == 0) continue;
-          dev::mbar_wait(dev::smem_addr(&q_full[X]), (uint32_t)(item_n[X] & 1), aborted, p.err);
+          pf::mbar_wait(dev::smem_addr(&q_full[X]), (uint32_t)(item_n[X] & 1), aborted, p.err,
+                        count);
           fence_after();
           qk(X, 0, slot);
         }
@@ -490,7 +529,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           const uint64_t v_desc =
               smem_desc(sbase + S::kOffRing + v_slot * S::kSlotBytes, S::kHalf, 1024);
           if (ragged && j == all - 1)
-            dev::mbar_wait(dev::smem_addr(v_clean), (uint32_t)(cleared++ & 1), aborted, p.err);
+            pf::mbar_wait(dev::smem_addr(v_clean), (uint32_t)(cleared++ & 1), aborted, p.err,
+                          count);
           advance();  // to K(j + 1)
           const int k_slot = slot, k_phase = phase;
           advance();  // to V(j + 1)
@@ -498,12 +538,12 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           for (int X = 0; X < 2; ++X) {
             if (j >= tiles[X]) continue;
             if (j == 0)  // the output of the block's item before has been read
-              dev::mbar_wait(dev::smem_addr(&o_empty[X]), (uint32_t)((item_n[X] & 1) ^ 1), aborted,
-                             p.err);
+              pf::mbar_wait(dev::smem_addr(&o_empty[X]), (uint32_t)((item_n[X] & 1) ^ 1), aborted,
+                            p.err, count);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {  // 64 tokens: 32 columns of P
-              dev::mbar_wait(dev::smem_addr(&p_full[2 * X + half]), (uint32_t)(tile_n[X] & 1),
-                             aborted, p.err);
+              pf::mbar_wait(dev::smem_addr(&p_full[2 * X + half]), (uint32_t)(tile_n[X] & 1),
+                            aborted, p.err, count);
               fence_after();
               umma4_ts(tmem + 256 + X * 128, tmem + X * 128 + half * 32,
                        v_desc + half * (64 * 128 / 16), kIdescPV, j > 0 || half > 0);
@@ -541,8 +581,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     int tile_n = 0, item_n = 0;
     int sn = 0;  // SC: tiles so far, of all blocks
     auto scales_full = [&] {
-      dev::mbar_wait(dev::smem_addr(&sc_full[sn % S::kScaleSlots]),
-                     (uint32_t)((sn / S::kScaleSlots) & 1), aborted, p.err);
+      pf::mbar_wait(dev::smem_addr(&sc_full[sn % S::kScaleSlots]),
+                    (uint32_t)((sn / S::kScaleSlots) & 1), aborted, p.err, count);
     };
     auto scales_read = [&] {
       dev::release_stage(dev::smem_addr(&sc_empty[sn % S::kScaleSlots]), lane);
@@ -582,7 +622,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
       for (int j = 0; j < tiles; ++j, ++tile_n) {
         const float page_scale = next_scale;
         if constexpr (SC == kScalePerBlock) next_scale = block_scale(j + 1);
-        dev::mbar_wait(dev::smem_addr(&s_full[X]), (uint32_t)(tile_n & 1), aborted, p.err);
+        pf::mbar_wait(dev::smem_addr(&s_full[X]), (uint32_t)(tile_n & 1), aborted, p.err, count);
         fence_after();
         float s[kTok];
         {
@@ -687,11 +727,12 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         float lo, hi;
         f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), lo, hi);
         d += lo + hi;
+        if (lane == 0) count_on(count);
       }
       skip_scales(w, tiles);
       // ---- the row's output
       if (tiles > 0) {
-        dev::mbar_wait(dev::smem_addr(&o_full[X]), (uint32_t)(item_n & 1), aborted, p.err);
+        pf::mbar_wait(dev::smem_addr(&o_full[X]), (uint32_t)(item_n & 1), aborted, p.err, count);
         fence_after();
       }
       const bool ok = tok < w.tokens;
@@ -799,7 +840,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           fix_row<T, D, SC>(p, w.entry + w.t0 * kPages,
                         max(0, min(w.pos0 + t + 1 - w.t0 * kTok, end)), end, w.head,
                         row_l * p.q_token + head * p.q_head, scale, ml == -INFINITY ? 0.f : ml, il,
-                        to, w.slot >= 0);
+                        to, w.slot >= 0, count);
         }
       }
       if (ok) {
