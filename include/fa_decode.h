@@ -755,6 +755,9 @@ int fa_prefill_plan(const int32_t* indptr_host, const int32_t* indices_dev,
  *  o          [rows, num_qo_heads, head_dim] contiguous, q dtype, device, 32-byte
  *             aligned; not q itself.
  *  lse        [rows, num_qo_heads] float32, device, or NULL.
+ * Scores, sums and lse are fp32.  The softmax weights enter the product with V rounded
+ * to q's type (half a step of each), and o once more; an f16 weight below 2^-21 of the
+ * row's largest is subnormal, and what it adds may be 2^-32 |v| off.
  * One to three kernels on cuda_stream, no allocation, no synchronisation: it can
  * be captured into a CUDA graph.  Results are bitwise reproducible for a plan.
  * Two runs that may be in flight together need two plans and workspaces.

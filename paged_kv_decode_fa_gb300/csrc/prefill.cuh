@@ -7,7 +7,8 @@
 // c = sm_scale log2 e, with a running reference m: the largest score so far, moved
 // only when a tile's maximum passes it by more than 2^8 (an exact rescale of o and
 // of the sum), so that weights stay within 2^8 and the division at the end
-// removes m.  lse = (m + log2 sum) ln 2.
+// removes m.  (In f16 the reference stands 2^7 below that score: weights within 2^15.)
+// lse = (m + log2 sum) ln 2.
 //
 // Work.  An item is one kv head, up to 256 rows of one request and a range of
 // its 128-token tiles.  Rows are (token, query head of the group), a token's heads
@@ -45,7 +46,10 @@
 // q's 16 bits, the operand type that P V takes, while their sum takes them unrounded
 // (lse has fp32's precision).  Half a step a weight, independent: over 9000 keys the
 // output is 2.9e-4 off in f16 (rms; 2.1e-4 by its own rounding alone), 2.3e-3 in bf16
-// (1.7e-3).  Weights in two terms would halve the rate of P V.
+// (1.7e-3).  Weights in two terms would halve the rate of P V.  f16 has no weights
+// below its smallest subnormal, 2^-24: next to a reference 2^7 below the largest score
+// a weight is held to 2^-32 of the largest, and one below that is lost to the output,
+// however large its v - 2^-32 sum |v| in all (2^-25 with the reference at the score).
 //
 // What bounds it.  Long prompts: the tensor cores under the power limit.  8192 rows on a
 // context of 24576 (32 / 8 heads, head_dim 128, bf16): 2.44-2.57 ms = 1.50-1.58
@@ -92,7 +96,12 @@ constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kIssueRegs = 104;
 static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs,
               "a larger share would be waited for without end");
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleAbove = 8.f;             // log2 units
+// Log2 units: how far a maximum may pass the reference's score before that moves, and
+// how far the reference stands below its score (f16: 2^(8 + 7) and its rounding are in
+// range, and the smallest weights are as far from the subnormals' end as they can be).
+constexpr float kRescaleAbove = 8.f;
+template <typename T>
+constexpr float kBelowScore = std::is_same<T, __half>::value ? 7.f : 0.f;
 constexpr int kItemInts = 8;
 
 struct Params {
@@ -679,8 +688,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                          fmaxf(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[4]),
                                max3(m8[5], m8[6], m8[7]));
         // the reference moves only when the maximum passes it by more than 2^8
-        const bool rebase = mt > m + kRescaleAbove;
-        const float m_new = rebase ? mt : m;
+        const bool rebase = mt > m + (kRescaleAbove + kBelowScore<T>);
+        const float m_new = rebase ? mt - kBelowScore<T> : m;
         const float alpha = m == -INFINITY ? 0.f : dev::fast_exp2(m - m_new);
         if (j > 0 && __any_sync(0xffffffffu, rebase)) {
           // O holds the tiles before j
