@@ -241,8 +241,9 @@ struct Worker {
     // s[0], s[1]: token n, columns 2c, + 1; s[2], s[3]: token n + 8
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      // (a column behind the last sees nothing: its zeros times an infinite K are NaN)
-      const int last = 2 * c + e < columns ? before + ((2 * c + e) >> p.group_log2) : -1;
+      // a column behind the last, or whose row has an lse of -inf, adds nothing, whatever
+      // its score is (zeros times an infinite K are NaN, as may be a padded row's q)
+      const int last = lse[e] != INFINITY ? before + ((2 * c + e) >> p.group_log2) : -1;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         if (pos + 8 * t <= last) sum[t] += dev::fast_exp2(fmaf(s[2 * t + e], scale[t], -lse[e]));

@@ -51,7 +51,8 @@ struct Smem {
   // raw_full, raw_empty
   static constexpr int kNumBars = 2 * kQSlots + 4 + 8 + 2;
   static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
-  static constexpr int kBytes = kOffTmem + 16 + 1024;
+  static constexpr int kOffDead = kOffTmem + 16;  // [slot] a tile has columns that add nothing
+  static constexpr int kBytes = kOffDead + 4 * kQSlots + 1024;
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -160,11 +161,14 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
                                    : -INFINITY;
             if (lse[i] == INFINITY) lse[i] = -INFINITY;  // a row that saw nothing: weight 0
           }
+          const bool dead = __any_sync(0xffffffffu, lse[0] == -INFINITY || lse[1] == -INFINITY ||
+                                                        lse[2] == -INFINITY || lse[3] == -INFINITY);
           dev::mbar_wait(dev::smem_addr(&q_empty[s]), (uint32_t)(((n / kQSlots) & 1) ^ 1), aborted,
                          p.err);
           float* to = reinterpret_cast<float*>(smem + S::kOffLse) + s * kTok;
 #pragma unroll
           for (int i = 0; i < 4; ++i) to[lane + 32 * i] = lse[i];
+          if (lane == 0) *reinterpret_cast<int*>(smem + S::kOffDead + 4 * s) = dead;
           __syncwarp();
           if (lane == 0) {
             const uint32_t full = dev::smem_addr(&q_full[s]);
@@ -360,7 +364,8 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
           fence_after();
           ++cnt;
           const int lo = seen - t * kTok, hi = w.columns - t * kTok;
-          const bool whole = warp_seen <= t * kTok && hi >= kTok;
+          const bool whole = warp_seen <= t * kTok &&
+                             *reinterpret_cast<const int*>(smem + S::kOffDead + 4 * qs) == 0;
           // 16 columns at a time: the next ones' scores and lse on their way
           const uint32_t lse_at = sbase + S::kOffLse + qs * (kTok * 4);
           const int steps = min(kTok / 16, (hi + 15) / 16);
@@ -393,9 +398,12 @@ __global__ void __launch_bounds__(wt::threads(!std::is_same<T, KVT>::value), 1)
                 x0 = dev::fast_exp2(x0);
                 x1 = dev::fast_exp2(x1);
                 if (!all) {
+                  // (columns behind the last have a -lse of -inf too)
                   const int col = 16 * c + 2 * i;
-                  x0 = col >= lo && col < hi ? x0 : 0.f;
-                  x1 = col + 1 >= lo && col + 1 < hi ? x1 : 0.f;
+                  float n0, n1;
+                  f2_split(neg[c & 1][i], n0, n1);
+                  x0 = col >= lo && n0 != -INFINITY ? x0 : 0.f;
+                  x1 = col + 1 >= lo && n1 != -INFINITY ? x1 : 0.f;
                 }
                 acc[i % 4] = add2(acc[i % 4], f2(x0, x1));
               }
