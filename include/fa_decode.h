@@ -748,7 +748,7 @@ int fa_prefill_plan(const int32_t* indptr_host, const int32_t* indices_dev,
  *  q          [rows, num_qo_heads, head_dim] by address and strides (fa_rows,
  *             above; rows = qo_indptr[batch]), device: a slice of a fused
  *             projection needs no copy.  Strides of dims longer than one are
- *             positive.
+ *             positive and below 2^39.
  *  paged_kv, num_pages, sm_scale: as fa_decode_run.
  *  k_scale,   per-tensor scales of an E4M3 cache, 0 or positive; 1 for other kv
  *  v_scale    types (FA_ERR_INVALID_ARG otherwise).

@@ -408,10 +408,8 @@ int prefill_run(fa_prefill_plan_s* plan, int sc, const fa_rows* q, const void* p
                 const float* v_scales, void* o, float* lse, void* cuda_stream) {
   if (plan->rows == 0) return FA_OK;
   if (!q || !q->data || !paged_kv || !o || num_pages <= 0 || num_pages >= (1 << 30) ||
-      reinterpret_cast<uintptr_t>(paged_kv) % 16 || reinterpret_cast<uintptr_t>(q->data) % 16 ||
-      reinterpret_cast<uintptr_t>(o) % 32 || reinterpret_cast<uintptr_t>(lse) % 4 ||
-      q->token_stride % 8 || q->head_stride % 8 || (plan->rows > 1 && q->token_stride <= 0) ||
-      (plan->hq > 1 && q->head_stride <= 0))
+      reinterpret_cast<uintptr_t>(paged_kv) % 16 || reinterpret_cast<uintptr_t>(o) % 32 ||
+      reinterpret_cast<uintptr_t>(lse) % 4 || !q_rows_fit(*q, plan->rows, plan->hq))
     return FA_ERR_INVALID_ARG;
   if (!(k_scale >= 0.f && k_scale < INFINITY && v_scale >= 0.f && v_scale < INFINITY))
     return FA_ERR_INVALID_ARG;

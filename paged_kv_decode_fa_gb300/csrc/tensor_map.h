@@ -37,6 +37,15 @@ inline bool encode_map(CUtensorMap* map, fa_dtype dt, int rank, const void* base
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether q's rows can be described to the tensor copies: strides that are taken are
+// positive, whole 16 bytes and below 2^40 bytes.
+inline bool q_rows_fit(const fa_rows& q, int64_t rows, int heads) {
+  const auto fits = [](int64_t stride) { return stride > 0 && stride < (int64_t)1 << 39; };
+  return reinterpret_cast<uintptr_t>(q.data) % 16 == 0 && q.token_stride % 8 == 0 &&
+         q.head_stride % 8 == 0 && (rows <= 1 || fits(q.token_stride)) &&
+         (heads <= 1 || fits(q.head_stride));
+}
+
 // q [rows, heads, D]: a box is the `group` heads of 128 / group rows, 64 dims.
 inline bool encode_q_rows(CUtensorMap* map, fa_dtype dt, const fa_rows& q, int64_t rows,
                           int heads, int D, int group) {

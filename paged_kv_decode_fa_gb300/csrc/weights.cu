@@ -400,10 +400,9 @@ int weights_run(fa_weights_plan_s* plan, int sc, const fa_rows* q, const void* p
                 const float* head_k, const float* k_scales, float* weights, void* cuda_stream) {
   if (plan->few + plan->many == 0) return FA_OK;
   if (!q || !q->data || !paged_kv || !lse || !weights || num_pages <= 0 ||
-      reinterpret_cast<uintptr_t>(paged_kv) % 16 || reinterpret_cast<uintptr_t>(q->data) % 16 ||
+      num_pages >= (1 << 30) || reinterpret_cast<uintptr_t>(paged_kv) % 16 ||
       reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(weights) % 4 ||
-      q->token_stride % 8 || q->head_stride % 8 || num_pages >= (1 << 30) ||
-      (plan->rows > 1 && q->token_stride <= 0) || (plan->hq > 1 && q->head_stride <= 0))
+      !q_rows_fit(*q, plan->rows, plan->hq))
     return FA_ERR_INVALID_ARG;
   if (!std::isfinite(k_scale)) return FA_ERR_INVALID_ARG;
   int dev = 0;
@@ -430,6 +429,30 @@ int weights_run(fa_weights_plan_s* plan, int sc, const fa_rows* q, const void* p
   p.scale = sm_scale * k_scale * 1.4426950408889634f;
   const bool e4m3 = plan->kv_dtype == FA_DTYPE_E4M3;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  // all that can be refused comes before the first launch
+  CUtensorMap maps[2];
+  const void* tc = nullptr;
+  const int smem = plan->d == 128 ? wt::Smem<128>::kBytes : wt::Smem<64>::kBytes;
+  if (plan->many > 0) {
+    std::memset(maps, 0, sizeof maps);
+    if (!encode_q_rows(&maps[0], plan->q_dtype, *q, plan->rows, plan->hq, plan->d,
+                       plan->hq / plan->hkv) ||
+        !(e4m3 ? encode_codes(&maps[1], paged_kv, num_pages, plan->hkv, plan->d)
+               : encode_pages(&maps[1], plan->q_dtype, paged_kv, num_pages, plan->hkv, plan->d)))
+      return FA_ERR_CUDA;
+    tc = plan->d == 128 ? find_weights_tc_kernel<128>(plan->q_dtype, e4m3, sc)
+                        : find_weights_tc_kernel<64>(plan->q_dtype, e4m3, sc);
+    if (!plan->ready[sc]) {
+      // the kernel's warpgroups share out the registers it is launched with
+      cudaFuncAttributes attr;
+      if (cudaFuncGetAttributes(&attr, tc) != cudaSuccess ||
+          (e4m3 && attr.numRegs < wt::kLaunchRegs) ||
+          cudaFuncSetAttribute(tc, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+              cudaSuccess)
+        return FA_ERR_CUDA;
+      plan->ready[sc] = true;
+    }
+  }
   if (plan->few > 0) {
     const WeightsFn f = plan->d == 128 ? find_weights_kernel<128>(plan->q_dtype, e4m3, sc)
                                        : find_weights_kernel<64>(plan->q_dtype, e4m3, sc);
@@ -441,29 +464,9 @@ int weights_run(fa_weights_plan_s* plan, int sc, const fa_rows* q, const void* p
   }
   if (plan->many > 0) {
     p.units += plan->few;
-    const int G = plan->hq / plan->hkv;
-    CUtensorMap maps[2];
-    std::memset(maps, 0, sizeof maps);
-    if (!encode_q_rows(&maps[0], plan->q_dtype, *q, plan->rows, plan->hq, plan->d, G) ||
-        !(e4m3 ? encode_codes(&maps[1], paged_kv, num_pages, plan->hkv, plan->d)
-               : encode_pages(&maps[1], plan->q_dtype, paged_kv, num_pages, plan->hkv, plan->d)))
-      return FA_ERR_CUDA;
-    const void* f = plan->d == 128 ? find_weights_tc_kernel<128>(plan->q_dtype, e4m3, sc)
-                                   : find_weights_tc_kernel<64>(plan->q_dtype, e4m3, sc);
-    const int smem = plan->d == 128 ? wt::Smem<128>::kBytes : wt::Smem<64>::kBytes;
     int jobs = (int)(plan->many * plan->hkv);
     void* args[4] = {&maps[0], &maps[1], &p, &jobs};
-    if (!plan->ready[sc]) {
-      // the kernel's warpgroups share out the registers it is launched with
-      cudaFuncAttributes attr;
-      if (cudaFuncGetAttributes(&attr, f) != cudaSuccess ||
-          (e4m3 && attr.numRegs < wt::kLaunchRegs) ||
-          cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-              cudaSuccess)
-        return FA_ERR_CUDA;
-      plan->ready[sc] = true;
-    }
-    if (cudaLaunchKernel(f, dim3((unsigned)std::min(jobs, plan->sms)), dim3(wt::threads(e4m3)),
+    if (cudaLaunchKernel(tc, dim3((unsigned)std::min(jobs, plan->sms)), dim3(wt::threads(e4m3)),
                          args, (size_t)smem, st) != cudaSuccess)
       return FA_ERR_CUDA;
   }
