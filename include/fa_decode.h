@@ -838,12 +838,13 @@ int fa_weights_plan(const int32_t* indptr_host, const int32_t* indices_dev,
  *            outside [0, num_pages) is skipped and sets the device-check word.
  *  k_scale   per-tensor scale of an E4M3 cache's K; 1 for other kv types.
  *  lse       [rows, num_qo_heads] float32, device: what the attention of these rows
- *            returned (natural log); a row of -inf adds nothing.
+ *            returned (natural log); a row of -inf adds nothing, whatever its q.
  *  weights   read and written, as above.
- * One kernel on cuda_stream, no allocation, no synchronisation.  Each token gets one
- * addition a run, so results are bitwise reproducible, but for pages that two
- * requests (or two entries of one) share: they get all their requests' weights, in
- * no fixed order of the fp32 additions.
+ * One or two kernels on cuda_stream (one for the requests of up to eight columns -
+ * query rows x heads of a kv head -, one for the others), no allocation, no
+ * synchronisation.  Each token gets one addition a run, so results are bitwise
+ * reproducible, but for pages that two requests (or two entries of one) share: they get
+ * all their requests' weights, in no fixed order of the fp32 additions.
  * Errors as fa_prefill_run. */
 int fa_weights_run(fa_weights_plan_t plan, const fa_rows* q, const void* paged_kv,
                    int64_t num_pages, float sm_scale, float k_scale, const float* lse,
