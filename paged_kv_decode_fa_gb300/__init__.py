@@ -322,11 +322,19 @@ def _host_i32(t) -> np.ndarray:
     if isinstance(t, torch.Tensor):
         if t.device.type == "cpu" and t.dtype == torch.int32 and t.is_contiguous():
             return t.detach().numpy()  # no copy
-        t = t.detach().to("cpu")
-        return np.ascontiguousarray(t.numpy(), dtype=np.int32)
+        t = t.detach().to("cpu").numpy()
     if isinstance(t, np.ndarray) and t.dtype == np.int32 and t.flags.c_contiguous:
         return t
-    return np.ascontiguousarray(np.asarray(t), dtype=np.int32)
+    t = np.asarray(t)
+    try:
+        with np.errstate(invalid="ignore"):
+            a = np.ascontiguousarray(t, dtype=np.int32)
+        fits = t.dtype == np.int32 or np.array_equal(a, t.reshape(a.shape))
+    except OverflowError:
+        fits = False
+    if not fits:
+        raise ValueError("host arrays must hold whole numbers of 32 bits")
+    return a
 
 
 def _host_i32_ptr(t):
@@ -1614,10 +1622,10 @@ def plan_evict(indptr, indices: torch.Tensor, last_page_len, keep, num_kv_heads:
         raise ValueError("last_page_len shorter than the batch")
     budgets = []
     for v in (keep, recent):
-        a = np.full(B, v, np.int64) if np.ndim(v) == 0 else np.asarray(_host_i32(v), np.int64)
-        if a.shape != (B,) or (a < 0).any() or (a >= 2 ** 31).any():
+        a = _host_i32(np.full(B, v) if np.ndim(v) == 0 else v)
+        if a.shape != (B,) or (a < 0).any():
             raise ValueError("keep and recent must be one number, or one per request, from 0")
-        budgets.append(np.ascontiguousarray(a, np.int32))
+        budgets.append(a)
     _check_indices(indices, indptr_p, B)
     total = max(_i32_at(indptr_p, B), 0) * page_size
     workspace = _plan_workspace(
