@@ -61,21 +61,6 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       : "memory");
 }
 
-// Non-blocking probe of an mbarrier phase (try_wait may suspend the thread
-// for a while, which would stall a scheduler polling several barriers).
-// Called by a whole warp: lane 0's answer is everyone's.
-__device__ __forceinline__ bool ready(const uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(dev::smem_addr(bar)), "r"(parity)
-      : "memory");
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
 __device__ __forceinline__ void fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
