@@ -822,8 +822,8 @@ size_t fa_weights_workspace_size(int batch, int64_t total_pages);
 /* plan: arguments as fa_prefill_plan, with any n_i >= 0 (rows before a request's
  * first token see nothing): one row a request after a decode step, or the rows
  * of a prompt or of its last tokens.  Built for page_size 16, head_dim 64 and 128,
- * groups 1, 2, 4, 8 and (q, kv) = (BF16, BF16), (F16, F16), (BF16, E4M3),
- * (F16, E4M3).  Errors as fa_decode_plan. */
+ * groups 1, 2, 4, 8, (q, kv) = (BF16, BF16), (F16, F16), (BF16, E4M3), (F16, E4M3) and
+ * up to 2^26 columns (n_i x group) a request.  Errors as fa_decode_plan. */
 int fa_weights_plan(const int32_t* indptr_host, const int32_t* indices_dev,
                     const int32_t* last_page_len_host, const int32_t* qo_indptr_host, int batch,
                     int num_qo_heads, int num_kv_heads, int head_dim, int page_size,

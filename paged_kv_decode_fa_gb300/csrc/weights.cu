@@ -347,6 +347,9 @@ int run_pages(int64_t total_pages, int heads, int sms) {
 // columns 33 and 83; over an E4M3 cache 29 and 29, 30 and 42, 35 and 70.)
 constexpr int kFewColumns = 8;
 constexpr int kTcPages = 2 * wt::kPages;
+// Columns of one request.  A job passes through them all, 128 a tile of at most 1.7 us
+// (2460 cycles with masks, at 1.5 GHz), and the kernel's other warps wait for it 2 s.
+constexpr int64_t kMostColumns = (int64_t)1 << 26;
 
 // Runs of a batch's requests of many columns (`many`) or of the others; -1 for
 // malformed arguments.
@@ -508,6 +511,9 @@ int fa_weights_plan(const int32_t* indptr_host, const int32_t* indices_dev,
   // the arguments are checked before any CUDA call
   const int64_t many = units(true, kTcPages, nullptr);
   if (many < 0) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < batch; ++i)
+    if (((int64_t)qo_indptr_host[i + 1] - qo_indptr_host[i]) * G > kMostColumns)
+      return FA_ERR_UNSUPPORTED;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FA_ERR_CUDA;

@@ -11,8 +11,9 @@
 //    copied aside, and warps 12-19 widen them (exactly) into the same layout;
 //  - warp 8, one lane, issues the MMAs into two score buffers a block;
 //  - warps 0-3 and 4-7 turn the scores of the two blocks into sums.
-// The grid is persistent and nothing waits for a whole CTA between jobs.  Waits are
-// bounded as in prefill.cuh.
+// The grid is persistent and nothing waits for a whole CTA between jobs.  Every wait is
+// bounded (2 s; a job takes less, by the plan's limit on columns); one that runs out sets
+// bit 1 of the device-check word and the CTA drains.
 //
 // What bounds it.  32 rows of 4 heads over 16 prompts of 2048-8192 tokens, 8 kv heads:
 // 36 us from a 16-bit cache (168 MB: 25 us at the copy rate), where a job of one
