@@ -21,13 +21,15 @@
 //     and written once.  Rows already in their slots are left.
 //
 // What bounds it.  64 requests of 2048-8192 tokens kept to 2048 (8 kv heads, head_dim 128,
-// bf16), a CTA each: 219 us for a first eviction, 1.07 GB moved = 4.9 TB/s, 0.73 of the
-// copy rate; 24 us of it select, in which no row moves.  (129 us over the same cache
-// again and again, whose kept rows lie together.)  One E4M3 request of 65536 tokens kept
-// to 8000, eight CTAs a kv head: 31 us, the border's four passes 11 and the rows 10: the
-// cluster's barriers and chains of loads.  With 256 threads there as well 51 us; ranks
-// looked up a chunk at a time, in front of its rows, 54.  In the batch's loop, pieces'
-// addresses by divisions a piece cost 40-60 us, a cluster barrier a chunk 15.
+// bf16), a CTA each: 219-231 us for a first eviction, 1.07 GB moved = 4.6-4.9 TB/s,
+// 0.70-0.73 of the copy rate; 24 us of it select, in which no row moves.  One E4M3 request
+// of 65536 tokens kept to 8000, eight CTAs a kv head: 49 us, 34 MB (5.1 at the copy rate):
+// the cluster's barriers and chains of loads, the border's four passes 11 of them.
+// Evicted again and again, the two calls take 129 and 31 us, in which 256 of 2048 and 33
+// of 8000 ranks a head move (the recent tokens alone).  Measured so: with 256 threads
+// for the long request as well 51 us for 31; ranks looked up a chunk at a time, in front of
+// its rows, 54.  In the batch's loop, pieces' addresses by divisions a piece cost 40-60 us,
+// a cluster barrier a chunk 15.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

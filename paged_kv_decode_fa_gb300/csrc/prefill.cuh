@@ -52,11 +52,11 @@
 // however large its v - 2^-32 sum |v| in all (2^-25 with the reference at the score).
 //
 // What bounds it.  Long prompts: the tensor cores under the power limit.  8192 rows on a
-// context of 24576 (32 / 8 heads, head_dim 128, bf16): 2.44-2.57 ms = 1.50-1.58
-// PFLOP/s, 0.85-0.90 of what cuBLAS holds for seconds (0.78 of its burst).  A
+// context of 24576 (32 / 8 heads, head_dim 128, bf16): 2.44-2.62 ms = 1.47-1.58
+// PFLOP/s, 0.84-0.90 of what cuBLAS holds for seconds (0.78 of its burst).  A
 // tile of both blocks takes 2100-2600 cycles: 2048 of MMAs at head_dim 128 (1024 at
 // 64, where the two softmaxes, 1250 cycles each and half overlapped, set it).  Whole
-// prompts of 2048-6144 tokens 1.06-1.20 ms (1.35-1.52): an item's output and the next
+// prompts of 2048-6144 tokens 1.06-1.24 ms (1.30-1.52): an item's output and the next
 // one's first scores cost about two tiles, of 17 on average.
 // On the way (8192 rows on 24576): 4.52 ms with the MMAs issued by a whole warp and
 // 514 bytes of spills in the softmax; 2.65 with the registers split by warpgroup; 2.58
