@@ -642,7 +642,8 @@ int fa_append_plan(const int32_t* indptr_host, const int32_t* indices_dev,
  *                  each axis, any int32.  Kept by pointer and read by every run
  *                  of this plan, so that they may change between runs.
  *  pair_axis_host  [rotary_dim / 2] int32, host: 0 to num_axes - 1 each.  Read
- *                  during the call; rotary_dim is 16 at least.
+ *                  during the call; rotary_dim above 0 and up to head_dim
+ *                  (FA_ERR_INVALID_ARG otherwise).
  * Arguments, runs and errors otherwise as fa_append_plan. */
 int fa_append_plan_axes(const int32_t* indptr_host, const int32_t* indices_dev,
                         const int32_t* last_page_len_host, const int32_t* append_indptr_host,
