@@ -726,7 +726,7 @@ typedef struct fa_prefill_plan_s* fa_prefill_plan_t;
 /* Workspace that fa_prefill_plan needs for this batch (the same host arrays), on
  * the current device: the work list, fp32 partial states of rows whose keys
  * are split over SMs (few rows over long contexts), and, for an E4M3 cache, its
- * pages in bf16 and its K scales by token (a little over twice the bytes of the
+ * pages in bf16 and its scales by token (a little over twice the bytes of the
  * requests' pages).  0 for invalid arguments. */
 size_t fa_prefill_workspace_size(const int32_t* indptr_host, const int32_t* last_page_len_host,
                                  const int32_t* qo_indptr_host, int batch, int num_qo_heads,
@@ -776,9 +776,9 @@ int fa_prefill_run(fa_prefill_plan_t plan, const fa_rows* q, const void* paged_k
  * fa_decode_run_head_scales, fa_decode_run_token_scales and
  * fa_decode_run_block_scales read them (0 or positive).  K's multiply the logits in
  * fp32.  V's multiply the output in fp32 where there is one per tensor or per kv head;
- * those per token and per block multiply the elements, which are then rounded to
- * bf16 (exactly where the scale is a power of two, as fa_append_run_block_scales
- * writes them). */
+ * those per token the softmax weights, before these are rounded; those per block the
+ * elements, which are then rounded to bf16 (exactly where the scale is a power of
+ * two, as fa_append_run_block_scales writes them). */
 int fa_prefill_run_head_scales(fa_prefill_plan_t plan, const fa_rows* q, const void* paged_kv,
                                int64_t num_pages, float sm_scale, const float* k_head_scales,
                                const float* v_head_scales, void* o, float* lse,

@@ -176,12 +176,13 @@ void make_work(const std::vector<Block>& blocks, int heads, int max_ctas, Prefil
 }
 
 // Device-check word, the work list, the table entries to widen, then the partial
-// states and, for an E4M3 cache, its pages in q's type.
+// states and, for an E4M3 cache, its scales by table entry and its pages in q's type.
 struct PrefillLayout {
-  size_t offsets, items, merge, entries, meta, part_o, part_lse, scales, wide, total;
+  size_t offsets, items, merge, entries, meta, part_o, part_lse, scales, rests, wide, total;
 };
 
-// scale_bytes, wide_bytes: of an E4M3 cache's K scales by token and its pages.
+// scale_bytes, wide_bytes: of an E4M3 cache's scales by token (K's, and the rests of
+// V's), and its pages.
 PrefillLayout layout_of(const PrefillWork& w, size_t entries, size_t scale_bytes,
                         size_t wide_bytes, int D) {
   PrefillLayout L;
@@ -193,7 +194,8 @@ PrefillLayout layout_of(const PrefillWork& w, size_t entries, size_t scale_bytes
   L.part_o = L.meta;
   L.part_lse = align_up(L.part_o + 4 * (size_t)w.slots * 256 * D);
   L.scales = align_up(L.part_lse + 4 * (size_t)w.slots * 256);
-  L.wide = align_up(L.scales + scale_bytes);
+  L.rests = align_up(L.scales + scale_bytes);
+  L.wide = align_up(L.rests + scale_bytes);
   L.total = align_up(L.wide + wide_bytes);
   return L;
 }
@@ -259,15 +261,17 @@ struct WidenParams {
   const float* k_scales;    // kScalePerToken [pages, Hkv, 16], kScalePerBlock [pages, Hkv]
   const float* v_scales;
   float* out_scales;        // the K scales by table entry: [entries, Hkv(, 16)]
+  float* out_rests;         // per token: the rests of V's likewise (pf::scale_rest)
   int* err;
   int64_t num_pages;
   int hkv;
 };
 
 // One page of an E4M3 cache in bf16: the codes as they are (4 significant bits:
-// exact).  Scales per token or block: V's multiply its elements (exact for powers of
-// two; otherwise one rounding of 2^-9, as the weights' own); K's are laid out by table
-// entry, for the scores, whose precision lse has.  A streaming pass over the cache, read
+// exact).  Scales per block: V's multiply its elements (exact for powers of two, which
+// append writes; otherwise one rounding, as the weights' own); per token the power of
+// two in V's, exactly, and the rests are laid out by table entry for the weights.  K's
+// are laid out so for the scores, whose precision lse has.  A streaming pass over the cache, read
 // once here and as bf16 by every block of rows: bound by HBM, 97 us for the 202 MB of
 // 6155 pages of 8 heads of 128 (6.2 TB/s, read and written).
 template <int D, int SC>
@@ -281,8 +285,12 @@ __global__ void __launch_bounds__(256) fa_prefill_widen_kernel(const WidenParams
   uint4* dst = p.out + (int64_t)entry * groups * 2;
   if constexpr (SC != kScaleNone) {
     const int n = p.hkv * (SC == kScalePerToken ? kPageSize : 1);
-    for (int i = threadIdx.x; i < n; i += 256)
-      p.out_scales[(int64_t)entry * n + i] = ok ? __ldg(p.k_scales + (int64_t)page * n + i) : 0.f;
+    for (int i = threadIdx.x; i < n; i += 256) {
+      const int64_t from = (int64_t)page * n + i, to = (int64_t)entry * n + i;
+      p.out_scales[to] = ok ? __ldg(p.k_scales + from) : 0.f;
+      if constexpr (SC == kScalePerToken)
+        p.out_rests[to] = ok ? pf::scale_rest(__ldg(p.v_scales + from)) : 1.f;
+    }
   }
   for (int i = threadIdx.x; i < groups; i += 256) {
     const uint4 c = ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
@@ -291,7 +299,8 @@ __global__ void __launch_bounds__(256) fa_prefill_widen_kernel(const WidenParams
       const int row = i / (D / 16), head = row % p.hkv, slot = row / p.hkv % kPageSize;
       const int64_t at = (int64_t)page * p.hkv + head;
       if (ok && row >= kPageSize * p.hkv)
-        scale = __ldg(p.v_scales + (SC == kScalePerToken ? at * kPageSize + slot : at));
+        scale = SC == kScalePerToken ? pf::scale_power(__ldg(p.v_scales + at * kPageSize + slot))
+                                     : __ldg(p.v_scales + at);
     }
     const uint32_t in[4] = {c.x, c.y, c.z, c.w};
     uint32_t out[8];
@@ -438,6 +447,7 @@ int prefill_run(fa_prefill_plan_s* plan, int sc, const fa_rows* q, const void* p
   p.kv = kv;
   p.num_kv_heads = hkv;
   p.k_scales = reinterpret_cast<const float*>(plan->ws + plan->layout.scales);
+  p.v_rests = reinterpret_cast<const float*>(plan->ws + plan->layout.rests);
   p.o = o;
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(plan->ws + plan->layout.part_o);
@@ -460,6 +470,7 @@ int prefill_run(fa_prefill_plan_s* plan, int sc, const fa_rows* q, const void* p
     w.k_scales = k_scales;
     w.v_scales = v_scales;
     w.out_scales = reinterpret_cast<float*>(plan->ws + plan->layout.scales);
+    w.out_rests = reinterpret_cast<float*>(plan->ws + plan->layout.rests);
     w.err = p.err;
     w.num_pages = num_pages;
     w.hkv = hkv;

@@ -113,6 +113,7 @@ struct Params {
   const void* kv;
   const float* k_scales;       // SC: times scores; [table entries, Hkv, 16] by token or
                                // [table entries, Hkv] by block
+  const float* v_rests;        // SC per token: V's rests, times weights, [entries, Hkv, 16]
   int num_kv_heads;
   void* o;                     // [rows, Hq, D]
   float* lse;                  // [rows, Hq] or nullptr
@@ -167,12 +168,16 @@ struct Smem {
   static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
   // kv_full[n], kv_empty[n]; q_full, q_empty, s_full [2], p_full [2][2], o_full, o_empty [2],
   // v_there, v_clean; sc_full, sc_empty [kScaleSlots]
-  static constexpr int kScaleSlots = 3;
+  static constexpr int kScaleSlots = D == 128 ? 2 : 3;
+  static constexpr int kScaleBytes = kTok * 8;           // of a slot: K's scales, V's rests
   static constexpr int kNumBars = 2 * kSlots + 16 + 2 * kScaleSlots;
   static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
   static constexpr int kOffProgress = kOffTmem + 4;      // what the softmax warps count
-  static constexpr int kOffScales = kOffTmem + 16;       // SC: K scales of a tile's tokens
-  static constexpr int kBytes = kOffScales + kScaleSlots * kTok * 4 + 1024;  // and alignment
+  static constexpr int kOffScales = kOffTmem + 16;       // SC per token: of a tile's tokens
+  // Room to start at a multiple of 1024 bytes.  (The array is declared so, and does; the
+  // kernel checks that this room is enough.)
+  static constexpr int kPad = 512;
+  static constexpr int kBytes = kPad + kOffScales + kScaleSlots * kScaleBytes;
   static_assert(kOffScales % 16 == 0, "bulk copies");
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
@@ -205,6 +210,26 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, bool& a
     before = now;
     t0 = dev::global_timer_ns();
   }
+}
+
+// A scale of V per token in two factors: a power of two, which V's elements take exactly,
+// and the rest in [1, 2), which the weights take before they are rounded.  (The whole of
+// it multiplied into the elements rounds each of them, as much as the weights' own
+// rounding: 2.6e-3 of the output for 2.1e-3.)  What is no normal number is the first.
+__device__ __forceinline__ float scale_power(float s) {
+  const uint32_t b = __float_as_uint(s), e = b & 0x7f800000u;
+  return e == 0 || e == 0x7f800000u ? s : __uint_as_float(b & 0xff800000u);
+}
+__device__ __forceinline__ float scale_rest(float s) {
+  const uint32_t b = __float_as_uint(s), e = b & 0x7f800000u;
+  return e == 0 || e == 0x7f800000u ? 1.f : __uint_as_float((b & 0x7fffffu) | 0x3f800000u);
+}
+
+// a * b of two pairs
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 }  // namespace pf
@@ -270,7 +295,10 @@ __device__ __forceinline__ void fix_row(const pf::Params& p, int entry, int seen
       const int64_t at = (int64_t)(entry + t / kPageSize) * p.num_kv_heads + head;
       s *= __ldg(p.k_scales + (SC == kScalePerToken ? at * kPageSize + t % kPageSize : at));
     }
-    const float w = dev::fast_exp2(fmaf(s, scale, -m));
+    float w = dev::fast_exp2(fmaf(s, scale, -m));
+    if constexpr (SC == kScalePerToken)
+      w *= __ldg(p.v_rests + ((int64_t)(entry + t / kPageSize) * p.num_kv_heads + head) *
+                                 kPageSize + t % kPageSize);
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = fmaf(w, v[i], o[i]);
   }
@@ -286,7 +314,8 @@ __device__ __forceinline__ void fix_row(const pf::Params& p, int entry, int seen
 
 // SC: K's elements are their scales short (an E4M3 cache's, kScalePerToken or
 // kScalePerBlock): the scales multiply the scores, whose precision lse has.  Per token
-// they come through a ring of their own; per block, a group of 16 columns, they join
+// they come through a ring of their own, with the rests of V's (scale_rest), which
+// multiply the weights; per block, a group of 16 columns, they join
 // the factors of its maximum and exponents, read a tile ahead.  (16 requests of 500
 // rows behind 1024-8192, 64 / 8 heads: 1236 us per token, 1104 per block, for 1070
 // with the scales multiplied into K's elements, whose rounding to bf16 then cost
@@ -304,7 +333,12 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
   constexpr uint32_t kIdescPV = instr_desc(kBf16, kRows, D, 1);
   constexpr int kSlots = S::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (dev::smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t pad = (1024u - (dev::smem_addr(smem_raw) & 1023u)) & 1023u;
+  if (pad > S::kPad) {
+    atomicOr(p.err, 2);
+    return;
+  }
+  uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = dev::smem_addr(smem), count = sbase + S::kOffProgress;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
   uint64_t* kv_full = bars;
@@ -346,6 +380,14 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     }
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(count), "r"(0) : "memory");
     dev::fence_barrier_init();
+  }
+  if constexpr (SC == kScalePerToken) {
+    // what stands behind a tile's last page meets weights of 0, so it has to be finite: 0
+    // at first, then what a tile before left there
+    for (int i = threadIdx.x; i < S::kScaleSlots * S::kScaleBytes / 4; i += kThreads)
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(sbase + S::kOffScales + 4 * i), "r"(0)
+                   : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -450,7 +492,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         const int last_block = w.tokens > block_tokens ? 1 : 0;
         const int keys = w.keys(last_block, block_tokens), all = w.tiles(last_block, block_tokens);
         n += 2 * all;
-        if constexpr (SC == kScalePerToken) {  // the item's K scales, a tile a slot
+        if constexpr (SC == kScalePerToken) {  // the item's scales, a tile a slot
           const int pages = (min(keys, w.t1 * kTok) + kPageSize - 1) / kPageSize;
           for (int j = 0; j < all; ++j, ++sn) {
             const int slot = sn % S::kScaleSlots, page = (w.t0 + j) * kPages + lane;
@@ -458,13 +500,16 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             pf::mbar_wait(dev::smem_addr(&sc_empty[slot]),
                           (uint32_t)(((sn / S::kScaleSlots) & 1) ^ 1), aborted, p.err, count);
             const int there = min(kPages, pages - (w.t0 + j) * kPages);
-            if (lane == 0) dev::mbar_arrive_expect_tx(full, there * kPageSize * 4);
+            if (lane == 0) dev::mbar_arrive_expect_tx(full, there * kPageSize * 8);
             __syncwarp();
-            if (lane < there)
-              dev::bulk_load(sbase + S::kOffScales + slot * (kTok * 4) + lane * (kPageSize * 4),
-                             p.k_scales + ((int64_t)(w.entry + page) * p.num_kv_heads + w.head) *
-                                              kPageSize,
-                             kPageSize * 4, full);
+            if (lane < there) {
+              const int64_t at =
+                  ((int64_t)(w.entry + page) * p.num_kv_heads + w.head) * kPageSize;
+              const uint32_t to =
+                  sbase + S::kOffScales + slot * S::kScaleBytes + lane * (kPageSize * 4);
+              dev::bulk_load(to, p.k_scales + at, kPageSize * 4, full);
+              dev::bulk_load(to + kTok * 4, p.v_rests + at, kPageSize * 4, full);
+            }
             __syncwarp();
           }
         }
@@ -646,19 +691,18 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(raw[c][i]);
           }
         }
+        const uint32_t scales_at = sbase + S::kOffScales + sn % S::kScaleSlots * S::kScaleBytes;
         if constexpr (SC == kScalePerToken) {
           scales_full();
-          const uint32_t at = sbase + S::kOffScales + sn % S::kScaleSlots * (kTok * 4);
 #pragma unroll
           for (int i = 0; i < kTok / 4; ++i) {
             float k[4];
             asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                          : "=f"(k[0]), "=f"(k[1]), "=f"(k[2]), "=f"(k[3])
-                         : "r"(at + i * 16));
+                         : "r"(scales_at + i * 16));
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[4 * i + e] *= k[e];
           }
-          scales_read();
         }
         if (fewest < (j + 1) * kTok) {
           const int valid = seen - j * kTok;
@@ -715,15 +759,26 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kTok / 32; ++c) {
           uint32_t pk[16];
+          uint64_t rests[2];  // SC per token: V's, of four columns
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
+            if constexpr (SC == kScalePerToken)
+              if (i % 2 == 0)
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                             : "=l"(rests[0]), "=l"(rests[1])
+                             : "r"(scales_at + kTok * 4 + (32 * c + 2 * i) * 4));
             float x0, x1;
             const float factor = by_page[2 * c + i / 8];
             f2_split(fma2(f2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), f2(factor, factor),
                           neg_m2), x0, x1);
             const float a0 = dev::fast_exp2(x0), a1 = dev::fast_exp2(x1);
-            pk[i] = mma::pack2(a0, a1, kBf16);
             acc[i % 4] = add2(acc[i % 4], f2(a0, a1));
+            if constexpr (SC == kScalePerToken) {
+              f2_split(mul2(f2(a0, a1), rests[i % 2]), x0, x1);
+              pk[i] = mma::pack2(x0, x1, kBf16);
+            } else {
+              pk[i] = mma::pack2(a0, a1, kBf16);
+            }
           }
           st16u(tS + c * 16, pk);
           if (c % 2) {  // half of the weights: P V may begin on them
@@ -733,6 +788,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             if (lane == 0) dev::mbar_arrive(dev::smem_addr(&p_full[2 * X + c / 2]));
           }
         }
+        if constexpr (SC == kScalePerToken) scales_read();
         float lo, hi;
         f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), lo, hi);
         d += lo + hi;
