@@ -785,14 +785,16 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             fence_before();
             __syncwarp();
-            if (lane == 0) dev::mbar_arrive(dev::smem_addr(&p_full[2 * X + c / 2]));
+            if (lane == 0) {
+              dev::mbar_arrive(dev::smem_addr(&p_full[2 * X + c / 2]));
+              if (c / 2) count_on(count);
+            }
           }
         }
         if constexpr (SC == kScalePerToken) scales_read();
         float lo, hi;
         f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), lo, hi);
         d += lo + hi;
-        if (lane == 0) count_on(count);
       }
       skip_scales(w, tiles);
       // ---- the row's output
