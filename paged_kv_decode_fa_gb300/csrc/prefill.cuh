@@ -315,11 +315,12 @@ __device__ __forceinline__ void fix_row(const pf::Params& p, int entry, int seen
 // SC: K's elements are their scales short (an E4M3 cache's, kScalePerToken or
 // kScalePerBlock): the scales multiply the scores, whose precision lse has.  Per token
 // they come through a ring of their own, with the rests of V's (scale_rest), which
-// multiply the weights; per block, a group of 16 columns, they join
-// the factors of its maximum and exponents, read a tile ahead.  (16 requests of 500
-// rows behind 1024-8192, 64 / 8 heads: 1236 us per token, 1104 per block, for 1070
-// with the scales multiplied into K's elements, whose rounding to bf16 then cost
-// lse 2^-9 of the logits unless they were powers of two.)
+// multiply the weights; per block, a group of 16 columns, they join the factors of its
+// maximum and exponents, read a tile ahead.  (16 requests of 500 rows behind 1024-8192,
+// 64 / 8 heads: 1370 us per token, 1113 per block, 1082 per tensor.  K's scales multiplied
+// into K's elements, 1070, cost lse 2^-9 of the logits by their rounding to bf16; V's per
+// token whole in V's elements, 1239, a quarter more of o's error.  The loads of a column's
+// two factors, the same for all lanes, are what the per-token form waits for.)
 template <typename T, int D, int SC>
 __global__ void __launch_bounds__(pf::kThreads, 1)
     fa_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
