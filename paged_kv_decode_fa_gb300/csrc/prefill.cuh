@@ -319,8 +319,9 @@ __device__ __forceinline__ void fix_row(const pf::Params& p, int entry, int seen
 // maximum and exponents, read a tile ahead.  (16 requests of 500 rows behind 1024-8192,
 // 64 / 8 heads: 1370 us per token, 1113 per block, 1082 per tensor.  K's scales multiplied
 // into K's elements, 1070, cost lse 2^-9 of the logits by their rounding to bf16; V's per
-// token whole in V's elements, 1239, a quarter more of o's error.  The loads of a column's
-// two factors, the same for all lanes, are what the per-token form waits for.)
+// token whole in V's elements, 1239, a quarter more of o's error.  The per-token form's
+// softmax is longer by the two factors' loads and products: issue slots are half full
+// under it, shared memory a third; loading the factors earlier changed nothing.)
 template <typename T, int D, int SC>
 __global__ void __launch_bounds__(pf::kThreads, 1)
     fa_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
